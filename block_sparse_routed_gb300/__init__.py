@@ -14,6 +14,9 @@ Two calls, backed by hand-written CUDA kernels in a C-ABI library:
 * ``sparse_attn_spark_fwd`` / ``spark_attn``: Spark's merged attention: the
   exact lists plus one summary key per skipped video block, from a per-head
   anchor (the mean of the target-video queries).
+* ``cache_write`` / ``cache_read`` / ``paged_attn``: a paged key/value cache of
+  many sequences (BF16, or E4M3 with a scale a row) and attention of new
+  tokens over it (``paged.py``).
 * ``spark_reblock``: Spark's token reblocking, a per-head permutation of the
   tokens into 64-token blocks by a landmark tree, and its inverse.
 
@@ -33,6 +36,7 @@ from ._native import (  # noqa: F401
     SA_ETIMEOUT,
     SA_EUNSUPPORTED,
     SA_OK,
+    SaPagedParams,
     SaParams,
     SaReblockParams,
     SaReweightParams,
@@ -42,10 +46,25 @@ from ._native import (  # noqa: F401
     sparse_attn_status_string,
 )
 
+from .paged import (  # noqa: F401
+    cache_read,
+    cache_write,
+    paged_attn,
+    paged_cache,
+    paged_workspace,
+    paged_ws_bytes,
+)
+
 __all__ = [
     "Params",
     "SparseAttnError",
+    "cache_read",
+    "cache_write",
     "load_library",
+    "paged_attn",
+    "paged_cache",
+    "paged_workspace",
+    "paged_ws_bytes",
     "sparse_attn",
     "sparse_attn_fwd",
     "sparse_attn_last_device_status",

@@ -24,6 +24,9 @@ SA_ETIMEOUT = 5
 SA_TAIL_DENSE = 0
 SA_TAIL_PAD = 1
 
+SA_CACHE_BF16 = 0
+SA_CACHE_E4M3 = 1
+
 ENTRY_POINTS = (
     "sparse_attn_query",
     "sparse_attn_plan",
@@ -36,6 +39,10 @@ ENTRY_POINTS = (
     "sparse_attn_fused",
     "sparse_attn_reblock_ws_bytes",
     "sparse_attn_spark_reblock",
+    "sparse_attn_cache_write",
+    "sparse_attn_cache_read",
+    "sparse_attn_paged_ws_bytes",
+    "sparse_attn_paged_fwd",
     "sparse_attn_last_device_status",
     "sparse_attn_set_single_probe_waits",
     "sparse_attn_last_cuda_error",
@@ -96,6 +103,30 @@ class SaReweightParams(ctypes.Structure):
     ]
 
 
+class SaPagedParams(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("kind", ctypes.c_int32),
+        ("pages", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("seqs", ctypes.c_int32),
+        ("table_width", ctypes.c_int32),
+        ("table_stride", ctypes.c_int64),
+        ("rows", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("Hq", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("a_token_stride", ctypes.c_int64),
+        ("a_head_stride", ctypes.c_int64),
+        ("b_token_stride", ctypes.c_int64),
+        ("b_head_stride", ctypes.c_int64),
+    ]
+
+
 class SparseAttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = int(status)
@@ -150,6 +181,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sparse_attn_reblock_ws_bytes.restype = ctypes.c_int
     lib.sparse_attn_spark_reblock.argtypes = [P(SaReblockParams), vp, vp, vp, vp, sz, vp]
     lib.sparse_attn_spark_reblock.restype = ctypes.c_int
+    lib.sparse_attn_cache_write.argtypes = [P(SaPagedParams)] + [vp] * 11
+    lib.sparse_attn_cache_write.restype = ctypes.c_int
+    lib.sparse_attn_cache_read.argtypes = [P(SaPagedParams)] + [vp] * 11
+    lib.sparse_attn_cache_read.restype = ctypes.c_int
+    lib.sparse_attn_paged_ws_bytes.argtypes = [P(SaPagedParams), P(ctypes.c_uint64)]
+    lib.sparse_attn_paged_ws_bytes.restype = ctypes.c_int
+    lib.sparse_attn_paged_fwd.argtypes = [P(SaPagedParams)] + [vp] * 11 + [sz, vp]
+    lib.sparse_attn_paged_fwd.restype = ctypes.c_int
     lib.sparse_attn_status_string.argtypes = [ctypes.c_int]
     lib.sparse_attn_status_string.restype = ctypes.c_char_p
     _lib = lib

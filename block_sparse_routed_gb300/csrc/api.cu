@@ -116,6 +116,12 @@ sa_status check_device() {
   return state[dev] == 1 ? SA_OK : SA_EUNSUPPORTED;
 }
 
+}  // namespace
+
+int sa::device_status() { return check_device(); }
+
+namespace {
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

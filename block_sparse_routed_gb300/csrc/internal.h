@@ -110,6 +110,10 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size
 // defined in api.cu); returns true when `e` is an error.
 bool cuda_failed(cudaError_t e);
 
+// SA_OK when the current device is an sm_103 part (cached per device), else
+// SA_EUNSUPPORTED or SA_ECUDA; an int of enum sa_status.
+int device_status();
+
 // Launchers (defined in the kernel translation units).
 cudaError_t launch_pool(const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_route_topk(const PlanArgs& a, cudaStream_t s);
@@ -146,6 +150,45 @@ cudaError_t launch_reblock(const ReblockArgs& r, cudaStream_t s);
 int anchor_chunks(int Nv);
 cudaError_t launch_video_query_mean(const uint16_t* q, float* partial, uint16_t* anchor, int H, int Nv,
                                     cudaStream_t s);
+
+// Paged key/value cache (see sparse_attn.h for the batch and its checks).
+struct PagedArgs {
+  int kind;                  // sa_cache_kind
+  int pages, H, page_size, page_shift;
+  int seqs, table_width, rows, max_new;
+  int64_t table_stride;
+  const int32_t* table;
+  const int32_t* row_start;  // [seqs + 1]
+  const int32_t* kv_len;     // [seqs]
+  uint8_t* k_pages;          // BF16 or E4M3 [pages, H, page_size, 128]
+  uint8_t* v_pages;
+  uint8_t* k_exp;            // [pages, H, page_size] (E4M3)
+  uint8_t* v_exp;
+  int32_t* status;           // device status word, or null
+};
+
+// Rows in (cache_write) or out (cache_read: contiguous).
+struct CacheRows {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t k_token, k_head, v_token, v_head;  // strides, elements
+};
+
+struct PagedAttnArgs {
+  PagedArgs c;
+  const uint16_t* q;
+  int64_t q_token, q_head;
+  int Hq, group;             // group = Hq / H query heads a key head
+  int causal, window;
+  float scale;
+  uint16_t* o;               // BF16 [rows, Hq, 128]
+  float* lse;                // [rows, Hq] or null
+};
+
+cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
+cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+
 size_t route_topk_smem_bytes(const Geometry& g);
 size_t attention_smem_bytes();
 

@@ -1,0 +1,186 @@
+// Writing rows of K and V into a paged cache and reading them back, for
+// sm_103a: BF16 rows are moved as they are; E4M3 rows are quantised with one
+// power-of-two scale a row (see include/sparse_attn.h for the format).
+//
+// Both are bound by memory: a row of one head is 256 bytes of BF16 against
+// 256, or 128 + 1, in the cache.  A warp takes one token and kHeads heads of
+// it; its halves take K and V, 16 lanes a row, 8 elements a lane, so a row's
+// largest magnitude is a 16-bit integer maximum over 8 values and four
+// shuffles.  The rows' loads do not wait for the look-up of the sequence and
+// its page; in cache_read they have to.
+#include <cstdint>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeads = 4;  // heads a warp moves at once
+
+// The row of page table that holds the token of packed row r, as the index
+// page * page_size * H + slot of head 0 (heads are page_size rows apart); -1
+// when there is none.  `pos` is the token's position (below 0: no token).
+__device__ __forceinline__ int64_t slot_of(const PagedArgs& c, int r, int lane, bool& member, int& pos) {
+  member = false;
+  pos = -1;
+  const int s = paged_find(c, r, lane);
+  if (s < 0) return -1;
+  bool bad;
+  const PagedSeq q = paged_seq(c, s, bad);
+  if (bad) {
+    if (lane == 0) paged_fail(c);
+    return -1;
+  }
+  if (r < q.row0 || r >= q.row0 + q.n) return -1;
+  member = true;
+  pos = q.len - q.n + (r - q.row0);
+  if (pos < 0) return -1;
+  const int page = c.table[s * c.table_stride + (pos >> c.page_shift)];
+  if (page < 0 || page >= c.pages) {
+    if (lane == 0) paged_fail(c);
+    return -1;
+  }
+  return (static_cast<int64_t>(page) * c.H << c.page_shift) + (pos & (c.page_size - 1));
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c, const CacheRows rows, int blocks_h) {
+  if (blockIdx.x == 0) paged_check_all(c);
+  const int lane = threadIdx.x % 32;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  if (item >= static_cast<int64_t>(c.rows) * blocks_h) return;
+  const int r = static_cast<int>(item / blocks_h), h0 = static_cast<int>(item % blocks_h) * kHeads;
+  const bool is_v = lane >= 16;
+  const int sub = lane % 16;
+  const uint16_t* src = (is_v ? rows.v + r * rows.v_token : rows.k + r * rows.k_token) + sub * 8;
+  const int64_t head = is_v ? rows.v_head : rows.k_head;
+  uint4 x[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (h0 + i < c.H) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (h0 + i) * head));
+  }
+  bool member;
+  int pos;
+  const int64_t slot = slot_of(c, r, lane, member, pos);
+  if (slot < 0) return;
+  uint8_t* pages = is_v ? c.v_pages : c.k_pages;
+  uint8_t* exps = is_v ? c.v_exp : c.k_exp;
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (h0 + i >= c.H) break;
+    const int64_t row = slot + (static_cast<int64_t>(h0 + i) << c.page_shift);
+    if constexpr (!kE4m3) {
+      *reinterpret_cast<uint4*>(pages + row * 256 + sub * 16) = x[i];
+    } else {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      // largest finite magnitude: BF16 bits without the sign order as integers
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t a = w[k] & 0x7FFF7FFFu;
+        m2 = __vmaxu2(m2, a & ~__vcmpgeu2(a, 0x7F807F80u));
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, d));
+      const uint32_t m = max(m2 >> 16, m2 & 0xFFFFu);
+      // amax = (1 + M / 128) 2^(E - 127) <= 1.75 * 2^8 * 2^e with M <= 96 for e = E - 135
+      const int e = max(1, static_cast<int>(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0));
+      const float inv = exp_scale(254 - e);
+      uint32_t code[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint16_t half[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t v = w[2 * k + t];
+          float lo = __uint_as_float(v << 16) * inv, hi = __uint_as_float(v & 0xFFFF0000u) * inv;
+          // the conversion would saturate an infinity: store NaN for it
+          if ((v & 0x7F80u) == 0x7F80u) lo = __uint_as_float(0x7FFFFFFFu);
+          if ((v & 0x7F800000u) == 0x7F800000u) hi = __uint_as_float(0x7FFFFFFFu);
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(half[t]) : "f"(hi), "f"(lo));
+        }
+        code[k] = half[0] | (static_cast<uint32_t>(half[1]) << 16);
+      }
+      *reinterpret_cast<uint2*>(pages + row * 128 + sub * 8) = make_uint2(code[0], code[1]);
+      if (sub == 0) exps[row] = static_cast<uint8_t>(e);
+    }
+  }
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const PagedArgs c, const CacheRows rows, int blocks_h) {
+  if (blockIdx.x == 0) paged_check_all(c);
+  const int lane = threadIdx.x % 32;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  if (item >= static_cast<int64_t>(c.rows) * blocks_h) return;
+  const int r = static_cast<int>(item / blocks_h), h0 = static_cast<int>(item % blocks_h) * kHeads;
+  const bool is_v = lane >= 16;
+  const int sub = lane % 16;
+  uint16_t* dst = (is_v ? rows.v + r * rows.v_token : rows.k + r * rows.k_token) + sub * 8;
+  const int64_t head = is_v ? rows.v_head : rows.k_head;
+  bool member;
+  int pos;
+  const int64_t slot = slot_of(c, r, lane, member, pos);
+  if (!member) return;
+  const uint8_t* pages = is_v ? c.v_pages : c.k_pages;
+  const uint8_t* exps = is_v ? c.v_exp : c.k_exp;
+  uint4 x[kHeads];
+  uint32_t e[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    e[i] = 0;
+    if (h0 + i >= c.H || slot < 0) continue;
+    const int64_t row = slot + (static_cast<int64_t>(h0 + i) << c.page_shift);
+    if constexpr (!kE4m3) {
+      x[i] = __ldg(reinterpret_cast<const uint4*>(pages + row * 256 + sub * 16));
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(pages + row * 128 + sub * 8));
+      x[i].x = v.x;
+      x[i].y = v.y;
+      e[i] = __ldg(exps + row);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (h0 + i >= c.H) break;
+    if constexpr (kE4m3) {
+      const float two = exp_scale(e[i]);
+      const uint32_t v[2] = {x[i].x, x[i].y};
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        e4m3x2_f32(static_cast<uint16_t>(v[k / 2] >> (16 * (k % 2))), lo, hi);
+        w[k] = pack_bf16x2(lo * two, hi * two);  // exact: 4 significant bits
+      }
+      x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *reinterpret_cast<uint4*>(dst + (h0 + i) * head) = x[i];
+  }
+}
+
+template <typename K>
+cudaError_t launch_rows(K kern, const PagedArgs& c, const CacheRows& r, cudaStream_t s) {
+  const int blocks_h = (c.H + kHeads - 1) / kHeads;
+  const int64_t items = static_cast<int64_t>(c.rows) * blocks_h;
+  const int64_t grid = (items + kThreads / 32 - 1) / (kThreads / 32);
+  kern<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(c, r, blocks_h);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStream_t s) {
+  return c.kind ? launch_rows(cache_write_kernel<true>, c, r, s) : launch_rows(cache_write_kernel<false>, c, r, s);
+}
+
+cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s) {
+  return c.kind ? launch_rows(cache_read_kernel<true>, c, r, s) : launch_rows(cache_read_kernel<false>, c, r, s);
+}
+
+}  // namespace sa

@@ -313,6 +313,124 @@ sa_status sparse_attn_spark_reblock(const sa_reblock_params* p, const void* x, i
                                     int32_t* inv, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Paged key/value cache, and attention of new tokens over it.  Whoever
+ * generates chunk by chunk (a video continued from a cached clip, a language
+ * model that serves many users) keeps K and V between calls, for many
+ * sequences of uneven length, and attends from the new tokens only.
+ *
+ * Cache.  k_pages, v_pages [pages, H, page_size, 128], contiguous, in one of
+ *   two kinds:
+ *   SA_CACHE_BF16  BF16 rows as they came.
+ *   SA_CACHE_E4M3  8-bit E4M3 codes, each row (one token of one head) with
+ *                  a power-of-two scale: with amax the row's largest finite
+ *                  magnitude, e is the smallest integer >= -126 such that
+ *                  amax <= 448 * 2^e, a code is x * 2^-e rounded to nearest
+ *                  even, and k_exp, v_exp uint8 [pages, H, page_size] hold
+ *                  e + 127.  Scaling by 2^e is exact both ways, so the
+ *                  code's own rounding is the only one, and what a code
+ *                  stands for is a BF16 value (above 2^127 * 1.9375 it is
+ *                  infinite).  NaN and infinities are stored as NaN.
+ * Batch (device memory, int32, read by every call).  Sequence s < seqs has
+ *   kv_len[s] tokens; token j is in slot j % page_size of page
+ *   table[s * table_stride + j / page_size].  The rows row_start[s] ..
+ *   row_start[s + 1] - 1 of a packed tensor are its last tokens: with n of
+ *   them, row i is the token at position kv_len[s] - n + i.  A position below
+ *   0 is no token: it is not written, reads as zeros and attends to nothing
+ *   (with causal = 0, to every token, like the others).  Rows before
+ *   row_start[0] or from row_start[seqs] on belong to no sequence and are
+ *   left as they were.
+ *   Table entries of pages that no token of the call needs are not read.  A
+ *   page may stand in several rows of the table (a shared prefix); a slot
+ *   that two rows of one write call reach holds either row's values after it,
+ *   in the E4M3 kind possibly one's codes and the other's exponent.
+ * Checked on the device, before any access that depends on it: 0 <=
+ *   row_start[s] <= row_start[s + 1] <= rows, at most max_new rows a sequence,
+ *   0 <= kv_len[s] <= table_width * page_size, and every page used in
+ *   [0, pages).  What fails is SA_EINVAL in the status word of `ws`
+ *   (sparse_attn_last_device_status): the sequence, or the tokens of the
+ *   page, are left out, and the outputs of that sequence are unspecified.
+ */
+typedef enum sa_cache_kind { SA_CACHE_BF16 = 0, SA_CACHE_E4M3 = 1 } sa_cache_kind;
+
+typedef struct sa_paged_params {
+  uint32_t abi_version;  /* must be SA_ABI_VERSION                              */
+  int32_t kind;          /* sa_cache_kind                                       */
+  int32_t pages;         /* pages of the pool, >= 1                             */
+  int32_t H;             /* key heads, >= 1                                     */
+  int32_t page_size;     /* tokens a page: 16, 32, 64 or 128                    */
+  int32_t D;             /* head dimension, must be 128                         */
+  int32_t seqs;          /* sequences, >= 0                                     */
+  int32_t table_width;   /* page-table entries a sequence, >= 0                 */
+  int64_t table_stride;  /* elements between the table rows, >= 0               */
+  int32_t rows;          /* rows of the packed tensors, >= 0                    */
+  int32_t max_new;       /* most rows of one sequence, >= 0 (rows is always
+                            right; a tight bound lets paged_fwd pick the form
+                            for few tokens)                                     */
+  int32_t Hq;            /* query heads, a multiple of H: query head i reads
+                            key head i / (Hq / H) (paged_fwd only)              */
+  int32_t causal;        /* 1: a row sees keys up to its own position; 0: all
+                            kv_len keys of its sequence (paged_fwd only)        */
+  int32_t window;        /* w > 0: only the last w of the keys a causal row
+                            sees, its own among them; 0: all (paged_fwd only)   */
+  float scale;           /* logit of a key: scale * (q . k), finite (paged_fwd) */
+  int64_t a_token_stride, a_head_stride; /* elements, of k (cache_write) or q
+                            (paged_fwd): multiples of 8                         */
+  int64_t b_token_stride, b_head_stride; /* of v (cache_write)                  */
+} sa_paged_params;
+
+/*
+ * Writes rows of K and V into the cache.
+ *   k, v   BF16 rows (r, h) at k + r * a_token_stride + h * a_head_stride and
+ *          v + r * b_token_stride + h * b_head_stride, 128 contiguous elements
+ *   ws     optional (may be NULL): 256 bytes whose first word takes the
+ *          status; without it what is left out is not reported
+ * Errors before launch: SA_EINVAL (null or misaligned pointer: 16 bytes for
+ * k, v and the pages, 4 for the batch, 256 for ws; k_exp, v_exp null with
+ * SA_CACHE_E4M3; a field outside its range; a stride that is negative or no
+ * multiple of 8; kind or page_size unknown); SA_EUNSUPPORTED (D != 128,
+ * pages * H * page_size >= 2^31, rows * H >= 2^31 or rows * Hq >= 2^31, a
+ * device that is not sm_103).  SA_ECUDA if a launch fails.
+ */
+sa_status sparse_attn_cache_write(const sa_paged_params* p, const void* k, const void* v, void* k_pages,
+                                  void* v_pages, uint8_t* k_exp, uint8_t* v_exp, const int32_t* table,
+                                  const int32_t* row_start, const int32_t* kv_len, void* ws,
+                                  cudaStream_t stream);
+
+/*
+ * Reads cached rows back as BF16: the inverse of sparse_attn_cache_write, and
+ * with row_start spanning whole contexts the packed [T, H, 128] tensors that
+ * sparse_attn_plan and sparse_attn_fwd take.
+ *   k, v   BF16 [rows, H, 128], contiguous
+ * Errors: as sparse_attn_cache_write.
+ */
+sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, const void* v_pages,
+                                 const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* table,
+                                 const int32_t* row_start, const int32_t* kv_len, void* k, void* v, void* ws,
+                                 cudaStream_t stream);
+
+/*
+ * Attention of rows of Q over the cached keys of their sequence (their own
+ * tokens' K and V are in the cache already).  One softmax a row, in FP32;
+ * logits scale * (q . k).
+ *   q     BF16 rows (r, h) at q + r * a_token_stride + h * a_head_stride
+ *   o     BF16 [rows, Hq, 128], contiguous; zeros for a row that sees no key
+ *   lse   optional (may be NULL) float32 [rows, Hq]: natural logarithm of the
+ *         sum of exp(logit), -inf for a row that sees no key
+ *   ws    workspace of sparse_attn_paged_ws_bytes(p) bytes: the status word
+ *         in the first 256, then scratch of this call
+ * Cached values behind kv_len, or below the window of every row, are never
+ * used, whatever they are.
+ * Errors: as sparse_attn_cache_write, and SA_EINVAL for Hq not a multiple of
+ * H, causal not 0 or 1, window < 0 or with causal = 0, scale not finite, o
+ * not 16-byte or lse not 4-byte aligned, a short workspace.
+ */
+sa_status sparse_attn_paged_ws_bytes(const sa_paged_params* p, uint64_t* out);
+sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, const void* k_pages,
+                                const void* v_pages, const uint8_t* k_exp, const uint8_t* v_exp,
+                                const int32_t* table, const int32_t* row_start, const int32_t* kv_len,
+                                void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Reads the device status word of `ws` (written by the last plan or fwd
  * enqueued with it).  Synchronises `stream`.  SA_ECUDA if the copy fails.
  */

@@ -38,3 +38,4 @@ from .spark import (  # noqa: F401
     video_query_anchor,
 )
 from .reblock import reblock_bytes, spark_reblock  # noqa: F401
+from . import paged  # noqa: F401
