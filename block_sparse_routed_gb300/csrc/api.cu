@@ -151,6 +151,23 @@ bool make_map_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+bool sa::make_map_rows(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int elem, uint32_t box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
+  cuuint32_t box[2] = {128u / elem, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 // [T rows, H*128 columns] view of a BF16 [T, H, 128] tensor.
 bool make_map(CUtensorMap* m, const void* ptr, const Geometry& g, uint32_t box_rows) {
   return make_map_2d(m, ptr, static_cast<uint64_t>(g.T), static_cast<uint64_t>(g.H) * kHeadDim, box_rows);

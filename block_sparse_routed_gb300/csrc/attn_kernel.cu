@@ -1084,6 +1084,8 @@ __global__ void bias_prep_kernel(const float* __restrict__ bias, float* __restri
   }
 }
 
+}  // namespace
+
 int sm_count() {
   static int cached[128] = {0};
   int dev = 0;
@@ -1095,8 +1097,6 @@ int sm_count() {
   }
   return cached[dev];
 }
-
-}  // namespace
 
 size_t attention_smem_bytes() { return kSmemBytes; }
 

@@ -185,9 +185,50 @@ struct PagedAttnArgs {
   float* lse;                // [rows, Hq] or null
 };
 
+// What the joining kernel needs of the unit (a tile of packed rows of one
+// sequence and key head) that begins in a CTA's part of the work and does not
+// end there.
+struct JoinDesc {
+  int pieces;  // 0: none
+  int row0;    // first row of the sequence
+  int rho0;    // first packed row of the tile
+  int rows;    // packed rows of the tile
+  int h;
+  int pad[3];
+};
+
+// Workspace of paged_fwd: the status words, then a word and a JoinDesc of each
+// CTA, then two partial results of each: FP32 [row_tile][128] sums relative to
+// the row's reference, and [row_tile] (reference in log2 units, sum).
+struct PagedScratch {
+  int32_t* cta_status;  // [ctas]
+  JoinDesc* join;       // [ctas]
+  float* part;          // [ctas][2][row_tile][128]
+  float2* ml;           // [ctas][2][row_tile]
+};
+
+constexpr int kPagedFewRows = 32;   // most packed rows of the form for few rows
+constexpr int kPagedFewCtas = 320;  // most CTAs of it (two an SM)
+
+struct PagedForm {
+  int row_tile;  // packed rows of a unit
+  int max_ctas;
+  bool few;
+};
+
 cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
-cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
+                             const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
+cudaError_t launch_paged_simple(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
+
+// Multiprocessors of the current device (cached).
+int sm_count();
+
+// Tensor map of a row-major 2-D array of `elem`-byte elements, box
+// [box_rows, 128 bytes], 128-byte swizzle, zeros past the last row.
+bool make_map_rows(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int elem, uint32_t box_rows);
 
 size_t route_topk_smem_bytes(const Geometry& g);
 size_t attention_smem_bytes();

@@ -59,8 +59,10 @@ __device__ __forceinline__ int paged_find(const PagedArgs& c, int r, int lane) {
   }
 }
 
-// 2^(e - 127) of an exponent byte.
-__device__ __forceinline__ float exp_scale(uint32_t e) { return __uint_as_float(e << 23); }
+// 2^(e - 127) of an exponent byte; 255 is a row that is not a number.
+__device__ __forceinline__ float exp_scale(uint32_t e) {
+  return __uint_as_float(e == 255 ? 0x7FFFFFFFu : e << 23);
+}
 
 // Two E4M3 codes (the low 16 bits) as FP32 values.
 __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
@@ -69,6 +71,249 @@ __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
       : "=f"(lo), "=f"(hi)
       : "r"(h));
+}
+
+// ---- work of paged_fwd
+//
+// The rows of a sequence under one key head are packed as rho = i * group + g
+// (new token i, query head g of the group), so that a tile of them reads the
+// same keys.  A unit is a tile of `row_tile` packed rows of one sequence and
+// key head; its work is the key tiles of 2^key_shift keys between the first
+// key of its first row and the last key of its last one (one empty tile when
+// there is none, so that every unit writes its rows).  All key tiles of all
+// units, in the order (sequence, head, row tile, key tile), are one line that
+// is cut into equal parts, one a CTA: every CTA streams the same number of
+// keys however ragged the batch is.  A unit that a cut divides is joined from
+// its parts by join_kernel.
+
+struct UnitKeys {
+  int lo, hi;  // keys that some row of the unit sees: [lo, hi)
+  int t0, nt;  // key tiles
+};
+
+// First key that the row at position pos sees.
+__device__ __forceinline__ int row_lo(const PagedAttnArgs& a, int pos) {
+  return a.window ? static_cast<int>(max(int64_t(0), int64_t(pos) + 1 - a.window)) : 0;
+}
+
+__device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p, int row_tile,
+                                              int key_shift) {
+  const int rows = q.n * a.group;
+  const int i0 = p * row_tile / a.group, i1 = (min((p + 1) * row_tile, rows) - 1) / a.group;
+  UnitKeys u;
+  u.hi = a.causal ? min(q.len, q.len - q.n + i1 + 1) : q.len;
+  u.lo = row_lo(a, q.len - q.n + i0);
+  if (u.hi <= u.lo) u.lo = u.hi = 0;
+  u.t0 = u.lo >> key_shift;
+  u.nt = max(1, ((u.hi + (1 << key_shift) - 1) >> key_shift) - u.t0);
+  return u;
+}
+
+// Key tiles of one sequence and head.
+__device__ __forceinline__ int64_t seq_tiles(const PagedAttnArgs& a, const PagedSeq& q, int row_tile, int key_shift,
+                                             int first, int step) {
+  int64_t t = 0;
+  const int tiles = (q.n * a.group + row_tile - 1) / row_tile;
+  for (int p = first; p < tiles; p += step) t += unit_keys(a, q, p, row_tile, key_shift).nt;
+  return t;
+}
+
+// Where a CTA's part of the line begins.
+struct LineStart {
+  int64_t total;        // tiles of the line
+  int64_t begin, end;   // this CTA's
+  int64_t off;          // tiles of sequence s before `begin` (over all heads)
+  int s;
+  int ctas;             // CTAs with work: all, or fewer when tiles are few
+};
+
+constexpr int kLineSeqs = 1024;  // sequences looked at in one go
+
+// By all threads of the CTA; `tiles` is shared scratch for kLineSeqs values.
+// Returns (to all) the part of CTA `cta` of `ctas`; sets *bad when a sequence
+// fails its checks.  kWarpPerSeq: sequences may have many row tiles.
+template <bool kWarpPerSeq>
+__device__ __forceinline__ void line_start(const PagedAttnArgs& a, int row_tile, int key_shift, int cta, int ctas,
+                                           int64_t* tiles, LineStart* out, int* bad) {
+  const PagedArgs& c = a.c;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  auto fill = [&](int base) {
+    const int n = min(kLineSeqs, c.seqs - base);
+    bool any_bad = false;
+    if constexpr (kWarpPerSeq) {
+      for (int i = warp; i < n; i += warps) {
+        bool b;
+        const PagedSeq q = paged_seq(c, base + i, b);
+        any_bad |= b;
+        int64_t t = seq_tiles(a, q, row_tile, key_shift, lane, 32);
+        for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+        if (lane == 0) tiles[i] = t;
+      }
+    } else {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        bool b;
+        const PagedSeq q = paged_seq(c, base + i, b);
+        any_bad |= b;
+        tiles[i] = seq_tiles(a, q, row_tile, key_shift, 0, 1);
+      }
+    }
+    if (any_bad) *bad = 1;
+    __syncthreads();
+    return n;
+  };
+  int64_t total = 0;  // (warp 0)
+  for (int base = 0; base < c.seqs; base += kLineSeqs) {
+    const int n = fill(base);
+    if (warp == 0) {
+      int64_t t = 0;
+      for (int i = lane; i < n; i += 32) t += tiles[i];
+      for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+      total += t;
+    }
+    if (base + kLineSeqs < c.seqs) __syncthreads();
+  }
+  if (warp == 0 && lane == 0) {
+    out->total = total * c.H;
+    // (a part without tiles must not lie between two of one unit)
+    const int used = static_cast<int>(min(static_cast<int64_t>(ctas), out->total));
+    out->ctas = used;
+    out->begin = cta < used ? cta * out->total / used : 0;
+    out->end = cta < used ? (cta + 1) * out->total / used : 0;
+    out->off = 0;
+    out->s = c.seqs;
+  }
+  __syncthreads();
+  if (out->begin >= out->end) return;
+  int64_t before = 0;  // tiles (over all heads) of the sequences looked at
+  for (int base = 0; base < c.seqs; base += kLineSeqs) {
+    const int n = c.seqs > kLineSeqs ? fill(base) : c.seqs;
+    if (warp == 0) {
+      for (int i0 = 0; i0 < n && out->s == c.seqs; i0 += 32) {
+        const int64_t mine = i0 + lane < n ? tiles[i0 + lane] * c.H : 0;
+        int64_t upto = mine;
+        for (int d = 1; d < 32; d *= 2) {
+          const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+          if (lane >= d) upto += y;
+        }
+        const int64_t left = out->begin - before;
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
+        if (hit && lane == __ffs(hit) - 1) {
+          out->s = base + i0 + lane;
+          out->off = left - (upto - mine);
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+    if (out->s < c.seqs) break;
+  }
+}
+
+// The CTA that holds tile t of the line.
+__device__ __forceinline__ int line_owner(int64_t t, int64_t total, int ctas) {
+  return static_cast<int>(((t + 1) * ctas - 1) / total);
+}
+
+// One step of a CTA: some key tiles of a unit.
+struct Segment {
+  int valid;       // 0: no more
+  int row0, n, len, h, rho0, rows;
+  int lo, hi;      // keys that some row sees
+  int t0, nt;      // key tiles of this step
+  int part;        // -1: the unit's output; else the partial result's slot (0 or 1)
+  int s;
+};
+
+// Walks the steps of a CTA's part of the line (by a whole warp, all lanes
+// alike).
+struct LineWalk {
+  int64_t at, end, total;
+  int ctas, s, h, p, skip;  // skip: key tiles of the unit that earlier CTAs have
+  PagedSeq q;
+  int tiles;          // row tiles of the sequence
+};
+
+__device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w, int row_tile) {
+  bool bad;
+  w.q = paged_seq(a.c, w.s, bad);
+  w.tiles = (w.q.n * a.group + row_tile - 1) / row_tile;
+}
+
+__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, const LineStart& l, LineWalk& w, int row_tile,
+                                           int key_shift) {
+  w.at = l.begin;
+  w.end = l.end;
+  w.total = l.total;
+  w.ctas = l.ctas;
+  w.s = l.s;
+  w.h = w.p = w.skip = 0;
+  if (w.at >= w.end) return;
+  const int lane = threadIdx.x % 32;
+  walk_seq(a, w, row_tile);
+  int64_t t = seq_tiles(a, w.q, row_tile, key_shift, lane, 32);
+  for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+  w.h = static_cast<int>(l.off / t);
+  int64_t left = l.off % t;
+  for (int p0 = 0;; p0 += 32) {
+    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, row_tile, key_shift).nt : 0;
+    int64_t upto = mine;
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      w.p = p0 + src;
+      w.skip = static_cast<int>(__shfl_sync(0xFFFFFFFFu, left - (upto - mine), src));
+      return;
+    }
+    left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+}
+
+// The next step (valid = 0 at the end); `join` is filled when it leaves a
+// unit unfinished that it began.
+__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_shift, int cta,
+                                             JoinDesc& join) {
+  Segment g;
+  g.valid = 0;
+  if (w.at >= w.end) return g;
+  while (w.p >= w.tiles) {  // next head, next sequence with rows
+    w.p = 0;
+    if (w.tiles == 0 || ++w.h >= a.c.H) {
+      w.h = 0;
+      ++w.s;
+      walk_seq(a, w, row_tile);
+    }
+  }
+  const UnitKeys u = unit_keys(a, w.q, w.p, row_tile, key_shift);
+  g.valid = 1;
+  g.row0 = w.q.row0;
+  g.n = w.q.n;
+  g.len = w.q.len;
+  g.h = w.h;
+  g.s = w.s;
+  g.rho0 = w.p * row_tile;
+  g.rows = min(row_tile, w.q.n * a.group - g.rho0);
+  g.lo = u.lo;
+  g.hi = u.hi;
+  g.t0 = u.t0 + w.skip;
+  g.nt = static_cast<int>(min(static_cast<int64_t>(u.nt - w.skip), w.end - w.at));
+  const bool first = w.skip == 0, last = w.skip + g.nt == u.nt;
+  g.part = first && last ? -1 : (first ? 1 : 0);
+  if (first && !last) {
+    join.pieces = line_owner(w.at + u.nt - 1, w.total, w.ctas) - cta + 1;
+    join.row0 = g.row0;
+    join.rho0 = g.rho0;
+    join.rows = g.rows;
+    join.h = g.h;
+  }
+  w.at += g.nt;
+  w.skip = 0;
+  ++w.p;
+  return g;
 }
 
 }  // namespace sa

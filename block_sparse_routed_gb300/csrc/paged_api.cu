@@ -27,7 +27,7 @@ sa_status check_paged(const sa_paged_params* p) {
   if (p->seqs < 0 || p->rows < 0 || p->max_new < 0 || p->table_width < 0 || p->table_stride < 0) return SA_EINVAL;
   const int64_t lim = int64_t(1) << 31;
   if (int64_t(p->pages) * p->H >= lim || int64_t(p->pages) * p->H * p->page_size >= lim) return SA_EUNSUPPORTED;
-  if (int64_t(p->table_width) * p->page_size >= lim) return SA_EUNSUPPORTED;
+  if (int64_t(p->table_width) * p->page_size >= lim - 256) return SA_EUNSUPPORTED;
   if (int64_t(p->rows) * p->H >= lim) return SA_EUNSUPPORTED;
   return SA_OK;
 }
@@ -80,6 +80,37 @@ PagedArgs paged_args(const sa_paged_params* p, const void* kp, const void* vp, c
   c.v_exp = const_cast<uint8_t*>(ve);
   c.status = static_cast<int32_t*>(ws);
   return c;
+}
+
+// The form that computes a call: by the most packed rows of one sequence and
+// key head, from the host's bound.
+PagedForm form_of(const sa_paged_params* p) {
+  PagedForm f;
+  const int64_t rows = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H);
+  f.few = rows <= kPagedFewRows;
+  f.row_tile = rows <= 16 ? 16 : 32;
+  f.max_ctas = kPagedFewCtas;
+  return f;
+}
+
+constexpr uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255); }
+
+// Workspace layout; returns its bytes.
+uint64_t scratch_of(void* ws, const PagedForm& f, PagedScratch* out) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint64_t off = kStatusBytes;
+  const uint64_t n = f.max_ctas;
+  const uint64_t status = off; off += align256(n * 4);
+  const uint64_t join = off;   off += align256(n * sizeof(JoinDesc));
+  const uint64_t ml = off;     off += align256(n * 2 * f.row_tile * 8);
+  const uint64_t part = off;   off += n * 2 * f.row_tile * kHeadDim * 4;
+  if (out) {
+    out->cta_status = reinterpret_cast<int32_t*>(w + status);
+    out->join = reinterpret_cast<JoinDesc*>(w + join);
+    out->ml = reinterpret_cast<float2*>(w + ml);
+    out->part = reinterpret_cast<float*>(w + part);
+  }
+  return off;
 }
 
 sa_status clear_status(void* ws, cudaStream_t stream) {
@@ -144,7 +175,8 @@ SA_API sa_status sparse_attn_paged_ws_bytes(const sa_paged_params* p, uint64_t* 
   if (out == nullptr) return SA_EINVAL;
   const sa_status st = check_attn(p);
   if (st != SA_OK) return st;
-  *out = kStatusBytes;
+  const PagedForm f = form_of(p);
+  *out = scratch_of(nullptr, f, nullptr);
   return SA_OK;
 }
 
@@ -164,8 +196,7 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   if (ws_bytes < need) return SA_EINVAL;
   st = static_cast<sa_status>(device_status());
   if (st != SA_OK) return st;
-  st = clear_status(ws, stream);
-  if (st != SA_OK || p->rows == 0 || p->seqs == 0) return st;
+  if (p->rows == 0 || p->seqs == 0) return clear_status(ws, stream);
   PagedAttnArgs a;
   a.c = paged_args(p, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, ws);
   a.q = static_cast<const uint16_t*>(q);
@@ -178,5 +209,25 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   a.scale = p->scale;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  return cuda_failed(launch_paged_attention(a, stream)) ? SA_ECUDA : SA_OK;
+  const PagedForm f = form_of(p);
+  if (!f.few) {
+    st = clear_status(ws, stream);
+    if (st != SA_OK) return st;
+    return cuda_failed(launch_paged_simple(a, stream)) ? SA_ECUDA : SA_OK;
+  }
+  PagedScratch scratch;
+  scratch_of(ws, f, &scratch);
+  CUtensorMap tk, tv;
+  const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
+  const int elem = p->kind == SA_CACHE_BF16 ? 2 : 1;
+  const uint32_t box = p->page_size < 64 ? p->page_size : 64;
+  if (!make_map_rows(&tk, k_pages, cached, kHeadDim, elem, box) ||
+      !make_map_rows(&tv, v_pages, cached, kHeadDim, elem, box))
+    return SA_ECUDA;
+  // no more CTAs than the longest contexts that the table can hold have tiles
+  const int64_t most = int64_t(p->seqs) * p->H * ((int64_t(p->table_width) * p->page_size + 63) / 64 + 1);
+  int ctas = 2 * sm_count() < f.max_ctas ? 2 * sm_count() : f.max_ctas;
+  if (most < ctas) ctas = static_cast<int>(most);
+  if (cuda_failed(launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream))) return SA_ECUDA;
+  return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, stream)) ? SA_ECUDA : SA_OK;
 }

@@ -77,19 +77,17 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c
       *reinterpret_cast<uint4*>(pages + row * 256 + sub * 16) = x[i];
     } else {
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      // largest finite magnitude: BF16 bits without the sign order as integers
+      // largest magnitude: BF16 bits without the sign order as integers
       uint32_t m2 = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t a = w[k] & 0x7FFF7FFFu;
-        m2 = __vmaxu2(m2, a & ~__vcmpgeu2(a, 0x7F807F80u));
-      }
+      for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7FFF7FFFu);
 #pragma unroll
       for (int d = 1; d < 16; d *= 2) m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, d));
       const uint32_t m = max(m2 >> 16, m2 & 0xFFFFu);
       // amax = (1 + M / 128) 2^(E - 127) <= 1.75 * 2^8 * 2^e with M <= 96 for e = E - 135
-      const int e = max(1, static_cast<int>(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0));
-      const float inv = exp_scale(254 - e);
+      const bool finite = m < 0x7F80u;
+      const int e = finite ? max(1, static_cast<int>(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0)) : 255;
+      const float inv = exp_scale(finite ? 254 - e : 255);  // NaN: every code of the row is
       uint32_t code[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -97,10 +95,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const uint32_t v = w[2 * k + t];
-          float lo = __uint_as_float(v << 16) * inv, hi = __uint_as_float(v & 0xFFFF0000u) * inv;
-          // the conversion would saturate an infinity: store NaN for it
-          if ((v & 0x7F80u) == 0x7F80u) lo = __uint_as_float(0x7FFFFFFFu);
-          if ((v & 0x7F800000u) == 0x7F800000u) hi = __uint_as_float(0x7FFFFFFFu);
+          const float lo = __uint_as_float(v << 16) * inv, hi = __uint_as_float(v & 0xFFFF0000u) * inv;
           asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(half[t]) : "f"(hi), "f"(lo));
         }
         code[k] = half[0] | (static_cast<uint32_t>(half[1]) << 16);

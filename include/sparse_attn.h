@@ -322,14 +322,18 @@ sa_status sparse_attn_spark_reblock(const sa_reblock_params* p, const void* x, i
  *   two kinds:
  *   SA_CACHE_BF16  BF16 rows as they came.
  *   SA_CACHE_E4M3  8-bit E4M3 codes, each row (one token of one head) with
- *                  a power-of-two scale: with amax the row's largest finite
+ *                  a power-of-two scale: with amax the row's largest
  *                  magnitude, e is the smallest integer >= -126 such that
  *                  amax <= 448 * 2^e, a code is x * 2^-e rounded to nearest
  *                  even, and k_exp, v_exp uint8 [pages, H, page_size] hold
  *                  e + 127.  Scaling by 2^e is exact both ways, so the
  *                  code's own rounding is the only one, and what a code
- *                  stands for is a BF16 value (above 2^127 * 1.9375 it is
- *                  infinite).  NaN and infinities are stored as NaN.
+ *                  stands for is a BF16 value (it is infinite where rounding
+ *                  to 4 bits passes the largest one).  A row that holds a NaN
+ *                  or an infinity has the exponent byte 255 and NaN codes:
+ *                  all of it stands for NaN.  (NaN codes under another
+ *                  exponent byte, which cache_write never makes, are +-480
+ *                  to paged_fwd.)
  * Batch (device memory, int32, read by every call).  Sequence s < seqs has
  *   kv_len[s] tokens; token j is in slot j % page_size of page
  *   table[s * table_stride + j / page_size].  The rows row_start[s] ..

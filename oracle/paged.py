@@ -31,17 +31,15 @@ def e4m3_values() -> np.ndarray:
 def quantise_row(bits: np.ndarray):
     """(codes uint8 [128], exponent byte) of one BF16 row, by definition."""
     x = decode_bf16(bits)
-    fin = np.abs(x[np.isfinite(x)])
-    amax = float(fin.max()) if fin.size else 0.0
+    if not np.all(np.isfinite(x)):  # the whole row is not a number
+        return np.full(x.shape, 127, dtype=np.uint8), 255
+    amax = float(np.abs(x).max())
     e = -126
     while amax > 448.0 * 2.0 ** e:
         e += 1
     vals = e4m3_values()[:127]  # the magnitudes, ascending with the code
     codes = np.empty(x.shape, dtype=np.uint8)
     for i, v in enumerate(x):
-        if not np.isfinite(v):
-            codes[i] = 127
-            continue
         a = abs(v) * 2.0 ** -e
         hi = int(np.searchsorted(vals, a))  # vals[hi - 1] < a <= vals[hi]
         lo = max(hi - 1, 0)

@@ -224,8 +224,8 @@ def test_quantised_extremes(bsr):
         want, byte = OP.quantise_row(bits(x)[r, 0])
         same = (codes[r] & 127 == 127) & (want & 127 == 127)  # any NaN
         assert exps[r] == byte and np.all(same | (codes[r] == want)), r
-    k, v = bsr.cache_read(*b.where, rows=8, **b.exps)
-    assert torch.equal(k, v) or torch.equal(k.isnan(), v.isnan())
+    k, _ = bsr.cache_read(*b.where, rows=8, **b.exps)
+    assert k[3:5].isnan().all() and not k[:2].isnan().any() and not k[5:].isnan().any()
 
 
 # ---- attention
