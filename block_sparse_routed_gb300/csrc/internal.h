@@ -207,7 +207,7 @@ struct PagedScratch {
   float2* ml;           // [ctas][2][row_tile]
 };
 
-constexpr int kPagedFewRows = 32;   // most packed rows of the form for few rows
+constexpr int kPagedFewRows = 16;   // most packed rows of the form for few rows
 constexpr int kPagedFewCtas = 320;  // most CTAs of it (two an SM)
 
 struct PagedForm {

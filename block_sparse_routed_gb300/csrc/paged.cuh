@@ -84,7 +84,7 @@ __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
 // units, in the order (sequence, head, row tile, key tile), are one line that
 // is cut into equal parts, one a CTA: every CTA streams the same number of
 // keys however ragged the batch is.  A unit that a cut divides is joined from
-// its parts by join_kernel.
+// its parts by the joining kernel.
 
 struct UnitKeys {
   int lo, hi;  // keys that some row of the unit sees: [lo, hi)
@@ -96,10 +96,19 @@ __device__ __forceinline__ int row_lo(const PagedAttnArgs& a, int pos) {
   return a.window ? static_cast<int>(max(int64_t(0), int64_t(pos) + 1 - a.window)) : 0;
 }
 
+__device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const PagedSeq& q, int row_tile) {
+  return static_cast<int>((static_cast<uint32_t>(q.n) * static_cast<uint32_t>(a.group) + row_tile - 1) /
+                          static_cast<uint32_t>(row_tile));
+}
+
 __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p, int row_tile,
                                               int key_shift) {
   const int rows = q.n * a.group;
-  const int i0 = p * row_tile / a.group, i1 = (min((p + 1) * row_tile, rows) - 1) / a.group;
+  int i0 = 0, i1 = q.n - 1;  // first and last new token of the tile
+  if (rows > row_tile) {
+    i0 = p * row_tile / a.group;
+    i1 = (min((p + 1) * row_tile, rows) - 1) / a.group;
+  }
   UnitKeys u;
   u.hi = a.causal ? min(q.len, q.len - q.n + i1 + 1) : q.len;
   u.lo = row_lo(a, q.len - q.n + i0);
@@ -109,110 +118,58 @@ __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const Page
   return u;
 }
 
-// Key tiles of one sequence and head.
-__device__ __forceinline__ int64_t seq_tiles(const PagedAttnArgs& a, const PagedSeq& q, int row_tile, int key_shift,
-                                             int first, int step) {
-  int64_t t = 0;
-  const int tiles = (q.n * a.group + row_tile - 1) / row_tile;
-  for (int p = first; p < tiles; p += step) t += unit_keys(a, q, p, row_tile, key_shift).nt;
+__device__ __forceinline__ int64_t warp_sum(int64_t t) {
+#pragma unroll
+  for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+  return t;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t t, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, t, d);
+    if (lane >= d) t += y;
+  }
   return t;
 }
 
-// Where a CTA's part of the line begins.
-struct LineStart {
-  int64_t total;        // tiles of the line
-  int64_t begin, end;   // this CTA's
-  int64_t off;          // tiles of sequence s before `begin` (over all heads)
-  int s;
-  int ctas;             // CTAs with work: all, or fewer when tiles are few
-};
-
-constexpr int kLineSeqs = 1024;  // sequences looked at in one go
-
-// By all threads of the CTA; `tiles` is shared scratch for kLineSeqs values.
-// Returns (to all) the part of CTA `cta` of `ctas`; sets *bad when a sequence
-// fails its checks.  kWarpPerSeq: sequences may have many row tiles.
-template <bool kWarpPerSeq>
-__device__ __forceinline__ void line_start(const PagedAttnArgs& a, int row_tile, int key_shift, int cta, int ctas,
-                                           int64_t* tiles, LineStart* out, int* bad) {
-  const PagedArgs& c = a.c;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  auto fill = [&](int base) {
-    const int n = min(kLineSeqs, c.seqs - base);
-    bool any_bad = false;
-    if constexpr (kWarpPerSeq) {
-      for (int i = warp; i < n; i += warps) {
-        bool b;
-        const PagedSeq q = paged_seq(c, base + i, b);
-        any_bad |= b;
-        int64_t t = seq_tiles(a, q, row_tile, key_shift, lane, 32);
-        for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-        if (lane == 0) tiles[i] = t;
-      }
-    } else {
-      for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        bool b;
-        const PagedSeq q = paged_seq(c, base + i, b);
-        any_bad |= b;
-        tiles[i] = seq_tiles(a, q, row_tile, key_shift, 0, 1);
-      }
-    }
-    if (any_bad) *bad = 1;
-    __syncthreads();
-    return n;
-  };
-  int64_t total = 0;  // (warp 0)
-  for (int base = 0; base < c.seqs; base += kLineSeqs) {
-    const int n = fill(base);
-    if (warp == 0) {
-      int64_t t = 0;
-      for (int i = lane; i < n; i += 32) t += tiles[i];
-      for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-      total += t;
-    }
-    if (base + kLineSeqs < c.seqs) __syncthreads();
-  }
-  if (warp == 0 && lane == 0) {
-    out->total = total * c.H;
-    // (a part without tiles must not lie between two of one unit)
-    const int used = static_cast<int>(min(static_cast<int64_t>(ctas), out->total));
-    out->ctas = used;
-    out->begin = cta < used ? cta * out->total / used : 0;
-    out->end = cta < used ? (cta + 1) * out->total / used : 0;
-    out->off = 0;
-    out->s = c.seqs;
-  }
-  __syncthreads();
-  if (out->begin >= out->end) return;
-  int64_t before = 0;  // tiles (over all heads) of the sequences looked at
-  for (int base = 0; base < c.seqs; base += kLineSeqs) {
-    const int n = c.seqs > kLineSeqs ? fill(base) : c.seqs;
-    if (warp == 0) {
-      for (int i0 = 0; i0 < n && out->s == c.seqs; i0 += 32) {
-        const int64_t mine = i0 + lane < n ? tiles[i0 + lane] * c.H : 0;
-        int64_t upto = mine;
-        for (int d = 1; d < 32; d *= 2) {
-          const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-          if (lane >= d) upto += y;
-        }
-        const int64_t left = out->begin - before;
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
-        if (hit && lane == __ffs(hit) - 1) {
-          out->s = base + i0 + lane;
-          out->off = left - (upto - mine);
-        }
-        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
-        __syncwarp();
-      }
-    }
-    __syncthreads();
-    if (out->s < c.seqs) break;
-  }
+// x * y / z, in 32 bits where they hold it (a 64-bit division is long).
+__device__ __forceinline__ int64_t muldiv(int64_t x, int64_t y, int64_t z) {
+  const uint64_t v = static_cast<uint64_t>(x) * static_cast<uint64_t>(y);
+  if ((v | static_cast<uint64_t>(z)) >> 32 == 0) return static_cast<uint32_t>(v) / static_cast<uint32_t>(z);
+  return static_cast<int64_t>(v / static_cast<uint64_t>(z));
 }
 
-// The CTA that holds tile t of the line.
-__device__ __forceinline__ int line_owner(int64_t t, int64_t total, int ctas) {
-  return static_cast<int>(((t + 1) * ctas - 1) / total);
+// Key tiles of one head of the sequences base + lane, one a lane (0 past the
+// last).  Sequences of many row tiles are summed by the whole warp.
+__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, int row_tile, int key_shift, int lane,
+                                              bool& bad) {
+  const int s = base + lane;
+  PagedSeq q;
+  q.n = 0;
+  if (s < a.c.seqs) {
+    bool b;
+    q = paged_seq(a.c, s, b);
+    bad |= b;
+  }
+  const int tiles = row_tiles(a, q, row_tile);
+  int64_t t = 0;
+  if (tiles <= 4)
+    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, row_tile, key_shift).nt;
+  unsigned many = __ballot_sync(0xFFFFFFFFu, tiles > 4);
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    PagedSeq r;
+    r.row0 = 0;
+    r.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
+    r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
+    const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
+    int64_t y = 0;
+    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, row_tile, key_shift).nt;
+    y = warp_sum(y);
+    if (lane == src) t = y;
+  }
+  return t;
 }
 
 // One step of a CTA: some key tiles of a unit.
@@ -229,39 +186,64 @@ struct Segment {
 // alike).
 struct LineWalk {
   int64_t at, end, total;
-  int ctas, s, h, p, skip;  // skip: key tiles of the unit that earlier CTAs have
+  int ctas;     // CTAs with work: all, or fewer when tiles are few
+  int s, h, p;
+  int skip;     // key tiles of the unit that earlier CTAs have
   PagedSeq q;
-  int tiles;          // row tiles of the sequence
+  int tiles;    // row tiles of the sequence
 };
 
 __device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w, int row_tile) {
   bool bad;
   w.q = paged_seq(a.c, w.s, bad);
-  w.tiles = (w.q.n * a.group + row_tile - 1) / row_tile;
+  w.tiles = row_tiles(a, w.q, row_tile);
 }
 
-__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, const LineStart& l, LineWalk& w, int row_tile,
-                                           int key_shift) {
-  w.at = l.begin;
-  w.end = l.end;
-  w.total = l.total;
-  w.ctas = l.ctas;
-  w.s = l.s;
-  w.h = w.p = w.skip = 0;
-  if (w.at >= w.end) return;
-  const int lane = threadIdx.x % 32;
+// Finds the part of CTA `cta` of `ctas`; each takes min_tiles at least, while
+// there are any.  Sets `bad` when a sequence fails its checks.
+__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_shift, int cta,
+                                           int ctas, int min_tiles, bool& bad) {
+  const int lane = threadIdx.x % 32, seqs = a.c.seqs;
+  int64_t t = 0, first = 0;
+  for (int base = 0; base < seqs; base += 32) {
+    t += lane_tiles(a, base, row_tile, key_shift, lane, bad);
+    if (base == 0) first = t;
+  }
+  w.total = warp_sum(t) * a.c.H;
+  const int64_t most = (w.total + min_tiles - 1) / min_tiles;
+  w.ctas = static_cast<int>(min(static_cast<int64_t>(ctas), most));
+  // (a part without tiles must not lie between two of one unit)
+  w.at = w.end = 0;
+  w.s = w.h = w.p = w.skip = 0;
+  if (cta >= w.ctas) return;
+  w.at = muldiv(cta, w.total, w.ctas);
+  w.end = muldiv(cta + 1, w.total, w.ctas);
+  int64_t left = w.at;
+  for (int base = 0;; base += 32) {
+    bool b;
+    const int64_t mine = (base == 0 ? first : lane_tiles(a, base, row_tile, key_shift, lane, b)) * a.c.H;
+    const int64_t upto = warp_scan(mine, lane);
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      w.s = base + src;
+      left = __shfl_sync(0xFFFFFFFFu, left - (upto - mine), src);
+      t = __shfl_sync(0xFFFFFFFFu, mine, src);  // of all heads
+      break;
+    }
+    left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
   walk_seq(a, w, row_tile);
-  int64_t t = seq_tiles(a, w.q, row_tile, key_shift, lane, 32);
-  for (int d = 16; d; d /= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-  w.h = static_cast<int>(l.off / t);
-  int64_t left = l.off % t;
+  t = muldiv(t, 1, a.c.H);
+  w.h = static_cast<int>(muldiv(left, 1, t));
+  left -= w.h * t;
+  if (w.tiles == 1) {
+    w.skip = static_cast<int>(left);
+    return;
+  }
   for (int p0 = 0;; p0 += 32) {
     const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, row_tile, key_shift).nt : 0;
-    int64_t upto = mine;
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if (lane >= d) upto += y;
-    }
+    const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
       const int src = __ffs(hit) - 1;
@@ -304,7 +286,9 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
   const bool first = w.skip == 0, last = w.skip + g.nt == u.nt;
   g.part = first && last ? -1 : (first ? 1 : 0);
   if (first && !last) {
-    join.pieces = line_owner(w.at + u.nt - 1, w.total, w.ctas) - cta + 1;
+    // the CTA that holds the unit's last tile
+    const int owner = static_cast<int>(muldiv((w.at + u.nt) * w.ctas - 1, 1, w.total));
+    join.pieces = owner - cta + 1;
     join.row0 = g.row0;
     join.rho0 = g.rho0;
     join.rows = g.rows;

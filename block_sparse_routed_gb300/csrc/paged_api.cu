@@ -88,7 +88,7 @@ PagedForm form_of(const sa_paged_params* p) {
   PagedForm f;
   const int64_t rows = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H);
   f.few = rows <= kPagedFewRows;
-  f.row_tile = rows <= 16 ? 16 : 32;
+  f.row_tile = rows <= 8 ? 8 : 16;
   f.max_ctas = kPagedFewCtas;
   return f;
 }

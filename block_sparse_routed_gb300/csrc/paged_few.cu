@@ -1,35 +1,38 @@
 // Attention over a paged cache for few rows a sequence and key head: single
-// tokens and short drafts (at most 32 packed rows), sm_103a.
+// tokens and short drafts (at most 16 packed rows), sm_103a.
 //
 //   o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m),   x_j = scale log2(e) (q . k_j)
 //
 // Every cached row is used once for all rows of the unit, so the kernel is
 // bound by memory: 512 bytes a token and key head (258 in the E4M3 kind)
-// against 16 to 32 rows' worth of products.  What it needs is many bytes in
+// against 8 or 16 rows' worth of products.  What it needs is many bytes in
 // flight and an even share for every SM however ragged the batch is: the line
 // of all key tiles is cut into equal parts, one a CTA (paged.cuh), and each
 // CTA streams its part through a ring of 64-key stages of K and V.  A
-// producer warp fills the ring with TMA boxes, one a page (64 keys of one
-// page and head are contiguous), and four warps take 16 keys of a stage each,
-// with a softmax reference, sum and output of their own until the unit's keys
-// end: nothing passes between warps inside the loop.
+// producer warp fills the ring with TMA boxes, one a page (the keys of one
+// page and head are contiguous), and each consumer warp takes 16 keys of a
+// stage, with a softmax reference, sum and output of its own until the unit's
+// keys end: nothing passes between warps inside the loop.
 //
-// Products are mma.sync m16n8k16: with 16 rows a tcgen05 instruction (128
-// rows) would be seven eighths padding, and the tensor pipe is not what
-// bounds the kernel.  A warp's keys are the N of Q K^T and the K of P V, so
-// the probabilities go from one accumulator layout to the other operand's
-// without leaving the registers.
+// Products are mma.sync m16n8k16 with the keys (then the dimensions) as M and
+// eight rows as N:  S^T = K Q^T,  O^T = V^T P^T.  A tcgen05 instruction takes
+// 128 rows, of which seven eighths or more would be padding, and here the
+// tensor pipe is not what bounds; with the rows as M, eight of sixteen would
+// still be.  P^T leaves the first product's accumulators as pairs of rows and
+// enters the second as pairs of keys: one movmatrix for eight keys.
 //
-// E4M3 codes are widened to BF16 in registers (exact): exponent and fraction
-// moved into place, then one packed multiplication by 2^120.  A 32-bit word of
-// four codes c0..c3 gives the pairs (c0, c2) and (c1, c3) without a byte
-// permutation; for K the dimensions' order within 16 is free (Q's fragment
-// takes the same one), for V, read transposed, the pairs are two keys of one
-// dimension.  A key's scale is a power of two: K's multiplies the logit, V's
-// the probability.
+// E4M3 (exact in both products).  K: two cvt make four FP16 values of a word;
+// Q is held in FP16 too, each row scaled by a power of two that brings its
+// largest magnitude to 2^14 (what lies 2^29 below that is lost, far below the
+// FP32 sum's own rounding).  V: BF16, since a probability times its key's
+// scale can leave FP16's range; a word's codes c0..c3 are two dimensions of two keys,
+// and exponent and fraction shifted into place, times 2^120, give the pairs
+// (c0, c2) and (c1, c3) without a byte permutation.  A key's scale is a power
+// of two: K's multiplies the logit, V's the probability.
 //
-// Two CTAs of 160 threads an SM; three 32 KB stages each (six in the E4M3
-// kind).
+// Two CTAs an SM: four consumer warps and three stages of 32 KB, or, for up
+// to eight rows over E4M3 pages, where the widening takes more instructions
+// than the products, eight warps (four on every other stage) and six of 16 KB.
 #include <cstdint>
 
 #include "internal.h"
@@ -41,35 +44,37 @@ namespace {
 
 constexpr int kKeyShift = 6;  // 64 keys a stage
 constexpr int kTileKeys = 1 << kKeyShift;
-constexpr int kConsumers = 4;  // warps
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kSegs = 4;       // steps described ahead
+constexpr int kSegs = 4;      // steps described ahead
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMergeRow = 132;  // floats a row of the merge area (128 and padding)
 
-template <int kKind>
-struct Ring {
+template <int kKind, int kN>
+struct Cfg {
+  static constexpr int kGroups = kKind == 1 && kN == 1 ? 2 : 1;  // of four consumer warps, on stages in turn
+  static constexpr int kConsumers = 4 * kGroups;
+  static constexpr int kThreads = 32 * (kConsumers + 1);
+  // Every stage belongs to one group: a group that skipped phases of a stage
+  // could take the phase before the awaited one for it.
   static constexpr int kStages = kKind == 0 ? 3 : 6;
-  static constexpr uint32_t kRow = kKind == 0 ? 256 : 128;              // bytes of a cached row
-  static constexpr uint32_t kHalf = kTileKeys * kRow;                   // K or V of a stage
+  static_assert(kStages % kGroups == 0, "stages of a group");
+  static constexpr uint32_t kRow = kKind == 0 ? 256 : 128;            // bytes of a cached row
+  static constexpr uint32_t kHalf = kTileKeys * kRow;                 // K or V of a stage
   static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr uint32_t kExp = kKind == 0 ? 0 : 2 * kTileKeys;      // exponent bytes of a stage
+  static constexpr uint32_t kExp = kKind == 0 ? 0 : 2 * kTileKeys;    // exponent bytes of a stage
+  // Shared memory, from a 1024-byte boundary.
+  static constexpr uint32_t kOffExp = kStages * kStage;
+  static constexpr uint32_t kOffMerge = kOffExp + kStages * kExp;     // kRegions x 8 rows
+  static constexpr int kRegions = 2;
+  static constexpr uint32_t kOffMl = kOffMerge + kRegions * 8 * kMergeRow * 4;  // [2][8 warps][16] floats
+  static constexpr uint32_t kOffSeg = kOffMl + 1024;                  // kSegs x Segment
+  static constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
+  static constexpr uint32_t kOffMisc = kOffBar + 256;
+  static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
-constexpr uint32_t kRingBytes = 3 * 32768;
-static_assert(Ring<0>::kStages * Ring<0>::kStage == kRingBytes && Ring<1>::kStages * Ring<1>::kStage == kRingBytes, "");
+static_assert(sizeof(Segment) <= 64, "");
 
-// Shared memory, from a 1024-byte boundary.
-constexpr uint32_t kOffExp = kRingBytes;                 // 6 x 128 exponent bytes
-constexpr uint32_t kOffMerge = kOffExp + 768;            // 8 KB: merging the warps' outputs
-constexpr uint32_t kOffMl = kOffMerge + 8192;            // [2][4][32] floats
-constexpr uint32_t kOffSeg = kOffMl + 1024;              // kSegs x Segment
-constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
-constexpr uint32_t kOffMisc = kOffBar + 256;
-constexpr uint32_t kSmemBytes = kOffMisc + 128 + 1024;
-static_assert(sizeof(Segment) <= 64 && sizeof(LineStart) <= 64, "");
-static_assert(kLineSeqs * 8 <= kRingBytes, "the scan's scratch lies over the ring");
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
-
-enum { BAR_FULL = 0, BAR_EMPTY = 6, BAR_SFULL = 12, BAR_SEMPTY = 16, NUM_BARS = 20 };
+enum { BAR_FULL = 0, BAR_EMPTY = 8, BAR_SFULL = 16, BAR_SEMPTY = 20, NUM_BARS = 24 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -83,14 +88,26 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
 }
-// Codes (c0, c2) and (c1, c3) of a word as BF16 pairs.  The seven magnitude
-// bits land on BF16's exponent and upper fraction, as x 2^-120 (subnormal
-// codes as subnormals).
+template <bool kHalfs>  // FP16 operands, else BF16
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (kHalfs)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Codes (c0, c2) and (c1, c3) of a word as BF16 pairs: the seven magnitude
+// bits land on BF16's exponent and upper fraction as the value times 2^-120
+// (subnormal codes as subnormals).
 __device__ __forceinline__ uint32_t times_2_120(uint32_t v) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x7B807B80u));
@@ -102,19 +119,37 @@ __device__ __forceinline__ uint32_t codes_even(uint32_t w) {
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
   return times_2_120(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u));
 }
-// The consumers agree: true for all when it is for one (a wait that gave up in
-// one warp must not leave the others at a barrier).
+// Codes (c0, c1) and (c2, c3) as FP16 pairs.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// The consumers meet (barrier 1) and agree: true for all when it is for one
+// (a wait that gave up in one warp must not leave the others at a barrier).
+template <int kThreads>
 __device__ __forceinline__ bool bar_any(bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      "bar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(pred))
+      : "r"(static_cast<uint32_t>(pred)), "n"(kThreads)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int kThreads>
+__device__ __forceinline__ void bar_all() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -122,52 +157,51 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-template <int kKind, int kM>  // kM: m-tiles of 16 rows
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kKind, int kN>  // kN: tiles of eight rows
+__global__ void __launch_bounds__(Cfg<kKind, kN>::kThreads, 2)
 paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const PagedAttnArgs a, const PagedScratch ws) {
-  using R = Ring<kKind>;
-  constexpr int kRows = 16 * kM;
+  using C = Cfg<kKind, kN>;
+  constexpr int kRows = 8 * kN;
+  constexpr int kWorkers = 32 * C::kConsumers;
   const PagedArgs& c = a.c;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(base);
-  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * i; };
-  Segment* segs = reinterpret_cast<Segment*>(base + kOffSeg);
-  volatile int32_t* s_abort = reinterpret_cast<volatile int32_t*>(base + kOffMisc);
-  int32_t* s_bad = reinterpret_cast<int32_t*>(base + kOffMisc + 4);
-  LineStart* line = reinterpret_cast<LineStart*>(base + kOffMisc + 16);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * i; };
+  Segment* segs = reinterpret_cast<Segment*>(base + C::kOffSeg);
+  volatile int32_t* s_abort = reinterpret_cast<volatile int32_t*>(base + C::kOffMisc);
+  int32_t* s_bad = reinterpret_cast<int32_t*>(base + C::kOffMisc + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     *s_abort = 0;
     *s_bad = 0;
-    for (int i = 0; i < R::kStages; ++i) {
+    for (int i = 0; i < C::kStages; ++i) {
       mbar_init(bar(BAR_FULL + i), 1);
-      mbar_init(bar(BAR_EMPTY + i), kConsumers);
+      mbar_init(bar(BAR_EMPTY + i), 4);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(BAR_SFULL + i), 1);
-      mbar_init(bar(BAR_SEMPTY + i), kConsumers);
+      mbar_init(bar(BAR_SEMPTY + i), C::kConsumers);
     }
     fence_barrier_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
   }
   __syncthreads();
-  // (a unit is one row tile here: the host chose the form by max_new)
-  line_start<false>(a, kRows, kKeyShift, blockIdx.x, gridDim.x, reinterpret_cast<int64_t*>(base), line, s_bad);
-  fence_proxy_async_smem();  // the scan's scratch is written by TMA next
-  __syncthreads();
 
-  if (warp == kConsumers) {
+  if (warp == C::kConsumers) {
     // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
     LineWalk w;
-    walk_begin(a, *line, w, kRows, kKeyShift);
+    bool bad = false;
+    walk_begin(a, w, kRows, kKeyShift, blockIdx.x, gridDim.x, 1, bad);
     JoinDesc join;
     join.pieces = 0;
-    bool ok = true, bad_page = false;
+    bool ok = true;
     int stage = 0, seq = 0;
     const int per_page = min(c.page_size, kTileKeys);        // keys of a tile in one page
     const int tile_pages = kTileKeys / per_page;
@@ -194,24 +228,23 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const int at = have * 32 + lane;
           entry = at >= p_lo && at < p_hi ? __ldg(table + at) : 0;
           const bool wrong = entry < 0 || entry >= c.pages;
-          bad_page |= wrong;
+          bad |= wrong;
           if (wrong) entry = -1;
         }
         const int first = max(page0, p_lo), last = min(page0 + tile_pages, p_hi);  // [first, last)
-        ok = seq < R::kStages || __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_EMPTY + stage),
-                                                                  ((seq / R::kStages) & 1) ^ 1, kWaitLimitNs));
+        ok = seq < C::kStages || __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_EMPTY + stage),
+                                                                  ((seq / C::kStages) & 1) ^ 1, kWaitLimitNs));
         if (!ok) break;
         const int at = page0 + pg;
         const int page = __shfl_sync(0xFFFFFFFFu, entry, at % 32);
         const bool mine = pg < tile_pages && at >= first && at < last && page >= 0;
         const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine && sub == 0));
         if (lane == 0)
-          mbar_arrive_expect_tx(bar(BAR_FULL + stage),
-                                loads * per_page * (2 * R::kRow + (kKind ? 2 : 0)));
+          mbar_arrive_expect_tx(bar(BAR_FULL + stage), loads * per_page * (2 * C::kRow + (kKind ? 2 : 0)));
         __syncwarp();
         if (mine) {
           const int64_t row = ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (key0 & (c.page_size - 1));
-          const uint32_t to = sbase + stage * R::kStage + (sub / 2) * R::kHalf + pg * per_page * 128;
+          const uint32_t to = sbase + stage * C::kStage + (sub / 2) * C::kHalf + pg * per_page * 128;
           const CUtensorMap* map = sub / 2 ? &tm_v : &tm_k;
           if constexpr (kKind == 0) {
             tma_load_2d(to + (sub % 2) * (kTileKeys * 128), map, bar(BAR_FULL + stage), (sub % 2) * 64,
@@ -219,107 +252,143 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           } else if (sub % 2 == 0) {
             tma_load_2d(to, map, bar(BAR_FULL + stage), 0, static_cast<int>(row));
           } else {
-            bulk_load(sbase + kOffExp + stage * R::kExp + (sub / 2) * kTileKeys + pg * per_page,
+            bulk_load(sbase + C::kOffExp + stage * C::kExp + (sub / 2) * kTileKeys + pg * per_page,
                       (sub / 2 ? c.v_exp : c.k_exp) + row, per_page, bar(BAR_FULL + stage));
           }
         }
         ++seq;
-        stage = stage + 1 == R::kStages ? 0 : stage + 1;
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
         ok = !__any_sync(0xFFFFFFFFu, *s_abort != 0);
         if (!ok) break;
       }
     }
-    bad_page = __any_sync(0xFFFFFFFFu, bad_page);
+    bad = __any_sync(0xFFFFFFFFu, bad);
     if (!ok) {
       *s_abort = 1;
       // copies in flight land before the CTA ends (bounded)
-      for (int q = max(0, seq - R::kStages); q < seq; ++q)
-        mbar_wait(bar(BAR_FULL + q % R::kStages), (q / R::kStages) & 1, kWaitLimitNs);
+      for (int q = max(0, seq - C::kStages); q < seq; ++q)
+        mbar_wait(bar(BAR_FULL + q % C::kStages), (q / C::kStages) & 1, kWaitLimitNs);
     }
     if (lane == 0) {
       ws.join[blockIdx.x] = join;
-      if (bad_page) *s_bad = 1;
+      if (bad) *s_bad = 1;
     }
   } else {
     // ------------------------------------------------------------ consumers
-    const int r = lane / 4, t4 = lane % 4;
-    float* merge = reinterpret_cast<float*>(base + kOffMerge);
-    float* s_m = reinterpret_cast<float*>(base + kOffMl);
-    float* s_l = s_m + 4 * 32;
+    const int u = lane / 4, t4 = lane % 4;
+    const int quarter = warp % 4, grp = warp / 4;  // 16 keys of the stages that are the group's
+    float* merge = reinterpret_cast<float*>(base + C::kOffMerge);
+    float* s_m = reinterpret_cast<float*>(base + C::kOffMl);  // [warp][row]
+    float* s_l = s_m + C::kConsumers * kRows;
     const float c2 = a.scale * 1.4426950408889634f;
-    // ldmatrix rows: lane l gives row l % 8 of matrix l / 8
+    // ldmatrix rows: lane l gives row l % 8 of matrix l / 8.  K: (keys 0-7,
+    // chunk i), (8-15, i), (0-7, i + 1), (8-15, i + 1); V the same in the
+    // E4M3 kind, else (0-7, i), (0-7, i + 1), (8-15, i), (8-15, i + 1).
     const int mrow = lane % 8, mat = lane / 8;
+    const int krow = 16 * quarter + (mat & 1) * 8 + mrow, kchunk = mat / 2;
+    const int vrow = kKind == 0 ? 16 * quarter + (mat / 2) * 8 + mrow : krow;
+    const int vchunk = kKind == 0 ? (mat & 1) : kchunk;
+    auto chunk_at = [](int row, int chunk) -> uint32_t {
+      return row * 128 + (chunk / 8) * (kTileKeys * 128) + ((chunk % 8) ^ (row & 7)) * 16;
+    };
     bool ok = true;
-    int stage = 0, seq = 0;
+    int tile = 0;  // tiles of the CTA so far
     for (int k = 0; ok; ++k) {
-      ok = !bar_any(!mbar_wait(bar(BAR_SFULL + k % kSegs), (k / kSegs) & 1, kWaitLimitNs));
+      ok = !bar_any<kWorkers>(!mbar_wait(bar(BAR_SFULL + k % kSegs), (k / kSegs) & 1, kWaitLimitNs));
       if (!ok) break;
       const Segment g = segs[k % kSegs];
       if (!g.valid) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + k % kSegs));
-      // Q fragments and the keys that this thread's rows see
-      uint32_t qf[kM][8][4];
-      int lo[kM][2], hi[kM][2];
+      // Q as the second operand: row u of each tile, dimensions 2t, 2t + 1
+      // and 2t + 8, 2t + 9 of 16 (4t .. 4t + 3 in the E4M3 kind)
+      uint32_t qf[kN][8][2];
+      float qinv[kN][2];  // E4M3: undoes the scaling of rows 2t, 2t + 1
 #pragma unroll
-      for (int m = 0; m < kM; ++m) {
+      for (int n = 0; n < kN; ++n) {
+        const int rho = g.rho0 + 8 * n + u;
+        const bool real = 8 * n + u < g.rows;
+        const int i = rho / a.group;
+        const uint16_t* src = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
+                              static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rho = g.rho0 + 16 * m + r + 8 * e;
-          const bool real = 16 * m + r + 8 * e < g.rows;
-          const int i = rho / a.group;
-          const int pos = g.len - g.n + i;
-          lo[m][e] = real ? row_lo(a, pos) : 0;
-          hi[m][e] = real ? (a.causal ? min(g.len, pos + 1) : g.len) : 0;
-          const uint16_t* src = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
-                                static_cast<int64_t>(g.h * a.group + rho % a.group) * a.q_head;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            uint32_t x = 0, y = 0;
-            if (real) {
-              if constexpr (kKind == 0) {
-                x = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
-                y = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
-              } else {  // dimensions 4t, 4t + 2 and 4t + 1, 4t + 3, as the codes come
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
-                x = __byte_perm(v.x, v.y, 0x5410);
-                y = __byte_perm(v.x, v.y, 0x7632);
-              }
+        for (int kk = 0; kk < 8; ++kk) {
+          qf[n][kk][0] = qf[n][kk][1] = 0;
+          if (real) {
+            if constexpr (kKind == 0) {
+              qf[n][kk][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
+              qf[n][kk][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
+              qf[n][kk][0] = v.x;
+              qf[n][kk][1] = v.y;
             }
-            qf[m][kk][e] = x;
-            qf[m][kk][2 + e] = y;
           }
         }
-      }
-      const int all_lo = row_lo(a, g.len - g.n + (g.rho0 + g.rows - 1) / a.group);
-      const int all_hi = a.causal ? min(g.len, g.len - g.n + g.rho0 / a.group + 1) : g.len;
-      float acc[kM][16][4], ref[kM][2], sum[kM][2];
+        if constexpr (kKind != 0) {
+          uint32_t m2 = 0;
 #pragma unroll
-      for (int m = 0; m < kM; ++m) {
+          for (int kk = 0; kk < 8; ++kk)
+            m2 = __vmaxu2(m2, __vmaxu2(qf[n][kk][0] & 0x7FFF7FFFu, qf[n][kk][1] & 0x7FFF7FFFu));
+          m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 1));
+          m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 2));
+          // largest magnitude 2^(E - 127): times 2^(141 - E), at most 2^127
+          const int e = min(127, 141 - static_cast<int>(max(m2 >> 16, m2 & 0xFFFFu) >> 7));
+          const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+          for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          ref[m][e] = -INFINITY;
-          sum[m][e] = 0.f;
+            for (int x = 0; x < 2; ++x)
+              qf[n][kk][x] = pack_f16x2(bf_lo(qf[n][kk][x]) * f, bf_hi(qf[n][kk][x]) * f);
+          // 2^-e, a subnormal number for e = 127
+          const float inv = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          qinv[n][0] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t4);
+          qinv[n][1] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t4 + 4);
         }
       }
+      // keys that this thread's rows 2t, 2t + 1 of each tile see
+      int lo[kN][2], hi[kN][2];
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n + 2 * t4 + e;
+          const int pos = g.len - g.n + (g.rho0 + row) / a.group;
+          lo[n][e] = row < g.rows ? row_lo(a, pos) : 0;
+          hi[n][e] = row < g.rows ? (a.causal ? min(g.len, pos + 1) : g.len) : 0;
+        }
+      // [all_lo, all_hi): what every row sees
+      const int all_lo = row_lo(a, g.len - g.n + (g.rho0 + g.rows - 1) / a.group);
+      const int all_hi = a.causal ? min(g.len, g.len - g.n + g.rho0 / a.group + 1) : g.len;
+      float acc[kN][8][4], ref[kN][2], sum[kN][2];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ref[n][e] = -INFINITY;
+          sum[n][e] = 0.f;
+        }
+      }
+      const int step = C::kGroups;
+      const int skip = (grp - tile % C::kGroups + C::kGroups) % C::kGroups;  // the group's first tile of this unit
 #pragma unroll 1
-      for (int t = g.t0; t < g.t0 + g.nt; ++t) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_FULL + stage), (seq / R::kStages) & 1, kWaitLimitNs));
+      for (int t = skip; t < g.nt; t += step) {
+        const int use = tile + t, stage = use % C::kStages;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_FULL + stage), (use / C::kStages) & 1, kWaitLimitNs));
         if (!ok) break;
-        const uint32_t sk = sbase + stage * R::kStage, sv = sk + R::kHalf;
-        uint8_t* ex = base + kOffExp + stage * R::kExp;
-        const int key0 = (t << kKeyShift) + 16 * warp;
+        const uint32_t sk = sbase + stage * C::kStage, sv = sk + C::kHalf;
+        const int key0 = ((g.t0 + t) << kKeyShift) + 16 * quarter;
         // Slots that no row sees may hold anything: this warp's V rows there
         // become zeros (their probabilities are 0, and 0 * NaN is not).
         const bool ragged = key0 < g.lo || key0 + 16 > g.hi;
         if (ragged) {
-          const int u = lane / 2;
-          if (key0 + u < g.lo || key0 + u >= g.hi) {
-            uint8_t* v = base + stage * R::kStage + R::kHalf + (16 * warp + u) * 128;
+          const int x = lane / 2;
+          if (key0 + x < g.lo || key0 + x >= g.hi) {
+            uint8_t* v = base + stage * C::kStage + C::kHalf + (16 * quarter + x) * 128;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               *reinterpret_cast<uint4*>(v + (lane % 2) * 64 + 16 * i) = make_uint4(0, 0, 0, 0);
@@ -329,213 +398,197 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           }
           __syncwarp();
         }
-        // ---- S = Q K^T of 16 keys: two n-tiles
-        float s[kM][2][4];
+        // ---- S^T = K Q^T: keys u and u + 8, rows 2t and 2t + 1
+        float s[kN][4];
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[m][0][e] = s[m][1][e] = 0.f;
-        {
-          // matrices: keys 0-7 chunk c, c + 1, keys 8-15 chunk c, c + 1
-          const int row = 16 * warp + (mat / 2) * 8 + mrow;
-          const uint32_t rb = sk + row * 128;
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
-          for (int kk = 0; kk < (kKind == 0 ? 8 : 4); ++kk) {
-            const int chunk = 2 * kk + (mat & 1);
-            uint32_t b[4];
-            ldsm4(b, rb + (kKind == 0 ? (chunk / 8) * (kTileKeys * 128) : 0) + ((chunk % 8) ^ (row & 7)) * 16);
-            if constexpr (kKind == 0) {
+        for (int kk = 0; kk < (kKind == 0 ? 8 : 4); ++kk) {
+          uint32_t b[4];
+          ldsm4(b, sk + chunk_at(krow, 2 * kk + kchunk));
+          if constexpr (kKind == 0) {
 #pragma unroll
-              for (int m = 0; m < kM; ++m) {
-                mma(s[m][0], qf[m][kk], b[0], b[1]);
-                mma(s[m][1], qf[m][kk], b[2], b[3]);
-              }
-            } else {
+            for (int n = 0; n < kN; ++n) mma<false>(s[n], b[0], b[1], b[2], b[3], qf[n][kk][0], qf[n][kk][1]);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {  // keys 8 (i / 2).., dimensions 16 (2 kk + i % 2)..
-                const uint32_t b0 = codes_even(b[i]), b1 = codes_odd(b[i]);
+            for (int i = 0; i < 2; ++i) {  // 16 dimensions of chunk 2 kk + i
+              uint32_t l0, h0, l1, h1;
+              codes_f16(b[2 * i], l0, h0);
+              codes_f16(b[2 * i + 1], l1, h1);
 #pragma unroll
-                for (int m = 0; m < kM; ++m) mma(s[m][i / 2], qf[m][2 * kk + i % 2], b0, b1);
-              }
+              for (int n = 0; n < kN; ++n)
+                mma<true>(s[n], l0, l1, h0, h1, qf[n][2 * kk + i][0], qf[n][2 * kk + i][1]);
             }
           }
         }
-        float ks[2][2], vs[2][2];
+        float ks[2], vs[2];
         if constexpr (kKind != 0) {
+          const uint8_t* ex = base + C::kOffExp + stage * C::kExp + 16 * quarter + u;
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int u = 16 * warp + 8 * nt + 2 * t4;
-            const uint32_t ke = *reinterpret_cast<const uint16_t*>(ex + u);
-            const uint32_t ve = *reinterpret_cast<const uint16_t*>(ex + kTileKeys + u);
-            ks[nt][0] = exp_scale(ke & 255u) * c2;
-            ks[nt][1] = exp_scale(ke >> 8) * c2;
-            vs[nt][0] = exp_scale(ve & 255u);
-            vs[nt][1] = exp_scale(ve >> 8);
+          for (int e = 0; e < 2; ++e) {
+            ks[e] = exp_scale(ex[8 * e]) * c2;
+            vs[e] = exp_scale(ex[kTileKeys + 8 * e]);
           }
         }
         const bool cut = ragged || key0 < all_lo || key0 + 16 > all_hi;  // some row misses some key
-        uint32_t p[kM][4];
+        uint32_t p[kN][2];
 #pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          bool moves = false;
-          float mx[2] = {-INFINITY, -INFINITY};
+        for (int n = 0; n < kN; ++n) {
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int e = 0; e < 4; ++e) {
+            s[n][e] *= kKind == 0 ? c2 : qinv[n][e & 1];
+            if constexpr (kKind != 0) s[n][e] *= ks[e / 2];
+          }
+          if (cut) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = s[m][nt][e] * (kKind == 0 ? c2 : ks[nt][e & 1]);
-              if (cut) {
-                const int key = key0 + 8 * nt + 2 * t4 + (e & 1);
-                if (key < lo[m][e / 2] || key >= hi[m][e / 2]) x = -INFINITY;
-              }
-              s[m][nt][e] = x;
-              mx[e / 2] = fmaxf(mx[e / 2], x);
+              const int key = key0 + u + 8 * (e / 2);
+              if (key < lo[n][e & 1] || key >= hi[n][e & 1]) s[n][e] = -INFINITY;
             }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-            moves |= mx[e] > ref[m][e] + kRescaleLog2;
           }
-          // The reference follows the maximum only when it is passed by 2^8:
-          // p <= 256 keeps the sums far inside FP32.
-          if (__any_sync(0xFFFFFFFFu, moves)) {
+          // The reference follows the maximum only when some key passes it by
+          // 2^8 (p <= 256 keeps the sums far inside FP32): the lanes need not
+          // agree on a maximum before that.
+          float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
+          if (__any_sync(0xFFFFFFFFu, mx[0] > ref[n][0] + kRescaleLog2 || mx[1] > ref[n][1] + kRescaleLog2)) {
+            float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float to = mx[e] > ref[m][e] + kRescaleLog2 ? mx[e] : ref[m][e];
-              const float f = to == ref[m][e] ? 1.f : ex2_approx(ref[m][e] - to);  // first keys: 2^-inf = 0
-              ref[m][e] = to;
-              sum[m][e] *= f;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                acc[m][i][2 * e] *= f;
-                acc[m][i][2 * e + 1] *= f;
-              }
+              for (int d = 4; d < 32; d *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], d));
+              const float to = mx[e] > ref[n][e] + kRescaleLog2 ? mx[e] : ref[n][e];
+              f[e] = to == ref[n][e] ? 1.f : ex2_approx(ref[n][e] - to);  // the first keys: 2^-inf = 0
+              ref[n][e] = to;
+              sum[n][e] *= f[e];
             }
-          }
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            float y[4];
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float rf = ref[m][e / 2] == -INFINITY ? 0.f : ref[m][e / 2];
-              const float x = ex2_approx(s[m][nt][e] - rf);
-              sum[m][e / 2] += x;
-              // a hidden key's scale may be NaN
-              y[e] = kKind == 0 ? x : (x == 0.f ? 0.f : x * vs[nt][e & 1]);
-            }
-            p[m][2 * nt] = pack_bf16x2(y[0], y[1]);
-            p[m][2 * nt + 1] = pack_bf16x2(y[2], y[3]);
+              for (int e = 0; e < 4; ++e) acc[n][i][e] *= f[e & 1];
           }
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = ex2_approx(s[n][e] - (ref[n][e & 1] == -INFINITY ? 0.f : ref[n][e & 1]));
+            sum[n][e & 1] += x;
+            y[e] = kKind == 0 ? x : (x == 0.f ? 0.f : x * vs[e / 2]);  // (a hidden key's scale may be NaN)
+          }
+          p[n][0] = transpose8(pack_bf16x2(y[0], y[1]));
+          p[n][1] = transpose8(pack_bf16x2(y[2], y[3]));
         }
-        // ---- O += P V: matrices keys 0-7, 8-15 of chunk c, then of chunk c + 1
-        {
-          const int row = 16 * warp + (mat & 1) * 8 + mrow;
-          const uint32_t rb = sv + row * 128;
+        // ---- O^T += V^T P^T: dimensions u, u + 8 of 16 (2u, 2u + 1 in the E4M3 kind)
 #pragma unroll
-          for (int j = 0; j < (kKind == 0 ? 8 : 4); ++j) {
-            const int chunk = 2 * j + mat / 2;
-            uint32_t b[4];
-            ldsm4_t(b, rb + (kKind == 0 ? (chunk / 8) * (kTileKeys * 128) : 0) + ((chunk % 8) ^ (row & 7)) * 16);
+        for (int j = 0; j < (kKind == 0 ? 8 : 4); ++j) {
+          uint32_t b[4];
+          ldsm4_t(b, sv + chunk_at(vrow, 2 * j + vchunk));
+          if constexpr (kKind == 0) {
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma<false>(acc[n][j], b[0], b[1], b[2], b[3], p[n][0], p[n][1]);
+          } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if constexpr (kKind == 0) {
+              const uint32_t e0 = codes_even(b[2 * i]), o0 = codes_odd(b[2 * i]);
+              const uint32_t e1 = codes_even(b[2 * i + 1]), o1 = codes_odd(b[2 * i + 1]);
 #pragma unroll
-                for (int m = 0; m < kM; ++m) mma(acc[m][2 * j + i], p[m], b[2 * i], b[2 * i + 1]);
-              } else {  // even and odd dimensions of 16
-                const uint32_t e0 = codes_even(b[2 * i]), e1 = codes_even(b[2 * i + 1]);
-                const uint32_t o0 = codes_odd(b[2 * i]), o1 = codes_odd(b[2 * i + 1]);
-#pragma unroll
-                for (int m = 0; m < kM; ++m) {
-                  mma(acc[m][4 * j + 2 * i], p[m], e0, e1);
-                  mma(acc[m][4 * j + 2 * i + 1], p[m], o0, o1);
-                }
-              }
+              for (int n = 0; n < kN; ++n) mma<false>(acc[n][2 * j + i], e0, o0, e1, o1, p[n][0], p[n][1]);
             }
           }
         }
         if (ragged) fence_proxy_async_smem();  // zeros written here, TMA writes next
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_EMPTY + stage));
-        ++seq;
-        stage = stage + 1 == R::kStages ? 0 : stage + 1;
       }
-      ok = !bar_any(!ok || *s_abort != 0);
-      if (!ok) break;
-      // ---- the four warps' results into one
+      tile += g.nt;
+      // ---- the warps' results into one
 #pragma unroll
-      for (int m = 0; m < kM; ++m)
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sum[m][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[m][e], 1);
-          sum[m][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[m][e], 2);
-          if (t4 == 0) {
-            s_m[warp * 32 + 16 * m + r + 8 * e] = ref[m][e];
-            s_l[warp * 32 + 16 * m + r + 8 * e] = sum[m][e];
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) sum[n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][e], d);
+          if (u == 0) {
+            s_m[warp * kRows + 8 * n + 2 * t4 + e] = ref[n][e];
+            s_l[warp * kRows + 8 * n + 2 * t4 + e] = sum[n][e];
           }
         }
-      bar_consumers();
-      float f[kM][2];
+      ok = !bar_any<kWorkers>(!ok || *s_abort != 0);
+      if (!ok) break;
+      auto top = [&](int row) {
+        float m = -INFINITY;
 #pragma unroll
-      for (int m = 0; m < kM; ++m)
+        for (int w = 0; w < C::kConsumers; ++w) m = fmaxf(m, s_m[w * kRows + row]);
+        return m;
+      };
+      float* mine = merge + warp % C::kRegions * 8 * kMergeRow;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 16 * m + r + 8 * e;
-          const float mt = fmaxf(fmaxf(s_m[row], s_m[32 + row]), fmaxf(s_m[64 + row], s_m[96 + row]));
-          f[m][e] = ref[m][e] == -INFINITY ? 0.f : ex2_approx(ref[m][e] - mt);
-        }
-      constexpr int kCols = 128 / kM;  // columns a pass: 8 KB of FP32
+      for (int n = 0; n < kN; ++n) {
+        float f[2];
 #pragma unroll
-      for (int pass = 0; pass < kM; ++pass) {
-        for (int w = 0; w < kConsumers; ++w) {
-          if (warp == w) {
+        for (int e = 0; e < 2; ++e)
+          f[e] = ref[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - top(8 * n + 2 * t4 + e));
 #pragma unroll
-            for (int m = 0; m < kM; ++m)
+        for (int gr = 0; gr < C::kConsumers / C::kRegions; ++gr) {  // warp after warp adds to its region
+          if (warp / C::kRegions == gr) {
 #pragma unroll
-              for (int i = 0; i < 16 / kM; ++i) {
-                const int n = pass * (16 / kM) + i;
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int col = kKind == 0 ? 8 * i + 2 * t4 + (e & 1)
-                                             : 16 * (i / 2) + 4 * t4 + 2 * (e & 1) + (i & 1);
-                  float* d = merge + (16 * m + r + 8 * (e / 2)) * kCols + col;
-                  const float y = acc[m][n][e] * f[m][e / 2];
-                  *d = w == 0 ? y : *d + y;
-                }
+              for (int e = 0; e < 4; ++e) {
+                const int d = 16 * j + (kKind == 0 ? u + 8 * (e / 2) : 2 * u + e / 2);
+                float* to = mine + (2 * t4 + (e & 1)) * kMergeRow + d;
+                const float y = acc[n][j][e] * f[e & 1];
+                *to = gr == 0 ? y : *to + y;
               }
           }
-          bar_consumers();
+          bar_all<kWorkers>();
         }
-        // 16 kM rows x kCols columns: 16 values a thread, in one row
-        const int row = threadIdx.x * 16 / kCols, col = threadIdx.x * 16 % kCols;
-        const float mt = fmaxf(fmaxf(s_m[row], s_m[32 + row]), fmaxf(s_m[64 + row], s_m[96 + row]));
-        float l = 0.f;
+        // 8 rows x 128 columns of the regions' sums
+        constexpr int kPer = 8 * 128 / kWorkers;  // 8 or 4 columns a thread
+        const int row = threadIdx.x * kPer / 128, col = threadIdx.x * kPer % 128;
+        if (8 * n + row < g.rows) {
+          float o[kPer];
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w)
-          l += s_m[32 * w + row] == -INFINITY ? 0.f : s_l[32 * w + row] * ex2_approx(s_m[32 * w + row] - mt);
-        const float* src = merge + row * kCols + col;
-        if (row < g.rows) {
+          for (int i = 0; i < kPer; i += 4) {
+            float4 y = *reinterpret_cast<const float4*>(merge + row * kMergeRow + col + i);
+#pragma unroll
+            for (int x = 1; x < C::kRegions; ++x) {
+              const float4 z = *reinterpret_cast<const float4*>(merge + (8 * x + row) * kMergeRow + col + i);
+              y.x += z.x;
+              y.y += z.y;
+              y.z += z.z;
+              y.w += z.w;
+            }
+            o[i] = y.x;
+            o[i + 1] = y.y;
+            o[i + 2] = y.z;
+            o[i + 3] = y.w;
+          }
+          const float m = top(8 * n + row);
+          float l = 0.f;
+#pragma unroll
+          for (int w = 0; w < C::kConsumers; ++w) {
+            const float mw = s_m[w * kRows + 8 * n + row];
+            l += mw == -INFINITY ? 0.f : s_l[w * kRows + 8 * n + row] * ex2_approx(mw - m);
+          }
           if (g.part < 0) {
-            const int rho = g.rho0 + row;
-            const int64_t at = static_cast<int64_t>(g.row0 + rho / a.group) * a.Hq + g.h * a.group + rho % a.group;
+            const int rho = g.rho0 + 8 * n + row, i = rho / a.group;
+            const int64_t at = static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + rho - i * a.group;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-            uint32_t y[8];
+            uint2* dst = reinterpret_cast<uint2*>(a.o + at * kHeadDim + col);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(src[2 * i] * inv, src[2 * i + 1] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(a.o + at * kHeadDim + pass * kCols + col);
-            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-            if (a.lse && pass == 0 && col == 0)
-              a.lse[at] = l == 0.f ? -INFINITY : (mt + log2f(l)) * 0.6931471805599453f;
+            for (int x = 0; x < kPer; x += 4)
+              dst[x / 4] = make_uint2(pack_bf16x2(o[x] * inv, o[x + 1] * inv), pack_bf16x2(o[x + 2] * inv, o[x + 3] * inv));
+            if (a.lse && col == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
           } else {
-            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + row;
-            float4* dst = reinterpret_cast<float4*>(ws.part + at * kHeadDim + pass * kCols + col);
+            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + 8 * n + row;
+            float4* dst = reinterpret_cast<float4*>(ws.part + at * kHeadDim + col);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = reinterpret_cast<const float4*>(src)[i];
-            if (pass == 0 && col == 0) ws.ml[at] = make_float2(mt, l);
+            for (int x = 0; x < kPer; x += 4) dst[x / 4] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            if (col == 0) ws.ml[at] = make_float2(m, l);
           }
         }
-        bar_consumers();
+        if (n + 1 < kN) bar_all<kWorkers>();  // (the next unit's first barrier otherwise)
       }
     }
     if (!ok) *s_abort = 1;
@@ -545,18 +598,24 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   griddep_launch_dependents();
 }
 
-}  // namespace
+template <int kKind, int kN>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, const PagedScratch& ws,
+                   int ctas, cudaStream_t s) {
+  using C = Cfg<kKind, kN>;
+  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<kKind, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  paged_few_kernel<kKind, kN><<<ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a, ws);
+  return cudaGetLastError();
+}
 
-size_t paged_few_smem() { return kSmemBytes; }
+}  // namespace
 
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s) {
-  auto* kern = a.c.kind == 0 ? (row_tile == 16 ? paged_few_kernel<0, 1> : paged_few_kernel<0, 2>)
-                             : (row_tile == 16 ? paged_few_kernel<1, 1> : paged_few_kernel<1, 2>);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, kSmemBytes, s>>>(tk, tv, a, ws);
-  return cudaGetLastError();
+  if (a.c.kind == 0)
+    return row_tile == 8 ? launch<0, 1>(tk, tv, a, ws, ctas, s) : launch<0, 2>(tk, tv, a, ws, ctas, s);
+  return row_tile == 8 ? launch<1, 1>(tk, tv, a, ws, ctas, s) : launch<1, 2>(tk, tv, a, ws, ctas, s);
 }
 
 }  // namespace sa
