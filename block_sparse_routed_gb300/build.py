@@ -19,7 +19,7 @@ OUT = os.path.join(HERE, "_build")
 LIB_NAME = "libsparse_attn.so"
 LIB_PATH = os.path.join(OUT, LIB_NAME)
 SOURCES = ["api.cu", "plan_kernels.cu", "attn_kernel.cu", "plan_static.cu", "spark_reweight.cu", "reblock.cu",
-           "paged_api.cu", "paged_cache.cu", "paged_attn.cu", "paged_few.cu"]
+           "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_chunk.cu", "paged_join.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-lineinfo",

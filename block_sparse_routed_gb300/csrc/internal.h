@@ -209,6 +209,8 @@ struct PagedScratch {
 
 constexpr int kPagedFewRows = 16;   // most packed rows of the form for few rows
 constexpr int kPagedFewCtas = 320;  // most CTAs of it (two an SM)
+constexpr int kPagedChunkRows = 256;  // packed rows of a unit of the form for chunks
+constexpr int kPagedChunkCtas = 160;
 
 struct PagedForm {
   int row_tile;  // packed rows of a unit
@@ -220,7 +222,8 @@ cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStrea
 cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
-cudaError_t launch_paged_simple(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
+                               const PagedScratch& ws, int ctas, cudaStream_t s);
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
 
 // Multiprocessors of the current device (cached).

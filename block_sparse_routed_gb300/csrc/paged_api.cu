@@ -39,7 +39,7 @@ sa_status check_attn(const sa_paged_params* p) {
   if (int64_t(p->rows) * p->Hq >= (int64_t(1) << 31)) return SA_EUNSUPPORTED;
   if (p->causal != 0 && p->causal != 1) return SA_EINVAL;
   if (p->window < 0 || (p->window > 0 && !p->causal)) return SA_EINVAL;
-  if (!std::isfinite(p->scale)) return SA_EINVAL;
+  if (!std::isfinite(p->scale) || !(p->scale > 0.0f)) return SA_EINVAL;
   return SA_OK;
 }
 
@@ -88,8 +88,8 @@ PagedForm form_of(const sa_paged_params* p) {
   PagedForm f;
   const int64_t rows = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H);
   f.few = rows <= kPagedFewRows;
-  f.row_tile = rows <= 8 ? 8 : 16;
-  f.max_ctas = kPagedFewCtas;
+  f.row_tile = rows <= 8 ? 8 : (f.few ? kPagedFewRows : kPagedChunkRows);
+  f.max_ctas = f.few ? kPagedFewCtas : kPagedChunkCtas;
   return f;
 }
 
@@ -210,24 +210,25 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
   const PagedForm f = form_of(p);
-  if (!f.few) {
-    st = clear_status(ws, stream);
-    if (st != SA_OK) return st;
-    return cuda_failed(launch_paged_simple(a, stream)) ? SA_ECUDA : SA_OK;
-  }
   PagedScratch scratch;
   scratch_of(ws, f, &scratch);
   CUtensorMap tk, tv;
   const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
   const int elem = p->kind == SA_CACHE_BF16 ? 2 : 1;
-  const uint32_t box = p->page_size < 64 ? p->page_size : 64;
+  // a box holds the keys of a page that fall into a key tile (64 or 128 keys)
+  const int tile = f.few ? 64 : 128;
+  const uint32_t box = p->page_size < tile ? p->page_size : tile;
   if (!make_map_rows(&tk, k_pages, cached, kHeadDim, elem, box) ||
       !make_map_rows(&tv, v_pages, cached, kHeadDim, elem, box))
     return SA_ECUDA;
-  // no more CTAs than the longest contexts that the table can hold have tiles
-  const int64_t most = int64_t(p->seqs) * p->H * ((int64_t(p->table_width) * p->page_size + 63) / 64 + 1);
-  int ctas = 2 * sm_count() < f.max_ctas ? 2 * sm_count() : f.max_ctas;
+  // no more CTAs than units times the key tiles of the longest context that the table can hold
+  const int64_t units = p->seqs + (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile;
+  const int64_t most = units * p->H * ((int64_t(p->table_width) * p->page_size + tile - 1) / tile + 1);
+  int ctas = (f.few ? 2 : 1) * sm_count();
+  if (ctas > f.max_ctas) ctas = f.max_ctas;
   if (most < ctas) ctas = static_cast<int>(most);
-  if (cuda_failed(launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream))) return SA_ECUDA;
+  const cudaError_t e = f.few ? launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream)
+                              : launch_paged_chunk(tk, tv, a, scratch, ctas, stream);
+  if (cuda_failed(e)) return SA_ECUDA;
   return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, stream)) ? SA_ECUDA : SA_OK;
 }

@@ -376,7 +376,7 @@ typedef struct sa_paged_params {
                             kv_len keys of its sequence (paged_fwd only)        */
   int32_t window;        /* w > 0: only the last w of the keys a causal row
                             sees, its own among them; 0: all (paged_fwd only)   */
-  float scale;           /* logit of a key: scale * (q . k), finite (paged_fwd) */
+  float scale;           /* logit of a key: scale * (q . k); > 0, finite (paged_fwd) */
   int64_t a_token_stride, a_head_stride; /* elements, of k (cache_write) or q
                             (paged_fwd): multiples of 8                         */
   int64_t b_token_stride, b_head_stride; /* of v (cache_write)                  */
@@ -425,7 +425,7 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, 
  * Cached values behind kv_len, or below the window of every row, are never
  * used, whatever they are.
  * Errors: as sparse_attn_cache_write, and SA_EINVAL for Hq not a multiple of
- * H, causal not 0 or 1, window < 0 or with causal = 0, scale not finite, o
+ * H, causal not 0 or 1, window < 0 or with causal = 0, scale not positive and finite, o
  * not 16-byte or lse not 4-byte aligned, a short workspace.
  */
 sa_status sparse_attn_paged_ws_bytes(const sa_paged_params* p, uint64_t* out);

@@ -282,9 +282,9 @@ def test_a_window_leaves_freed_pages_unread(bsr, kind):
     check_attention(b, q, o, lse, True, 50)
 
 
-def test_scale_zero_negative_and_large_logits(bsr):
+def test_scales(bsr):
     b = Batch([333, 64], [20, 1], 2, 64, seed=3)
-    for scale in (0.0, -0.05, 3.0):
+    for scale in (1e-6, 0.05, 3.0):
         q, o, lse = run_attention(bsr, b, 4, scale=scale)
         check_attention(b, q, o, lse, scale=scale)
 
@@ -422,6 +422,8 @@ def test_refusals_of_the_python_layer(bsr):
         call(ws=torch.empty(255, dtype=torch.uint8, device="cuda"))
     with pytest.raises(bsr.SparseAttnError):
         call(scale=math.inf)
+    with pytest.raises(bsr.SparseAttnError):
+        call(scale=-0.1)
     with pytest.raises(ValueError):
         call(k_exp=torch.zeros(1, device="cuda"))
     with pytest.raises(ValueError):

@@ -142,7 +142,7 @@ def test_copies_refuse_their_own(native):
 def test_attention_refuses_its_own(native):
     E = native.SA_EINVAL
     for bad in (dict(Hq=3), dict(Hq=0), dict(causal=2), dict(window=-1), dict(causal=0, window=4),
-                dict(scale=float("nan")), dict(scale=float("inf")), dict(at=4), dict(ah=-128)):
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-1.0), dict(at=4), dict(ah=-128)):
         assert _fwd(native, _p(native, **bad)) == E, bad
     p = _p(native)
     for bad in (dict(q=None), dict(o=None), dict(ws=None), dict(q=A + 8), dict(o=A + 8), dict(lse=A + 2), dict(n=255)):
