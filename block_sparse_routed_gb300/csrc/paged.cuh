@@ -78,7 +78,7 @@ __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
 // The rows of a sequence under one key head are packed as rho = i * group + g
 // (new token i, query head g of the group), so that a tile of them reads the
 // same keys.  A unit is a tile of `row_tile` packed rows of one sequence and
-// key head; its work is the key tiles of 2^key_shift keys between the first
+// key head; its work is the tiles of key_tile keys between the first
 // key of its first row and the last key of its last one (one empty tile when
 // there is none, so that every unit writes its rows).  All key tiles of all
 // units, in the order (sequence, head, row tile, key tile), are one line that
@@ -102,7 +102,7 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const PagedSeq&
 }
 
 __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p, int row_tile,
-                                              int key_shift) {
+                                              int key_tile) {
   const int rows = q.n * a.group;
   int i0 = 0, i1 = q.n - 1;  // first and last new token of the tile
   if (rows > row_tile) {
@@ -113,8 +113,8 @@ __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const Page
   u.hi = a.causal ? min(q.len, q.len - q.n + i1 + 1) : q.len;
   u.lo = row_lo(a, q.len - q.n + i0);
   if (u.hi <= u.lo) u.lo = u.hi = 0;
-  u.t0 = u.lo >> key_shift;
-  u.nt = max(1, ((u.hi + (1 << key_shift) - 1) >> key_shift) - u.t0);
+  u.t0 = u.lo / static_cast<uint32_t>(key_tile);
+  u.nt = max(1, static_cast<int>((u.hi + static_cast<uint32_t>(key_tile) - 1) / static_cast<uint32_t>(key_tile)) - u.t0);
   return u;
 }
 
@@ -141,7 +141,7 @@ __device__ __forceinline__ int64_t muldiv(int64_t x, int64_t y, int64_t z) {
 
 // Key tiles of one head of the sequences base + lane, one a lane (0 past the
 // last).  Sequences of many row tiles are summed by the whole warp.
-__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, int row_tile, int key_shift, int lane,
+__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, int row_tile, int key_tile, int lane,
                                               bool& bad) {
   const int s = base + lane;
   PagedSeq q;
@@ -154,7 +154,7 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
   const int tiles = row_tiles(a, q, row_tile);
   int64_t t = 0;
   if (tiles <= 4)
-    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, row_tile, key_shift).nt;
+    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, row_tile, key_tile).nt;
   unsigned many = __ballot_sync(0xFFFFFFFFu, tiles > 4);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -165,7 +165,7 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
     r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
     const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
     int64_t y = 0;
-    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, row_tile, key_shift).nt;
+    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, row_tile, key_tile).nt;
     y = warp_sum(y);
     if (lane == src) t = y;
   }
@@ -201,12 +201,12 @@ __device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w, in
 
 // Finds the part of CTA `cta` of `ctas`; each takes min_tiles at least, while
 // there are any.  Sets `bad` when a sequence fails its checks.
-__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_shift, int cta,
+__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_tile, int cta,
                                            int ctas, int min_tiles, bool& bad) {
   const int lane = threadIdx.x % 32, seqs = a.c.seqs;
   int64_t t = 0, first = 0;
   for (int base = 0; base < seqs; base += 32) {
-    t += lane_tiles(a, base, row_tile, key_shift, lane, bad);
+    t += lane_tiles(a, base, row_tile, key_tile, lane, bad);
     if (base == 0) first = t;
   }
   w.total = warp_sum(t) * a.c.H;
@@ -221,7 +221,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
   int64_t left = w.at;
   for (int base = 0;; base += 32) {
     bool b;
-    const int64_t mine = (base == 0 ? first : lane_tiles(a, base, row_tile, key_shift, lane, b)) * a.c.H;
+    const int64_t mine = (base == 0 ? first : lane_tiles(a, base, row_tile, key_tile, lane, b)) * a.c.H;
     const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
@@ -242,7 +242,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
     return;
   }
   for (int p0 = 0;; p0 += 32) {
-    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, row_tile, key_shift).nt : 0;
+    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, row_tile, key_tile).nt : 0;
     const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
@@ -257,7 +257,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
 
 // The next step (valid = 0 at the end); `join` is filled when it leaves a
 // unit unfinished that it began.
-__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_shift, int cta,
+__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_tile, int cta,
                                              JoinDesc& join) {
   Segment g;
   g.valid = 0;
@@ -270,7 +270,7 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
       walk_seq(a, w, row_tile);
     }
   }
-  const UnitKeys u = unit_keys(a, w.q, w.p, row_tile, key_shift);
+  const UnitKeys u = unit_keys(a, w.q, w.p, row_tile, key_tile);
   g.valid = 1;
   g.row0 = w.q.row0;
   g.n = w.q.n;

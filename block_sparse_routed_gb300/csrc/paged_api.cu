@@ -215,9 +215,9 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   CUtensorMap tk, tv;
   const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
   const int elem = p->kind == SA_CACHE_BF16 ? 2 : 1;
-  // a box holds the keys of a page that fall into a key tile (64 or 128 keys)
-  const int tile = f.few ? 64 : 128;
-  const uint32_t box = p->page_size < tile ? p->page_size : tile;
+  // a box holds the keys of a page that fall into a tile of 64 keys, or 16 keys (the tiles of 80)
+  const uint32_t box = f.few ? (p->page_size < 64 ? p->page_size : 64) : 16;
+  const int tile = f.few ? 64 : 80;
   if (!make_map_rows(&tk, k_pages, cached, kHeadDim, elem, box) ||
       !make_map_rows(&tv, v_pages, cached, kHeadDim, elem, box))
     return SA_ECUDA;

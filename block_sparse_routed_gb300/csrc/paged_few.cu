@@ -198,7 +198,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     LineWalk w;
     bool bad = false;
-    walk_begin(a, w, kRows, kKeyShift, blockIdx.x, gridDim.x, 1, bad);
+    walk_begin(a, w, kRows, kTileKeys, blockIdx.x, gridDim.x, 1, bad);
     JoinDesc join;
     join.pieces = 0;
     bool ok = true;
@@ -207,7 +207,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int tile_pages = kTileKeys / per_page;
     const int sub = lane % 4, pg = lane / 4;                  // lane: page pg of the tile, box sub
     for (int k = 0; ok; ++k) {
-      const Segment g = walk_next(a, w, kRows, kKeyShift, blockIdx.x, join);
+      const Segment g = walk_next(a, w, kRows, kTileKeys, blockIdx.x, join);
       ok = k < kSegs ||
            __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_SEMPTY + k % kSegs), ((k / kSegs) & 1) ^ 1, kWaitLimitNs));
       if (!ok) break;
