@@ -233,6 +233,11 @@ int sm_count();
 // [box_rows, 128 bytes], 128-byte swizzle, zeros past the last row.
 bool make_map_rows(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int elem, uint32_t box_rows);
 
+// Tensor map of BF16 rows [rows, 128] (rows a multiple of 8) as [rows / 8][2
+// halves][8 rows][64 columns]: a box is box_rows rows, written as one 1 KB
+// block (8 rows x 128 bytes, 128-byte swizzle) for each half of each 8 rows.
+bool make_map_groups(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows);
+
 size_t route_topk_smem_bytes(const Geometry& g);
 size_t attention_smem_bytes();
 

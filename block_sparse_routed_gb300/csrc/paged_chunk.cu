@@ -43,8 +43,10 @@ constexpr int kTileKeys = 80;
 constexpr int kBoxKeys = 16;             // keys of a TMA box: divides pages and tiles
 constexpr int kBoxes = kTileKeys / kBoxKeys;
 constexpr int kUnitRows = kPagedChunkRows;
-constexpr uint32_t kHalfBytes = kTileKeys * 128;     // 64 dimensions of a K or V tile
-constexpr uint32_t kSlotBytes = 2 * kHalfBytes;
+// A K or V tile: for each 8 keys two blocks of 1 KB, [8 keys x 64 dimensions]
+// with 128-byte swizzle, one for each half of the dimensions.
+constexpr uint32_t kSlotBytes = kTileKeys * 256;
+constexpr uint32_t kGroupBytes = 2048, kHalfBytes = 1024;
 constexpr uint32_t kQBytes = 32768;      // of a tile: 2 column halves x [128 rows x 128 B]
 constexpr int kSegs = 2;
 constexpr int kStageSlots = 4;           // staged code tiles (E4M3): [80 keys x 128 B]
@@ -132,10 +134,10 @@ __device__ __forceinline__ float max80(const uint32_t (&s)[kTileKeys]) {
   return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// Arrives on `bar` when this thread's cp.async so far have completed (counted
+// among the barrier's arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 bytes, or zeros when !real.
@@ -168,7 +170,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (kKind) mbar_init(bar(BAR_FULL + i), 2);  // the widening warps
       mbar_init(bar(BAR_EMPTY + i), i % 2 ? 1 : 2);  // K: both tiles' issuers; V: one issuer
     }
-    for (int i = 0; i < kStageSlots; ++i) mbar_init(bar(BAR_SGEMPTY + i), 2);
+    for (int i = 0; i < kStageSlots; ++i) {
+      mbar_init(bar(BAR_SGFULL + i), 1 + kBoxes);  // the codes' TMA, the exponents
+      mbar_init(bar(BAR_SGEMPTY + i), 2);
+    }
     for (int i = 0; i < kSegs; ++i) mbar_init(bar(BAR_SEGEMPTY + i), kKind ? 15 : 11);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(BAR_SREAD + t), 4);
@@ -205,7 +210,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   };
   // K's slot of the CTA's x-th key tile is 2x, V's 2x + 1 of one sequence.
   constexpr int kSlots = C::kSlots;
-  auto slot_addr = [&](int q) { return sbase + C::kOffRing + (q % kSlots) * kSlotBytes; };
   bool ok = true;
 
   if (warp < 4) setmaxnreg_dec<C::kRegsControl>();
@@ -220,8 +224,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     walk_begin(a, w, kUnitRows, kTileKeys, blockIdx.x, gridDim.x, kMinTiles, bad);
     JoinDesc join;
     join.pieces = 0;
-    int q = 0;  // tiles of K or V so far
-    const int sub = lane % 2, box = lane / 2;  // lane: 16 keys of the tile, half the dimensions
+    int q = 0, buf = 0, round = 0;  // tiles of K or V so far, the next one's slot and use of it
+    const uint32_t elect = elect_one();
     constexpr int kBufs = kKind ? kStageSlots : kSlots;
     constexpr int kFull = kKind ? BAR_SGFULL : BAR_FULL, kEmpty = kKind ? BAR_SGEMPTY : BAR_EMPTY;
     for (int k = 0; ok; ++k) {
@@ -246,30 +250,46 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           bad |= wrong;
           if (wrong) entry = -1;
         }
-        const int key = t * kTileKeys + box * kBoxKeys, at = key >> c.page_shift;
+        // lane i < 5: row of the cache where the i-th 16 keys begin (-1: not to be loaded)
+        const int key = t * kTileKeys + lane * kBoxKeys, at = key >> c.page_shift;
         const int page = __shfl_sync(0xFFFFFFFFu, entry, (at - have) & 31);
-        const bool mine = box < kBoxes && at >= p_lo && at < p_hi && page >= 0;
-        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine && sub == 0));
-        const int row = static_cast<int>(((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) +
-                                         (key & (c.page_size - 1)));
+        const bool mine = lane < kBoxes && at >= p_lo && at < p_hi && page >= 0;
+        const int row = mine ? static_cast<int>(((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) +
+                                                (key & (c.page_size - 1)))
+                             : -1;
+        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        int rows[kBoxes];
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) rows[i] = __shfl_sync(0xFFFFFFFFu, row, i);
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++q) {
-          const int b = q % kBufs;
-          ok = q < kBufs || __all_sync(0xFFFFFFFFu, wait(kEmpty + b, q / kBufs - 1));
+        for (int kv = 0; kv < 2; ++kv) {
+          const CUtensorMap* map = kv ? &tm_v : &tm_k;
+          const int b = buf;
+          ok = q < kBufs || all_wait(kEmpty + b, round - 1);
           if (!ok) break;
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 + 1 : 256));
-          __syncwarp();
-          if (mine) {
-            const CUtensorMap* map = kv ? &tm_v : &tm_k;
-            if constexpr (kKind == 0) {
-              tma_load_2d(slot_addr(q) + sub * kHalfBytes + box * kBoxKeys * 128, map, bar(kFull + b), sub * 64, row);
-            } else if (sub == 0) {
-              tma_load_2d(sbase + C::kOffStage + b * kStageBytes + box * kBoxKeys * 128, map, bar(kFull + b), 0, row);
-            } else {
-              bulk_load(sbase + C::kOffExp + b * kTileKeys + box * kBoxKeys, (kv ? c.v_exp : c.k_exp) + row, kBoxKeys,
-                        bar(kFull + b));
+          if (kKind != 0 && lane < kBoxes) {  // the exponents, 16 bytes a box
+            if (mine)
+              cp_async16(sbase + C::kOffExp + b * kTileKeys + lane * kBoxKeys, (kv ? c.v_exp : c.k_exp) + row, true);
+            cp_async_arrive(bar(kFull + b));
+          }
+          if (elect) {
+            mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 : 256));
+#pragma unroll
+            for (int i = 0; i < kBoxes; ++i) {
+              if (rows[i] < 0) continue;
+              if constexpr (kKind == 0)
+                tma_load_4d(sbase + C::kOffRing + b * kSlotBytes + i * (kBoxKeys * 256), map, bar(kFull + b), 0, 0, 0,
+                            rows[i] / 8);
+              else
+                tma_load_2d(sbase + C::kOffStage + b * kStageBytes + i * (kBoxKeys * 128), map, bar(kFull + b), 0,
+                            rows[i]);
             }
+          }
+          __syncwarp();
+          ++q;
+          if (++buf == kBufs) {
+            buf = 0;
+            ++round;
           }
         }
         if (__any_sync(0xFFFFFFFFu, *s_abort != 0)) ok = false;
@@ -279,6 +299,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (!ok) {
       *s_abort = 1;
       // copies in flight land before the CTA ends (bounded)
+      if (kKind) asm volatile("cp.async.wait_all;" ::: "memory");
       for (int x = max(0, q - kBufs); x < q; ++x) wait(kFull + x % kBufs, x / kBufs);
     }
     if (lane == 0) {
@@ -337,7 +358,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (!ok) break;
         if (rows) {
           tc_fence_after();
-          const uint64_t ks = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, 16, 1024);
+          const uint64_t ks = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, 16, kGroupBytes);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_ss_elect(s_col, q_base + qmaj_off(kk), ks + kmaj_off(kk), id_s, kk > 0 ? 1u : 0u, elect);
@@ -368,7 +389,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   } else if (warp == 3) {
     // ------------------------------------------------------------ O += P V of both tiles
     const uint32_t id_o = idesc_bf16(128, 128, false, true);
-    auto vmaj_off = [](int kk) { return static_cast<uint64_t>((kk * 2048) >> 4); };
+    auto vmaj_off = [](int kk) { return static_cast<uint64_t>((kk * 2 * kGroupBytes) >> 4); };
     const uint32_t elect = elect_one();
     int slot = 1, phase = 0;
     int y0 = 0, y1 = 0, units1 = 0;  // key tiles of row tile 0 and 1, units in which tile 1 has rows
@@ -380,7 +401,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       const int tiles = g.rows > 128 ? 2 : 1;
 #pragma unroll 1
       for (int j = 0; j < g.nt && ok; ++j) {
-        const uint64_t vs = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, kHalfBytes, 1024);
+        const uint64_t vs = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, kHalfBytes, kGroupBytes);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= tiles) break;
@@ -459,7 +480,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           ok = __all_sync(0xFFFFFFFFu, wait(BAR_FULL + q % kSlots, q / kSlots));
           if (!ok) break;
           if (row < kTileKeys && (key0 + row < g.lo || key0 + row >= g.hi)) {
-            uint8_t* v = base + C::kOffRing + (q % kSlots) * kSlotBytes + row * 128;
+            uint8_t* v = base + C::kOffRing + (q % kSlots) * kSlotBytes + (row / 8) * kGroupBytes + (row % 8) * 128;
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
               *reinterpret_cast<uint4*>(v + 16 * b) = make_uint4(0, 0, 0, 0);
@@ -627,11 +648,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
             for (int w = 0; w < 8; ++w) out[w] = bf16x2_mul(out[w], more);
           }
+          // (eight lanes a row: half of them write the second chunk first, so
+          // that the two halves of the dimensions do not meet in the same banks)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int cc = 2 * ch + h;
-            *reinterpret_cast<uint4*>(dst + (cc / 8) * kHalfBytes + row * 128 + ((cc % 8) ^ (row & 7)) * 16) =
-                make_uint4(out[4 * h], out[4 * h + 1], out[4 * h + 2], out[4 * h + 3]);
+            const bool second = (h != 0) != (ch >= 4);
+            const int cc = 2 * ch + (second ? 1 : 0);
+            const uint4 z = second ? make_uint4(out[4], out[5], out[6], out[7]) : make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4*>(dst + (row / 8) * kGroupBytes + (cc / 8) * kHalfBytes + (row % 8) * 128 +
+                                      ((cc % 8) ^ (row & 7)) * 16) = z;
           }
         }
         fence_proxy_async_smem();  // read by the products
