@@ -134,6 +134,18 @@ __device__ __forceinline__ float max80(const uint32_t (&s)[kTileKeys]) {
   return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
 
+__device__ __forceinline__ void lds128(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
 // Arrives on `bar` when this thread's cp.async so far have completed (counted
 // among the barrier's arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -621,42 +633,58 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (ok) ok = !__any_sync(0xFFFFFFFFu, *s_abort != 0);
         if (!ok) break;
         const int key0 = (g.t0 + j) * kTileKeys;
-        const uint8_t* src = base + C::kOffStage + b * kStageBytes;
-        uint8_t* dst = base + C::kOffRing + slot * kSlotBytes;
+        const uint32_t src = sbase + C::kOffStage + b * kStageBytes, dst = sbase + C::kOffRing + slot * kSlotBytes;
+        const int ch = thread % 8;
+        // Rows are taken five at a time, all loads first.
 #pragma unroll
-        for (int it = 0; it < kTileKeys * 8 / 64; ++it) {
-          const int row = it * 8 + thread / 8, ch = thread % 8;
-          // Codes land as the value times 2^-120; then 2^120 and the row's
-          // scale are multiplied, together up to 2^127.  0 where no row sees
-          // the key, whatever was there; NaN for the exponent byte 255.  (A
-          // byte of 0 is no exponent of cache_write.)
-          const uint32_t e = key0 + row >= g.lo && key0 + row < g.hi ? base[C::kOffExp + b * kTileKeys + row] : 0u;
-          const uint32_t e1 = min(e, 134u);
-          const uint32_t two = e == 0 ? 0u : e == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
-          const uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + (ch ^ (row & 7)) * 16);
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t out[8];
+        for (int half = 0; half < 2; ++half) {
+          uint32_t in[5][4], e[5];
+          bool large = false;
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
+          for (int i = 0; i < 5; ++i) {
+            const int row = (half * 5 + i) * 8 + thread / 8;
+            lds128(in[i], src + row * 128 + (ch ^ (row & 7)) * 16);
+            e[i] = lds8(sbase + C::kOffExp + b * kTileKeys + row);
+            if (key0 + row < g.lo || key0 + row >= g.hi) e[i] = 0;
+            large |= e[i] > 134 && e[i] != 255;
+          }
+          large = __any_sync(0xFFFFFFFFu, large);
+#pragma unroll
+          for (int i = 0; i < 5; ++i) {
+            const int row = (half * 5 + i) * 8 + thread / 8;
+            // Codes land as the value times 2^-120; then 2^120 and the row's
+            // scale are multiplied, together up to 2^127.  0 where no row sees
+            // the key, whatever was there; NaN for the exponent byte 255.  (A
+            // byte of 0 is no exponent of cache_write.)
+            const uint32_t e1 = min(e[i], 134u);
+            const uint32_t two = e[i] == 0 ? 0u : e[i] == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
+            uint32_t out[2][4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t p = __byte_perm(in[i][w], 0, h ? 0x3424 : 0x1404);  // a code in each upper byte
+                out[w / 2][2 * (w % 2) + h] = bf16x2_mul(((p >> 4) & 0x07F007F0u) | (p & 0x80008000u), two);
+              }
+            if (large) {
+              const uint32_t more = (e[i] - e1 + 127) * 0x00800080u;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                out[0][w] = bf16x2_mul(out[0][w], more);
+                out[1][w] = bf16x2_mul(out[1][w], more);
+              }
+            }
+            // (eight lanes a row: half of them write the second chunk first, so
+            // that the two halves of the dimensions do not meet in the same banks)
+            const uint32_t to = dst + (row / 8) * kGroupBytes + (ch / 4) * kHalfBytes + (row % 8) * 128;
+            const bool swap = ch >= 4;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t p = __byte_perm(in[w], 0, h ? 0x3424 : 0x1404);  // a code in each upper byte
-              out[2 * w + h] = bf16x2_mul(((p >> 4) & 0x07F007F0u) | (p & 0x80008000u), two);
+              uint32_t z[4];
+#pragma unroll
+              for (int w = 0; w < 4; ++w) z[w] = swap ? out[1 - h][w] : out[h][w];
+              sts128(to + (((2 * ch + (swap ? 1 - h : h)) % 8) ^ (row & 7)) * 16, z);
             }
-          if (__any_sync(0xFFFFFFFFu, e > e1 && e != 255)) {
-            const uint32_t more = (e - e1 + 127) * 0x00800080u;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) out[w] = bf16x2_mul(out[w], more);
-          }
-          // (eight lanes a row: half of them write the second chunk first, so
-          // that the two halves of the dimensions do not meet in the same banks)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool second = (h != 0) != (ch >= 4);
-            const int cc = 2 * ch + (second ? 1 : 0);
-            const uint4 z = second ? make_uint4(out[4], out[5], out[6], out[7]) : make_uint4(out[0], out[1], out[2], out[3]);
-            *reinterpret_cast<uint4*>(dst + (row / 8) * kGroupBytes + (cc / 8) * kHalfBytes + (row % 8) * 128 +
-                                      ((cc % 8) ^ (row & 7)) * 16) = z;
           }
         }
         fence_proxy_async_smem();  // read by the products
