@@ -26,7 +26,10 @@
 // row a thread; E4M3 pages have four more, 12-15, that widen codes to BF16: a
 // staged tile of codes becomes the K or V tile that the BF16 kind loads, scale
 // applied (the scales are powers of two: what results is exactly the BF16
-// value that cache_read gives).
+// value that cache_read gives).  What bounds that kind is the widening's
+// integer instructions, so a word's codes c0..c3 are taken as the pairs
+// (c0, c2), (c1, c3), which need no byte permutation; Q's dimensions are
+// brought into that order too, and the output's back.
 //
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
 // tile t in [256 + 128 t, + 80), P in the 40 columns behind it.
@@ -359,6 +362,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (kKind != 0) {  // K's order of dimensions (each lane its own 16 bytes)
+#pragma unroll 8
+          for (int r = 0; r < 128; r += 2) {
+            const int row = r + lane / 16;
+            uint32_t v[4], z[4];
+            lds128(v, to + row * 128 + ((chunk % 8) ^ (row & 7)) * 16);
+#pragma unroll
+            for (int w = 0; w < 4; w += 2) {
+              z[w] = __byte_perm(v[w], v[w + 1], 0x5410);
+              z[w + 1] = __byte_perm(v[w], v[w + 1], 0x7632);
+            }
+            sts128(to + row * 128 + ((chunk % 8) ^ (row & 7)) * 16, z);
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
       }
@@ -570,7 +587,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           break;
         }
       }
-      // ---- the unit's output, or this step's part of it
+      // ---- the unit's output, or this step's part of it (the widened codes of
+      // four dimensions lie in the order 0, 2, 1, 3)
+      auto dim = [](int d) constexpr { return kKind == 0 || d % 4 == 0 || d % 4 == 3 ? d : d % 4 == 1 ? d + 1 : d - 1; };
       ok = ok && __all_sync(0xFFFFFFFFu, wait(BAR_PVDONE + t, y + g.nt - 1));
       if (!ok) break;
       tc_fence_after();
@@ -590,13 +609,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               uint32_t z[4];
 #pragma unroll
               for (int f = 0; f < 4; ++f)
-                z[f] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+                z[f] = pack_bf16x2(__uint_as_float(o[dim(8 * e + 2 * f)]) * inv,
+                                   __uint_as_float(o[dim(8 * e + 2 * f + 1)]) * inv);
               dst[e] = make_uint4(z[0], z[1], z[2], z[3]);
             }
           } else {
             uint4* dst = reinterpret_cast<uint4*>(ws.part + at * kHeadDim + 32 * b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_uint4(o[dim(4 * e)], o[dim(4 * e + 1)], o[dim(4 * e + 2)], o[dim(4 * e + 3)]);
           }
         }
       }
@@ -620,7 +641,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     // of slots, the same slots always: they see every phase of their barriers).
     static_assert(kSlots % 2 == 0 && kStageSlots % 2 == 0, "slots of the widening warps");
     const int kv = (warp - 12) / 2;
-    const int thread = threadIdx.x % 64;  // 16 codes of a key at a time: 80 x 8 of them
     int q = kv;
     for (int k = 0; ok; ++k) {
       Segment g;
@@ -634,57 +654,51 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (!ok) break;
         const int key0 = (g.t0 + j) * kTileKeys;
         const uint32_t src = sbase + C::kOffStage + b * kStageBytes, dst = sbase + C::kOffRing + slot * kSlotBytes;
-        const int ch = thread % 8;
-        // Rows are taken five at a time, all loads first.
+        // A warp takes 16 codes of 4 rows x 8 chunks at a time.  Eight lanes
+        // are two rows and half of the chunks, so that their stores, every
+        // other chunk of a half of the dimensions, meet in no bank.
+        const int ch = lane % 4 + 4 * (lane / 8 % 2), row0 = (warp % 2) * 4 + lane / 4 % 2 + 2 * (lane / 16);
+        const bool inside = key0 >= g.lo && key0 + kTileKeys <= g.hi;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t in[5][4], e[5];
-          bool large = false;
+          bool plain = inside;
 #pragma unroll
-          for (int i = 0; i < 5; ++i) {
-            const int row = (half * 5 + i) * 8 + thread / 8;
+          for (int i = 0; i < 5; ++i) {  // all loads first
+            const int row = (half * 5 + i) * 8 + row0;
             lds128(in[i], src + row * 128 + (ch ^ (row & 7)) * 16);
             e[i] = lds8(sbase + C::kOffExp + b * kTileKeys + row);
-            if (key0 + row < g.lo || key0 + row >= g.hi) e[i] = 0;
-            large |= e[i] > 134 && e[i] != 255;
+            plain = plain && e[i] <= 134;
           }
-          large = __any_sync(0xFFFFFFFFu, large);
+          plain = __all_sync(0xFFFFFFFFu, plain);
 #pragma unroll
           for (int i = 0; i < 5; ++i) {
-            const int row = (half * 5 + i) * 8 + thread / 8;
-            // Codes land as the value times 2^-120; then 2^120 and the row's
-            // scale are multiplied, together up to 2^127.  0 where no row sees
-            // the key, whatever was there; NaN for the exponent byte 255.  (A
-            // byte of 0 is no exponent of cache_write.)
-            const uint32_t e1 = min(e[i], 134u);
-            const uint32_t two = e[i] == 0 ? 0u : e[i] == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
-            uint32_t out[2][4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t p = __byte_perm(in[i][w], 0, h ? 0x3424 : 0x1404);  // a code in each upper byte
-                out[w / 2][2 * (w % 2) + h] = bf16x2_mul(((p >> 4) & 0x07F007F0u) | (p & 0x80008000u), two);
-              }
-            if (large) {
-              const uint32_t more = (e[i] - e1 + 127) * 0x00800080u;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                out[0][w] = bf16x2_mul(out[0][w], more);
-                out[1][w] = bf16x2_mul(out[1][w], more);
-              }
+            const int row = (half * 5 + i) * 8 + row0;
+            // Codes land as the value times 2^-120; one factor of 2^120 and
+            // the row's scale then (up to 2^127 in the plain case).
+            uint32_t two = (e[i] + 120) * 0x00800080u, more = 0;
+            if (!plain) {
+              // 0 where no row sees the key, whatever was there; NaN for the
+              // exponent byte 255 (a byte of 0 is no exponent of cache_write)
+              if (key0 + row < g.lo || key0 + row >= g.hi) e[i] = 0;
+              const uint32_t e1 = min(e[i], 134u);
+              two = e[i] == 0 ? 0u : e[i] == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
+              more = (e[i] - e1 + 127) * 0x00800080u;
             }
-            // (eight lanes a row: half of them write the second chunk first, so
-            // that the two halves of the dimensions do not meet in the same banks)
+            uint32_t out[8];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {  // (c0, c2) and (c1, c3) of a word
+              const uint32_t v = in[i][w];
+              out[2 * w] = bf16x2_mul(((v * 16) & 0x07F007F0u) | ((v * 256) & 0x80008000u), two);
+              out[2 * w + 1] = bf16x2_mul(((v >> 4) & 0x07F007F0u) | (v & 0x80008000u), two);
+            }
+            if (!plain) {
+#pragma unroll
+              for (int w = 0; w < 8; ++w) out[w] = bf16x2_mul(out[w], more);
+            }
             const uint32_t to = dst + (row / 8) * kGroupBytes + (ch / 4) * kHalfBytes + (row % 8) * 128;
-            const bool swap = ch >= 4;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t z[4];
-#pragma unroll
-              for (int w = 0; w < 4; ++w) z[w] = swap ? out[1 - h][w] : out[h][w];
-              sts128(to + (((2 * ch + (swap ? 1 - h : h)) % 8) ^ (row & 7)) * 16, z);
-            }
+            sts128(to + ((2 * ch % 8) ^ (row & 7)) * 16, *reinterpret_cast<uint32_t(*)[4]>(&out[0]));
+            sts128(to + (((2 * ch + 1) % 8) ^ (row & 7)) * 16, *reinterpret_cast<uint32_t(*)[4]>(&out[4]));
           }
         }
         fence_proxy_async_smem();  // read by the products
