@@ -1,6 +1,7 @@
 // Definitions shared by the host side of the C ABI and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -105,6 +106,21 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
+
+// Raises a kernel's shared-memory limit once on each device (a static member
+// of each launcher; setting it again is harmless).
+struct SmemOnce {
+  std::atomic<uint8_t> done[128] = {};
+  cudaError_t set(const void* kern, uint32_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && dev >= 0 && dev < 128) done[dev].store(1, std::memory_order_release);
+    return e;
+  }
+};
 
 // Records a failed CUDA call for sparse_attn_last_cuda_error (thread-local,
 // defined in api.cu); returns true when `e` is an error.

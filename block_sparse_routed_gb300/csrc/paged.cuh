@@ -83,8 +83,16 @@ __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
 // there is none, so that every unit writes its rows).  All key tiles of all
 // units, in the order (sequence, head, row tile, key tile), are one line that
 // is cut into equal parts, one a CTA: every CTA streams the same number of
-// keys however ragged the batch is.  A unit that a cut divides is joined from
-// its parts by the joining kernel.
+// keys however ragged the batch is.  A unit's beginning and end cost time too:
+// in front of its key tiles the line has `over` places without one.  A unit
+// that a cut divides is joined from its parts by the joining kernel.
+
+struct LineShape {
+  int row_tile;   // packed rows of a unit
+  int key_tile;   // keys of a tile
+  int over;       // places of a unit without a key tile
+  int min_tiles;  // places of a CTA at least, while there are any
+};
 
 struct UnitKeys {
   int lo, hi;  // keys that some row of the unit sees: [lo, hi)
@@ -101,8 +109,8 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const PagedSeq&
                           static_cast<uint32_t>(row_tile));
 }
 
-__device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p, int row_tile,
-                                              int key_tile) {
+__device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p, LineShape line) {
+  const int row_tile = line.row_tile, key_tile = line.key_tile;
   const int rows = q.n * a.group;
   int i0 = 0, i1 = q.n - 1;  // first and last new token of the tile
   if (rows > row_tile) {
@@ -139,10 +147,9 @@ __device__ __forceinline__ int64_t muldiv(int64_t x, int64_t y, int64_t z) {
   return static_cast<int64_t>(v / static_cast<uint64_t>(z));
 }
 
-// Key tiles of one head of the sequences base + lane, one a lane (0 past the
+// Places of one head of the sequences base + lane, one a lane (0 past the
 // last).  Sequences of many row tiles are summed by the whole warp.
-__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, int row_tile, int key_tile, int lane,
-                                              bool& bad) {
+__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, LineShape line, int lane, bool& bad) {
   const int s = base + lane;
   PagedSeq q;
   q.n = 0;
@@ -151,10 +158,10 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
     q = paged_seq(a.c, s, b);
     bad |= b;
   }
-  const int tiles = row_tiles(a, q, row_tile);
+  const int tiles = row_tiles(a, q, line.row_tile);
   int64_t t = 0;
   if (tiles <= 4)
-    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, row_tile, key_tile).nt;
+    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, line).nt + line.over;
   unsigned many = __ballot_sync(0xFFFFFFFFu, tiles > 4);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -165,7 +172,7 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
     r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
     const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
     int64_t y = 0;
-    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, row_tile, key_tile).nt;
+    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, line).nt + line.over;
     y = warp_sum(y);
     if (lane == src) t = y;
   }
@@ -188,7 +195,7 @@ struct LineWalk {
   int64_t at, end, total;
   int ctas;     // CTAs with work: all, or fewer when tiles are few
   int s, h, p;
-  int skip;     // key tiles of the unit that earlier CTAs have
+  int skip;     // places of the unit that earlier CTAs have
   PagedSeq q;
   int tiles;    // row tiles of the sequence
 };
@@ -199,18 +206,18 @@ __device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w, in
   w.tiles = row_tiles(a, w.q, row_tile);
 }
 
-// Finds the part of CTA `cta` of `ctas`; each takes min_tiles at least, while
-// there are any.  Sets `bad` when a sequence fails its checks.
-__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_tile, int cta,
-                                           int ctas, int min_tiles, bool& bad) {
+// Finds the part of CTA `cta` of `ctas`.  Sets `bad` when a sequence fails its
+// checks.
+__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, LineShape line, int cta, int ctas,
+                                           bool& bad) {
   const int lane = threadIdx.x % 32, seqs = a.c.seqs;
   int64_t t = 0, first = 0;
   for (int base = 0; base < seqs; base += 32) {
-    t += lane_tiles(a, base, row_tile, key_tile, lane, bad);
+    t += lane_tiles(a, base, line, lane, bad);
     if (base == 0) first = t;
   }
   w.total = warp_sum(t) * a.c.H;
-  const int64_t most = (w.total + min_tiles - 1) / min_tiles;
+  const int64_t most = (w.total + line.min_tiles - 1) / line.min_tiles;
   w.ctas = static_cast<int>(min(static_cast<int64_t>(ctas), most));
   // (a part without tiles must not lie between two of one unit)
   w.at = w.end = 0;
@@ -221,7 +228,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
   int64_t left = w.at;
   for (int base = 0;; base += 32) {
     bool b;
-    const int64_t mine = (base == 0 ? first : lane_tiles(a, base, row_tile, key_tile, lane, b)) * a.c.H;
+    const int64_t mine = (base == 0 ? first : lane_tiles(a, base, line, lane, b)) * a.c.H;
     const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
@@ -233,7 +240,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
     }
     left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
-  walk_seq(a, w, row_tile);
+  walk_seq(a, w, line.row_tile);
   t = muldiv(t, 1, a.c.H);
   w.h = static_cast<int>(muldiv(left, 1, t));
   left -= w.h * t;
@@ -242,7 +249,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
     return;
   }
   for (int p0 = 0;; p0 += 32) {
-    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, row_tile, key_tile).nt : 0;
+    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, line).nt + line.over : 0;
     const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
@@ -257,46 +264,52 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
 
 // The next step (valid = 0 at the end); `join` is filled when it leaves a
 // unit unfinished that it began.
-__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, int row_tile, int key_tile, int cta,
+__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, LineShape line, int cta,
                                              JoinDesc& join) {
   Segment g;
   g.valid = 0;
-  if (w.at >= w.end) return g;
-  while (w.p >= w.tiles) {  // next head, next sequence with rows
-    w.p = 0;
-    if (w.tiles == 0 || ++w.h >= a.c.H) {
-      w.h = 0;
-      ++w.s;
-      walk_seq(a, w, row_tile);
+  while (w.at < w.end) {
+    while (w.p >= w.tiles) {  // next head, next sequence with rows
+      w.p = 0;
+      if (w.tiles == 0 || ++w.h >= a.c.H) {
+        w.h = 0;
+        ++w.s;
+        walk_seq(a, w, line.row_tile);
+      }
     }
+    const UnitKeys u = unit_keys(a, w.q, w.p, line);
+    const int places = u.nt + line.over;
+    const int take = static_cast<int>(min(static_cast<int64_t>(places - w.skip), w.end - w.at));
+    const int from = max(0, w.skip - line.over), to = max(0, w.skip + take - line.over);  // key tiles
+    if (to > from) {
+      g.valid = 1;
+      g.row0 = w.q.row0;
+      g.n = w.q.n;
+      g.len = w.q.len;
+      g.h = w.h;
+      g.s = w.s;
+      g.rho0 = w.p * line.row_tile;
+      g.rows = min(line.row_tile, w.q.n * a.group - g.rho0);
+      g.lo = u.lo;
+      g.hi = u.hi;
+      g.t0 = u.t0 + from;
+      g.nt = to - from;
+      g.part = from == 0 ? (to == u.nt ? -1 : 1) : 0;
+      if (g.part == 1) {
+        // the CTA that holds the unit's last tile
+        const int owner = static_cast<int>(muldiv((w.at - w.skip + places) * w.ctas - 1, 1, w.total));
+        join.pieces = owner - cta + 1;
+        join.row0 = g.row0;
+        join.rho0 = g.rho0;
+        join.rows = g.rows;
+        join.h = g.h;
+      }
+    }
+    w.at += take;
+    w.skip = 0;
+    ++w.p;
+    if (g.valid) break;
   }
-  const UnitKeys u = unit_keys(a, w.q, w.p, row_tile, key_tile);
-  g.valid = 1;
-  g.row0 = w.q.row0;
-  g.n = w.q.n;
-  g.len = w.q.len;
-  g.h = w.h;
-  g.s = w.s;
-  g.rho0 = w.p * row_tile;
-  g.rows = min(row_tile, w.q.n * a.group - g.rho0);
-  g.lo = u.lo;
-  g.hi = u.hi;
-  g.t0 = u.t0 + w.skip;
-  g.nt = static_cast<int>(min(static_cast<int64_t>(u.nt - w.skip), w.end - w.at));
-  const bool first = w.skip == 0, last = w.skip + g.nt == u.nt;
-  g.part = first && last ? -1 : (first ? 1 : 0);
-  if (first && !last) {
-    // the CTA that holds the unit's last tile
-    const int owner = static_cast<int>(muldiv((w.at + u.nt) * w.ctas - 1, 1, w.total));
-    join.pieces = owner - cta + 1;
-    join.row0 = g.row0;
-    join.rho0 = g.rho0;
-    join.rows = g.rows;
-    join.h = g.h;
-  }
-  w.at += g.nt;
-  w.skip = 0;
-  ++w.p;
   return g;
 }
 

@@ -55,6 +55,7 @@ constexpr int kSegs = 2;
 constexpr int kStageSlots = 4;           // staged code tiles (E4M3): [80 keys x 128 B]
 constexpr uint32_t kStageBytes = kTileKeys * 128;
 constexpr float kRescaleLog2 = 32.0f;
+constexpr int kOver = 2;                 // a unit's beginning and end, in key tiles
 constexpr int kMinTiles = 6;             // key tiles of a CTA at least, while there are any
 
 template <int kKind>
@@ -236,7 +237,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     LineWalk w;
     bool bad = false;
-    walk_begin(a, w, kUnitRows, kTileKeys, blockIdx.x, gridDim.x, kMinTiles, bad);
+    constexpr LineShape line = {kUnitRows, kTileKeys, kOver, kMinTiles};
+    walk_begin(a, w, line, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
     int q = 0, buf = 0, round = 0;  // tiles of K or V so far, the next one's slot and use of it
@@ -244,7 +246,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     constexpr int kBufs = kKind ? kStageSlots : kSlots;
     constexpr int kFull = kKind ? BAR_SGFULL : BAR_FULL, kEmpty = kKind ? BAR_SGEMPTY : BAR_EMPTY;
     for (int k = 0; ok; ++k) {
-      const Segment g = walk_next(a, w, kUnitRows, kTileKeys, blockIdx.x, join);
+      const Segment g = walk_next(a, w, line, blockIdx.x, join);
       ok = k < kSegs || __all_sync(0xFFFFFFFFu, wait(BAR_SEGEMPTY + k % kSegs, k / kSegs - 1));
       if (!ok) break;
       if (lane == 0) {
@@ -725,7 +727,8 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn
                    int ctas, cudaStream_t s) {
   using C = Cfg<kKind>;
   auto* kern = paged_chunk_kernel<kKind>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   // The register split redistributes the launch allocation; a build with
   // fewer registers a thread would make setmaxnreg.inc wait forever.

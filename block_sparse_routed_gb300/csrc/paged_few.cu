@@ -46,6 +46,8 @@ constexpr int kKeyShift = 6;  // 64 keys a stage
 constexpr int kTileKeys = 1 << kKeyShift;
 constexpr int kSegs = 4;      // steps described ahead
 constexpr float kRescaleLog2 = 8.0f;
+// A unit's beginning (its Q) and end (joining the warps), in stages.
+constexpr int kOverBf16 = 2, kOverE4m3 = 3;
 constexpr int kMergeRow = 132;  // floats a row of the merge area (128 and padding)
 
 template <int kKind, int kN>
@@ -198,7 +200,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     LineWalk w;
     bool bad = false;
-    walk_begin(a, w, kRows, kTileKeys, blockIdx.x, gridDim.x, 1, bad);
+    constexpr LineShape line = {kRows, kTileKeys, kKind == 0 ? kOverBf16 : kOverE4m3, 1};
+    walk_begin(a, w, line, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
     bool ok = true;
@@ -207,7 +210,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int tile_pages = kTileKeys / per_page;
     const int sub = lane % 4, pg = lane / 4;                  // lane: page pg of the tile, box sub
     for (int k = 0; ok; ++k) {
-      const Segment g = walk_next(a, w, kRows, kTileKeys, blockIdx.x, join);
+      const Segment g = walk_next(a, w, line, blockIdx.x, join);
       ok = k < kSegs ||
            __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_SEMPTY + k % kSegs), ((k / kSegs) & 1) ^ 1, kWaitLimitNs));
       if (!ok) break;
@@ -602,8 +605,8 @@ template <int kKind, int kN>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, const PagedScratch& ws,
                    int ctas, cudaStream_t s) {
   using C = Cfg<kKind, kN>;
-  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<kKind, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(C::kSmem));
+  static SmemOnce once;
+  const cudaError_t e = once.set(reinterpret_cast<const void*>(paged_few_kernel<kKind, kN>), C::kSmem);
   if (e != cudaSuccess) return e;
   paged_few_kernel<kKind, kN><<<ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a, ws);
   return cudaGetLastError();
