@@ -48,7 +48,7 @@ constexpr int kSegs = 4;      // steps described ahead
 constexpr float kRescaleLog2 = 8.0f;
 // A unit's beginning (its Q) and end (joining the warps), in stages.
 constexpr int kOverBf16 = 2, kOverE4m3 = 3;
-constexpr int kMergeRow = 132;  // floats a row of the merge area (128 and padding)
+constexpr uint32_t kRegionBytes = 4096;  // of the merge area: 8 rows x 128 floats
 
 template <int kKind, int kN>
 struct Cfg {
@@ -67,8 +67,8 @@ struct Cfg {
   static constexpr uint32_t kOffExp = kStages * kStage;
   static constexpr uint32_t kOffMerge = kOffExp + kStages * kExp;     // kRegions x 8 rows
   static constexpr int kRegions = 2;
-  static constexpr uint32_t kOffMl = kOffMerge + kRegions * 8 * kMergeRow * 4;  // [2][8 warps][16] floats
-  static constexpr uint32_t kOffSeg = kOffMl + 1024;                  // kSegs x Segment
+  static constexpr uint32_t kOffMl = kOffMerge + kRegions * kRegionBytes;  // [8 warps][16 rows] float2
+  static constexpr uint32_t kOffSeg = kOffMl + 1152;                  // kSegs x Segment
   static constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
   static constexpr uint32_t kOffMisc = kOffBar + 256;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -94,6 +94,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f4(uint32_t addr, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 template <bool kHalfs>  // FP16 operands, else BF16
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -280,9 +288,11 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     // ------------------------------------------------------------ consumers
     const int u = lane / 4, t4 = lane % 4;
     const int quarter = warp % 4, grp = warp / 4;  // 16 keys of the stages that are the group's
-    float* merge = reinterpret_cast<float*>(base + C::kOffMerge);
-    float* s_m = reinterpret_cast<float*>(base + C::kOffMl);  // [warp][row]
-    float* s_l = s_m + C::kConsumers * kRows;
+    float2* s_ml = reinterpret_cast<float2*>(base + C::kOffMl);  // [warp][row]: reference, sum
+    float2* s_row = s_ml + C::kConsumers * kRows;                  // [row]: of all warps
+    // Token of a packed row: there are at most 16, so FP32 divides exactly.
+    const float inv_group = 1.0f / static_cast<float>(a.group);
+    auto div_group = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
     const float c2 = a.scale * 1.4426950408889634f;
     // ldmatrix rows: lane l gives row l % 8 of matrix l / 8.  K: (keys 0-7,
     // chunk i), (8-15, i), (0-7, i + 1), (8-15, i + 1); V the same in the
@@ -309,9 +319,9 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       float qinv[kN][2];  // E4M3: undoes the scaling of rows 2t, 2t + 1
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        const int rho = g.rho0 + 8 * n + u;
-        const bool real = 8 * n + u < g.rows;
-        const int i = rho / a.group;
+        const int rho = 8 * n + u;  // (a unit is one row tile here: rho0 is 0)
+        const bool real = rho < g.rows;
+        const int i = div_group(rho);
         const uint16_t* src = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
                               static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head;
 #pragma unroll
@@ -356,13 +366,13 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = 8 * n + 2 * t4 + e;
-          const int pos = g.len - g.n + (g.rho0 + row) / a.group;
+          const int pos = g.len - g.n + div_group(row);
           lo[n][e] = row < g.rows ? row_lo(a, pos) : 0;
           hi[n][e] = row < g.rows ? (a.causal ? min(g.len, pos + 1) : g.len) : 0;
         }
       // [all_lo, all_hi): what every row sees
-      const int all_lo = row_lo(a, g.len - g.n + (g.rho0 + g.rows - 1) / a.group);
-      const int all_hi = a.causal ? min(g.len, g.len - g.n + g.rho0 / a.group + 1) : g.len;
+      const int all_lo = row_lo(a, g.len - 1);
+      const int all_hi = a.causal ? min(g.len, g.len - g.n + 1) : g.len;
       float acc[kN][8][4], ref[kN][2], sum[kN][2];
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
@@ -504,91 +514,112 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (lane == 0) mbar_arrive(bar(BAR_EMPTY + stage));
       }
       tile += g.nt;
-      // ---- the warps' results into one
+      // ---- the warps' results into one: references and sums first
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) sum[n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][e], d);
-          if (u == 0) {
-            s_m[warp * kRows + 8 * n + 2 * t4 + e] = ref[n][e];
-            s_l[warp * kRows + 8 * n + 2 * t4 + e] = sum[n][e];
-          }
+          if (u == 0) s_ml[warp * kRows + 8 * n + 2 * t4 + e] = make_float2(ref[n][e], sum[n][e]);
         }
       ok = !bar_any<kWorkers>(!ok || *s_abort != 0);
       if (!ok) break;
-      auto top = [&](int row) {
-        float m = -INFINITY;
+      if (threadIdx.x < kRows) {  // a row over all warps
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < C::kConsumers; ++w) m = fmaxf(m, s_m[w * kRows + row]);
-        return m;
-      };
-      float* mine = merge + warp % C::kRegions * 8 * kMergeRow;
+        for (int w = 0; w < C::kConsumers; ++w) m = fmaxf(m, s_ml[w * kRows + threadIdx.x].x);
+#pragma unroll
+        for (int w = 0; w < C::kConsumers; ++w) {
+          const float2 ml = s_ml[w * kRows + threadIdx.x];
+          l += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - m);
+        }
+        s_row[threadIdx.x] = make_float2(m, l);
+      }
+      bar_all<kWorkers>();
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        float f[2];
+        float m[2], l[2], f[2];  // rows 8n + 2t, 2t + 1
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          f[e] = ref[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - top(8 * n + 2 * t4 + e));
+        for (int e = 0; e < 2; ++e) {
+          const float2 ml = s_row[8 * n + 2 * t4 + e];
+          m[e] = ml.x;
+          l[e] = ml.y;
+          f[e] = ref[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - m[e]);
+        }
+        // The outputs, in the accumulators' own order (a float4 of 16
+        // dimensions j for each lane): warp after warp adds to its region.
+        const uint32_t mine = sbase + C::kOffMerge + (warp % C::kRegions) * kRegionBytes + lane * 16;
 #pragma unroll
-        for (int gr = 0; gr < C::kConsumers / C::kRegions; ++gr) {  // warp after warp adds to its region
+        for (int gr = 0; gr < C::kConsumers / C::kRegions; ++gr) {
           if (warp / C::kRegions == gr) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j0 = 0; j0 < 8; j0 += 4) {
+              float4 y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int d = 16 * j + (kKind == 0 ? u + 8 * (e / 2) : 2 * u + e / 2);
-                float* to = mine + (2 * t4 + (e & 1)) * kMergeRow + d;
-                const float y = acc[n][j][e] * f[e & 1];
-                *to = gr == 0 ? y : *to + y;
+              for (int j = 0; j < 4; ++j) {
+                y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (gr > 0) y[j] = lds_f4(mine + (j0 + j) * 512);
               }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float(&c4)[4] = acc[n][j0 + j];
+                sts_f4(mine + (j0 + j) * 512, make_float4(fmaf(c4[0], f[0], y[j].x), fmaf(c4[1], f[1], y[j].y),
+                                                          fmaf(c4[2], f[0], y[j].z), fmaf(c4[3], f[1], y[j].w)));
+              }
+            }
           }
           bar_all<kWorkers>();
         }
-        // 8 rows x 128 columns of the regions' sums
-        constexpr int kPer = 8 * 128 / kWorkers;  // 8 or 4 columns a thread
-        const int row = threadIdx.x * kPer / 128, col = threadIdx.x * kPer % 128;
-        if (8 * n + row < g.rows) {
-          float o[kPer];
+        // Each warp writes 8 / kConsumers of the 8 times 16 dimensions.
+        int64_t at[2];
+        bool real[2];
+        float inv[2];
 #pragma unroll
-          for (int i = 0; i < kPer; i += 4) {
-            float4 y = *reinterpret_cast<const float4*>(merge + row * kMergeRow + col + i);
-#pragma unroll
-            for (int x = 1; x < C::kRegions; ++x) {
-              const float4 z = *reinterpret_cast<const float4*>(merge + (8 * x + row) * kMergeRow + col + i);
-              y.x += z.x;
-              y.y += z.y;
-              y.z += z.z;
-              y.w += z.w;
-            }
-            o[i] = y.x;
-            o[i + 1] = y.y;
-            o[i + 2] = y.z;
-            o[i + 3] = y.w;
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n + 2 * t4 + e, i = div_group(row);
+          real[e] = row < g.rows;
+          at[e] = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + row - i * a.group
+                             : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + row;
+          inv[e] = g.part >= 0 ? 1.f : l[e] > 0.f ? 1.f / l[e] : (l[e] == 0.f ? 0.f : l[e]);  // (NaN stays)
+          if (warp == 0 && u == 0 && real[e]) {
+            if (g.part >= 0)
+              ws.ml[at[e]] = make_float2(m[e], l[e]);
+            else if (a.lse)
+              a.lse[at[e]] = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * 0.6931471805599453f;
           }
-          const float m = top(8 * n + row);
-          float l = 0.f;
+        }
 #pragma unroll
-          for (int w = 0; w < C::kConsumers; ++w) {
-            const float mw = s_m[w * kRows + 8 * n + row];
-            l += mw == -INFINITY ? 0.f : s_l[w * kRows + 8 * n + row] * ex2_approx(mw - m);
+        for (int x = 0; x < 8 / C::kConsumers; ++x) {
+          const int j = warp * (8 / C::kConsumers) + x;
+          float4 y = lds_f4(sbase + C::kOffMerge + lane * 16 + j * 512);
+#pragma unroll
+          for (int w = 1; w < C::kRegions; ++w) {
+            const float4 z = lds_f4(sbase + C::kOffMerge + w * kRegionBytes + lane * 16 + j * 512);
+            y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
           }
-          if (g.part < 0) {
-            const int rho = g.rho0 + 8 * n + row, i = rho / a.group;
-            const int64_t at = static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + rho - i * a.group;
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-            uint2* dst = reinterpret_cast<uint2*>(a.o + at * kHeadDim + col);
-#pragma unroll
-            for (int x = 0; x < kPer; x += 4)
-              dst[x / 4] = make_uint2(pack_bf16x2(o[x] * inv, o[x + 1] * inv), pack_bf16x2(o[x + 2] * inv, o[x + 3] * inv));
-            if (a.lse && col == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-          } else {
-            const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + 8 * n + row;
-            float4* dst = reinterpret_cast<float4*>(ws.part + at * kHeadDim + col);
-#pragma unroll
-            for (int x = 0; x < kPer; x += 4) dst[x / 4] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-            if (col == 0) ws.ml[at] = make_float2(m, l);
+          y.x *= inv[0];
+          y.y *= inv[1];
+          y.z *= inv[0];
+          y.w *= inv[1];
+          // two neighbouring dimensions of a row: d and d + 1
+          auto put = [&](int e, int d, float lo, float hi) {
+            if (!(e ? real[1] : real[0])) return;
+            const int64_t to = (e ? at[1] : at[0]) * kHeadDim + d;
+            if (g.part < 0)
+              *reinterpret_cast<uint32_t*>(a.o + to) = pack_bf16x2(lo, hi);
+            else
+              *reinterpret_cast<float2*>(ws.part + to) = make_float2(lo, hi);
+          };
+          if constexpr (kKind != 0) {  // the lane has dimensions 2u, 2u + 1 of both rows
+            put(0, 16 * j + 2 * u, y.x, y.z);
+            put(1, 16 * j + 2 * u, y.y, y.w);
+          } else {  // dimensions u and u + 8: lanes u and u ^ 1 exchange rows
+            const bool odd = u & 1;
+            const float a0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.x : y.y, 4);
+            const float a1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.z : y.w, 4);
+            put(odd, 16 * j + (u & ~1), odd ? a0 : y.x, odd ? y.y : a0);
+            put(odd, 16 * j + 8 + (u & ~1), odd ? a1 : y.z, odd ? y.w : a1);
           }
         }
         if (n + 1 < kN) bar_all<kWorkers>();  // (the next unit's first barrier otherwise)
