@@ -20,6 +20,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;  // heads a warp moves at once
 
+// 16 bytes that this kernel reads once.
+__device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // The row of page table that holds the token of packed row r, as the index
 // page * page_size * H + slot of head 0 (heads are page_size rows apart); -1
 // when there is none.  `pos` is the token's position (below 0: no token).
@@ -49,59 +58,80 @@ __device__ __forceinline__ int64_t slot_of(const PagedArgs& c, int r, int lane, 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c, const CacheRows rows, int blocks_h) {
   if (blockIdx.x == 0) paged_check_all(c);
-  const int lane = threadIdx.x % 32;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  if (item >= static_cast<int64_t>(c.rows) * blocks_h) return;
-  const int r = static_cast<int>(item / blocks_h), h0 = static_cast<int>(item % blocks_h) * kHeads;
+  constexpr int kTile = kThreads / 32;  // rows of the CTA, one a warp
+  __shared__ int64_t s_slot[kTile];
+  __shared__ uint8_t s_exp[2][kHeads][kTile];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int r = static_cast<int>(blockIdx.x / blocks_h) * kTile + warp, h0 = static_cast<int>(blockIdx.x % blocks_h) * kHeads;
   const bool is_v = lane >= 16;
   const int sub = lane % 16;
-  const uint16_t* src = (is_v ? rows.v + r * rows.v_token : rows.k + r * rows.k_token) + sub * 8;
-  const int64_t head = is_v ? rows.v_head : rows.k_head;
+  const int64_t head = is_v ? rows.v_head : rows.k_head, token = is_v ? rows.v_token : rows.k_token;
+  const uint16_t* src = (is_v ? rows.v : rows.k) + r * token + h0 * head + sub * 8;
   uint4 x[kHeads];
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
     x[i] = make_uint4(0, 0, 0, 0);
-    if (h0 + i < c.H) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (h0 + i) * head));
+    if (r < c.rows && h0 + i < c.H) x[i] = ld_once(src + i * head);
   }
+  uint8_t* pages = is_v ? c.v_pages : c.k_pages;
   bool member;
   int pos;
-  const int64_t slot = slot_of(c, r, lane, member, pos);
-  if (slot < 0) return;
-  uint8_t* pages = is_v ? c.v_pages : c.k_pages;
-  uint8_t* exps = is_v ? c.v_exp : c.k_exp;
+  const int64_t slot = r < c.rows ? slot_of(c, r, lane, member, pos) : -1;
+  if (kE4m3 && lane == 0) s_slot[warp] = slot;
+  // E4M3: the largest magnitude of a row over its 16 lanes.  BF16 bits without
+  // the sign order as integers; two heads' maxima share a word.
+  uint32_t top[kHeads / 2];
+  if constexpr (kE4m3) {
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (h0 + i >= c.H) break;
-    const int64_t row = slot + (static_cast<int64_t>(h0 + i) << c.page_shift);
-    if constexpr (!kE4m3) {
-      *reinterpret_cast<uint4*>(pages + row * 256 + sub * 16) = x[i];
-    } else {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      // largest magnitude: BF16 bits without the sign order as integers
-      uint32_t m2 = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7FFF7FFFu);
-#pragma unroll
-      for (int d = 1; d < 16; d *= 2) m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, d));
-      const uint32_t m = max(m2 >> 16, m2 & 0xFFFFu);
-      // amax = (1 + M / 128) 2^(E - 127) <= 1.75 * 2^8 * 2^e with M <= 96 for e = E - 135
-      const bool finite = m < 0x7F80u;
-      const int e = finite ? max(1, static_cast<int>(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0)) : 255;
-      const float inv = exp_scale(finite ? 254 - e : 255);  // NaN: every code of the row is
-      uint32_t code[2];
+    for (int i = 0; i < kHeads; i += 2) {
+      uint32_t m[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        uint16_t half[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t v = w[2 * k + t];
-          const float lo = __uint_as_float(v << 16) * inv, hi = __uint_as_float(v & 0xFFFF0000u) * inv;
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(half[t]) : "f"(hi), "f"(lo));
-        }
-        code[k] = half[0] | (static_cast<uint32_t>(half[1]) << 16);
+        const uint4 v = x[i + k];
+        m[k] = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
       }
-      *reinterpret_cast<uint2*>(pages + row * 128 + sub * 8) = make_uint2(code[0], code[1]);
-      if (sub == 0) exps[row] = static_cast<uint8_t>(e);
+      uint32_t y = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) y = __vmaxu2(y, __shfl_xor_sync(0xFFFFFFFFu, y, d));
+      top[i / 2] = y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int64_t row = slot + (static_cast<int64_t>(h0 + i) << c.page_shift);
+    const bool real = slot >= 0 && h0 + i < c.H;
+    if constexpr (!kE4m3) {
+      if (real) *reinterpret_cast<uint4*>(pages + row * 256 + sub * 16) = x[i];
+    } else {
+      const uint32_t m = i % 2 ? top[i / 2] >> 16 : top[i / 2] & 0xFFFFu;
+      // amax = (1 + M / 128) 2^(E - 127) <= 1.75 * 2^8 * 2^e with M <= 96 for e = E - 135
+      const bool finite = m < 0x7F80u;
+      const int e = finite ? max(1, static_cast<int>((m + 31) >> 7) - 8) : 255;
+      // times 2^(127 - e), exact in BF16; NaN makes every code of the row one
+      const uint32_t inv = finite ? (254 - e) * 0x00800080u : 0x7FFF7FFFu;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint16_t half[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t v;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(w[k]), "r"(inv));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+            : "=h"(half[k])
+            : "f"(__uint_as_float(v & 0xFFFF0000u)), "f"(__uint_as_float(v << 16)));
+      }
+      if (real)
+        *reinterpret_cast<uint2*>(pages + row * 128 + sub * 8) =
+            make_uint2(half[0] | (static_cast<uint32_t>(half[1]) << 16), half[2] | (static_cast<uint32_t>(half[3]) << 16));
+      if (sub == 0) s_exp[is_v][i][warp] = static_cast<uint8_t>(e);
+    }
+  }
+  if constexpr (kE4m3) {
+    // the exponents of consecutive tokens of one head lie side by side
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kHeads * kTile; i += kThreads) {
+      const int t = i % kTile, h = i / kTile % kHeads, v = i / (kTile * kHeads);
+      if (s_slot[t] >= 0 && h0 + h < c.H)
+        (v ? c.v_exp : c.k_exp)[s_slot[t] + (static_cast<int64_t>(h0 + h) << c.page_shift)] = s_exp[v][h][t];
     }
   }
 }
@@ -110,9 +140,9 @@ template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const PagedArgs c, const CacheRows rows, int blocks_h) {
   if (blockIdx.x == 0) paged_check_all(c);
   const int lane = threadIdx.x % 32;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  if (item >= static_cast<int64_t>(c.rows) * blocks_h) return;
-  const int r = static_cast<int>(item / blocks_h), h0 = static_cast<int>(item % blocks_h) * kHeads;
+  const int r = static_cast<int>(blockIdx.x / blocks_h) * (kThreads / 32) + threadIdx.x / 32;
+  const int h0 = static_cast<int>(blockIdx.x % blocks_h) * kHeads;
+  if (r >= c.rows) return;
   const bool is_v = lane >= 16;
   const int sub = lane % 16;
   uint16_t* dst = (is_v ? rows.v + r * rows.v_token : rows.k + r * rows.k_token) + sub * 8;
@@ -162,8 +192,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const PagedArgs c,
 template <typename K>
 cudaError_t launch_rows(K kern, const PagedArgs& c, const CacheRows& r, cudaStream_t s) {
   const int blocks_h = (c.H + kHeads - 1) / kHeads;
-  const int64_t items = static_cast<int64_t>(c.rows) * blocks_h;
-  const int64_t grid = (items + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t grid = (static_cast<int64_t>(c.rows) + kThreads / 32 - 1) / (kThreads / 32) * blocks_h;
   kern<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(c, r, blocks_h);
   return cudaGetLastError();
 }
