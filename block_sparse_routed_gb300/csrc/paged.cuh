@@ -184,6 +184,7 @@ struct Segment {
   int valid;       // 0: no more
   int row0, n, len, h, rho0, rows;
   int lo, hi;      // keys that some row sees
+  int all_lo, all_hi;  // keys that every row sees
   int t0, nt;      // key tiles of this step
   int part;        // -1: the unit's output; else the partial result's slot (0 or 1)
   int s;
@@ -292,6 +293,9 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
       g.rows = min(line.row_tile, w.q.n * a.group - g.rho0);
       g.lo = u.lo;
       g.hi = u.hi;
+      const int base = w.q.len - w.q.n;
+      g.all_lo = row_lo(a, base + (g.rho0 + g.rows - 1) / a.group);
+      g.all_hi = a.causal ? min(w.q.len, base + g.rho0 / a.group + 1) : w.q.len;
       g.t0 = u.t0 + from;
       g.nt = to - from;
       g.part = from == 0 ? (to == u.nt ? -1 : 1) : 0;

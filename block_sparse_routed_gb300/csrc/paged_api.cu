@@ -190,7 +190,7 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   if (st != SA_OK) return st;
   if (bad_stride(p->a_token_stride) || bad_stride(p->a_head_stride)) return SA_EINVAL;
   if (!ws || (p->rows > 0 && (!q || !o))) return SA_EINVAL;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return SA_EINVAL;
+  if (!aligned(q, 16) || !aligned(o, 32) || !aligned(lse, 4)) return SA_EINVAL;
   st = check_pointers(p, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, ws);
   if (st != SA_OK) return st;
   if (ws_bytes < need) return SA_EINVAL;

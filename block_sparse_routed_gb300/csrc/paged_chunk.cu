@@ -34,6 +34,7 @@
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
 // tile t in [256 + 128 t, + 80), P in the 40 columns behind it.
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -76,7 +77,8 @@ struct Cfg {
   static constexpr uint32_t kOffSeg = kOffExp + (kKind ? kStageSlots * kTileKeys : 0);
   static constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
   static constexpr uint32_t kOffMisc = kOffBar + 512;
-  static constexpr uint32_t kSmem = kOffMisc + 64 + 1024;
+  static constexpr uint32_t kOffOdd = kOffMisc + 64;  // [slots][2][3]: bits of keys with odd values
+  static constexpr uint32_t kSmem = kOffOdd + 256 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
 static_assert(sizeof(Segment) <= 64, "");
@@ -92,9 +94,10 @@ enum {
   BAR_SREAD = 34,   // the softmax has S in registers
   BAR_PFULL = 36,
   BAR_PVDONE = 38,
-  BAR_OEMPTY = 40,  // the output has been read
-  BAR_DRAIN = 42,   // +issuer (3): products in flight have completed (abort)
-  NUM_BARS = 45
+  BAR_ODD = 40,     // a tile's softmax warps have looked through V
+  BAR_VREADY = 42,  // +tile: V of a tile at the mask's edge has landed
+  BAR_DRAIN = 44,   // +issuer (3): products in flight have completed (abort)
+  NUM_BARS = 47
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -161,6 +164,65 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
+// A key's V in shared memory (at v, as a tile's row): zeros when it is hidden
+// from every row, or when it holds a NaN or an infinity, which sets `bit`.
+__device__ __noinline__ void odd_scan(uint32_t v, bool hidden, uint32_t* bits, uint32_t bit) {
+  const uint32_t turn = (v / 128) & 7;  // (rows start at different banks)
+  bool clear = hidden;
+  if (!clear) {
+    uint32_t m2 = 0;
+#pragma unroll 4
+    for (int b = 0; b < 16; ++b) {
+      uint32_t z[4];
+      lds128(z, v + (b / 8) * kHalfBytes + ((b % 8) ^ turn) * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, z[e] & 0x7FFF7FFFu);
+    }
+    if ((m2 >> 16) >= 0x7F80u || (m2 & 0xFFFFu) >= 0x7F80u) {
+      atomicOr(bits, bit);
+      __threadfence_block();  // the bit, then the zeros that hide it from the other tile's scan
+      clear = true;
+    }
+  }
+  if (clear) {
+    const uint32_t zero[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int b = 0; b < 16; ++b) sts128(v + (b / 8) * kHalfBytes + ((b % 8) ^ turn) * 16, zero);
+  }
+}
+
+// O of this thread's row (tensor memory, the whole warp) += p V of the cached
+// row `at`, for the threads that see it: p from Q and K themselves.
+__device__ __noinline__ void odd_add(uint32_t o_col, const uint16_t* q, const uint8_t* k_pages, const uint8_t* v_pages,
+                                     int64_t at, bool see, float c2, float neg) {
+  const uint16_t* k = reinterpret_cast<const uint16_t*>(k_pages) + at * kHeadDim;
+  const uint16_t* v = reinterpret_cast<const uint16_t*>(v_pages) + at * kHeadDim;
+  float dot = 0.f;
+  if (see) {
+#pragma unroll 1
+    for (int d = 0; d < kHeadDim; d += 2) {
+      const uint32_t qv = *reinterpret_cast<const uint32_t*>(q + d), kv = *reinterpret_cast<const uint32_t*>(k + d);
+      dot = fmaf(__uint_as_float(qv << 16), __uint_as_float(kv << 16), dot);
+      dot = fmaf(__uint_as_float(qv & 0xFFFF0000u), __uint_as_float(kv & 0xFFFF0000u), dot);
+    }
+  }
+  __syncwarp();
+  const float p = ex2_approx(fmaf(dot, c2, neg));
+#pragma unroll 1
+  for (int d = 0; d < kHeadDim; d += 32) {
+    uint32_t o[32];
+    tmem_ld32(o_col + d, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (see)
+        o[e] = __float_as_uint(fmaf(p, __uint_as_float(static_cast<uint32_t>(v[d + e]) << 16), __uint_as_float(o[e])));
+    __syncwarp();
+    tmem_st32(o_col + d, o);
+    tmem_wait_st();
+  }
+}
+
 template <int kKind>
 __global__ void __launch_bounds__(Cfg<kKind>::kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -176,8 +238,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   volatile int32_t* s_abort = reinterpret_cast<volatile int32_t*>(base + C::kOffMisc);
   int32_t* s_bad = reinterpret_cast<int32_t*>(base + C::kOffMisc + 4);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(base + C::kOffMisc + 8);
+  uint32_t* s_odd = reinterpret_cast<uint32_t*>(base + C::kOffOdd);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
+  if (threadIdx.x < 64) s_odd[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     *s_abort = 0;
     *s_bad = 0;
@@ -194,7 +258,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(BAR_SREAD + t), 4);
       mbar_init(bar(BAR_PFULL + t), 4);
-      mbar_init(bar(BAR_OEMPTY + t), 4);
+      mbar_init(bar(BAR_ODD + t), 4);
     }
     fence_barrier_init();
   }
@@ -290,6 +354,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             cp_async_arrive(bar(kFull + b));
           }
           if (elect) {
+            if (kKind == 0) s_odd[6 * b] = s_odd[6 * b + 1] = s_odd[6 * b + 2] = 0;
             mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 : 256));
 #pragma unroll
             for (int i = 0; i < kBoxes; ++i) {
@@ -419,11 +484,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ O += P V of both tiles
+    // (the softmax makes O zeros before a unit's first P)
     const uint32_t id_o = idesc_bf16(128, 128, false, true);
     auto vmaj_off = [](int kk) { return static_cast<uint64_t>((kk * 2 * kGroupBytes) >> 4); };
     const uint32_t elect = elect_one();
     int slot = 1, phase = 0;
-    int y0 = 0, y1 = 0, units1 = 0;  // key tiles of row tile 0 and 1, units in which tile 1 has rows
+    int y0 = 0, y1 = 0;  // key tiles of row tile 0 and 1
     bool issued = false;
     for (int k = 0; ok; ++k) {
       Segment g;
@@ -433,19 +499,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll 1
       for (int j = 0; j < g.nt && ok; ++j) {
         const uint64_t vs = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, kHalfBytes, kGroupBytes);
+        const int key0 = (g.t0 + j) * kTileKeys;
+        if (key0 < g.all_lo || key0 + kTileKeys > g.all_hi) {  // the softmax looks through V first
+          ok = all_wait(BAR_FULL + slot, phase);
+          if (!ok) break;
+          if (lane < tiles) mbar_arrive(bar(BAR_VREADY + lane));
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= tiles) break;
           ok = all_wait2(BAR_FULL + slot, phase, BAR_PFULL + t, (t ? y1 : y0) + j);
-          // the unit's first PV overwrites O: the last unit's must have been read
-          const int before = t ? units1 : k;
-          if (ok && j == 0 && before > 0) ok = all_wait(BAR_OEMPTY + t, before - 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTileKeys / 16; ++kk)
             umma_ts_elect(tmem + 128 * t, tmem + 256 + 128 * t + kTileKeys + kk * 8, vs + vmaj_off(kk), id_o,
-                          (j > 0 || kk > 0) ? 1u : 0u, elect);
+                          1u, elect);
           if (elect) {
             if (t + 1 == tiles) umma_commit(bar(BAR_EMPTY + slot));
             umma_commit(bar(BAR_PVDONE + t));
@@ -460,10 +529,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
       }
       y0 += g.nt;
-      if (tiles == 2) {
-        y1 += g.nt;
-        ++units1;
-      }
+      if (tiles == 2) y1 += g.nt;
     }
     if (!ok) {
       *s_abort = 1;
@@ -480,7 +546,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_addr + 256 + 128 * t, p_col = s_col + kTileKeys, o_col = tmem + lane_addr + 128 * t;
     const float c2 = a.scale * 1.4426950408889634f;
-    int x = 0, y = 0;
+    int x = 0, y = 0, edges = 0;
     for (int k = 0; ok; ++k) {
       Segment g;
       ok = next_seg(k, g);
@@ -497,28 +563,51 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       const int lo = real ? row_lo(a, pos) : 0;
       const int hi = real ? (a.causal ? min(g.len, pos + 1) : g.len) : 0x7FFFFFFF;
       float ref = -INFINITY, l = 0.f;
-#pragma unroll 1
-      for (int j = 0; j < g.nt; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, wait(BAR_SFULL + t, y + j));
-        if (!ok) break;
+      float whole = 1.f;  // NaN once the row has seen a value that is NaN as a whole
+      // O starts as zeros (PV accumulates; the last unit's O has been read)
+      {
+        uint32_t zero[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) zero[e] = 0;
+#pragma unroll
+        for (int b = 0; b < 128; b += 32) tmem_st32(o_col + b, zero);
+      }
+      // One key tile; false when a wait gave up.  edge: some row of the unit
+      // does not see some key of it.  (Two copies of the code: the tiles that
+      // every row sees whole are most of them.)
+      auto tile = [&](auto edge, int j) -> bool {
+        constexpr bool kEdge = decltype(edge)::value;
+        if (!all_wait(BAR_SFULL + t, y + j)) return false;
         tc_fence_after();
         const int key0 = (g.t0 + j) * kTileKeys;
-        // BF16 pages: slots that no row sees may hold anything, and their V
-        // must become zeros (their probabilities are 0, and 0 * NaN is not).
-        // Both tiles' warps write them, each before its own products.
-        if (kKind == 0 && (key0 < g.lo || key0 + kTileKeys > g.hi)) {
-          const int q = 2 * (x + j) + 1;
-          ok = __all_sync(0xFFFFFFFFu, wait(BAR_FULL + q % kSlots, q / kSlots));
-          if (!ok) break;
-          if (row < kTileKeys && (key0 + row < g.lo || key0 + row >= g.hi)) {
-            uint8_t* v = base + C::kOffRing + (q % kSlots) * kSlotBytes + (row / 8) * kGroupBytes + (row % 8) * 128;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              *reinterpret_cast<uint4*>(v + 16 * b) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(v + kHalfBytes + 16 * b) = make_uint4(0, 0, 0, 0);
-            }
+        // At the mask's edge a key of the tile may be hidden from a row that
+        // its probability 0 would still multiply with what V holds, and
+        // 0 * NaN is not 0.  Slots that no row sees may hold anything; keys
+        // that only some rows see hold tokens, but these may have a NaN or an
+        // infinity.  Both kinds of rows become zeros in shared memory; the
+        // tokens among them (a bit each in s_odd) are added one by one below.
+        // BF16: both tiles' warps do it, each before its own products.  E4M3:
+        // the widening warps have done it.
+        uint32_t odd[3] = {0, 0, 0};
+        if constexpr (kEdge) {
+          const int slot = (2 * (x + j) + 1) % kSlots;
+          // (told by the PV warp, which sees every phase of V's slots)
+          if (!all_wait(BAR_VREADY + t, edges)) return false;
+          if constexpr (kKind == 0) {
+            if (row < kTileKeys)
+              odd_scan(sbase + C::kOffRing + slot * kSlotBytes + (row / 8) * kGroupBytes + (row % 8) * 128,
+                       key0 + row < g.lo || key0 + row >= g.hi, &s_odd[6 * slot + row / 32], 1u << (row % 32));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(BAR_ODD + t));
+            if (!all_wait(BAR_ODD + t, edges)) return false;
           }
-          fence_proxy_async_smem();
+          ++edges;
+#pragma unroll
+          for (int w = 0; w < 3; ++w) {
+            odd[w] = *reinterpret_cast<volatile uint32_t*>(&s_odd[6 * slot + w]);
+            if (kKind != 0) odd[w] |= *reinterpret_cast<volatile uint32_t*>(&s_odd[6 * slot + 3 + w]);
+          }
         }
         uint32_t s[kTileKeys];
         tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
@@ -528,7 +617,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_SREAD + t));
-        if (!__all_sync(0xFFFFFFFFu, key0 >= lo && key0 + kTileKeys <= hi)) {
+        if constexpr (kEdge) {
           const int a0 = lo - key0, a1 = hi - key0;
 #pragma unroll
           for (int b = 0; b < kTileKeys; ++b)
@@ -556,8 +645,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         // O holds the tiles before j, and P_(j-1)'s place is free, when PV_(j-1) has completed
         if (j > 0) {
-          ok = __all_sync(0xFFFFFFFFu, wait(BAR_PVDONE + t, y + j - 1));
-          if (!ok) break;
+          if (!all_wait(BAR_PVDONE + t, y + j - 1)) return false;
           tc_fence_after();
         }
         if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -580,14 +668,37 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         tmem_st32(p_col, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
         tmem_st8(p_col + 32, *reinterpret_cast<uint32_t(*)[8]>(&p[32]));
+        if (kEdge && (odd[0] | odd[1] | odd[2])) {
+          tmem_wait_st();
+#pragma unroll 1
+          for (int b = 0; b < kTileKeys; ++b) {
+            if (!((b < 32 ? odd[0] : b < 64 ? odd[1] : odd[2]) >> (b % 32) & 1)) continue;
+            const int key = key0 + b;
+            const bool see = real && key >= lo && key < hi;
+            if constexpr (kKind != 0) {
+              if (see) whole = __uint_as_float(0x7FFFFFFFu);  // all of the value is NaN
+            } else {
+              const int page = c.table[g.s * c.table_stride + (key >> c.page_shift)];
+              if (page < 0 || page >= c.pages) continue;  // (reported by the producer)
+              odd_add(o_col,
+                      a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
+                          static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head,
+                      c.k_pages, c.v_pages,
+                      ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (key & (c.page_size - 1)), see, c2,
+                      neg);
+            }
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_PFULL + t));
-        if (__any_sync(0xFFFFFFFFu, *s_abort != 0)) {
-          ok = false;
-          break;
-        }
+        return !__any_sync(0xFFFFFFFFu, *s_abort != 0);
+      };
+#pragma unroll 1
+      for (int j = 0; j < g.nt && ok; ++j) {
+        const int key0 = (g.t0 + j) * kTileKeys;
+        ok = key0 < g.all_lo || key0 + kTileKeys > g.all_hi ? tile(std::true_type(), j) : tile(std::false_type(), j);
       }
       // ---- the unit's output, or this step's part of it (the widened codes of
       // four dimensions lie in the order 0, 2, 1, 3)
@@ -597,7 +708,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       tc_fence_after();
       const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + (rho - i * a.group)
                                     : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows + 128 * t + row;
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+      const float inv = (g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * whole;  // (NaN stays)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         uint32_t o[32];
@@ -605,21 +716,24 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         tmem_wait_ld();
         if (real) {
           if (g.part < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.o + at * kHeadDim + 32 * b);
+            // (32-byte stores: whole sectors)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t z[4];
+            for (int e = 0; e < 2; ++e) {
+              uint32_t z[8];
 #pragma unroll
-              for (int f = 0; f < 4; ++f)
-                z[f] = pack_bf16x2(__uint_as_float(o[dim(8 * e + 2 * f)]) * inv,
-                                   __uint_as_float(o[dim(8 * e + 2 * f + 1)]) * inv);
-              dst[e] = make_uint4(z[0], z[1], z[2], z[3]);
+              for (int f = 0; f < 8; ++f)
+                z[f] = pack_bf16x2(__uint_as_float(o[dim(16 * e + 2 * f)]) * inv,
+                                   __uint_as_float(o[dim(16 * e + 2 * f + 1)]) * inv);
+              st_global_v8(a.o + at * kHeadDim + 32 * b + 16 * e, z);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(ws.part + at * kHeadDim + 32 * b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_uint4(o[dim(4 * e)], o[dim(4 * e + 1)], o[dim(4 * e + 2)], o[dim(4 * e + 3)]);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t z[8];
+#pragma unroll
+              for (int f = 0; f < 8; ++f) z[f] = __float_as_uint(__uint_as_float(o[dim(8 * e + f)]) * inv);
+              st_global_v8(ws.part + at * kHeadDim + 32 * b + 8 * e, z);
+            }
           }
         }
       }
@@ -629,9 +743,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         else if (a.lse)
           a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_OEMPTY + t));
       x += g.nt;
       y += g.nt;
     }
@@ -661,6 +772,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         // other chunk of a half of the dimensions, meet in no bank.
         const int ch = lane % 4 + 4 * (lane / 8 % 2), row0 = (warp % 2) * 4 + lane / 4 % 2 + 2 * (lane / 16);
         const bool inside = key0 >= g.lo && key0 + kTileKeys <= g.hi;
+        const bool edge = key0 < g.all_lo || key0 + kTileKeys > g.all_hi;
+        if (kv == 1 && edge) {
+          // (see the softmax) values that are NaN: a bit, and exponent 0 for zeros
+          uint32_t* bits = &s_odd[6 * slot + 3 * (warp % 2)];
+          if (lane < 3) bits[lane] = 0;
+          __syncwarp();
+          for (int row = lane; row < kTileKeys; row += 32) {
+            uint8_t* e = base + C::kOffExp + b * kTileKeys + row;
+            if (*e == 255 && key0 + row >= g.lo && key0 + row < g.hi) {
+              atomicOr(&bits[row / 32], 1u << (row % 32));
+              *e = 0;
+            }
+          }
+          __syncwarp();
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t in[5][4], e[5];
@@ -670,7 +796,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const int row = (half * 5 + i) * 8 + row0;
             lds128(in[i], src + row * 128 + (ch ^ (row & 7)) * 16);
             e[i] = lds8(sbase + C::kOffExp + b * kTileKeys + row);
-            plain = plain && e[i] <= 134;
+            plain = plain && e[i] - 1u < 134u;
           }
           plain = __all_sync(0xFFFFFFFFu, plain);
 #pragma unroll

@@ -370,9 +370,6 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           lo[n][e] = row < g.rows ? row_lo(a, pos) : 0;
           hi[n][e] = row < g.rows ? (a.causal ? min(g.len, pos + 1) : g.len) : 0;
         }
-      // [all_lo, all_hi): what every row sees
-      const int all_lo = row_lo(a, g.len - 1);
-      const int all_hi = a.causal ? min(g.len, g.len - g.n + 1) : g.len;
       float acc[kN][8][4], ref[kN][2], sum[kN][2];
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
@@ -445,7 +442,24 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             vs[e] = exp_scale(ex[kTileKeys + 8 * e]);
           }
         }
-        const bool cut = ragged || key0 < all_lo || key0 + 16 > all_hi;  // some row misses some key
+        const bool cut = ragged || key0 < g.all_lo || key0 + 16 > g.all_hi;  // some row misses some key
+        // BF16, rows of several tokens: a value of a key that one row sees and
+        // another does not must not reach that other one as 0 * NaN or
+        // 0 * infinity.  Keys with such values (a bit each) are left out of
+        // the product and added one by one.
+        uint32_t odd_keys = 0;
+        if (kKind == 0 && cut && g.n > 1) {
+          const uint32_t v = sv + (16 * quarter + lane / 2) * 128 + (lane % 2) * (kTileKeys * 128);
+          uint32_t m2 = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 f = lds_f4(v + 16 * i);
+            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(__float_as_uint(f.x) & 0x7FFF7FFFu, __float_as_uint(f.y) & 0x7FFF7FFFu),
+                                       __vmaxu2(__float_as_uint(f.z) & 0x7FFF7FFFu, __float_as_uint(f.w) & 0x7FFF7FFFu)));
+          }
+          const uint32_t by_lane = __ballot_sync(0xFFFFFFFFu, (m2 >> 16) >= 0x7F80u || (m2 & 0xFFFFu) >= 0x7F80u);
+          odd_keys = (by_lane | by_lane >> 1) & 0x55555555u;  // key x at bit 2x
+        }
         uint32_t p[kN][2];
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
@@ -490,6 +504,34 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           }
           p[n][0] = transpose8(pack_bf16x2(y[0], y[1]));
           p[n][1] = transpose8(pack_bf16x2(y[2], y[3]));
+          for (uint32_t left = odd_keys; left; left &= left - 1) {
+            const int x = (__ffs(left) - 1) / 2;  // key of the sixteen
+            const int from = (x % 8) * 4 + t4;    // the lane that has its probabilities of this thread's rows
+            const float p0 = __shfl_sync(0xFFFFFFFFu, x < 8 ? y[0] : y[2], from);
+            const float p1 = __shfl_sync(0xFFFFFFFFu, x < 8 ? y[1] : y[3], from);
+            const bool see0 = key0 + x >= lo[n][0] && key0 + x < hi[n][0];
+            const bool see1 = key0 + x >= lo[n][1] && key0 + x < hi[n][1];
+            const int row = 16 * quarter + x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {  // dimension 16 j + 8 e + u
+                uint16_t b;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(sv + chunk_at(row, 2 * j + e) + 2 * u));
+                const float v = __uint_as_float(static_cast<uint32_t>(b) << 16);
+                if (see0) acc[n][j][2 * e] = fmaf(p0, v, acc[n][j][2 * e]);
+                if (see1) acc[n][j][2 * e + 1] = fmaf(p1, v, acc[n][j][2 * e + 1]);
+              }
+          }
+        }
+        if (odd_keys) {
+          __syncwarp();
+          if ((odd_keys >> (lane & ~1)) & 1) {
+            const uint32_t v = sv + (16 * quarter + lane / 2) * 128 + (lane % 2) * (kTileKeys * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts_f4(v + 16 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+          }
+          __syncwarp();
         }
         // ---- O^T += V^T P^T: dimensions u, u + 8 of 16 (2u, 2u + 1 in the E4M3 kind)
 #pragma unroll
@@ -509,7 +551,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
           }
         }
-        if (ragged) fence_proxy_async_smem();  // zeros written here, TMA writes next
+        if (ragged || odd_keys) fence_proxy_async_smem();  // zeros written here, TMA writes next
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_EMPTY + stage));
       }

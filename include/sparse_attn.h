@@ -417,7 +417,8 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, 
  * tokens' K and V are in the cache already).  One softmax a row, in FP32;
  * logits scale * (q . k).
  *   q     BF16 rows (r, h) at q + r * a_token_stride + h * a_head_stride
- *   o     BF16 [rows, Hq, 128], contiguous; zeros for a row that sees no key
+ *   o     BF16 [rows, Hq, 128], contiguous, 32-byte aligned; zeros for a row
+ *         that sees no key
  *   lse   optional (may be NULL) float32 [rows, Hq]: natural logarithm of the
  *         sum of exp(logit), -inf for a row that sees no key
  *   ws    workspace of sparse_attn_paged_ws_bytes(p) bytes: the status word
@@ -426,7 +427,7 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, 
  * used, whatever they are.
  * Errors: as sparse_attn_cache_write, and SA_EINVAL for Hq not a multiple of
  * H, causal not 0 or 1, window < 0 or with causal = 0, scale not positive and finite, o
- * not 16-byte or lse not 4-byte aligned, a short workspace.
+ * not 32-byte or lse not 4-byte aligned, a short workspace.
  */
 sa_status sparse_attn_paged_ws_bytes(const sa_paged_params* p, uint64_t* out);
 sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, const void* k_pages,

@@ -282,6 +282,56 @@ def test_a_window_leaves_freed_pages_unread(bsr, kind):
     check_attention(b, q, o, lse, True, 50)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,news,H,Hq,window", [
+    ([100, 70], [3, 2], 2, 4, 0),          # few rows
+    ([100, 300], [4, 3], 1, 4, 20),
+    ([300, 150], [200, 90], 2, 4, 0),      # chunks
+    ([500, 260], [257, 130], 1, 3, 33),
+])
+def test_odd_values_reach_only_the_rows_that_see_them(bsr, kind, lens, news, H, Hq, window):
+    """NaN and infinities in K and V of tokens that only some rows of a tile
+    see: the others' results are those of a cache without them."""
+    for what in ("v nan", "v inf", "k nan", "v both"):
+        b = Batch(lens, news, H, 64, kind, seed=3)
+        bad = []
+        for s, (n, m) in enumerate(zip(lens, news)):  # the newest token, one in the middle of the new ones, one old one
+            bad += [(s, n - 1), (s, n - 1 - m // 2)] + ([(s, n - m - 30)] if window else [])
+        for s, j in bad:
+            pg, sl = b.table_np[s, j // 64], j % 64
+            t, t64, e = (b.k_pages, b.k64, b.k_exp) if what[0] == "k" else (b.v_pages, b.v64, b.v_exp)
+            if kind == "e4m3":
+                e[pg, :, sl] = 255
+                t64[pg, :, sl] = math.nan
+                continue
+            for d, x in {"nan": [(5, math.nan)], "inf": [(5, math.inf), (9, -math.inf)],
+                         "both": [(d, math.nan if d % 3 else math.inf) for d in range(0, 128, 7)]}[what[2:]]:
+                t[pg, :, sl, d] = x
+                t64[pg, :, sl, d] = x
+        q, o, lse = run_attention(bsr, b, Hq, window=window)
+        og, lg = o.double().cpu().numpy(), lse.double().cpu().numpy()
+        seen = []
+        for s, n in enumerate(lens):
+            rows, pos = zip(*OP.positions(b.starts, lens, s))
+            k, v = OP.gather(b.k64, b.table_np, s, n), OP.gather(b.v64, b.table_np, s, n)
+            with np.errstate(invalid="ignore"):
+                ro, rl, mass, reach = OP.paged_attention(q.double().cpu().numpy()[list(rows)], k, v, pos, n, True, window)
+            got = og[list(rows)]
+            fine = np.isfinite(ro)
+            assert np.array_equal(fine, np.isfinite(got)), (what, s)
+            assert np.array_equal(np.isnan(ro), np.isnan(got)) and np.array_equal(ro[np.isinf(ro)], got[np.isinf(ro)])
+            mass = np.where(np.isfinite(mass), mass, 0)
+            reach = np.where(np.isfinite(reach), reach, 0)
+            ds = (2 * 128 + 8) * U * reach
+            tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 4 * ds + 2.0 ** -21 + 2 * (n + 64) * U)[..., None] * mass
+            with np.errstate(invalid="ignore"):
+                assert np.all(np.abs(got - ro)[fine] <= tol[fine]), (what, s)
+            assert np.array_equal(np.isnan(rl), np.isnan(lg[list(rows)]))
+            seen.append(fine.reshape(-1))
+        seen = np.concatenate(seen)
+        assert seen.any() and not seen.all()  # both kinds of rows are there
+
+
 def test_scales(bsr):
     b = Batch([333, 64], [20, 1], 2, 64, seed=3)
     for scale in (1e-6, 0.05, 3.0):

@@ -145,7 +145,7 @@ def test_attention_refuses_its_own(native):
                 dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-1.0), dict(at=4), dict(ah=-128)):
         assert _fwd(native, _p(native, **bad)) == E, bad
     p = _p(native)
-    for bad in (dict(q=None), dict(o=None), dict(ws=None), dict(q=A + 8), dict(o=A + 8), dict(lse=A + 2), dict(n=255)):
+    for bad in (dict(q=None), dict(o=None), dict(ws=None), dict(q=A + 8), dict(o=A + 16), dict(lse=A + 2), dict(n=255)):
         assert _fwd(native, p, **bad) == E, bad
     assert _fwd(native, _p(native, Hq=1 << 20, H=1, rows=1 << 11, at=8)) == native.SA_EUNSUPPORTED
     assert native.load_library().sparse_attn_paged_ws_bytes(ctypes.byref(p), None) == E
