@@ -94,7 +94,6 @@ enum {
   BAR_SREAD = 34,   // the softmax has S in registers
   BAR_PFULL = 36,
   BAR_PVDONE = 38,
-  BAR_ODD = 40,     // a tile's softmax warps have looked through V
   BAR_VREADY = 42,  // +tile: V of a tile at the mask's edge has landed
   BAR_DRAIN = 44,   // +issuer (3): products in flight have completed (abort)
   NUM_BARS = 47
@@ -164,31 +163,43 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
-// A key's V in shared memory (at v, as a tile's row): zeros when it is hidden
-// from every row, or when it holds a NaN or an infinity, which sets `bit`.
-__device__ __noinline__ void odd_scan(uint32_t v, bool hidden, uint32_t* bits, uint32_t bit) {
-  const uint32_t turn = (v / 128) & 7;  // (rows start at different banks)
-  bool clear = hidden;
-  if (!clear) {
-    uint32_t m2 = 0;
-#pragma unroll 4
-    for (int b = 0; b < 16; ++b) {
-      uint32_t z[4];
-      lds128(z, v + (b / 8) * kHalfBytes + ((b % 8) ^ turn) * 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, z[e] & 0x7FFF7FFFu);
-    }
-    if ((m2 >> 16) >= 0x7F80u || (m2 & 0xFFFFu) >= 0x7F80u) {
-      atomicOr(bits, bit);
-      __threadfence_block();  // the bit, then the zeros that hide it from the other tile's scan
-      clear = true;
+// V of a tile at the mask's edge (by a warp): rows outside [first, end), which
+// no row of Q sees, become zeros, and so do rows that hold a NaN or an
+// infinity, which set their bit.
+__device__ __forceinline__ void edge_values(uint32_t v, int first, int end, uint32_t* bits, int lane) {
+  // 16 lanes a row, 16 bytes each; two rows at a time
+  auto at = [&](int row) {
+    return v + (row / 8) * kGroupBytes + (lane / 8 % 2) * kHalfBytes + (row % 8) * 128 + (lane % 8) * 16;
+  };
+  const uint32_t zero[4] = {0, 0, 0, 0};
+  const int row0 = lane / 16;
+  if (lane < 3) bits[lane] = 0;
+  if (first > 0 || end < kTileKeys) {
+    for (int row = row0; row < kTileKeys; row += 2)
+      if (row < first || row >= end) sts128(at(row), zero);
+  }
+  __syncwarp();
+  auto largest = [&](int row) {  // magnitudes as integers, two to a word
+    uint32_t z[4];
+    lds128(z, at(row));
+    return __vmaxu2(__vmaxu2(z[0] & 0x7FFF7FFFu, z[1] & 0x7FFF7FFFu), __vmaxu2(z[2] & 0x7FFF7FFFu, z[3] & 0x7FFF7FFFu));
+  };
+  auto not_finite = [](uint32_t m) { return (m >> 16) >= 0x7F80u || (m & 0xFFFFu) >= 0x7F80u; };
+  uint32_t m = 0;
+#pragma unroll 8
+  for (int row = row0; row < kTileKeys; row += 2) m = __vmaxu2(m, largest(row));
+  if (__any_sync(0xFFFFFFFFu, not_finite(m))) {
+#pragma unroll 1
+    for (int row = row0; row < kTileKeys; row += 2) {
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, not_finite(largest(row)));
+      if ((who >> (16 * row0)) & 0xFFFFu) {
+        sts128(at(row), zero);
+        if (lane % 16 == 0) atomicOr(&bits[row / 32], 1u << (row % 32));
+      }
     }
   }
-  if (clear) {
-    const uint32_t zero[4] = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int b = 0; b < 16; ++b) sts128(v + (b / 8) * kHalfBytes + ((b % 8) ^ turn) * 16, zero);
-  }
+  fence_proxy_async_smem();  // read by the products
+  __syncwarp();
 }
 
 // O of this thread's row (tensor memory, the whole warp) += p V of the cached
@@ -258,7 +269,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(BAR_SREAD + t), 4);
       mbar_init(bar(BAR_PFULL + t), 4);
-      mbar_init(bar(BAR_ODD + t), 4);
     }
     fence_barrier_init();
   }
@@ -354,7 +364,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             cp_async_arrive(bar(kFull + b));
           }
           if (elect) {
-            if (kKind == 0) s_odd[6 * b] = s_odd[6 * b + 1] = s_odd[6 * b + 2] = 0;
             mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 : 256));
 #pragma unroll
             for (int i = 0; i < kBoxes; ++i) {
@@ -500,9 +509,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       for (int j = 0; j < g.nt && ok; ++j) {
         const uint64_t vs = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, kHalfBytes, kGroupBytes);
         const int key0 = (g.t0 + j) * kTileKeys;
-        if (key0 < g.all_lo || key0 + kTileKeys > g.all_hi) {  // the softmax looks through V first
+        if (key0 < g.all_lo || key0 + kTileKeys > g.all_hi) {  // (see the softmax)
           ok = all_wait(BAR_FULL + slot, phase);
           if (!ok) break;
+          if constexpr (kKind == 0)
+            edge_values(sbase + C::kOffRing + slot * kSlotBytes, g.lo - key0, g.hi - key0, &s_odd[6 * slot], lane);
           if (lane < tiles) mbar_arrive(bar(BAR_VREADY + lane));
         }
 #pragma unroll
@@ -580,35 +591,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (!all_wait(BAR_SFULL + t, y + j)) return false;
         tc_fence_after();
         const int key0 = (g.t0 + j) * kTileKeys;
-        // At the mask's edge a key of the tile may be hidden from a row that
-        // its probability 0 would still multiply with what V holds, and
-        // 0 * NaN is not 0.  Slots that no row sees may hold anything; keys
-        // that only some rows see hold tokens, but these may have a NaN or an
-        // infinity.  Both kinds of rows become zeros in shared memory; the
-        // tokens among them (a bit each in s_odd) are added one by one below.
-        // BF16: both tiles' warps do it, each before its own products.  E4M3:
-        // the widening warps have done it.
-        uint32_t odd[3] = {0, 0, 0};
-        if constexpr (kEdge) {
-          const int slot = (2 * (x + j) + 1) % kSlots;
-          // (told by the PV warp, which sees every phase of V's slots)
-          if (!all_wait(BAR_VREADY + t, edges)) return false;
-          if constexpr (kKind == 0) {
-            if (row < kTileKeys)
-              odd_scan(sbase + C::kOffRing + slot * kSlotBytes + (row / 8) * kGroupBytes + (row % 8) * 128,
-                       key0 + row < g.lo || key0 + row >= g.hi, &s_odd[6 * slot + row / 32], 1u << (row % 32));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(BAR_ODD + t));
-            if (!all_wait(BAR_ODD + t, edges)) return false;
-          }
-          ++edges;
-#pragma unroll
-          for (int w = 0; w < 3; ++w) {
-            odd[w] = *reinterpret_cast<volatile uint32_t*>(&s_odd[6 * slot + w]);
-            if (kKind != 0) odd[w] |= *reinterpret_cast<volatile uint32_t*>(&s_odd[6 * slot + 3 + w]);
-          }
-        }
         uint32_t s[kTileKeys];
         tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
         tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -617,11 +599,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_SREAD + t));
-        if constexpr (kEdge) {
-          const int a0 = lo - key0, a1 = hi - key0;
+        if constexpr (kEdge) {  // a bit for each key that the row sees
 #pragma unroll
-          for (int b = 0; b < kTileKeys; ++b)
-            if (b < a0 || b >= a1) s[b] = __float_as_uint(-INFINITY);
+          for (int w = 0; w < 3; ++w) {
+            const int a0 = min(max(lo - key0 - 32 * w, 0), 32), a1 = min(max(hi - key0 - 32 * w, 0), 32);
+            const uint32_t seen = (a1 == 32 ? ~0u : (1u << a1) - 1u) & ~(a0 == 32 ? ~0u : (1u << a0) - 1u);
+#pragma unroll
+            for (int b = 0; b < 32; ++b)
+              if (32 * w + b < kTileKeys && !(seen & (1u << b))) s[32 * w + b] = __float_as_uint(-INFINITY);
+          }
         }
         // The reference follows the row's maximum only when that has passed it
         // by 2^32 (p <= 2^32 leaves FP32 room): O is seldom rescaled.
@@ -668,24 +654,41 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         tmem_st32(p_col, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
         tmem_st8(p_col + 32, *reinterpret_cast<uint32_t(*)[8]>(&p[32]));
-        if (kEdge && (odd[0] | odd[1] | odd[2])) {
-          tmem_wait_st();
+        if constexpr (kEdge) {
+          // At the mask's edge a key of the tile may be hidden from a row that
+          // its probability 0 would still multiply with what V holds, and
+          // 0 * NaN is not 0.  Slots that no row sees may hold anything; keys
+          // that only some rows see hold tokens, but these may have a NaN or
+          // an infinity.  The PV warp (in the E4M3 kind the widening warps)
+          // has made zeros of both; the tokens among them, a bit each in
+          // s_odd, are added here one by one.
+          if (!all_wait(BAR_VREADY + t, edges++)) return false;
+          const int slot = (2 * (x + j) + 1) % kSlots;
+          uint32_t odd[3];
+#pragma unroll
+          for (int w = 0; w < 3; ++w) {
+            odd[w] = *reinterpret_cast<volatile uint32_t*>(&s_odd[6 * slot + w]);
+            if (kKind != 0) odd[w] |= *reinterpret_cast<volatile uint32_t*>(&s_odd[6 * slot + 3 + w]);
+          }
+          if (odd[0] | odd[1] | odd[2]) {
+            tmem_wait_st();
 #pragma unroll 1
-          for (int b = 0; b < kTileKeys; ++b) {
-            if (!((b < 32 ? odd[0] : b < 64 ? odd[1] : odd[2]) >> (b % 32) & 1)) continue;
-            const int key = key0 + b;
-            const bool see = real && key >= lo && key < hi;
-            if constexpr (kKind != 0) {
-              if (see) whole = __uint_as_float(0x7FFFFFFFu);  // all of the value is NaN
-            } else {
-              const int page = c.table[g.s * c.table_stride + (key >> c.page_shift)];
-              if (page < 0 || page >= c.pages) continue;  // (reported by the producer)
-              odd_add(o_col,
-                      a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
-                          static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head,
-                      c.k_pages, c.v_pages,
-                      ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (key & (c.page_size - 1)), see, c2,
-                      neg);
+            for (int b = 0; b < kTileKeys; ++b) {
+              if (!((b < 32 ? odd[0] : b < 64 ? odd[1] : odd[2]) >> (b % 32) & 1)) continue;
+              const int key = key0 + b;
+              const bool see = real && key >= lo && key < hi;
+              if constexpr (kKind != 0) {
+                if (see) whole = __uint_as_float(0x7FFFFFFFu);  // all of the value is NaN
+              } else {
+                const int page = c.table[g.s * c.table_stride + (key >> c.page_shift)];
+                if (page < 0 || page >= c.pages) continue;  // (reported by the producer)
+                odd_add(o_col,
+                        a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
+                            static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head,
+                        c.k_pages, c.v_pages,
+                        ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (key & (c.page_size - 1)), see, c2,
+                        neg);
+              }
             }
           }
         }
