@@ -771,9 +771,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const int key0 = (g.t0 + j) * kTileKeys;
         const uint32_t src = sbase + C::kOffStage + b * kStageBytes, dst = sbase + C::kOffRing + slot * kSlotBytes;
         // A warp takes 16 codes of 4 rows x 8 chunks at a time.  Eight lanes
-        // are two rows and half of the chunks, so that their stores, every
-        // other chunk of a half of the dimensions, meet in no bank.
-        const int ch = lane % 4 + 4 * (lane / 8 % 2), row0 = (warp % 2) * 4 + lane / 4 % 2 + 2 * (lane / 16);
+        // are two rows, half of the chunks of one and the other half of the
+        // other, so that neither their loads nor their stores (every other
+        // chunk of a half of the dimensions) meet in a bank.
+        const int ch = lane % 4 + 4 * ((lane / 4 ^ lane / 8) % 2), row0 = (warp % 2) * 4 + lane / 4 % 2 + 2 * (lane / 16);
         const bool inside = key0 >= g.lo && key0 + kTileKeys <= g.hi;
         const bool edge = key0 < g.all_lo || key0 + kTileKeys > g.all_hi;
         if (kv == 1 && edge) {
