@@ -214,12 +214,13 @@ struct JoinDesc {
 };
 
 // Workspace of paged_fwd: the status words, then a word and a JoinDesc of each
-// CTA, then two partial results of each: FP32 [row_tile][128] sums relative to
-// the row's reference, and [row_tile] (reference in log2 units, sum).
+// CTA, then two partial results of each: FP32 sums relative to the row's
+// reference, [row_tile][128] in the form for few rows and [16][row_tile][8] in
+// the form for chunks, and [row_tile] (reference in log2 units, sum).
 struct PagedScratch {
   int32_t* cta_status;  // [ctas]
   JoinDesc* join;       // [ctas]
-  float* part;          // [ctas][2][row_tile][128]
+  float* part;          // [ctas][2][row_tile * 128]
   float2* ml;           // [ctas][2][row_tile]
 };
 

@@ -711,6 +711,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       tc_fence_after();
       const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + (rho - i * a.group)
                                     : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows + 128 * t + row;
+      float* part = ws.part + (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows * kHeadDim;  // (g.part >= 0)
       const float inv = (g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * whole;  // (NaN stays)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -735,7 +736,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               uint32_t z[8];
 #pragma unroll
               for (int f = 0; f < 8; ++f) z[f] = __float_as_uint(__uint_as_float(o[dim(8 * e + f)]) * inv);
-              st_global_v8(ws.part + at * kHeadDim + 32 * b + 8 * e, z);
+              // [8 columns][row]: a warp's stores lie side by side
+              st_global_v8(part + ((4 * b + e) * kUnitRows + 128 * t + row) * 8, z);
             }
           }
         }

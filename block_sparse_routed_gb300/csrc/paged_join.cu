@@ -2,10 +2,9 @@
 // each row of a unit that a cut of the work divided, over its parts in the
 // order of their keys,
 //   o = sum_i 2^(m_i - m) a_i / sum_i 2^(m_i - m) l_i,  m = max m_i.
-// Bound by latency and by what the parts weigh (512 bytes a row and part).
-// A warp takes a row, four columns a lane; where a unit of the form for few
-// rows has been cut into many parts (one long context alone on the GPU), four
-// warps share a row's parts.
+// Bound by latency, and in the form for chunks by what the parts weigh (512
+// bytes a row and part).  The first CTA also makes one status word of the
+// CTAs' words.
 #include <cstdint>
 
 #include "internal.h"
@@ -17,98 +16,143 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// kShare: the block's warps share one row's parts, else each takes a row.
-template <bool kShare>
-__global__ void __launch_bounds__(32 * kWarps) paged_join_kernel(const PagedAttnArgs a, const PagedScratch ws,
-                                                                 int row_tile) {
+__device__ __forceinline__ void join_status(const PagedAttnArgs& a, const PagedScratch& ws) {
+  if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= 32) return;
+  int st = 0;
+  for (int i = threadIdx.x; i < gridDim.x; i += 32) st = max(st, ws.cta_status[i]);
+  st = __reduce_max_sync(0xFFFFFFFFu, st);
+  if (threadIdx.x == 0) *a.c.status = st;
+}
+
+// Row of the i-th part of the unit that begins in CTA blockIdx.x.
+__device__ __forceinline__ int64_t part_row(int i, int row_tile, int row) {
+  return (static_cast<int64_t>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * row_tile + row;
+}
+
+__device__ __forceinline__ float join_inverse(float l) {
+  return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+}
+
+__device__ __forceinline__ float join_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// The form for few rows.  A block takes a row; its warps share the parts (one
+// long context alone on the GPU has 150 of them), four columns a lane.
+__global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const PagedAttnArgs a, const PagedScratch ws,
+                                                               int row_tile) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row = blockIdx.y;
+  griddep_wait();
+  const JoinDesc d = ws.join[blockIdx.x];
+  join_status(a, ws);
+  if (d.pieces == 0 || row >= d.rows) return;
+  // The references of 32 parts, one a lane, give the maximum so far; then the
+  // parts themselves, relative to it.
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = warp; i0 < d.pieces; i0 += 32 * kWarps) {
+    const int mine = i0 + lane * kWarps;
+    const float2 ml = mine < d.pieces ? ws.ml[part_row(mine, row_tile, row)] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int k = 16; k; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+    const float to = fmaxf(m, top);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - to);
+    m = to;
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+    const int n = min(32, (d.pieces - i0 + kWarps - 1) / kWarps);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(ws.part + part_row(i0 + i * kWarps, row_tile, row) * kHeadDim)[lane];
+      const float wi = __shfl_sync(0xFFFFFFFFu, w, i), li = __shfl_sync(0xFFFFFFFFu, ml.y, i);
+      l += wi * li;
+      o.x += wi * x.x;
+      o.y += wi * x.y;
+      o.z += wi * x.z;
+      o.w += wi * x.w;
+    }
+  }
+  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float4 s_o[kWarps][32];
+  s_o[warp][lane] = o;
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float f = s_m[w] == -INFINITY ? 0.f : ex2_approx(s_m[w] - m);
+    const float4 x = s_o[w][lane];
+    l += f * s_l[w];
+    o.x += f * x.x;
+    o.y += f * x.y;
+    o.z += f * x.z;
+    o.w += f * x.w;
+  }
+  const int rho = d.rho0 + row, i = rho / a.group;
+  const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
+  const float inv = join_inverse(l);
+  reinterpret_cast<uint2*>(a.o + at * kHeadDim)[lane] =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (a.lse && lane == 0) a.lse[at] = join_lse(m, l);
+}
+
+// The form for chunks.  A warp takes 8 rows x 32 columns: the parts are read
+// 256 bytes, the output written 64 bytes at a time.
+__global__ void __launch_bounds__(32 * kWarps) join_chunk_kernel(const PagedAttnArgs a, const PagedScratch ws) {
+  constexpr int kRows = kPagedChunkRows;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   griddep_wait();
   const JoinDesc d = ws.join[blockIdx.x];
-  // One status word of the CTAs' words.
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
-    int st = 0;
-    for (int i = lane; i < gridDim.x; i += 32) st = max(st, ws.cta_status[i]);
-    st = __reduce_max_sync(0xFFFFFFFFu, st);
-    if (lane == 0) *a.c.status = st;
-  }
-  const int rows_here = kShare ? 1 : kWarps;
-  for (int row = blockIdx.y * rows_here + (kShare ? 0 : warp); row < d.rows && d.pieces > 0;
-       row += gridDim.y * rows_here) {
-    auto slot = [&](int i) -> int64_t {
-      return (static_cast<int64_t>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * row_tile + row;
-    };
-    const int first = kShare ? warp : 0, step = kShare ? kWarps : 1;
-    // The references of 32 parts, one a lane, give the maximum so far; then
-    // the parts themselves, relative to it.
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = first; i0 < d.pieces; i0 += 32 * step) {
-      const int mine = i0 + lane * step;
-      const float2 ml = mine < d.pieces ? ws.ml[slot(mine)] : make_float2(-INFINITY, 0.f);
-      float top = ml.x;
+  join_status(a, ws);
+  if (d.pieces == 0) return;
+  // warp: columns 32 w ..; lane: row, 8 columns
+  const int row = blockIdx.y * 8 + lane % 8, chunk = warp * 4 + lane / 8;
+  if (row >= d.rows) return;
+  float m = -INFINITY, l = 0.f;
+  for (int i = 0; i < d.pieces; ++i) m = fmaxf(m, ws.ml[part_row(i, kRows, row)].x);
+  float o[8];
 #pragma unroll
-      for (int k = 16; k; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-      const float to = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.f : ex2_approx(m - to);
-      m = to;
-      l *= f;
-      o.x *= f;
-      o.y *= f;
-      o.z *= f;
-      o.w *= f;
-      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-      const int n = min(32, (d.pieces - i0 + step - 1) / step);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float4 x = reinterpret_cast<const float4*>(ws.part + slot(i0 + i * step) * kHeadDim)[lane];
-        const float wi = __shfl_sync(0xFFFFFFFFu, w, i), li = __shfl_sync(0xFFFFFFFFu, ml.y, i);
-        l += wi * li;
-        o.x += wi * x.x;
-        o.y += wi * x.y;
-        o.z += wi * x.z;
-        o.w += wi * x.w;
-      }
-    }
-    if constexpr (kShare) {
-      __shared__ float s_m[kWarps], s_l[kWarps];
-      __shared__ float4 s_o[kWarps][32];
-      __syncthreads();  // (the last row's have been read)
-      s_o[warp][lane] = o;
-      if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-      m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-      l = 0.f;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = s_m[w] == -INFINITY ? 0.f : ex2_approx(s_m[w] - m);
-        const float4 x = s_o[w][lane];
-        l += f * s_l[w];
-        o.x += f * x.x;
-        o.y += f * x.y;
-        o.z += f * x.z;
-        o.w += f * x.w;
-      }
-    }
-    const int rho = d.rho0 + row, i = rho / a.group;
-    const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-    reinterpret_cast<uint2*>(a.o + at * kHeadDim)[lane] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < d.pieces; ++i) {
+    const float2 ml = ws.ml[part_row(i, kRows, row)];
+    const float4* src = reinterpret_cast<const float4*>(ws.part + part_row(i, kRows, 0) * kHeadDim + (chunk * kRows + row) * 8);
+    const float4 x = src[0], y = src[1];
+    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+    l += f * ml.y;
+    o[0] += f * x.x;
+    o[1] += f * x.y;
+    o[2] += f * x.z;
+    o[3] += f * x.w;
+    o[4] += f * y.x;
+    o[5] += f * y.y;
+    o[6] += f * y.z;
+    o[7] += f * y.w;
   }
+  const int rho = d.rho0 + row, i = rho / a.group;
+  const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
+  const float inv = join_inverse(l);
+  uint32_t z[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) z[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  reinterpret_cast<uint4*>(a.o + at * kHeadDim)[chunk] = make_uint4(z[0], z[1], z[2], z[3]);
+  if (a.lse && chunk == 0) a.lse[at] = join_lse(m, l);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s) {
   if (row_tile <= kPagedFewRows)
-    return launch_dependent(paged_join_kernel<true>, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile);
-  return launch_dependent(paged_join_kernel<false>, dim3(ctas, 16), dim3(32 * kWarps), 0, s, a, ws, row_tile);
+    return launch_dependent(join_few_kernel, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile);
+  return launch_dependent(join_chunk_kernel, dim3(ctas, kPagedChunkRows / 8), dim3(32 * kWarps), 0, s, a, ws);
 }
 
 }  // namespace sa
