@@ -119,6 +119,7 @@ sa_status check_device() {
 }  // namespace
 
 int sa::device_status() { return check_device(); }
+uint64_t sa::wait_limit_ns() { return g_probe_once.load() ? 0 : kWaitLimitNs; }
 
 namespace {
 

@@ -130,6 +130,9 @@ bool cuda_failed(cudaError_t e);
 // SA_EUNSUPPORTED or SA_ECUDA; an int of enum sa_status.
 int device_status();
 
+// Limit of a pipeline wait: kWaitLimitNs, or 0 while the testing hook is on.
+uint64_t wait_limit_ns();
+
 // Launchers (defined in the kernel translation units).
 cudaError_t launch_pool(const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_route_topk(const PlanArgs& a, cudaStream_t s);
@@ -199,6 +202,7 @@ struct PagedAttnArgs {
   float scale;
   uint16_t* o;               // BF16 [rows, Hq, 128]
   float* lse;                // [rows, Hq] or null
+  uint64_t wait_limit;       // of a pipeline wait, ns (0, the testing hook: a single probe)
 };
 
 // What the joining kernel needs of the unit (a tile of packed rows of one

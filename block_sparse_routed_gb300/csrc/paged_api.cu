@@ -36,7 +36,7 @@ sa_status check_attn(const sa_paged_params* p) {
   const sa_status st = check_paged(p);
   if (st != SA_OK) return st;
   if (p->Hq < 1 || p->Hq % p->H != 0) return SA_EINVAL;
-  if (int64_t(p->rows) * p->Hq >= (int64_t(1) << 31)) return SA_EUNSUPPORTED;
+  if (int64_t(p->rows) * p->Hq >= (int64_t(1) << 31) - 4096) return SA_EUNSUPPORTED;  // (whole tiles of rows)
   if (p->causal != 0 && p->causal != 1) return SA_EINVAL;
   if (p->window < 0 || (p->window > 0 && !p->causal)) return SA_EINVAL;
   if (!std::isfinite(p->scale) || !(p->scale > 0.0f)) return SA_EINVAL;
@@ -209,6 +209,7 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   a.scale = p->scale;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
+  a.wait_limit = wait_limit_ns();
   const PagedForm f = form_of(p);
   PagedScratch scratch;
   scratch_of(ws, f, &scratch);

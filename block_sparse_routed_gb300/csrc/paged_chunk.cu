@@ -281,7 +281,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tslot, 0);
 
-  auto wait = [&](int b, int parity) -> bool { return mbar_wait(bar(b), parity & 1, kWaitLimitNs); };
+  auto wait = [&](int b, int parity) -> bool { return mbar_wait(bar(b), parity & 1, a.wait_limit); };
+  // What is in flight completes before the CTA ends, whatever the limit.
+  auto drain = [&](int b, int parity) { mbar_wait(bar(b), parity & 1, kWaitLimitNs); };
   // By a whole warp: one wait; two at once (parity < 0: only the first).  They
   // also fail once another warp has given up.
   auto all_wait = [&](int b, int parity) { return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0; };
@@ -391,7 +393,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       *s_abort = 1;
       // copies in flight land before the CTA ends (bounded)
       if (kKind) asm volatile("cp.async.wait_all;" ::: "memory");
-      for (int x = max(0, q - kBufs); x < q; ++x) wait(kFull + x % kBufs, x / kBufs);
+      for (int x = max(0, q - kBufs); x < q; ++x) drain(kFull + x % kBufs, x / kBufs);
     }
     if (lane == 0) {
       ws.join[blockIdx.x] = join;
@@ -484,12 +486,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       }
       if (rows) y += g.nt;
     }
-    if (!ok) {
-      *s_abort = 1;
-      if (elect && issued) {  // products in flight complete before the CTA ends (bounded)
-        umma_commit(bar(BAR_DRAIN + t));
-        wait(BAR_DRAIN + t, 0);
-      }
+    if (!ok) *s_abort = 1;
+    if (elect && issued) {  // products in flight complete before the CTA ends
+      umma_commit(bar(BAR_DRAIN + t));
+      drain(BAR_DRAIN + t, 0);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ O += P V of both tiles
@@ -542,12 +542,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       y0 += g.nt;
       if (tiles == 2) y1 += g.nt;
     }
-    if (!ok) {
-      *s_abort = 1;
-      if (elect && issued) {
-        umma_commit(bar(BAR_DRAIN + 2));
-        wait(BAR_DRAIN + 2, 0);
-      }
+    if (!ok) *s_abort = 1;
+    if (elect && issued) {
+      umma_commit(bar(BAR_DRAIN + 2));
+      drain(BAR_DRAIN + 2, 0);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ softmax of tile t

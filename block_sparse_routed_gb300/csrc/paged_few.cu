@@ -220,7 +220,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     for (int k = 0; ok; ++k) {
       const Segment g = walk_next(a, w, line, blockIdx.x, join);
       ok = k < kSegs ||
-           __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_SEMPTY + k % kSegs), ((k / kSegs) & 1) ^ 1, kWaitLimitNs));
+           __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_SEMPTY + k % kSegs), ((k / kSegs) & 1) ^ 1, a.wait_limit));
       if (!ok) break;
       if (lane == 0) {
         segs[k % kSegs] = g;
@@ -244,7 +244,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         const int first = max(page0, p_lo), last = min(page0 + tile_pages, p_hi);  // [first, last)
         ok = seq < C::kStages || __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_EMPTY + stage),
-                                                                  ((seq / C::kStages) & 1) ^ 1, kWaitLimitNs));
+                                                                  ((seq / C::kStages) & 1) ^ 1, a.wait_limit));
         if (!ok) break;
         const int at = page0 + pg;
         const int page = __shfl_sync(0xFFFFFFFFu, entry, at % 32);
@@ -307,7 +307,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     bool ok = true;
     int tile = 0;  // tiles of the CTA so far
     for (int k = 0; ok; ++k) {
-      ok = !bar_any<kWorkers>(!mbar_wait(bar(BAR_SFULL + k % kSegs), (k / kSegs) & 1, kWaitLimitNs));
+      ok = !bar_any<kWorkers>(!mbar_wait(bar(BAR_SFULL + k % kSegs), (k / kSegs) & 1, a.wait_limit));
       if (!ok) break;
       const Segment g = segs[k % kSegs];
       if (!g.valid) break;
@@ -388,7 +388,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll 1
       for (int t = skip; t < g.nt; t += step) {
         const int use = tile + t, stage = use % C::kStages;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_FULL + stage), (use / C::kStages) & 1, kWaitLimitNs));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_FULL + stage), (use / C::kStages) & 1, a.wait_limit));
         if (!ok) break;
         const uint32_t sk = sbase + stage * C::kStage, sv = sk + C::kHalf;
         const int key0 = ((g.t0 + t) << kKeyShift) + 16 * quarter;

@@ -392,8 +392,8 @@ typedef struct sa_paged_params {
  * k, v and the pages, 4 for the batch, 256 for ws; k_exp, v_exp null with
  * SA_CACHE_E4M3; a field outside its range; a stride that is negative or no
  * multiple of 8; kind or page_size unknown); SA_EUNSUPPORTED (D != 128,
- * pages * H * page_size >= 2^31, rows * H >= 2^31 or rows * Hq >= 2^31, a
- * device that is not sm_103).  SA_ECUDA if a launch fails.
+ * pages * H * page_size >= 2^31, table_width * page_size >= 2^31 - 256,
+ * rows * H >= 2^31 or rows * Hq >= 2^31 - 4096, a device that is not sm_103).  SA_ECUDA if a launch fails.
  */
 sa_status sparse_attn_cache_write(const sa_paged_params* p, const void* k, const void* v, void* k_pages,
                                   void* v_pages, uint8_t* k_exp, uint8_t* v_exp, const int32_t* table,
@@ -447,9 +447,9 @@ sa_status sparse_attn_last_device_status(const void* ws, cudaStream_t stream, sa
  * records SA_ETIMEOUT in the workspace status word, lets its own copies and
  * MMAs in flight finish (those waits keep the 1 s limit), frees its tensor
  * memory and returns; the outputs of that call are invalid.  With `on`
- * nonzero, later launches by sparse_attn_fwd, sparse_attn_spark_fwd and
- * sparse_attn_fused use a build of the kernel in which every pipeline wait
- * is a single probe, so that a call almost surely times out: it exists to
+ * nonzero, later launches by sparse_attn_fwd, sparse_attn_spark_fwd,
+ * sparse_attn_fused and sparse_attn_paged_fwd are ones in which every pipeline
+ * wait is a single probe, so that a call almost surely times out: it exists to
  * test that path.  Process-wide; returns the previous setting (0 or 1).
  * Host only: touches no device.
  */

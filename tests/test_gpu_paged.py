@@ -272,6 +272,31 @@ def test_long_context_is_split_and_joined(bsr, kind, news):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_many_sequences(bsr, kind):
+    """More sequences than the work's scan looks at in one go, most of them
+    without rows or tokens; in both forms."""
+    g = np.random.default_rng(5)
+    lens = [int(x) for x in g.integers(0, 40, 1100)]
+    for most in (1, 30):
+        news = [int(g.integers(0, most + 1)) if g.random() < 0.3 else 0 for _ in lens]
+        news[700] = most
+        b = Batch(lens, news, 1, 16, kind, seed=6)
+        q, o, lse = run_attention(bsr, b, 4)
+        check_attention(b, q, o, lse)
+        k, v = rows_of(b.rows, 1)
+        one = torch.empty(256, dtype=torch.uint8, device="cuda")
+        bsr.cache_write(k, v, *b.where, **b.exps, ws=one)
+        assert bsr.sparse_attn_last_device_status(one) == 0
+        back, _ = bsr.cache_read(*b.where, rows=b.rows, **b.exps, ws=one)
+        assert bsr.sparse_attn_last_device_status(one) == 0
+        pos = np.array([p for s in range(len(lens)) for _, p in OP.positions(b.starts, lens, s)])
+        there = torch.from_numpy(pos >= 0).cuda()
+        assert not back[~there].any()
+        if kind == "bf16":
+            assert torch.equal(back[there], k[there])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_a_window_leaves_freed_pages_unread(bsr, kind):
     b = Batch([1000, 900], [3, 40], 2, 32, kind, seed=8)
     t = b.table.clone()
@@ -504,6 +529,32 @@ def test_nothing_to_do(bsr):
     o = torch.full_like(q, 5.0)
     bsr.paged_attn(q, k, v, torch.empty((0, 2), **i32), torch.zeros(1, **i32), torch.zeros(0, **i32), o=o)
     assert (o == 5).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 300])
+def test_a_wait_that_gives_up_is_reported(bsr, kind, news):
+    """The testing hook makes every pipeline wait a single probe: the call
+    records the timeout and ends by itself, the next one is as ever."""
+    from block_sparse_routed_gb300 import _native
+
+    b = Batch([900, 70], [news, 1], 2, 64, kind, seed=9)
+    q, o, lse = run_attention(bsr, b, 4)
+    ws = bsr.paged_workspace(q, b.k_pages, b.table, news)
+    prev = _native.sparse_attn_set_single_probe_waits(True)
+    try:
+        statuses = []
+        for _ in range(5):  # a single probe almost surely comes too early
+            bsr.paged_attn(q, *b.where, max_new=news, **b.exps, ws=ws)
+            statuses.append(bsr.sparse_attn_last_device_status(ws))
+            if statuses[-1] == bsr.SA_ETIMEOUT:
+                break
+    finally:
+        _native.sparse_attn_set_single_probe_waits(bool(prev))
+    assert bsr.SA_ETIMEOUT in statuses
+    o2, l2 = bsr.paged_attn(q, *b.where, max_new=news, **b.exps, ws=ws)
+    assert bsr.sparse_attn_last_device_status(ws) == 0
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
 # ---- streams, graphs, repeatability
