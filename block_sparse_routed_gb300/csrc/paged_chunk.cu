@@ -791,46 +791,54 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           }
           __syncwarp();
         }
+        const uint32_t from = src + row0 * 128 + (ch ^ row0) * 16, exps = sbase + C::kOffExp + b * kTileKeys + row0;
+        const uint32_t to0 = dst + (ch / 4) * kHalfBytes + row0 * 128 + ((2 * ch % 8) ^ row0) * 16;
+        const uint32_t to1 = dst + (ch / 4) * kHalfBytes + row0 * 128 + (((2 * ch + 1) % 8) ^ row0) * 16;
+        // Codes land as the value times 2^-120; one factor then, of 2^120 and
+        // the row's scale.
+        auto widen = [&](const uint32_t(&in)[4], uint32_t two, uint32_t(&out)[8]) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t in[5][4], e[5];
-          bool plain = inside;
-#pragma unroll
-          for (int i = 0; i < 5; ++i) {  // all loads first
-            const int row = (half * 5 + i) * 8 + row0;
-            lds128(in[i], src + row * 128 + (ch ^ (row & 7)) * 16);
-            e[i] = lds8(sbase + C::kOffExp + b * kTileKeys + row);
-            plain = plain && e[i] - 1u < 134u;
+          for (int w = 0; w < 4; ++w) {  // (c0, c2) and (c1, c3) of a word
+            const uint32_t v = in[w];
+            out[2 * w] = bf16x2_mul(((v * 16) & 0x07F007F0u) | ((v * 256) & 0x80008000u), two);
+            out[2 * w + 1] = bf16x2_mul(((v >> 4) & 0x07F007F0u) | (v & 0x80008000u), two);
           }
-          plain = __all_sync(0xFFFFFFFFu, plain);
+        };
+        bool plain = inside;  // every row seen, and every factor at most 2^127
+        for (int row = lane; row < kTileKeys; row += 32)
+          plain = plain && lds8(sbase + C::kOffExp + b * kTileKeys + row) - 1u < 134u;
+        if (__all_sync(0xFFFFFFFFu, plain)) {
+#pragma unroll 1
+          for (int i0 = 0; i0 < kTileKeys / 8; i0 += 5) {
+            uint32_t in[5][4], e[5];
 #pragma unroll
-          for (int i = 0; i < 5; ++i) {
-            const int row = (half * 5 + i) * 8 + row0;
-            // Codes land as the value times 2^-120; one factor of 2^120 and
-            // the row's scale then (up to 2^127 in the plain case).
-            uint32_t two = (e[i] + 120) * 0x00800080u, more = 0;
-            if (!plain) {
-              // 0 where no row sees the key, whatever was there; NaN for the
-              // exponent byte 255 (a byte of 0 is no exponent of cache_write)
-              if (key0 + row < g.lo || key0 + row >= g.hi) e[i] = 0;
-              const uint32_t e1 = min(e[i], 134u);
-              two = e[i] == 0 ? 0u : e[i] == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
-              more = (e[i] - e1 + 127) * 0x00800080u;
+            for (int i = 0; i < 5; ++i) {  // all loads first
+              lds128(in[i], from + (i0 + i) * 1024);
+              e[i] = lds8(exps + (i0 + i) * 8);
             }
-            uint32_t out[8];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {  // (c0, c2) and (c1, c3) of a word
-              const uint32_t v = in[i][w];
-              out[2 * w] = bf16x2_mul(((v * 16) & 0x07F007F0u) | ((v * 256) & 0x80008000u), two);
-              out[2 * w + 1] = bf16x2_mul(((v >> 4) & 0x07F007F0u) | (v & 0x80008000u), two);
+            for (int i = 0; i < 5; ++i) {
+              uint32_t out[8];
+              widen(in[i], (e[i] + 120) * 0x00800080u, out);
+              sts128(to0 + (i0 + i) * kGroupBytes, *reinterpret_cast<uint32_t(*)[4]>(&out[0]));
+              sts128(to1 + (i0 + i) * kGroupBytes, *reinterpret_cast<uint32_t(*)[4]>(&out[4]));
             }
-            if (!plain) {
+          }
+        } else {
+          // 0 where no row sees the key, whatever was there; NaN for the
+          // exponent byte 255 (a byte of 0 is no exponent of cache_write); a
+          // second factor for large scales
+#pragma unroll 1
+          for (int i = 0; i < kTileKeys / 8; ++i) {
+            uint32_t in[4], out[8], e = lds8(exps + i * 8);
+            lds128(in, from + i * 1024);
+            if (key0 + row0 + 8 * i < g.lo || key0 + row0 + 8 * i >= g.hi) e = 0;
+            const uint32_t e1 = min(e, 134u), more = (e - e1 + 127) * 0x00800080u;
+            widen(in, e == 0 ? 0u : e == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u, out);
 #pragma unroll
-              for (int w = 0; w < 8; ++w) out[w] = bf16x2_mul(out[w], more);
-            }
-            const uint32_t to = dst + (row / 8) * kGroupBytes + (ch / 4) * kHalfBytes + (row % 8) * 128;
-            sts128(to + ((2 * ch % 8) ^ (row & 7)) * 16, *reinterpret_cast<uint32_t(*)[4]>(&out[0]));
-            sts128(to + (((2 * ch + 1) % 8) ^ (row & 7)) * 16, *reinterpret_cast<uint32_t(*)[4]>(&out[4]));
+            for (int w = 0; w < 8; ++w) out[w] = bf16x2_mul(out[w], more);
+            sts128(to0 + i * kGroupBytes, *reinterpret_cast<uint32_t(*)[4]>(&out[0]));
+            sts128(to1 + i * kGroupBytes, *reinterpret_cast<uint32_t(*)[4]>(&out[4]));
           }
         }
         fence_proxy_async_smem();  // read by the products
