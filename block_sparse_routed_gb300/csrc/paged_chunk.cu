@@ -711,7 +711,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                     : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows + 128 * t + row;
       float* part = ws.part + (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows * kHeadDim;  // (g.part >= 0)
       const float inv = (g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * whole;  // (NaN stays)
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         uint32_t o[32];
         tmem_ld32(o_col + 32 * b, o);
