@@ -64,6 +64,17 @@ __device__ __forceinline__ float exp_scale(uint32_t e) {
   return __uint_as_float(e == 255 ? 0x7FFFFFFFu : e << 23);
 }
 
+// Arrives on `bar` when this thread's cp.async so far have completed (counted
+// among the barrier's arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 16 bytes, or zeros when !real.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
 // Two E4M3 codes (the low 16 bits) as FP32 values.
 __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
   uint32_t h;

@@ -215,17 +215,15 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   scratch_of(ws, f, &scratch);
   CUtensorMap tk, tv;
   const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
-  const int elem = p->kind == SA_CACHE_BF16 ? 2 : 1;
   const int tile = f.few ? 64 : 80;  // keys
   bool maps;
-  if (f.few || elem == 1) {
-    // a box holds the keys of a page that fall into a tile of 64 keys, or 16 of the tiles of 80
-    const uint32_t box = f.few ? (p->page_size < 64 ? p->page_size : 64) : 16;
-    maps = make_map_rows(&tk, k_pages, cached, kHeadDim, elem, box) &&
-           make_map_rows(&tv, v_pages, cached, kHeadDim, elem, box);
-  } else {
-    maps = make_map_groups(&tk, k_pages, cached, 16) && make_map_groups(&tv, v_pages, cached, 16);
-  }
+  // a box holds the keys of a page that fall into a tile of 64 keys, or 16 of the tiles of 80
+  const uint32_t box = f.few ? (p->page_size < 64 ? p->page_size : 64) : 16;
+  if (p->kind == SA_CACHE_E4M3)
+    maps = make_map_rows(&tk, k_pages, cached, kHeadDim, 1, box) &&
+           make_map_rows(&tv, v_pages, cached, kHeadDim, 1, box);
+  else
+    maps = make_map_groups(&tk, k_pages, cached, box) && make_map_groups(&tv, v_pages, cached, box);
   if (!maps) return SA_ECUDA;
   // no more CTAs than units times the key tiles of the longest context that the table can hold
   const int64_t units = p->seqs + (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile;

@@ -161,12 +161,6 @@ __device__ __forceinline__ void bar_all() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 template <int kKind, int kN>  // kN: tiles of eight rows
 __global__ void __launch_bounds__(Cfg<kKind, kN>::kThreads, 2)
 paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -189,7 +183,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     *s_abort = 0;
     *s_bad = 0;
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(BAR_FULL + i), 1);
+      mbar_init(bar(BAR_FULL + i), kKind == 0 ? 1 : 9);  // TMA; 8 lanes' exponents
       mbar_init(bar(BAR_EMPTY + i), 4);
     }
     for (int i = 0; i < kSegs; ++i) {
@@ -216,7 +210,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     int stage = 0, seq = 0;
     const int per_page = min(c.page_size, kTileKeys);        // keys of a tile in one page
     const int tile_pages = kTileKeys / per_page;
-    const int sub = lane % 4, pg = lane / 4;                  // lane: page pg of the tile, box sub
+    const uint32_t elect = elect_one();
     for (int k = 0; ok; ++k) {
       const Segment g = walk_next(a, w, line, blockIdx.x, join);
       ok = k < kSegs ||
@@ -242,31 +236,46 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           bad |= wrong;
           if (wrong) entry = -1;
         }
-        const int first = max(page0, p_lo), last = min(page0 + tile_pages, p_hi);  // [first, last)
+        // lane i: row of the cache where the tile's i-th page begins (-1: not to be loaded)
+        const int at = page0 + lane;
+        const int page = __shfl_sync(0xFFFFFFFFu, entry, at % 32);
+        const bool mine = lane < tile_pages && at >= p_lo && at < p_hi && page >= 0;
+        const int row = mine ? static_cast<int>(((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) +
+                                                (key0 & (c.page_size - 1)))
+                             : -1;
+        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        int rows[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xFFFFFFFFu, row, i);
         ok = seq < C::kStages || __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_EMPTY + stage),
                                                                   ((seq / C::kStages) & 1) ^ 1, a.wait_limit));
         if (!ok) break;
-        const int at = page0 + pg;
-        const int page = __shfl_sync(0xFFFFFFFFu, entry, at % 32);
-        const bool mine = pg < tile_pages && at >= first && at < last && page >= 0;
-        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine && sub == 0));
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar(BAR_FULL + stage), loads * per_page * (2 * C::kRow + (kKind ? 2 : 0)));
-        __syncwarp();
-        if (mine) {
-          const int64_t row = ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (key0 & (c.page_size - 1));
-          const uint32_t to = sbase + stage * C::kStage + (sub / 2) * C::kHalf + pg * per_page * 128;
-          const CUtensorMap* map = sub / 2 ? &tm_v : &tm_k;
-          if constexpr (kKind == 0) {
-            tma_load_2d(to + (sub % 2) * (kTileKeys * 128), map, bar(BAR_FULL + stage), (sub % 2) * 64,
-                        static_cast<int>(row));
-          } else if (sub % 2 == 0) {
-            tma_load_2d(to, map, bar(BAR_FULL + stage), 0, static_cast<int>(row));
-          } else {
-            bulk_load(sbase + C::kOffExp + stage * C::kExp + (sub / 2) * kTileKeys + pg * per_page,
-                      (sub / 2 ? c.v_exp : c.k_exp) + row, per_page, bar(BAR_FULL + stage));
+        if constexpr (kKind != 0) {  // lanes 0-3, 4-7: 16 exponents each of K, of V
+          const int off = lane % 4 * 16;
+          const int from = __shfl_sync(0xFFFFFFFFu, row, off / per_page);
+          if (lane < 8) {
+            if (from >= 0)
+              cp_async16(sbase + C::kOffExp + stage * C::kExp + (lane / 4) * kTileKeys + off,
+                         (lane / 4 ? c.v_exp : c.k_exp) + from + off % per_page, true);
+            cp_async_arrive(bar(BAR_FULL + stage));
           }
         }
+        if (elect) {
+          mbar_arrive_expect_tx(bar(BAR_FULL + stage), loads * per_page * 2 * C::kRow);
+          const uint32_t to = sbase + stage * C::kStage;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (rows[i] < 0) continue;
+            if constexpr (kKind == 0) {
+              tma_load_4d(to + i * per_page * C::kRow, &tm_k, bar(BAR_FULL + stage), 0, 0, 0, rows[i] / 8);
+              tma_load_4d(to + C::kHalf + i * per_page * C::kRow, &tm_v, bar(BAR_FULL + stage), 0, 0, 0, rows[i] / 8);
+            } else {
+              tma_load_2d(to + i * per_page * C::kRow, &tm_k, bar(BAR_FULL + stage), 0, rows[i]);
+              tma_load_2d(to + C::kHalf + i * per_page * C::kRow, &tm_v, bar(BAR_FULL + stage), 0, rows[i]);
+            }
+          }
+        }
+        __syncwarp();
         ++seq;
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
         ok = !__any_sync(0xFFFFFFFFu, *s_abort != 0);
@@ -277,6 +286,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (!ok) {
       *s_abort = 1;
       // copies in flight land before the CTA ends (bounded)
+      if (kKind) asm volatile("cp.async.wait_all;" ::: "memory");
       for (int q = max(0, seq - C::kStages); q < seq; ++q)
         mbar_wait(bar(BAR_FULL + q % C::kStages), (q / C::kStages) & 1, kWaitLimitNs);
     }
@@ -302,7 +312,12 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int vrow = kKind == 0 ? 16 * quarter + (mat / 2) * 8 + mrow : krow;
     const int vchunk = kKind == 0 ? (mat & 1) : kchunk;
     auto chunk_at = [](int row, int chunk) -> uint32_t {
-      return row * 128 + (chunk / 8) * (kTileKeys * 128) + ((chunk % 8) ^ (row & 7)) * 16;
+      if (kKind == 0) return (row / 8) * 2048 + (chunk / 8) * 1024 + (row % 8) * 128 + ((chunk % 8) ^ (row & 7)) * 16;
+      return row * 128 + (chunk ^ (row & 7)) * 16;
+    };
+    // 128 bytes of a V row in a stage: of the second half of the dimensions if `half`
+    auto half_row = [](int row, int half) -> uint32_t {
+      return kKind == 0 ? (row / 8) * 2048 + half * 1024 + (row % 8) * 128 : row * 128;
     };
     bool ok = true;
     int tile = 0;  // tiles of the CTA so far
@@ -398,13 +413,9 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (ragged) {
           const int x = lane / 2;
           if (key0 + x < g.lo || key0 + x >= g.hi) {
-            uint8_t* v = base + stage * C::kStage + C::kHalf + (16 * quarter + x) * 128;
+            const uint32_t v = sv + half_row(16 * quarter + x, lane % 2) + (kKind == 0 ? 0 : (lane % 2) * 64);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              *reinterpret_cast<uint4*>(v + (lane % 2) * 64 + 16 * i) = make_uint4(0, 0, 0, 0);
-              if (kKind == 0)
-                *reinterpret_cast<uint4*>(v + kTileKeys * 128 + (lane % 2) * 64 + 16 * i) = make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < (kKind == 0 ? 8 : 4); ++i) sts_f4(v + 16 * i, make_float4(0.f, 0.f, 0.f, 0.f));
           }
           __syncwarp();
         }
@@ -449,7 +460,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // the product and added one by one.
         uint32_t odd_keys = 0;
         if (kKind == 0 && cut && g.n > 1) {
-          const uint32_t v = sv + (16 * quarter + lane / 2) * 128 + (lane % 2) * (kTileKeys * 128);
+          const uint32_t v = sv + half_row(16 * quarter + lane / 2, lane % 2);
           uint32_t m2 = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -527,7 +538,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (odd_keys) {
           __syncwarp();
           if ((odd_keys >> (lane & ~1)) & 1) {
-            const uint32_t v = sv + (16 * quarter + lane / 2) * 128 + (lane % 2) * (kTileKeys * 128);
+            const uint32_t v = sv + half_row(16 * quarter + lane / 2, lane % 2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sts_f4(v + 16 * i, make_float4(0.f, 0.f, 0.f, 0.f));
           }
@@ -567,16 +578,22 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
       ok = !bar_any<kWorkers>(!ok || *s_abort != 0);
       if (!ok) break;
-      if (threadIdx.x < kRows) {  // a row over all warps
+      if (warp == 0) {  // a row over all warps: 32 / kRows lanes share them
+        constexpr int kSteps = C::kConsumers * kRows / 32;
+        float2 ml[kSteps];
         float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < C::kConsumers; ++w) m = fmaxf(m, s_ml[w * kRows + threadIdx.x].x);
-#pragma unroll
-        for (int w = 0; w < C::kConsumers; ++w) {
-          const float2 ml = s_ml[w * kRows + threadIdx.x];
-          l += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - m);
+        for (int i = 0; i < kSteps; ++i) {
+          ml[i] = s_ml[i * 32 + lane];  // [warp][row]
+          m = fmaxf(m, ml[i].x);
         }
-        s_row[threadIdx.x] = make_float2(m, l);
+#pragma unroll
+        for (int d = kRows; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) l += ml[i].x == -INFINITY ? 0.f : ml[i].y * ex2_approx(ml[i].x - m);
+#pragma unroll
+        for (int d = kRows; d < 32; d *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        if (lane < kRows) s_row[lane] = make_float2(m, l);
       }
       bar_all<kWorkers>();
 #pragma unroll
@@ -592,7 +609,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // The outputs, in the accumulators' own order (a float4 of 16
         // dimensions j for each lane): warp after warp adds to its region.
         const uint32_t mine = sbase + C::kOffMerge + (warp % C::kRegions) * kRegionBytes + lane * 16;
-#pragma unroll
+#pragma unroll 1
         for (int gr = 0; gr < C::kConsumers / C::kRegions; ++gr) {
           if (warp / C::kRegions == gr) {
 #pragma unroll
