@@ -44,7 +44,7 @@ namespace {
 
 constexpr int kKeyShift = 6;  // 64 keys a stage
 constexpr int kTileKeys = 1 << kKeyShift;
-constexpr int kSegs = 4;      // steps described ahead
+constexpr uint32_t kQRow = 272;  // bytes of a row of Q in shared memory (256 and padding: other banks for each row)
 constexpr float kRescaleLog2 = 8.0f;
 // A unit's beginning (its Q) and end (joining the warps), in stages.
 constexpr int kOverBf16 = 2, kOverE4m3 = 3;
@@ -67,8 +67,11 @@ struct Cfg {
   static constexpr uint32_t kOffExp = kStages * kStage;
   static constexpr uint32_t kOffMerge = kOffExp + kStages * kExp;     // kRegions x 8 rows
   static constexpr int kRegions = 2;
-  static constexpr uint32_t kOffMl = kOffMerge + kRegions * kRegionBytes;  // [8 warps][16 rows] float2
-  static constexpr uint32_t kOffSeg = kOffMl + 1152;                  // kSegs x Segment
+  static constexpr int kSegs = kN == 1 ? 2 : 1;                       // steps described ahead, with their Q
+  static constexpr uint32_t kQBytes = 8 * kN * kQRow;
+  static constexpr uint32_t kOffQ = kOffMerge + kRegions * kRegionBytes;
+  static constexpr uint32_t kOffMl = kOffQ + kSegs * kQBytes;  // [8 warps][16 rows] float2, then by row
+  static constexpr uint32_t kOffSeg = kOffMl + 1024 + 16 * 24;        // kSegs x Segment
   static constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
   static constexpr uint32_t kOffMisc = kOffBar + 256;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -98,6 +101,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_b32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void sts_f4(uint32_t addr, float4 v) {
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(Cfg<kKind, kN>::kThreads, 2)
 paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const PagedAttnArgs a, const PagedScratch ws) {
   using C = Cfg<kKind, kN>;
-  constexpr int kRows = 8 * kN;
+  constexpr int kRows = 8 * kN, kSegs = C::kSegs;
   constexpr int kWorkers = 32 * C::kConsumers;
   const PagedArgs& c = a.c;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -187,12 +195,15 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       mbar_init(bar(BAR_EMPTY + i), 4);
     }
     for (int i = 0; i < kSegs; ++i) {
-      mbar_init(bar(BAR_SFULL + i), 1);
+      mbar_init(bar(BAR_SFULL + i), 33);  // the description; 32 lanes' copies of Q
       mbar_init(bar(BAR_SEMPTY + i), C::kConsumers);
     }
     fence_barrier_init();
   }
   __syncthreads();
+  // Token of a packed row: there are at most 16, so FP32 divides exactly.
+  const float inv_group = 1.0f / static_cast<float>(a.group);
+  auto div_group = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
 
   if (warp == C::kConsumers) {
     // ------------------------------------------------------------ producer
@@ -216,6 +227,18 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       ok = k < kSegs ||
            __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_SEMPTY + k % kSegs), ((k / kSegs) & 1) ^ 1, a.wait_limit));
       if (!ok) break;
+      if (g.valid) {  // (a unit is one row tile here: rho0 is 0)
+#pragma unroll
+        for (int x = 0; x < kRows / 2; ++x) {
+          const int row = 2 * x + lane / 16, i = div_group(row);
+          const uint16_t* src = a.q;
+          if (row < g.rows)
+            src += static_cast<int64_t>(g.row0 + i) * a.q_token +
+                   static_cast<int64_t>(g.h * a.group + row - i * a.group) * a.q_head + lane % 16 * 8;
+          cp_async16(sbase + C::kOffQ + k % kSegs * C::kQBytes + row * kQRow + lane % 16 * 16, src, row < g.rows);
+        }
+      }
+      cp_async_arrive(bar(BAR_SFULL + k % kSegs));
       if (lane == 0) {
         segs[k % kSegs] = g;
         mbar_arrive(bar(BAR_SFULL + k % kSegs));
@@ -299,10 +322,9 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int u = lane / 4, t4 = lane % 4;
     const int quarter = warp % 4, grp = warp / 4;  // 16 keys of the stages that are the group's
     float2* s_ml = reinterpret_cast<float2*>(base + C::kOffMl);  // [warp][row]: reference, sum
-    float2* s_row = s_ml + C::kConsumers * kRows;                  // [row]: of all warps
-    // Token of a packed row: there are at most 16, so FP32 divides exactly.
-    const float inv_group = 1.0f / static_cast<float>(a.group);
-    auto div_group = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
+    float2* s_row = s_ml + 8 * 16;                                  // [row]: of all warps
+    int64_t* s_at = reinterpret_cast<int64_t*>(s_row + 16);         // [row]: where its output goes
+    float* s_inv = reinterpret_cast<float*>(s_at + 16);             // [row]: its factor
     const float c2 = a.scale * 1.4426950408889634f;
     // ldmatrix rows: lane l gives row l % 8 of matrix l / 8.  K: (keys 0-7,
     // chunk i), (8-15, i), (0-7, i + 1), (8-15, i + 1); V the same in the
@@ -326,31 +348,21 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (!ok) break;
       const Segment g = segs[k % kSegs];
       if (!g.valid) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + k % kSegs));
       // Q as the second operand: row u of each tile, dimensions 2t, 2t + 1
       // and 2t + 8, 2t + 9 of 16 (4t .. 4t + 3 in the E4M3 kind)
       uint32_t qf[kN][8][2];
       float qinv[kN][2];  // E4M3: undoes the scaling of rows 2t, 2t + 1
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        const int rho = 8 * n + u;  // (a unit is one row tile here: rho0 is 0)
-        const bool real = rho < g.rows;
-        const int i = div_group(rho);
-        const uint16_t* src = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
-                              static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head;
+        const uint32_t src = sbase + C::kOffQ + k % kSegs * C::kQBytes + (8 * n + u) * kQRow;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          qf[n][kk][0] = qf[n][kk][1] = 0;
-          if (real) {
-            if constexpr (kKind == 0) {
-              qf[n][kk][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
-              qf[n][kk][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
-            } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
-              qf[n][kk][0] = v.x;
-              qf[n][kk][1] = v.y;
-            }
+          if constexpr (kKind == 0) {
+            qf[n][kk][0] = lds_b32(src + 32 * kk + 4 * t4);
+            qf[n][kk][1] = lds_b32(src + 32 * kk + 16 + 4 * t4);
+          } else {
+            qf[n][kk][0] = lds_b32(src + 32 * kk + 8 * t4);
+            qf[n][kk][1] = lds_b32(src + 32 * kk + 8 * t4 + 4);
           }
         }
         if constexpr (kKind != 0) {
@@ -374,6 +386,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           qinv[n][1] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t4 + 4);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + k % kSegs));
       // keys that this thread's rows 2t, 2t + 1 of each tile see
       int lo[kN][2], hi[kN][2];
 #pragma unroll
@@ -598,13 +612,22 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       bar_all<kWorkers>();
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        float m[2], l[2], f[2];  // rows 8n + 2t, 2t + 1
+        float f[2];  // rows 8n + 2t, 2t + 1
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 ml = s_row[8 * n + 2 * t4 + e];
-          m[e] = ml.x;
-          l[e] = ml.y;
-          f[e] = ref[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - m[e]);
+        for (int e = 0; e < 2; ++e)
+          f[e] = ref[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - s_row[8 * n + 2 * t4 + e].x);
+        // (the last warp's turn comes last: meanwhile, what concerns whole rows)
+        if (n == 0 && warp == C::kConsumers - 1 && lane < kRows) {
+          const float2 ml = s_row[lane];
+          const int i = div_group(lane);
+          const bool real = lane < g.rows;
+          const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + lane - i * a.group
+                                        : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + lane;
+          s_at[lane] = real ? at * kHeadDim : -1;
+          s_inv[lane] = g.part >= 0 ? 1.f : ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y);  // (NaN stays)
+          if (real && g.part >= 0) ws.ml[at] = ml;
+          if (real && g.part < 0 && a.lse)
+            a.lse[at] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
         }
         // The outputs, in the accumulators' own order (a float4 of 16
         // dimensions j for each lane): warp after warp adds to its region.
@@ -632,21 +655,11 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         // Each warp writes 8 / kConsumers of the 8 times 16 dimensions.
         int64_t at[2];
-        bool real[2];
         float inv[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = 8 * n + 2 * t4 + e, i = div_group(row);
-          real[e] = row < g.rows;
-          at[e] = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + row - i * a.group
-                             : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + row;
-          inv[e] = g.part >= 0 ? 1.f : l[e] > 0.f ? 1.f / l[e] : (l[e] == 0.f ? 0.f : l[e]);  // (NaN stays)
-          if (warp == 0 && u == 0 && real[e]) {
-            if (g.part >= 0)
-              ws.ml[at[e]] = make_float2(m[e], l[e]);
-            else if (a.lse)
-              a.lse[at[e]] = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * 0.6931471805599453f;
-          }
+          at[e] = s_at[8 * n + 2 * t4 + e];
+          inv[e] = s_inv[8 * n + 2 * t4 + e];
         }
 #pragma unroll
         for (int x = 0; x < 8 / C::kConsumers; ++x) {
@@ -663,8 +676,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           y.w *= inv[1];
           // two neighbouring dimensions of a row: d and d + 1
           auto put = [&](int e, int d, float lo, float hi) {
-            if (!(e ? real[1] : real[0])) return;
-            const int64_t to = (e ? at[1] : at[0]) * kHeadDim + d;
+            const int64_t to = (e ? at[1] : at[0]) + d;
+            if ((e ? at[1] : at[0]) < 0) return;  // no such row
             if (g.part < 0)
               *reinterpret_cast<uint32_t*>(a.o + to) = pack_bf16x2(lo, hi);
             else
