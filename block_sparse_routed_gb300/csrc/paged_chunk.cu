@@ -250,10 +250,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (kKind) mbar_init(bar(BAR_FULL + i), 2);  // the widening warps
       mbar_init(bar(BAR_EMPTY + i), i % 2 ? 1 : 2);  // K: both tiles' issuers; V: one issuer
     }
-    for (int i = 0; i < kStageSlots; ++i) {
-      mbar_init(bar(BAR_SGFULL + i), 1 + kBoxes);  // the codes' TMA, the exponents
-      mbar_init(bar(BAR_SGEMPTY + i), 2);
-    }
+    for (int i = 0; i < kStageSlots; ++i) mbar_init(bar(BAR_SGEMPTY + i), 2);
     for (int i = 0; i < kSegs; ++i) mbar_init(bar(BAR_SEGEMPTY + i), kKind ? 15 : 11);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(BAR_SREAD + t), 4);
@@ -349,22 +346,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const int b = buf;
           ok = q < kBufs || all_wait(kEmpty + b, round - 1);
           if (!ok) break;
-          if (kKind != 0 && lane < kBoxes) {  // the exponents, 16 bytes a box
-            if (mine)
-              cp_async16(sbase + C::kOffExp + b * kTileKeys + lane * kBoxKeys, (kv ? c.v_exp : c.k_exp) + row, true);
-            cp_async_arrive(bar(kFull + b));
-          }
           if (elect) {
-            mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 : 256));
+            mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 + 1 : 256));
 #pragma unroll
             for (int i = 0; i < kBoxes; ++i) {
               if (rows[i] < 0) continue;
-              if constexpr (kKind == 0)
+              if constexpr (kKind == 0) {
                 tma_load_4d(sbase + C::kOffRing + b * kSlotBytes + i * (kBoxKeys * 256), map, bar(kFull + b), 0, 0, 0,
                             rows[i] / 8);
-              else
+              } else {
                 tma_load_2d(sbase + C::kOffStage + b * kStageBytes + i * (kBoxKeys * 128), map, bar(kFull + b), 0,
                             rows[i]);
+                bulk_load(sbase + C::kOffExp + b * kTileKeys + i * kBoxKeys, (kv ? c.v_exp : c.k_exp) + rows[i], kBoxKeys,
+                          bar(kFull + b));
+              }
             }
           }
           __syncwarp();
@@ -381,7 +376,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (!ok) {
       *s_abort = 1;
       // copies in flight land before the CTA ends (bounded)
-      if (kKind) asm volatile("cp.async.wait_all;" ::: "memory");
       for (int x = max(0, q - kBufs); x < q; ++x) drain(kFull + x % kBufs, x / kBufs);
     }
     if (lane == 0) {

@@ -191,7 +191,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     *s_abort = 0;
     *s_bad = 0;
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bar(BAR_FULL + i), kKind == 0 ? 1 : 9);  // TMA; 8 lanes' exponents
+      mbar_init(bar(BAR_FULL + i), 1);
       mbar_init(bar(BAR_EMPTY + i), 4);
     }
     for (int i = 0; i < kSegs; ++i) {
@@ -273,18 +273,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         ok = seq < C::kStages || __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_EMPTY + stage),
                                                                   ((seq / C::kStages) & 1) ^ 1, a.wait_limit));
         if (!ok) break;
-        if constexpr (kKind != 0) {  // lanes 0-3, 4-7: 16 exponents each of K, of V
-          const int off = lane % 4 * 16;
-          const int from = __shfl_sync(0xFFFFFFFFu, row, off / per_page);
-          if (lane < 8) {
-            if (from >= 0)
-              cp_async16(sbase + C::kOffExp + stage * C::kExp + (lane / 4) * kTileKeys + off,
-                         (lane / 4 ? c.v_exp : c.k_exp) + from + off % per_page, true);
-            cp_async_arrive(bar(BAR_FULL + stage));
-          }
-        }
         if (elect) {
-          mbar_arrive_expect_tx(bar(BAR_FULL + stage), loads * per_page * 2 * C::kRow);
+          mbar_arrive_expect_tx(bar(BAR_FULL + stage), loads * per_page * (2 * C::kRow + (kKind ? 2 : 0)));
           const uint32_t to = sbase + stage * C::kStage;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -295,6 +285,10 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             } else {
               tma_load_2d(to + i * per_page * C::kRow, &tm_k, bar(BAR_FULL + stage), 0, rows[i]);
               tma_load_2d(to + C::kHalf + i * per_page * C::kRow, &tm_v, bar(BAR_FULL + stage), 0, rows[i]);
+              // (by the same lane: copies of eight lanes through their registers' path cost 8% of the call)
+              const uint32_t ex = sbase + C::kOffExp + stage * C::kExp + i * per_page;
+              bulk_load(ex, c.k_exp + rows[i], per_page, bar(BAR_FULL + stage));
+              bulk_load(ex + kTileKeys, c.v_exp + rows[i], per_page, bar(BAR_FULL + stage));
             }
           }
         }
@@ -309,7 +303,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (!ok) {
       *s_abort = 1;
       // copies in flight land before the CTA ends (bounded)
-      if (kKind) asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("cp.async.wait_all;" ::: "memory");
       for (int q = max(0, seq - C::kStages); q < seq; ++q)
         mbar_wait(bar(BAR_FULL + q % C::kStages), (q / C::kStages) & 1, kWaitLimitNs);
     }
