@@ -229,8 +229,10 @@ struct PagedScratch {
 };
 
 constexpr int kPagedFewRows = 16;   // most packed rows of the form for few rows
+constexpr int kPagedFewKeys = 64;   // keys of its tiles
 constexpr int kPagedFewCtas = 320;  // most CTAs of it (two an SM)
 constexpr int kPagedChunkRows = 256;  // packed rows of a unit of the form for chunks
+constexpr int kPagedChunkKeys = 80;   // keys of its tiles
 constexpr int kPagedChunkCtas = 160;
 
 struct PagedForm {
@@ -243,8 +245,13 @@ cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStrea
 cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
-cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
-                               const PagedScratch& ws, int ctas, cudaStream_t s);
+// K's and V's maps of the form for chunks, of BF16 pages: boxes of 16 (i + 1)
+// keys, as many as a page and a key tile can have in common.
+struct ChunkMaps {
+  CUtensorMap m[2][kPagedChunkKeys / 16];
+};
+cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScratch& ws, int ctas,
+                               cudaStream_t s);
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
 
 // Multiprocessors of the current device (cached).

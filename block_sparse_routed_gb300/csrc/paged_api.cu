@@ -213,17 +213,23 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   const PagedForm f = form_of(p);
   PagedScratch scratch;
   scratch_of(ws, f, &scratch);
-  CUtensorMap tk, tv;
   const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
-  const int tile = f.few ? 64 : 80;  // keys
-  bool maps;
-  // a box holds the keys of a page that fall into a tile of 64 keys, or 16 of the tiles of 80
-  const uint32_t box = f.few ? (p->page_size < 64 ? p->page_size : 64) : 16;
-  if (p->kind == SA_CACHE_E4M3)
-    maps = make_map_rows(&tk, k_pages, cached, kHeadDim, 1, box) &&
-           make_map_rows(&tv, v_pages, cached, kHeadDim, 1, box);
-  else
-    maps = make_map_groups(&tk, k_pages, cached, box) && make_map_groups(&tv, v_pages, cached, box);
+  const int tile = f.few ? kPagedFewKeys : kPagedChunkKeys;
+  CUtensorMap tk, tv;
+  ChunkMaps boxes{};
+  bool maps = true;
+  if (f.few) {  // a box holds the keys of a page that fall into a tile
+    const uint32_t box = p->page_size < tile ? p->page_size : tile;
+    if (p->kind == SA_CACHE_E4M3)
+      maps = make_map_rows(&tk, k_pages, cached, kHeadDim, 1, box) &&
+             make_map_rows(&tv, v_pages, cached, kHeadDim, 1, box);
+    else
+      maps = make_map_groups(&tk, k_pages, cached, box) && make_map_groups(&tv, v_pages, cached, box);
+  } else if (p->kind == SA_CACHE_BF16) {
+    for (int i = 0; 16 * i < tile && 16 * i < p->page_size; ++i)
+      maps = maps && make_map_groups(&boxes.m[0][i], k_pages, cached, 16 * (i + 1)) &&
+             make_map_groups(&boxes.m[1][i], v_pages, cached, 16 * (i + 1));
+  }
   if (!maps) return SA_ECUDA;
   // no more CTAs than units times the key tiles of the longest context that the table can hold
   const int64_t units = p->seqs + (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile;
@@ -232,7 +238,7 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   if (ctas > f.max_ctas) ctas = f.max_ctas;
   if (most < ctas) ctas = static_cast<int>(most);
   const cudaError_t e = f.few ? launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream)
-                              : launch_paged_chunk(tk, tv, a, scratch, ctas, stream);
+                              : launch_paged_chunk(boxes, a, scratch, ctas, stream);
   if (cuda_failed(e)) return SA_ECUDA;
   return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, stream)) ? SA_ECUDA : SA_OK;
 }

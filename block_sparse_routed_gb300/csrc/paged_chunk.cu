@@ -43,9 +43,9 @@
 namespace sa {
 namespace {
 
-constexpr int kTileKeys = 80;
-constexpr int kBoxKeys = 16;             // keys of a TMA box: divides pages and tiles
-constexpr int kBoxes = kTileKeys / kBoxKeys;
+constexpr int kTileKeys = kPagedChunkKeys;
+constexpr int kBoxKeys = 16;             // divides pages and tiles
+constexpr int kBoxes = kTileKeys / kBoxKeys;  // pages that a tile touches, at most
 constexpr int kUnitRows = kPagedChunkRows;
 // A K or V tile: for each 8 keys two blocks of 1 KB, [8 keys x 64 dimensions]
 // with 128-byte swizzle, one for each half of the dimensions.
@@ -225,8 +225,7 @@ __device__ __noinline__ void odd_add(uint32_t o_col, const uint16_t* q, const ui
 
 template <int kKind>
 __global__ void __launch_bounds__(Cfg<kKind>::kThreads, 1)
-paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const PagedAttnArgs a, const PagedScratch ws) {
+paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a, const PagedScratch ws) {
   using C = Cfg<kKind>;
   const PagedArgs& c = a.c;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -271,8 +270,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   // What is in flight completes before the CTA ends, whatever the limit.
   auto drain = [&](int b, int parity) { mbar_wait(bar(b), parity & 1, kWaitLimitNs); };
   // By a whole warp: one wait; two at once (parity < 0: only the first).  They
-  // also fail once another warp has given up.
-  auto all_wait = [&](int b, int parity) { return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0; };
+  // also fail once another warp has given up, which is looked at only by those
+  // that have to wait (whoever goes on without a wait soon needs one).
+  auto all_wait = [&](int b, int parity) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar(b), parity & 1))) return true;
+    return __all_sync(0xFFFFFFFFu, wait(b, parity) && *s_abort == 0) != 0;
+  };
   auto all_wait2 = [&](int b, int parity, int b2, int parity2) {
     const bool one = mbar_test_wait(bar(b), parity & 1), two = parity2 < 0 || mbar_test_wait(bar(b2), parity2 & 1);
     if (__all_sync(0xFFFFFFFFu, one && two)) return true;
@@ -280,7 +283,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   };
   // The next step's description; false when waiting failed.
   auto next_seg = [&](int k, Segment& g) -> bool {
-    if (!__all_sync(0xFFFFFFFFu, wait(BAR_SEGFULL + k % kSegs, k / kSegs))) return false;
+    if (!all_wait(BAR_SEGFULL + k % kSegs, k / kSegs)) return false;
     g = segs[k % kSegs];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(BAR_SEGEMPTY + k % kSegs));
@@ -293,10 +296,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   if (warp < 4) setmaxnreg_dec<C::kRegsControl>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
+    if (kKind == 0 && lane < 2 * min(kBoxes, c.page_size / kBoxKeys)) tma_prefetch_desc(&maps.m[lane % 2][lane / 2]);
     LineWalk w;
     bool bad = false;
     constexpr LineShape line = {kUnitRows, kTileKeys, kOver, kMinTiles};
@@ -307,9 +307,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t elect = elect_one();
     constexpr int kBufs = kKind ? kStageSlots : kSlots;
     constexpr int kFull = kKind ? BAR_SGFULL : BAR_FULL, kEmpty = kKind ? BAR_SGEMPTY : BAR_EMPTY;
+    auto next_buf = [&] {
+      ++q;
+      if (++buf == kBufs) {
+        buf = 0;
+        ++round;
+      }
+    };
     for (int k = 0; ok; ++k) {
       const Segment g = walk_next(a, w, line, blockIdx.x, join);
-      ok = k < kSegs || __all_sync(0xFFFFFFFFu, wait(BAR_SEGEMPTY + k % kSegs, k / kSegs - 1));
+      ok = k < kSegs || all_wait(BAR_SEGEMPTY + k % kSegs, k / kSegs - 1);
       if (!ok) break;
       if (lane == 0) {
         segs[k % kSegs] = g;
@@ -329,47 +336,65 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           bad |= wrong;
           if (wrong) entry = -1;
         }
-        // lane i < 5: row of the cache where the i-th 16 keys begin (-1: not to be loaded)
-        const int key = t * kTileKeys + lane * kBoxKeys, at = key >> c.page_shift;
-        const int page = __shfl_sync(0xFFFFFFFFu, entry, (at - have) & 31);
-        const bool mine = lane < kBoxes && at >= p_lo && at < p_hi && page >= 0;
-        const int row = mine ? static_cast<int>(((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) +
-                                                (key & (c.page_size - 1)))
-                             : -1;
-        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        int rows[kBoxes];
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i) rows[i] = __shfl_sync(0xFFFFFFFFu, row, i);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const CUtensorMap* map = kv ? &tm_v : &tm_k;
-          const int b = buf;
-          ok = q < kBufs || all_wait(kEmpty + b, round - 1);
-          if (!ok) break;
-          if (elect) {
-            mbar_arrive_expect_tx(bar(kFull + b), loads * kBoxKeys * (kKind ? 128 + 1 : 256));
-#pragma unroll
-            for (int i = 0; i < kBoxes; ++i) {
-              if (rows[i] < 0) continue;
-              if constexpr (kKind == 0) {
-                tma_load_4d(sbase + C::kOffRing + b * kSlotBytes + i * (kBoxKeys * 256), map, bar(kFull + b), 0, 0, 0,
-                            rows[i] / 8);
-              } else {
-                tma_load_2d(sbase + C::kOffStage + b * kStageBytes + i * (kBoxKeys * 128), map, bar(kFull + b), 0,
-                            rows[i]);
-                bulk_load(sbase + C::kOffExp + b * kTileKeys + i * kBoxKeys, (kv ? c.v_exp : c.k_exp) + rows[i], kBoxKeys,
-                          bar(kFull + b));
-              }
-            }
+        // Keys n of the cache from row r on, to the tile's place `first`.
+        auto load = [&](int kv, int b, uint32_t r, int first, int n) {
+          if constexpr (kKind == 0) {
+            tma_load_4d(sbase + C::kOffRing + b * kSlotBytes + first * 256, &maps.m[kv][n / kBoxKeys - 1],
+                        bar(kFull + b), 0, 0, 0, r / 8);
+          } else {
+            bulk_load(sbase + C::kOffStage + b * kStageBytes + first * 128,
+                      (kv ? c.v_pages : c.k_pages) + static_cast<uint64_t>(r) * 128, n * 128, bar(kFull + b));
+            bulk_load(sbase + C::kOffExp + b * kTileKeys + first, (kv ? c.v_exp : c.k_exp) + r, n, bar(kFull + b));
           }
-          __syncwarp();
-          ++q;
-          if (++buf == kBufs) {
-            buf = 0;
-            ++round;
+        };
+        const int key0 = t * kTileKeys;
+        if (c.page_shift >= 6) {
+          // at most two pages
+          const int key1 = page1 << c.page_shift, n0 = page0 == page1 ? kTileKeys : key1 - key0;
+          const int e0 = __shfl_sync(0xFFFFFFFFu, entry, (page0 - have) & 31);
+          const int e1 = __shfl_sync(0xFFFFFFFFu, entry, (page1 - have) & 31);
+          const bool on0 = page0 >= p_lo && e0 >= 0, on1 = n0 < kTileKeys && page1 < p_hi && e1 >= 0;
+          const uint32_t r0 = ((static_cast<uint32_t>(e0) * c.H + g.h) << c.page_shift) + (key0 & (c.page_size - 1));
+          const uint32_t r1 = (static_cast<uint32_t>(e1) * c.H + g.h) << c.page_shift;
+          const int all = (on0 ? n0 : 0) + (on1 ? kTileKeys - n0 : 0);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = q < kBufs || all_wait(kEmpty + buf, round - 1);
+            if (!ok) break;
+            if (elect) {
+              mbar_arrive_expect_tx(bar(kFull + buf), all * (kKind ? 128 + 1 : 256));
+              if (on0) load(kv, buf, r0, 0, n0);
+              if (on1) load(kv, buf, r1, n0, kTileKeys - n0);
+            }
+            __syncwarp();
+            next_buf();
+          }
+        } else {
+          // lane i < 5: row of the cache where the i-th 16 keys begin (-1: not to be loaded)
+          const int key = key0 + lane * kBoxKeys, at = key >> c.page_shift;
+          const int page = __shfl_sync(0xFFFFFFFFu, entry, (at - have) & 31);
+          const bool mine = lane < kBoxes && at >= p_lo && at < p_hi && page >= 0;
+          const int row = mine ? static_cast<int>(((static_cast<uint32_t>(page) * c.H + g.h) << c.page_shift) +
+                                                  (key & (c.page_size - 1)))
+                               : -1;
+          const int loads = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+          int rows[kBoxes];
+#pragma unroll
+          for (int i = 0; i < kBoxes; ++i) rows[i] = __shfl_sync(0xFFFFFFFFu, row, i);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = q < kBufs || all_wait(kEmpty + buf, round - 1);
+            if (!ok) break;
+            if (elect) {
+              mbar_arrive_expect_tx(bar(kFull + buf), loads * kBoxKeys * (kKind ? 128 + 1 : 256));
+#pragma unroll
+              for (int i = 0; i < kBoxes; ++i)
+                if (rows[i] >= 0) load(kv, buf, rows[i], i * kBoxKeys, kBoxKeys);
+            }
+            __syncwarp();
+            next_buf();
           }
         }
-        if (__any_sync(0xFFFFFFFFu, *s_abort != 0)) ok = false;
       }
     }
     bad = __any_sync(0xFFFFFFFFu, bad);
@@ -677,7 +702,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_PFULL + t));
-        return !__any_sync(0xFFFFFFFFu, *s_abort != 0);
+        return true;
       };
 #pragma unroll 1
       for (int j = 0; j < g.nt && ok; ++j) {
@@ -687,7 +712,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       // ---- the unit's output, or this step's part of it (the widened codes of
       // four dimensions lie in the order 0, 2, 1, 3)
       auto dim = [](int d) constexpr { return kKind == 0 || d % 4 == 0 || d % 4 == 3 ? d : d % 4 == 1 ? d + 1 : d - 1; };
-      ok = ok && __all_sync(0xFFFFFFFFu, wait(BAR_PVDONE + t, y + g.nt - 1));
+      ok = ok && all_wait(BAR_PVDONE + t, y + g.nt - 1);
       if (!ok) break;
       tc_fence_after();
       const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + (rho - i * a.group)
@@ -747,9 +772,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (!ok || !g.valid) break;
       for (int j = 0; j < g.nt; ++j, q += 2) {
         const int b = q % kStageSlots, slot = q % kSlots;
-        ok = __all_sync(0xFFFFFFFFu, wait(BAR_SGFULL + b, q / kStageSlots));
-        if (ok && q >= kSlots) ok = __all_sync(0xFFFFFFFFu, wait(BAR_EMPTY + slot, q / kSlots - 1));
-        if (ok) ok = !__any_sync(0xFFFFFFFFu, *s_abort != 0);
+        ok = all_wait2(BAR_SGFULL + b, q / kStageSlots, BAR_EMPTY + slot, q >= kSlots ? q / kSlots - 1 : -1);
         if (!ok) break;
         const int key0 = (g.t0 + j) * kTileKeys;
         const uint32_t src = sbase + C::kOffStage + b * kStageBytes, dst = sbase + C::kOffRing + slot * kSlotBytes;
@@ -774,7 +797,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           }
           __syncwarp();
         }
-        const uint32_t from = src + row0 * 128 + (ch ^ row0) * 16, exps = sbase + C::kOffExp + b * kTileKeys + row0;
+        const uint32_t from = src + row0 * 128 + ch * 16, exps = sbase + C::kOffExp + b * kTileKeys + row0;
         const uint32_t to0 = dst + (ch / 4) * kHalfBytes + row0 * 128 + ((2 * ch % 8) ^ row0) * 16;
         const uint32_t to1 = dst + (ch / 4) * kHalfBytes + row0 * 128 + (((2 * ch + 1) % 8) ^ row0) * 16;
         // Codes land as the value times 2^-120; one factor then, of 2^120 and
@@ -844,8 +867,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 }
 
 template <int kKind>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, const PagedScratch& ws,
-                   int ctas, cudaStream_t s) {
+cudaError_t launch(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScratch& ws, int ctas, cudaStream_t s) {
   using C = Cfg<kKind>;
   auto* kern = paged_chunk_kernel<kKind>;
   static SmemOnce once;
@@ -862,15 +884,15 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn
   }
   const int split = C::kRegsControl + 2 * C::kRegsSoftmax + (kKind ? C::kRegsConvert : 0);
   if (regs * (C::kThreads / 128) < split) return cudaErrorInvalidConfiguration;
-  kern<<<ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a, ws);
+  kern<<<ctas, C::kThreads, C::kSmem, s>>>(maps, a, ws);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_chunk(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
-                               const PagedScratch& ws, int ctas, cudaStream_t s) {
-  return a.c.kind == 0 ? launch<0>(tk, tv, a, ws, ctas, s) : launch<1>(tk, tv, a, ws, ctas, s);
+cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScratch& ws, int ctas,
+                               cudaStream_t s) {
+  return a.c.kind == 0 ? launch<0>(maps, a, ws, ctas, s) : launch<1>(maps, a, ws, ctas, s);
 }
 
 }  // namespace sa

@@ -43,7 +43,8 @@ namespace sa {
 namespace {
 
 constexpr int kKeyShift = 6;  // 64 keys a stage
-constexpr int kTileKeys = 1 << kKeyShift;
+constexpr int kTileKeys = kPagedFewKeys;
+static_assert(kTileKeys == 1 << kKeyShift, "");
 constexpr uint32_t kQRow = 272;  // bytes of a row of Q in shared memory (256 and padding: other banks for each row)
 constexpr float kRescaleLog2 = 8.0f;
 // A unit's beginning (its Q) and end (joining the warps), in stages.
