@@ -102,20 +102,26 @@ __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
 // there is none, so that every unit writes its rows).  All key tiles of all
 // units, in the order (sequence, head, row tile, key tile), are one line that
 // is cut into equal parts, one a CTA: every CTA streams the same number of
-// keys however ragged the batch is.  A unit's beginning and end cost time too:
-// in front of its key tiles the line has `over` places without one.  A unit
-// that a cut divides is joined from its parts by the joining kernel.
+// however ragged the batch is.  A unit's beginning and end cost time too:
+// in front of its key tiles the line has `over` places without one.  Nor does
+// a key tile cost the same under few rows as under many: it has `half` places
+// in units that fill at most half of the row tile, else `full`, and belongs to
+// the CTA that has the first of them.  A unit that a cut divides is joined
+// from its parts by the joining kernel.
 
 struct LineShape {
-  int row_tile;   // packed rows of a unit
-  int key_tile;   // keys of a tile
-  int over;       // places of a unit without a key tile
-  int min_tiles;  // places of a CTA at least, while there are any
+  int row_tile;    // packed rows of a unit
+  int key_tile;    // keys of a tile
+  int half, full;  // places of a key tile
+  int over;        // places of a unit without a key tile
+  int min_places;  // of a CTA at least (>= full), while there are any
 };
 
 struct UnitKeys {
   int lo, hi;  // keys that some row of the unit sees: [lo, hi)
   int t0, nt;  // key tiles
+  int each;    // places of one
+  int places;  // of the unit
 };
 
 // First key that the row at position pos sees.
@@ -142,6 +148,8 @@ __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const Page
   if (u.hi <= u.lo) u.lo = u.hi = 0;
   u.t0 = u.lo / static_cast<uint32_t>(key_tile);
   u.nt = max(1, static_cast<int>((u.hi + static_cast<uint32_t>(key_tile) - 1) / static_cast<uint32_t>(key_tile)) - u.t0);
+  u.each = line.half == line.full || rows - p * row_tile > row_tile / 2 ? line.full : line.half;
+  u.places = u.nt * u.each + line.over;
   return u;
 }
 
@@ -180,7 +188,7 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
   const int tiles = row_tiles(a, q, line.row_tile);
   int64_t t = 0;
   if (tiles <= 4)
-    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, line).nt + line.over;
+    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, line).places;
   unsigned many = __ballot_sync(0xFFFFFFFFu, tiles > 4);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -191,7 +199,7 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
     r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
     const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
     int64_t y = 0;
-    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, line).nt + line.over;
+    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, line).places;
     y = warp_sum(y);
     if (lane == src) t = y;
   }
@@ -237,7 +245,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
     if (base == 0) first = t;
   }
   w.total = warp_sum(t) * a.c.H;
-  const int64_t most = (w.total + line.min_tiles - 1) / line.min_tiles;
+  const int64_t most = (w.total + line.min_places - 1) / line.min_places;
   w.ctas = static_cast<int>(min(static_cast<int64_t>(ctas), most));
   // (a part without tiles must not lie between two of one unit)
   w.at = w.end = 0;
@@ -269,7 +277,7 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
     return;
   }
   for (int p0 = 0;; p0 += 32) {
-    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, line).nt + line.over : 0;
+    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, line).places : 0;
     const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
@@ -298,9 +306,10 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
       }
     }
     const UnitKeys u = unit_keys(a, w.q, w.p, line);
-    const int places = u.nt + line.over;
-    const int take = static_cast<int>(min(static_cast<int64_t>(places - w.skip), w.end - w.at));
-    const int from = max(0, w.skip - line.over), to = max(0, w.skip + take - line.over);  // key tiles
+    const int take = static_cast<int>(min(static_cast<int64_t>(u.places - w.skip), w.end - w.at));
+    // key tiles whose first place is among [skip, skip + take)
+    const auto tiles_before = [&](int place) { return (max(0, place - line.over) + u.each - 1) / u.each; };
+    const int from = tiles_before(w.skip), to = tiles_before(w.skip + take);
     if (to > from) {
       g.valid = 1;
       g.row0 = w.q.row0;
@@ -319,8 +328,8 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
       g.nt = to - from;
       g.part = from == 0 ? (to == u.nt ? -1 : 1) : 0;
       if (g.part == 1) {
-        // the CTA that holds the unit's last tile
-        const int owner = static_cast<int>(muldiv((w.at - w.skip + places) * w.ctas - 1, 1, w.total));
+        // the CTA that holds the first place of the unit's last tile
+        const int owner = static_cast<int>(muldiv((w.at - w.skip + u.places - u.each + 1) * w.ctas - 1, 1, w.total));
         join.pieces = owner - cta + 1;
         join.row0 = g.row0;
         join.rho0 = g.rho0;

@@ -34,7 +34,6 @@
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
 // tile t in [256 + 128 t, + 80), P in the 40 columns behind it.
 #include <cstdint>
-#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -56,7 +55,6 @@ constexpr int kSegs = 2;
 constexpr int kStageSlots = 4;           // staged code tiles (E4M3): [80 keys x 128 B]
 constexpr uint32_t kStageBytes = kTileKeys * 128;
 constexpr float kRescaleLog2 = 32.0f;
-constexpr int kOver = 2;                 // a unit's beginning and end, in key tiles
 constexpr int kMinTiles = 6;             // key tiles of a CTA at least, while there are any
 
 template <int kKind>
@@ -70,6 +68,10 @@ struct Cfg {
   static constexpr uint32_t kRegsConvert = 88;
   static_assert(kRegsControl + 2 * kRegsSoftmax + (kKind ? kRegsConvert : 0) <= (kThreads / 128) * kRegsLaunch, "");
   static constexpr int kSlots = kKind == 0 ? 8 : 6;  // K, V, K, V, ...
+  // The line's places (paged.cuh): what a key tile costs under one row tile
+  // and under two, and a unit's beginning, edges and end.
+  static constexpr int kHalfPlaces = kKind == 0 ? 3 : 4, kFullPlaces = 4;
+  static constexpr int kOver = 6 * kFullPlaces;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffRing = 2 * kQBytes;
   static constexpr uint32_t kOffStage = kOffRing + kSlots * kSlotBytes;
@@ -94,9 +96,9 @@ enum {
   BAR_SREAD = 34,   // the softmax has S in registers
   BAR_PFULL = 36,
   BAR_PVDONE = 38,
-  BAR_VREADY = 42,  // +tile: V of a tile at the mask's edge has landed
-  BAR_DRAIN = 44,   // +issuer (3): products in flight have completed (abort)
-  NUM_BARS = 47
+  BAR_VREADY = 42,  // +2 tile, + every other one: V of a tile at the mask's edge is ready
+  BAR_DRAIN = 46,   // +issuer (3): products in flight have completed (abort)
+  NUM_BARS = 49
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -299,7 +301,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     if (kKind == 0 && lane < 2 * min(kBoxes, c.page_size / kBoxKeys)) tma_prefetch_desc(&maps.m[lane % 2][lane / 2]);
     LineWalk w;
     bool bad = false;
-    constexpr LineShape line = {kUnitRows, kTileKeys, kOver, kMinTiles};
+    constexpr LineShape line = {kUnitRows, kTileKeys, C::kHalfPlaces, C::kFullPlaces, C::kOver, kMinTiles * C::kFullPlaces};
     walk_begin(a, w, line, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
@@ -416,9 +418,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     auto kmaj_off = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4); };
     const uint64_t q_base = sdesc_sw128(sbase + C::kOffQ + t * kQBytes, 16, 1024);
     const uint32_t elect = elect_one();
-    const int chunk = lane % 16;  // 16 bytes of a row of Q
-    int slot = 0, phase = 0;      // K's slot of the next key tile, and its phase
-    int y = 0;                    // key tiles of this row tile so far
+    const int q_row = lane / 16, q_chunk = lane % 16;  // 16 bytes of Q's rows q_row, q_row + 2, ..
+    const uint32_t q_to = sbase + C::kOffQ + t * kQBytes + (q_chunk / 8) * 16384;
+    int slot = 0, phase = 0;  // K's slot of the next key tile, and its phase
+    int y = 0;                // key tiles of this row tile so far
     bool issued = false;
     for (int k = 0; ok; ++k) {
       Segment g;
@@ -428,38 +431,39 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       if (rows) {
         // Q: rows past the last are zeros.  The last unit's last S, the last
         // reader of the tile's Q, has completed when its barrier says so.
+        // (What follows takes as long as the last unit's softmax and output.)
         ok = y == 0 || all_wait(BAR_SFULL + t, y - 1);
         if (!ok) break;
-        const uint32_t to = sbase + C::kOffQ + t * kQBytes + (chunk / 8) * 16384;
-        const int rho = g.rho0 + 128 * t + lane / 16;
+        const int rho = g.rho0 + 128 * t + q_row, left = g.rows - 128 * t;
         int i = rho / a.group, e = rho - i * a.group;
-        const int real = g.rho0 + g.rows - rho;  // rows 0, 2, .. below this are
-        int64_t at = static_cast<int64_t>(g.row0 + i) * a.q_token + static_cast<int64_t>(g.h * a.group + e) * a.q_head +
-                     chunk * 8;
+        const uint16_t* src = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
+                              static_cast<int64_t>(g.h * a.group + e) * a.q_head + q_chunk * 8;
+        const int i2 = 2 / a.group, e2 = 2 - i2 * a.group;  // two rows on: tokens and heads
+        const int64_t step = i2 * a.q_token + e2 * a.q_head, wrap = a.q_token - a.group * a.q_head;
+        auto at = [&](int r) { return q_to + r * 128 + ((q_chunk ^ r) & 7) * 16; };
 #pragma unroll 4
-        for (int r = 0; r < 128; r += 2) {
-          const int row = r + lane / 16;
-          cp_async16(to + row * 128 + ((chunk % 8) ^ (row & 7)) * 16, r < real ? a.q + at : a.q, r < real);
-          e += 2;
-          at += 2 * a.q_head;
-          while (e >= a.group) {
+        for (int r = q_row; r < 128; r += 2) {
+          const bool is = r < left;
+          cp_async16(at(r), is ? src : a.q, is);
+          src += step;
+          e += e2;
+          if (e >= a.group) {
             e -= a.group;
-            at += a.q_token - a.group * a.q_head;
+            src += wrap;
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (kKind != 0) {  // K's order of dimensions (each lane its own 16 bytes)
+        if constexpr (kKind != 0) {  // the order of dimensions that K gets (each lane its own 16 bytes)
 #pragma unroll 8
-          for (int r = 0; r < 128; r += 2) {
-            const int row = r + lane / 16;
+          for (int r = q_row; r < 128; r += 2) {
             uint32_t v[4], z[4];
-            lds128(v, to + row * 128 + ((chunk % 8) ^ (row & 7)) * 16);
+            lds128(v, at(r));
 #pragma unroll
             for (int w = 0; w < 4; w += 2) {
               z[w] = __byte_perm(v[w], v[w + 1], 0x5410);
               z[w + 1] = __byte_perm(v[w], v[w + 1], 0x7632);
             }
-            sts128(to + row * 128 + ((chunk % 8) ^ (row & 7)) * 16, z);
+            sts128(at(r), z);
           }
         }
         fence_proxy_async_smem();
@@ -506,24 +510,33 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     auto vmaj_off = [](int kk) { return static_cast<uint64_t>((kk * 2 * kGroupBytes) >> 4); };
     const uint32_t elect = elect_one();
     int slot = 1, phase = 0;
-    int y0 = 0, y1 = 0;  // key tiles of row tile 0 and 1
+    int y0 = 0, y1 = 0;          // key tiles of row tile 0 and 1
+    int edges0 = 0, edges1 = 0;  // those of them at the mask's edge
     bool issued = false;
     for (int k = 0; ok; ++k) {
       Segment g;
       ok = next_seg(k, g);
       if (!ok || !g.valid) break;
       const int tiles = g.rows > 128 ? 2 : 1;
+      // V at the mask's edge (see the softmax), a tile ahead of its product
+      auto prepare = [&](int j, int at, int parity) -> bool {
+        const int key0 = (g.t0 + j) * kTileKeys;
+        if (key0 >= g.all_lo && key0 + kTileKeys <= g.all_hi) return true;
+        if (!all_wait(BAR_FULL + at, parity)) return false;
+        if constexpr (kKind == 0)
+          edge_values(sbase + C::kOffRing + at * kSlotBytes, g.lo - key0, g.hi - key0, &s_odd[6 * at], lane);
+        if (lane < tiles) mbar_arrive(bar(BAR_VREADY + 2 * lane + ((lane ? edges1 : edges0) & 1)));
+        ++edges0;
+        if (tiles == 2) ++edges1;
+        return true;
+      };
+      ok = prepare(0, slot, phase);
 #pragma unroll 1
       for (int j = 0; j < g.nt && ok; ++j) {
+        const int slot2 = slot + 2 > kSlots ? 1 : slot + 2, phase2 = slot + 2 > kSlots ? phase ^ 1 : phase;
+        ok = j + 1 == g.nt || prepare(j + 1, slot2, phase2);
+        if (!ok) break;
         const uint64_t vs = sdesc_sw128(sbase + C::kOffRing + slot * kSlotBytes, kHalfBytes, kGroupBytes);
-        const int key0 = (g.t0 + j) * kTileKeys;
-        if (key0 < g.all_lo || key0 + kTileKeys > g.all_hi) {  // (see the softmax)
-          ok = all_wait(BAR_FULL + slot, phase);
-          if (!ok) break;
-          if constexpr (kKind == 0)
-            edge_values(sbase + C::kOffRing + slot * kSlotBytes, g.lo - key0, g.hi - key0, &s_odd[6 * slot], lane);
-          if (lane < tiles) mbar_arrive(bar(BAR_VREADY + lane));
-        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= tiles) break;
@@ -541,11 +554,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
           __syncwarp();
           issued = true;
         }
-        slot += 2;
-        if (slot > kSlots) {
-          slot = 1;
-          phase ^= 1;
-        }
+        slot = slot2;
+        phase = phase2;
       }
       y0 += g.nt;
       if (tiles == 2) y1 += g.nt;
@@ -590,13 +600,30 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         for (int b = 0; b < 128; b += 32) tmem_st32(o_col + b, zero);
       }
       // One key tile; false when a wait gave up.  edge: some row of the unit
-      // does not see some key of it.  (Two copies of the code: the tiles that
-      // every row sees whole are most of them.)
-      auto tile = [&](auto edge, int j) -> bool {
-        constexpr bool kEdge = decltype(edge)::value;
+      // does not see some key of it.
+      auto tile = [&](bool edge, int j) -> bool {
         if (!all_wait(BAR_SFULL + t, y + j)) return false;
         tc_fence_after();
         const int key0 = (g.t0 + j) * kTileKeys;
+        if (edge) {
+          // masked in place: what most tiles skip stays small and takes no
+          // registers from the rest (a second copy of the code, with the mask
+          // in it, cost more than it saved: it was never in the instruction cache)
+#pragma unroll 1
+          for (int b = 0; b < kTileKeys; b += 16) {
+            const int from = lo - key0 - b, to = hi - key0 - b;
+            if (__all_sync(0xFFFFFFFFu, from <= 0 && to >= 16)) continue;
+            uint32_t z[16];
+            tmem_ld16(s_col + b, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < from || e >= to) z[e] = __float_as_uint(-INFINITY);
+            tmem_st8(s_col + b, *reinterpret_cast<uint32_t(*)[8]>(&z[0]));
+            tmem_st8(s_col + b + 8, *reinterpret_cast<uint32_t(*)[8]>(&z[8]));
+          }
+          tmem_wait_st();
+        }
         uint32_t s[kTileKeys];
         tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
         tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -605,16 +632,6 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_SREAD + t));
-        if constexpr (kEdge) {  // a bit for each key that the row sees
-#pragma unroll
-          for (int w = 0; w < 3; ++w) {
-            const int a0 = min(max(lo - key0 - 32 * w, 0), 32), a1 = min(max(hi - key0 - 32 * w, 0), 32);
-            const uint32_t seen = (a1 == 32 ? ~0u : (1u << a1) - 1u) & ~(a0 == 32 ? ~0u : (1u << a0) - 1u);
-#pragma unroll
-            for (int b = 0; b < 32; ++b)
-              if (32 * w + b < kTileKeys && !(seen & (1u << b))) s[32 * w + b] = __float_as_uint(-INFINITY);
-          }
-        }
         // The reference follows the row's maximum only when that has passed it
         // by 2^32 (p <= 2^32 leaves FP32 room): O is seldom rescaled.
         const float mx = max80(s) * c2;  // (scale > 0)
@@ -660,7 +677,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         }
         tmem_st32(p_col, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
         tmem_st8(p_col + 32, *reinterpret_cast<uint32_t(*)[8]>(&p[32]));
-        if constexpr (kEdge) {
+        if (edge) {
           // At the mask's edge a key of the tile may be hidden from a row that
           // its probability 0 would still multiply with what V holds, and
           // 0 * NaN is not 0.  Slots that no row sees may hold anything; keys
@@ -668,7 +685,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
           // an infinity.  The PV warp (in the E4M3 kind the widening warps)
           // has made zeros of both; the tokens among them, a bit each in
           // s_odd, are added here one by one.
-          if (!all_wait(BAR_VREADY + t, edges++)) return false;
+          if (!all_wait(BAR_VREADY + 2 * t + (edges & 1), edges / 2)) return false;
+          ++edges;
           const int slot = (2 * (x + j) + 1) % kSlots;
           uint32_t odd[3];
 #pragma unroll
@@ -707,7 +725,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
 #pragma unroll 1
       for (int j = 0; j < g.nt && ok; ++j) {
         const int key0 = (g.t0 + j) * kTileKeys;
-        ok = key0 < g.all_lo || key0 + kTileKeys > g.all_hi ? tile(std::true_type(), j) : tile(std::false_type(), j);
+        ok = tile(key0 < g.all_lo || key0 + kTileKeys > g.all_hi, j);
       }
       // ---- the unit's output, or this step's part of it (the widened codes of
       // four dimensions lie in the order 0, 2, 1, 3)

@@ -214,7 +214,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     LineWalk w;
     bool bad = false;
-    constexpr LineShape line = {kRows, kTileKeys, kKind == 0 ? kOverBf16 : kOverE4m3, 1};
+    constexpr LineShape line = {kRows, kTileKeys, 1, 1, kKind == 0 ? kOverBf16 : kOverE4m3, 1};
     walk_begin(a, w, line, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
