@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr uint32_t kQBytes = 8 * kN * kQRow;
   static constexpr uint32_t kOffQ = kOffMerge + kRegions * kRegionBytes;
   static constexpr uint32_t kOffMl = kOffQ + kSegs * kQBytes;  // [8 warps][16 rows] float2, then by row
-  static constexpr uint32_t kOffSeg = kOffMl + 1024 + 16 * 24;        // kSegs x Segment
+  static constexpr uint32_t kOffSeg = kOffMl + 1024 + 16 * 24 + 64;       // kSegs x Segment
   static constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
   static constexpr uint32_t kOffMisc = kOffBar + 256;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -108,6 +108,9 @@ __device__ __forceinline__ uint32_t lds_b32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void sts_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void sts_f4(uint32_t addr, float4 v) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
@@ -320,6 +323,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     float2* s_row = s_ml + 8 * 16;                                  // [row]: of all warps
     int64_t* s_at = reinterpret_cast<int64_t*>(s_row + 16);         // [row]: where its output goes
     float* s_inv = reinterpret_cast<float*>(s_at + 16);             // [row]: its factor
+    float* s_qinv = s_inv + 16;                                     // [row]: 2^-e of its Q
     const float c2 = a.scale * 1.4426950408889634f;
     // ldmatrix rows: lane l gives row l % 8 of matrix l / 8.  K: (keys 0-7,
     // chunk i), (8-15, i), (0-7, i + 1), (8-15, i + 1); V the same in the
@@ -343,42 +347,47 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (!ok) break;
       const Segment g = segs[k % kSegs];
       if (!g.valid) break;
+      const uint32_t q_rows = sbase + C::kOffQ + k % kSegs * C::kQBytes;
+      if constexpr (kKind != 0) {
+        // Q in FP16, in place, a warp a row: a lane has dimensions 4 lane ..
+        // of it, and within 16 the pairs get K's order (first the first two
+        // codes of each word).
+#pragma unroll 1
+        for (int row = warp; row < kRows; row += C::kConsumers) {
+          const uint32_t at = q_rows + row * kQRow;
+          const uint32_t q0 = lds_b32(at + 8 * lane), q1 = lds_b32(at + 8 * lane + 4);
+          const uint32_t m2 = __vmaxu2(q0 & 0x7FFF7FFFu, q1 & 0x7FFF7FFFu);
+          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(m2 >> 16, m2 & 0xFFFFu));
+          // largest magnitude 2^(E - 127): times 2^(141 - E), at most 2^127
+          const int e = min(127, 141 - static_cast<int>(m >> 7));
+          const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          const uint32_t to = at + lane / 4 * 32 + lane % 4 * 4;
+          sts_b32(to, pack_f16x2(bf_lo(q0) * f, bf_hi(q0) * f));
+          sts_b32(to + 16, pack_f16x2(bf_lo(q1) * f, bf_hi(q1) * f));
+          // 2^-e, a subnormal number for e = 127
+          if (lane == 0)
+            s_qinv[row] = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        }
+        bar_all<kWorkers>();
+      }
       // Q as the second operand: row u of each tile, dimensions 2t, 2t + 1
-      // and 2t + 8, 2t + 9 of 16 (4t .. 4t + 3 in the E4M3 kind)
+      // and 2t + 8, 2t + 9 of 16
       uint32_t qf[kN][8][2];
       float qinv[kN][2];  // E4M3: undoes the scaling of rows 2t, 2t + 1
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        const uint32_t src = sbase + C::kOffQ + k % kSegs * C::kQBytes + (8 * n + u) * kQRow;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          if constexpr (kKind == 0) {
-            qf[n][kk][0] = lds_b32(src + 32 * kk + 4 * t4);
-            qf[n][kk][1] = lds_b32(src + 32 * kk + 16 + 4 * t4);
-          } else {
-            qf[n][kk][0] = lds_b32(src + 32 * kk + 8 * t4);
-            qf[n][kk][1] = lds_b32(src + 32 * kk + 8 * t4 + 4);
-          }
+        for (int kk = 0; kk < 8; kk += 2) {
+          uint32_t b[4];
+          ldsm4(b, q_rows + (8 * n + lane % 8) * kQRow + kk * 32 + lane / 8 * 16);
+          qf[n][kk][0] = b[0];
+          qf[n][kk][1] = b[1];
+          qf[n][kk + 1][0] = b[2];
+          qf[n][kk + 1][1] = b[3];
         }
         if constexpr (kKind != 0) {
-          uint32_t m2 = 0;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            m2 = __vmaxu2(m2, __vmaxu2(qf[n][kk][0] & 0x7FFF7FFFu, qf[n][kk][1] & 0x7FFF7FFFu));
-          m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 1));
-          m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 2));
-          // largest magnitude 2^(E - 127): times 2^(141 - E), at most 2^127
-          const int e = min(127, 141 - static_cast<int>(max(m2 >> 16, m2 & 0xFFFFu) >> 7));
-          const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              qf[n][kk][x] = pack_f16x2(bf_lo(qf[n][kk][x]) * f, bf_hi(qf[n][kk][x]) * f);
-          // 2^-e, a subnormal number for e = 127
-          const float inv = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          qinv[n][0] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t4);
-          qinv[n][1] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t4 + 4);
+          qinv[n][0] = s_qinv[8 * n + 2 * t4];
+          qinv[n][1] = s_qinv[8 * n + 2 * t4 + 1];
         }
       }
       __syncwarp();
