@@ -8,6 +8,11 @@
 // largest magnitude is a 16-bit integer maximum over 8 values and four
 // shuffles.  The rows' loads do not wait for the look-up of the sequence and
 // its page; in cache_read they have to.
+//
+// Measured (a copy reaches 6.78 TB/s): writing 9505 tokens of 56 heads as E4M3
+// 69 us, 5.94 TB/s (four tokens a warp instead of one: slower); reading
+// 67608 tokens of 24 heads back 186 us, 6.72 TB/s; one token of 32 sequences
+// and 8 heads 5.3 us, a launch and two dependent look-ups.
 #include <cstdint>
 
 #include "internal.h"
@@ -18,7 +23,10 @@ namespace sa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // heads a warp moves at once
+// Heads a warp moves at once, 16 bytes a lane of each in flight.  Eight take as
+// long for 56 heads (70 us) and longer for one token of 8 heads (6.2 against
+// 5.3 us); fourteen 75 us.
+constexpr int kHeads = 4;
 
 // 16 bytes that this kernel reads once.
 __device__ __forceinline__ uint4 ld_once(const uint16_t* p) {

@@ -15,21 +15,43 @@
 // 256; a tile has 128 left, and 80 FP32 scores with 40 columns of BF16
 // probabilities beside them are the most (in steps of 16) that fit without
 // overlap.  With P over S, as 128 keys need, S_(j+1) has to wait until PV_j
-// has completed: the pipe drains and refills twice a step (a phase of eight
-// MMAs then took 850 cycles for 512 of work; 1171 TFLOP/s at best).  Without
+// has completed: the pipe drains and refills twice a step, and the first form
+// of this kernel came to 1171 TFLOP/s where this one has 1460.  Without
 // overlap S_(j+1) is issued as soon as the softmax has S_j in registers.
 //
-// Warps: 0 walks the line and issues the TMA loads (16 keys a box, what pages
-// of any size have in common with tiles of 80); 1 and 2 gather the Q rows of
+// What bounds it is shared memory.  Of a step's (two tiles, 80 keys) products
+// S reads Q and K there, 2 x 52 KB, PV reads V, 2 x 20 KB, and the loads write
+// 40 KB: 1470 cycles at 128 bytes a cycle, against 1280 of the tensor pipe;
+// it runs at about 1500.  In the E4M3 kind the widening moves 60 KB more (and
+// the loads 20 KB less), about 1800 cycles; it runs at about 2000.  Q cannot
+// come from tensor memory, which is full.
+//
+// Warps: 0 walks the line and issues the loads; 1 and 2 gather the Q rows of
 // tile 0 and 1 (a group of any size, any strides) and issue S; 3 issues PV of
-// both; 4-7 and 8-11 are the softmax of tile 0 and 1, one
-// row a thread; E4M3 pages have four more, 12-15, that widen codes to BF16: a
-// staged tile of codes becomes the K or V tile that the BF16 kind loads, scale
-// applied (the scales are powers of two: what results is exactly the BF16
-// value that cache_read gives).  What bounds that kind is the widening's
-// integer instructions, so a word's codes c0..c3 are taken as the pairs
-// (c0, c2), (c1, c3), which need no byte permutation; Q's dimensions are
-// brought into that order too, and the output's back.
+// both; 4-7 and 8-11 are the softmax of tile 0 and 1, one row a thread; E4M3
+// pages have four more, 12-15, that widen codes to BF16: a staged tile of
+// codes becomes the K or V tile that the BF16 kind loads, scale applied (the
+// scales are powers of two: what results is exactly the BF16 value that
+// cache_read gives).  A word's codes c0..c3 are taken as the pairs (c0, c2),
+// (c1, c3), which need no byte permutation; Q's dimensions are brought into
+// that order too, and the output's back.
+//
+// The loads are one warp's, and one instruction takes it 60 to 150 cycles, so
+// their number counts: pages of 64 and 128 tokens come as the one or two runs
+// of whole keys that a tile has in them (boxes of 16 to 80 keys, or untiled
+// copies for codes), smaller ones as boxes of 16 keys.  2048 tokens over 17000
+// keys, 40 query and 8 key heads, BF16: 449 us with boxes of 16 for all, 435
+// with runs.
+//
+// Code that is seldom run is short here (the mask, the output): the softmax
+// fills the instruction cache, and what is not in it costs about 100 cycles
+// for every eight instructions.
+//
+// Measured (tensor rate of the visible pairs):
+//   2048 new of 33792, 40 / 8 heads, causal, BF16    940 us  1461 TFLOP/s
+//   8704 of 8704, 24 / 24 heads, causal, BF16        354 us  1317
+//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  331 us  1087
+// (a cuBLAS product of 8192^3 reaches 1949 alone and 1723 for seconds).
 //
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
 // tile t in [256 + 128 t, + 80), P in the 40 columns behind it.
@@ -69,7 +91,14 @@ struct Cfg {
   static_assert(kRegsControl + 2 * kRegsSoftmax + (kKind ? kRegsConvert : 0) <= (kThreads / 128) * kRegsLaunch, "");
   static constexpr int kSlots = kKind == 0 ? 8 : 6;  // K, V, K, V, ...
   // The line's places (paged.cuh): what a key tile costs under one row tile
-  // and under two, and a unit's beginning, edges and end.
+  // and under two, and a unit's beginning, edges and end.  A short prompt's
+  // units are unequal, so the last counts: 8704 of 8704 tokens, 24 heads, takes
+  // 387 us with 2 key tiles for it, 363 with 4, 354 with 6 and 356 with 8; a
+  // batch of seven sequences, up to 777 new each, 98, 87, 89 and 90.  Under one
+  // row tile a BF16 key tile costs less (no second tile's products): 12
+  // sequences of up to 100 new tokens, 63 us with 4 of 4 places, 56 with 3 (a
+  // unit's ends at 4); an E4M3 one does not (its widening is the same): 1320
+  // of 9505, 56 heads, 339 us with 4 of 4, 346 with 3.
   static constexpr int kHalfPlaces = kKind == 0 ? 3 : 4, kFullPlaces = 4;
   static constexpr int kOver = 6 * kFullPlaces;
   static constexpr uint32_t kOffQ = 0;

@@ -2,9 +2,10 @@
 // each row of a unit that a cut of the work divided, over its parts in the
 // order of their keys,
 //   o = sum_i 2^(m_i - m) a_i / sum_i 2^(m_i - m) l_i,  m = max m_i.
-// Bound by latency, and in the form for chunks by what the parts weigh (512
-// bytes a row and part).  The first CTA also makes one status word of the
-// CTAs' words.
+// Bound by latency (with its launch and the attention kernel's last stores 3
+// to 4 us after it in the form for few rows) and in the form for chunks by what
+// the parts weigh too: 512 bytes a row and part, two parts a CTA, 6 to 9 us.
+// The first CTA also makes one status word of the CTAs' words.
 #include <cstdint>
 
 #include "internal.h"
@@ -116,26 +117,45 @@ __global__ void __launch_bounds__(32 * kWarps) join_chunk_kernel(const PagedAttn
   // warp: columns 32 w ..; lane: row, 8 columns
   const int row = blockIdx.y * 8 + lane % 8, chunk = warp * 4 + lane / 8;
   if (row >= d.rows) return;
+  // Four parts at a time, references, sums and values by one round of loads.
   float m = -INFINITY, l = 0.f;
-  for (int i = 0; i < d.pieces; ++i) m = fmaxf(m, ws.ml[part_row(i, kRows, row)].x);
   float o[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < d.pieces; ++i) {
-    const float2 ml = ws.ml[part_row(i, kRows, row)];
-    const float4* src = reinterpret_cast<const float4*>(ws.part + part_row(i, kRows, 0) * kHeadDim + (chunk * kRows + row) * 8);
-    const float4 x = src[0], y = src[1];
-    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-    l += f * ml.y;
-    o[0] += f * x.x;
-    o[1] += f * x.y;
-    o[2] += f * x.z;
-    o[3] += f * x.w;
-    o[4] += f * y.x;
-    o[5] += f * y.y;
-    o[6] += f * y.z;
-    o[7] += f * y.w;
+#pragma unroll 1
+  for (int i0 = 0; i0 < d.pieces; i0 += 4) {
+    float2 ml[4];
+    float4 x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u, d.pieces - 1);
+      ml[u] = ws.ml[part_row(i, kRows, row)];
+      const float4* src = reinterpret_cast<const float4*>(ws.part + part_row(i, kRows, 0) * kHeadDim + (chunk * kRows + row) * 8);
+      x[u] = src[0];
+      y[u] = src[1];
+    }
+    float to = m;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) to = fmaxf(to, ml[u].x);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - to);
+    m = to;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i0 + u >= d.pieces) break;
+      const float w = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - m);
+      l += w * ml[u].y;
+      o[0] += w * x[u].x;
+      o[1] += w * x[u].y;
+      o[2] += w * x[u].z;
+      o[3] += w * x[u].w;
+      o[4] += w * y[u].x;
+      o[5] += w * y[u].y;
+      o[6] += w * y[u].z;
+      o[7] += w * y[u].w;
+    }
   }
   const int rho = d.rho0 + row, i = rho / a.group;
   const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
