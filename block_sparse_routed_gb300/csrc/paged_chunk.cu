@@ -384,7 +384,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
           const int key1 = page1 << c.page_shift, n0 = page0 == page1 ? kTileKeys : key1 - key0;
           const int e0 = __shfl_sync(0xFFFFFFFFu, entry, (page0 - have) & 31);
           const int e1 = __shfl_sync(0xFFFFFFFFu, entry, (page1 - have) & 31);
-          const bool on0 = page0 >= p_lo && e0 >= 0, on1 = n0 < kTileKeys && page1 < p_hi && e1 >= 0;
+          const bool on0 = page0 >= p_lo && page0 < p_hi && e0 >= 0, on1 = n0 < kTileKeys && page1 < p_hi && e1 >= 0;
           const uint32_t r0 = ((static_cast<uint32_t>(e0) * c.H + g.h) << c.page_shift) + (key0 & (c.page_size - 1));
           const uint32_t r1 = (static_cast<uint32_t>(e1) * c.H + g.h) << c.page_shift;
           const int all = (on0 ? n0 : 0) + (on1 ? kTileKeys - n0 : 0);

@@ -264,6 +264,22 @@ def test_chunks(bsr, kind, lens, news, H, Hq, page, causal, window, tight):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [64, 128])
+@pytest.mark.parametrize("lens,news,H,Hq,causal,window", [
+    ([1500, 333, 81], [140, 60, 80], 1, 4, True, 200),   # windows begin inside pages and tiles
+    ([1500, 333, 81], [140, 60, 80], 1, 4, False, 0),
+    ([2600, 900], [40, 100], 2, 2, True, 0),             # units of few rows, cut many times, beside full ones
+    ([2600, 900], [40, 600], 2, 2, True, 0),
+    ([400, 17], [20, 3], 1, 40, True, 0),                # a row tile holds few tokens
+    ([90, 170], [2, 3], 1, 300, True, 0),                # or less than one
+])
+def test_chunks_of_whole_page_runs(bsr, kind, page, lens, news, H, Hq, causal, window):
+    b = Batch(lens, news, H, page, kind, seed=page + len(lens), after=1)
+    q, o, lse = run_attention(bsr, b, Hq, causal=causal, window=window)
+    check_attention(b, q, o, lse, causal, window, filled=3.0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("news", [1, 150])
 def test_long_context_is_split_and_joined(bsr, kind, news):
     b = Batch([9505, 40], [news, 1], 2, 64, kind, seed=5)
