@@ -198,6 +198,8 @@ struct PagedAttnArgs {
   const uint16_t* q;
   int64_t q_token, q_head;
   int Hq, group;             // group = Hq / H query heads a key head
+  uint32_t group_mul;        // x / group = x group_mul >> group_shift for x < 2^31
+  int group_shift;
   int causal, window;
   float scale;
   uint16_t* o;               // BF16 [rows, Hq, 128]

@@ -109,13 +109,20 @@ __device__ __forceinline__ void e4m3x2_f32(uint16_t v, float& lo, float& hi) {
 // the CTA that has the first of them.  A unit that a cut divides is joined
 // from its parts by the joining kernel.
 
+template <int kRowTile, int kKeyTile, int kHalf, int kFull, int kOver, int kMinPlaces, bool kSingle>
 struct LineShape {
-  int row_tile;    // packed rows of a unit
-  int key_tile;    // keys of a tile
-  int half, full;  // places of a key tile
-  int over;        // places of a unit without a key tile
-  int min_places;  // of a CTA at least (>= full), while there are any
+  static constexpr int row_tile = kRowTile;           // packed rows of a unit
+  static constexpr int key_tile = kKeyTile;           // keys of a tile
+  static constexpr int half = kHalf, full = kFull;    // places of a key tile
+  static constexpr int over = kOver;                  // places of a unit without a key tile
+  static constexpr int min_places = kMinPlaces;       // of a CTA at least (>= full), while there are any
+  static constexpr bool single = kSingle;             // a sequence and key head are one unit at most
 };
+
+// x / group (x >= 0).
+__device__ __forceinline__ int div_group(const PagedAttnArgs& a, int x) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * a.group_mul) >> a.group_shift);
+}
 
 struct UnitKeys {
   int lo, hi;  // keys that some row of the unit sees: [lo, hi)
@@ -134,13 +141,14 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const PagedSeq&
                           static_cast<uint32_t>(row_tile));
 }
 
-__device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p, LineShape line) {
-  const int row_tile = line.row_tile, key_tile = line.key_tile;
+template <class Line>
+__device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p) {
+  constexpr int row_tile = Line::row_tile, key_tile = Line::key_tile;
   const int rows = q.n * a.group;
   int i0 = 0, i1 = q.n - 1;  // first and last new token of the tile
-  if (rows > row_tile) {
-    i0 = p * row_tile / a.group;
-    i1 = (min((p + 1) * row_tile, rows) - 1) / a.group;
+  if (!Line::single && rows > row_tile) {
+    i0 = div_group(a, p * row_tile);
+    i1 = div_group(a, min((p + 1) * row_tile, rows) - 1);
   }
   UnitKeys u;
   u.hi = a.causal ? min(q.len, q.len - q.n + i1 + 1) : q.len;
@@ -148,8 +156,8 @@ __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const Page
   if (u.hi <= u.lo) u.lo = u.hi = 0;
   u.t0 = u.lo / static_cast<uint32_t>(key_tile);
   u.nt = max(1, static_cast<int>((u.hi + static_cast<uint32_t>(key_tile) - 1) / static_cast<uint32_t>(key_tile)) - u.t0);
-  u.each = line.half == line.full || rows - p * row_tile > row_tile / 2 ? line.full : line.half;
-  u.places = u.nt * u.each + line.over;
+  u.each = Line::half == Line::full || rows - p * row_tile > row_tile / 2 ? Line::full : Line::half;
+  u.places = u.nt * u.each + Line::over;
   return u;
 }
 
@@ -176,34 +184,52 @@ __device__ __forceinline__ int64_t muldiv(int64_t x, int64_t y, int64_t z) {
 
 // Places of one head of the sequences base + lane, one a lane (0 past the
 // last).  Sequences of many row tiles are summed by the whole warp.
-__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, LineShape line, int lane, bool& bad) {
+template <class Line>
+__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, int lane, bool& bad) {
   const int s = base + lane;
   PagedSeq q;
-  q.n = 0;
+  q.n = q.len = 0;
   if (s < a.c.seqs) {
     bool b;
     q = paged_seq(a.c, s, b);
     bad |= b;
   }
-  const int tiles = row_tiles(a, q, line.row_tile);
-  int64_t t = 0;
-  if (tiles <= 4)
-    for (int p = 0; p < tiles; ++p) t += unit_keys(a, q, p, line).places;
-  unsigned many = __ballot_sync(0xFFFFFFFFu, tiles > 4);
-  while (many) {
-    const int src = __ffs(many) - 1;
-    many &= many - 1;
-    PagedSeq r;
-    r.row0 = 0;
-    r.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
-    r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
-    const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
-    int64_t y = 0;
-    for (int p = lane; p < n; p += 32) y += unit_keys(a, r, p, line).places;
-    y = warp_sum(y);
-    if (lane == src) t = y;
+  if constexpr (Line::single) {
+    return q.n > 0 ? unit_keys<Line>(a, q, 0).places : 0;
+  } else {
+    const int tiles = row_tiles(a, q, Line::row_tile);
+    int64_t t = 0;
+    if (tiles <= 4)
+#pragma unroll 1
+      for (int p = 0; p < tiles; ++p) t += unit_keys<Line>(a, q, p).places;
+    unsigned many = __ballot_sync(0xFFFFFFFFu, tiles > 4);
+    while (many) {
+      const int src = __ffs(many) - 1;
+      many &= many - 1;
+      PagedSeq r;
+      r.row0 = 0;
+      r.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
+      r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
+      const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
+      int64_t y = 0;
+#pragma unroll 1
+      for (int p = lane; p < n; p += 32) y += unit_keys<Line>(a, r, p).places;
+      y = warp_sum(y);
+      if (lane == src) t = y;
+    }
+    return t;
   }
-  return t;
+}
+// The same for sequences behind the first 32, out of the way where it is long:
+// a small batch's time is that of fetching the code that it runs.
+template <class Line>
+__device__ __noinline__ int64_t far_call(const PagedAttnArgs& a, int base, bool& bad) {
+  return lane_tiles<Line>(a, base, threadIdx.x % 32, bad);
+}
+template <class Line>
+__device__ __forceinline__ int64_t far_tiles(const PagedAttnArgs& a, int base, bool& bad) {
+  if constexpr (Line::single) return lane_tiles<Line>(a, base, threadIdx.x % 32, bad);
+  else return far_call<Line>(a, base, bad);
 }
 
 // One step of a CTA: some key tiles of a unit.
@@ -228,24 +254,24 @@ struct LineWalk {
   int tiles;    // row tiles of the sequence
 };
 
-__device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w, int row_tile) {
+template <class Line>
+__device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w) {
   bool bad;
   w.q = paged_seq(a.c, w.s, bad);
-  w.tiles = row_tiles(a, w.q, row_tile);
+  w.tiles = row_tiles(a, w.q, Line::row_tile);
 }
 
 // Finds the part of CTA `cta` of `ctas`.  Sets `bad` when a sequence fails its
 // checks.
-__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, LineShape line, int cta, int ctas,
-                                           bool& bad) {
-  const int lane = threadIdx.x % 32, seqs = a.c.seqs;
-  int64_t t = 0, first = 0;
-  for (int base = 0; base < seqs; base += 32) {
-    t += lane_tiles(a, base, line, lane, bad);
-    if (base == 0) first = t;
-  }
+template <class Line>
+__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, int cta, int ctas, bool& bad) {
+  const int lane = threadIdx.x % 32;
+  const int64_t first = lane_tiles<Line>(a, 0, lane, bad);
+  int64_t t = first;
+#pragma unroll 1
+  for (int base = 32; base < a.c.seqs; base += 32) t += far_tiles<Line>(a, base, bad);
   w.total = warp_sum(t) * a.c.H;
-  const int64_t most = (w.total + line.min_places - 1) / line.min_places;
+  const int64_t most = (w.total + Line::min_places - 1) / Line::min_places;
   w.ctas = static_cast<int>(min(static_cast<int64_t>(ctas), most));
   // (a part without tiles must not lie between two of one unit)
   w.at = w.end = 0;
@@ -254,9 +280,10 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
   w.at = muldiv(cta, w.total, w.ctas);
   w.end = muldiv(cta + 1, w.total, w.ctas);
   int64_t left = w.at;
+#pragma unroll 1
   for (int base = 0;; base += 32) {
     bool b;
-    const int64_t mine = (base == 0 ? first : lane_tiles(a, base, line, lane, b)) * a.c.H;
+    const int64_t mine = (base == 0 ? first : far_tiles<Line>(a, base, b)) * a.c.H;
     const int64_t upto = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (hit) {
@@ -268,32 +295,31 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
     }
     left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
-  walk_seq(a, w, line.row_tile);
+  walk_seq<Line>(a, w);
   t = muldiv(t, 1, a.c.H);
   w.h = static_cast<int>(muldiv(left, 1, t));
   left -= w.h * t;
-  if (w.tiles == 1) {
-    w.skip = static_cast<int>(left);
-    return;
-  }
-  for (int p0 = 0;; p0 += 32) {
-    const int64_t mine = p0 + lane < w.tiles ? unit_keys(a, w.q, p0 + lane, line).places : 0;
-    const int64_t upto = warp_scan(mine, lane);
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      w.p = p0 + src;
-      w.skip = static_cast<int>(__shfl_sync(0xFFFFFFFFu, left - (upto - mine), src));
-      return;
+  w.skip = static_cast<int>(left);
+  if constexpr (!Line::single) {
+    for (int p0 = 0; w.tiles > 1; p0 += 32) {
+      const int64_t mine = p0 + lane < w.tiles ? unit_keys<Line>(a, w.q, p0 + lane).places : 0;
+      const int64_t upto = warp_scan(mine, lane);
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        w.p = p0 + src;
+        w.skip = static_cast<int>(__shfl_sync(0xFFFFFFFFu, left - (upto - mine), src));
+        return;
+      }
+      left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
 }
 
 // The next step (valid = 0 at the end); `join` is filled when it leaves a
 // unit unfinished that it began.
-__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, LineShape line, int cta,
-                                             JoinDesc& join) {
+template <class Line>
+__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, int cta, JoinDesc& join) {
   Segment g;
   g.valid = 0;
   while (w.at < w.end) {
@@ -302,13 +328,13 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
       if (w.tiles == 0 || ++w.h >= a.c.H) {
         w.h = 0;
         ++w.s;
-        walk_seq(a, w, line.row_tile);
+        walk_seq<Line>(a, w);
       }
     }
-    const UnitKeys u = unit_keys(a, w.q, w.p, line);
+    const UnitKeys u = unit_keys<Line>(a, w.q, w.p);
     const int take = static_cast<int>(min(static_cast<int64_t>(u.places - w.skip), w.end - w.at));
     // key tiles whose first place is among [skip, skip + take)
-    const auto tiles_before = [&](int place) { return (max(0, place - line.over) + u.each - 1) / u.each; };
+    const auto tiles_before = [&](int place) { return (max(0, place - Line::over) + u.each - 1) / u.each; };
     const int from = tiles_before(w.skip), to = tiles_before(w.skip + take);
     if (to > from) {
       g.valid = 1;
@@ -317,13 +343,13 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
       g.len = w.q.len;
       g.h = w.h;
       g.s = w.s;
-      g.rho0 = w.p * line.row_tile;
-      g.rows = min(line.row_tile, w.q.n * a.group - g.rho0);
+      g.rho0 = w.p * Line::row_tile;
+      g.rows = min(Line::row_tile, w.q.n * a.group - g.rho0);
       g.lo = u.lo;
       g.hi = u.hi;
       const int base = w.q.len - w.q.n;
-      g.all_lo = row_lo(a, base + (g.rho0 + g.rows - 1) / a.group);
-      g.all_hi = a.causal ? min(w.q.len, base + g.rho0 / a.group + 1) : w.q.len;
+      g.all_lo = row_lo(a, base + div_group(a, g.rho0 + g.rows - 1));
+      g.all_hi = a.causal ? min(w.q.len, base + div_group(a, g.rho0) + 1) : w.q.len;
       g.t0 = u.t0 + from;
       g.nt = to - from;
       g.part = from == 0 ? (to == u.nt ? -1 : 1) : 0;

@@ -204,6 +204,11 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   a.q_head = p->a_head_stride;
   a.Hq = p->Hq;
   a.group = p->Hq / p->H;
+  // with 2^l >= group: m = ceil(2^(31 + l) / group) is off by less than 2^l / group, and x < 2^31
+  int l = 0;
+  while ((int64_t(1) << l) < a.group) ++l;
+  a.group_shift = 31 + l;
+  a.group_mul = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + a.group - 1) / a.group);
   a.causal = p->causal;
   a.window = p->window;
   a.scale = p->scale;

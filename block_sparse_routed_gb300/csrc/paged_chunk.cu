@@ -330,8 +330,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     if (kKind == 0 && lane < 2 * min(kBoxes, c.page_size / kBoxKeys)) tma_prefetch_desc(&maps.m[lane % 2][lane / 2]);
     LineWalk w;
     bool bad = false;
-    constexpr LineShape line = {kUnitRows, kTileKeys, C::kHalfPlaces, C::kFullPlaces, C::kOver, kMinTiles * C::kFullPlaces};
-    walk_begin(a, w, line, blockIdx.x, gridDim.x, bad);
+    using Line = LineShape<kUnitRows, kTileKeys, C::kHalfPlaces, C::kFullPlaces, C::kOver, kMinTiles * C::kFullPlaces, false>;
+    walk_begin<Line>(a, w, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
     int q = 0, buf = 0, round = 0;  // tiles of K or V so far, the next one's slot and use of it
@@ -346,7 +346,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       }
     };
     for (int k = 0; ok; ++k) {
-      const Segment g = walk_next(a, w, line, blockIdx.x, join);
+      const Segment g = walk_next<Line>(a, w, blockIdx.x, join);
       ok = k < kSegs || all_wait(BAR_SEGEMPTY + k % kSegs, k / kSegs - 1);
       if (!ok) break;
       if (lane == 0) {
@@ -464,10 +464,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         ok = y == 0 || all_wait(BAR_SFULL + t, y - 1);
         if (!ok) break;
         const int rho = g.rho0 + 128 * t + q_row, left = g.rows - 128 * t;
-        int i = rho / a.group, e = rho - i * a.group;
+        int i = div_group(a, rho), e = rho - i * a.group;
         const uint16_t* src = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
                               static_cast<int64_t>(g.h * a.group + e) * a.q_head + q_chunk * 8;
-        const int i2 = 2 / a.group, e2 = 2 - i2 * a.group;  // two rows on: tokens and heads
+        const int i2 = a.group == 1 ? 2 : a.group == 2 ? 1 : 0, e2 = 2 - i2 * a.group;  // two rows on: tokens and heads
         const int64_t step = i2 * a.q_token + e2 * a.q_head, wrap = a.q_token - a.group * a.q_head;
         auto at = [&](int r) { return q_to + r * 128 + ((q_chunk ^ r) & 7) * 16; };
 #pragma unroll 4
@@ -613,7 +613,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       }
       const int rho = g.rho0 + 128 * t + row;
       const bool real = 128 * t + row < g.rows;
-      const int i = rho / a.group;
+      const int i = div_group(a, rho);
       const int pos = g.len - g.n + i;
       // a row that does not exist has Q = 0: no mask, and no output
       const int lo = real ? row_lo(a, pos) : 0;

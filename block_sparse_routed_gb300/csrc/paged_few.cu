@@ -220,9 +220,10 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     fence_barrier_init();
   }
   __syncthreads();
-  // Token of a packed row: there are at most 16, so FP32 divides exactly.
+  // Token of a packed row: there are at most 16, so FP32 divides exactly (and
+  // takes the fewest registers).
   const float inv_group = 1.0f / static_cast<float>(a.group);
-  auto div_group = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
+  auto token_of = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
 
   if (warp == C::kConsumers) {
     // ------------------------------------------------------------ producer
@@ -232,8 +233,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     LineWalk w;
     bool bad = false;
-    constexpr LineShape line = {kRows, kTileKeys, 1, 1, kKind == 0 ? kOverBf16 : kOverE4m3, 1};
-    walk_begin(a, w, line, blockIdx.x, gridDim.x, bad);
+    using Line = LineShape<kRows, kTileKeys, 1, 1, kKind == 0 ? kOverBf16 : kOverE4m3, 1, true>;
+    walk_begin<Line>(a, w, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
     bool ok = true;
@@ -242,14 +243,30 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int tile_pages = kTileKeys / per_page;
     const uint32_t elect = elect_one();
     for (int k = 0; ok; ++k) {
-      const Segment g = walk_next(a, w, line, blockIdx.x, join);
+      const Segment g = walk_next<Line>(a, w, blockIdx.x, join);
       ok = k < kSegs ||
            __all_sync(0xFFFFFFFFu, mbar_wait(bar(BAR_SEMPTY + k % kSegs), ((k / kSegs) & 1) ^ 1, a.wait_limit));
       if (!ok) break;
+      // pages of this step's tiles, 32 table entries at a time (the first load
+      // is under way while Q's are issued)
+      const int p_lo = g.lo >> c.page_shift, p_hi = (g.hi + c.page_size - 1) >> c.page_shift;
+      int have = g.valid ? (g.t0 << kKeyShift >> c.page_shift) / 32 : 0;  // entry: page index 32 * have + lane
+      const int32_t* table = c.table + (g.valid ? g.s * c.table_stride : 0);
+      auto fetch = [&] {
+        const int at = have * 32 + lane;
+        return at >= p_lo && at < p_hi ? __ldg(table + at) : 0;
+      };
+      auto checked = [&](int e) {
+        const bool wrong = e < 0 || e >= c.pages;
+        bad |= wrong;
+        return wrong ? -1 : e;
+      };
+      int entry = 0;
       if (g.valid) {  // (a unit is one row tile here: rho0 is 0)
+        entry = fetch();
 #pragma unroll
         for (int x = 0; x < kRows / 2; ++x) {
-          const int row = 2 * x + lane / 16, i = div_group(row);
+          const int row = 2 * x + lane / 16, i = token_of(row);
           const uint16_t* src = a.q;
           if (row < g.rows)
             src += static_cast<int64_t>(g.row0 + i) * a.q_token +
@@ -263,20 +280,13 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_arrive(bar(BAR_SFULL + k % kSegs));
       }
       if (!g.valid) break;
-      const int32_t* table = c.table + g.s * c.table_stride;
-      // pages of this step's tiles, 32 table entries at a time
-      const int p_lo = g.lo >> c.page_shift, p_hi = (g.hi + c.page_size - 1) >> c.page_shift;
-      int have = -1, entry = 0;  // entry: page index 32 * have + lane
+      entry = checked(entry);
       for (int t = g.t0; t < g.t0 + g.nt; ++t) {
         const int key0 = t << kKeyShift;
         const int page0 = key0 >> c.page_shift;
         if (page0 / 32 != have) {
           have = page0 / 32;
-          const int at = have * 32 + lane;
-          entry = at >= p_lo && at < p_hi ? __ldg(table + at) : 0;
-          const bool wrong = entry < 0 || entry >= c.pages;
-          bad |= wrong;
-          if (wrong) entry = -1;
+          entry = checked(fetch());
         }
         // lane i: row of the cache where the tile's i-th page begins (-1: not to be loaded)
         const int at = page0 + lane;
@@ -414,7 +424,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = 8 * n + 2 * t4 + e;
-          const int pos = g.len - g.n + div_group(row);
+          const int pos = g.len - g.n + token_of(row);
           lo[n][e] = row < g.rows ? row_lo(a, pos) : 0;
           hi[n][e] = row < g.rows ? (a.causal ? min(g.len, pos + 1) : g.len) : 0;
         }
@@ -638,7 +648,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // (the last warp's turn comes last: meanwhile, what concerns whole rows)
         if (n == 0 && warp == C::kConsumers - 1 && lane < kRows) {
           const float2 ml = s_row[lane];
-          const int i = div_group(lane);
+          const int i = token_of(lane);
           const bool real = lane < g.rows;
           const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + lane - i * a.group
                                         : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + lane;

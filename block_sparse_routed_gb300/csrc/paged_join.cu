@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const PagedAttnAr
     o.z += f * x.z;
     o.w += f * x.w;
   }
-  const int rho = d.rho0 + row, i = rho / a.group;
+  const int rho = d.rho0 + row, i = div_group(a, rho);
   const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
   const float inv = join_inverse(l);
   reinterpret_cast<uint2*>(a.o + at * kHeadDim)[lane] =
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(32 * kWarps) join_chunk_kernel(const PagedAttn
       o[7] += w * y[u].w;
     }
   }
-  const int rho = d.rho0 + row, i = rho / a.group;
+  const int rho = d.rho0 + row, i = div_group(a, rho);
   const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
   const float inv = join_inverse(l);
   uint32_t z[4];
