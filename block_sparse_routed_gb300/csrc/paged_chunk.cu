@@ -16,7 +16,7 @@
 // probabilities beside them are the most (in steps of 16) that fit without
 // overlap.  With P over S, as 128 keys need, S_(j+1) has to wait until PV_j
 // has completed: the pipe drains and refills twice a step, and the first form
-// of this kernel came to 1171 TFLOP/s where this one has 1460.  Without
+// of this kernel came to 1171 TFLOP/s where this one has 1447.  Without
 // overlap S_(j+1) is issued as soon as the softmax has S_j in registers.
 //
 // What bounds it is shared memory.  Of a step's (two tiles, 80 keys) products
@@ -48,9 +48,9 @@
 // for every eight instructions.
 //
 // Measured (tensor rate of the visible pairs):
-//   2048 new of 33792, 40 / 8 heads, causal, BF16    940 us  1461 TFLOP/s
+//   2048 new of 33792, 40 / 8 heads, causal, BF16    950 us  1447 TFLOP/s
 //   8704 of 8704, 24 / 24 heads, causal, BF16        354 us  1317
-//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  331 us  1087
+//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  326 us  1103
 // (a cuBLAS product of 8192^3 reaches 1949 alone and 1723 for seconds).
 //
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
