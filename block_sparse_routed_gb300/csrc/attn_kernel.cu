@@ -1084,8 +1084,6 @@ __global__ void bias_prep_kernel(const float* __restrict__ bias, float* __restri
   }
 }
 
-}  // namespace
-
 int sm_count() {
   static int cached[128] = {0};
   int dev = 0;
@@ -1097,6 +1095,8 @@ int sm_count() {
   }
   return cached[dev];
 }
+
+}  // namespace
 
 size_t attention_smem_bytes() { return kSmemBytes; }
 

@@ -256,9 +256,6 @@ cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, co
                                cudaStream_t s);
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
 
-// Multiprocessors of the current device (cached).
-int sm_count();
-
 // Tensor map of a row-major 2-D array of `elem`-byte elements, box
 // [box_rows, 128 bytes], 128-byte swizzle, zeros past the last row.
 bool make_map_rows(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int elem, uint32_t box_rows);

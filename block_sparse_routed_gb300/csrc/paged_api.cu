@@ -1,6 +1,7 @@
 // Host side of the paged-cache entry points declared in include/sparse_attn.h:
 // argument checks, workspace layout and launches.  Every check happens before
 // anything is enqueued.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -91,6 +92,19 @@ PagedForm form_of(const sa_paged_params* p) {
   f.row_tile = rows <= 8 ? 8 : (f.few ? kPagedFewRows : kPagedChunkRows);
   f.max_ctas = f.few ? kPagedFewCtas : kPagedChunkCtas;
   return f;
+}
+
+// Of the current device (0: none could be asked).
+int multiprocessors() {
+  static std::atomic<int> cached[128];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 constexpr uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255); }
@@ -239,7 +253,8 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   // no more CTAs than units times the key tiles of the longest context that the table can hold
   const int64_t units = p->seqs + (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile;
   const int64_t most = units * p->H * ((int64_t(p->table_width) * p->page_size + tile - 1) / tile + 1);
-  int ctas = (f.few ? 2 : 1) * sm_count();
+  int ctas = (f.few ? 2 : 1) * multiprocessors();
+  if (ctas <= 0) return SA_ECUDA;
   if (ctas > f.max_ctas) ctas = f.max_ctas;
   if (most < ctas) ctas = static_cast<int>(most);
   const cudaError_t e = f.few ? launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream)

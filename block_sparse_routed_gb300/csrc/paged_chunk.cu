@@ -55,6 +55,7 @@
 //
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
 // tile t in [256 + 128 t, + 80), P in the 40 columns behind it.
+#include <atomic>
 #include <cstdint>
 
 #include "internal.h"
@@ -922,12 +923,14 @@ cudaError_t launch(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScr
   if (e != cudaSuccess) return e;
   // The register split redistributes the launch allocation; a build with
   // fewer registers a thread would make setmaxnreg.inc wait forever.
-  static int regs = -1;
-  if (regs < 0) {
+  static std::atomic<int> known{0};
+  int regs = known.load(std::memory_order_relaxed);
+  if (regs == 0) {
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     regs = fa.numRegs;
+    known.store(regs, std::memory_order_relaxed);
   }
   const int split = C::kRegsControl + 2 * C::kRegsSoftmax + (kKind ? C::kRegsConvert : 0);
   if (regs * (C::kThreads / 128) < split) return cudaErrorInvalidConfiguration;
