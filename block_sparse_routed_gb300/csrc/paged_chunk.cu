@@ -49,8 +49,8 @@
 //
 // Measured (tensor rate of the visible pairs):
 //   2048 new of 33792, 40 / 8 heads, causal, BF16    950 us  1447 TFLOP/s
-//   8704 of 8704, 24 / 24 heads, causal, BF16        354 us  1317
-//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  326 us  1103
+//   8704 of 8704, 24 / 24 heads, causal, BF16        348 us  1338
+//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  324 us  1110
 // (a cuBLAS product of 8192^3 reaches 1949 alone and 1723 for seconds).
 //
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
@@ -642,10 +642,15 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
 #pragma unroll 1
           for (int b = 0; b < kTileKeys; b += 16) {
             const int from = lo - key0 - b, to = hi - key0 - b;
-            if (__all_sync(0xFFFFFFFFu, from <= 0 && to >= 16)) continue;
+            if (__all_sync(0xFFFFFFFFu, !real || (from <= 0 && to >= 16))) continue;
             uint32_t z[16];
-            tmem_ld16(s_col + b, z);
-            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(-INFINITY);
+            // (a load's way there and back is most of the 400 cycles of a block)
+            if (!__all_sync(0xFFFFFFFFu, !real || to <= 0 || from >= 16)) {
+              tmem_ld16(s_col + b, z);
+              tmem_wait_ld();
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (e < from || e >= to) z[e] = __float_as_uint(-INFINITY);
@@ -767,32 +772,51 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
                                     : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows + 128 * t + row;
       float* part = ws.part + (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows * kHeadDim;  // (g.part >= 0)
       const float inv = (g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * whole;  // (NaN stays)
+      // Output rows are Hq rows apart, and a store of one row a lane touches 32
+      // lines: lanes 4 x .. 4 x + 3 exchange their rows' quarters of 64 bytes
+      // first, so that each store has 8 rows of them.
+      int64_t to[4];
+      const uint32_t reals = __ballot_sync(0xFFFFFFFFu, real);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) to[f] = __shfl_sync(0xFFFFFFFFu, at, (lane & ~3) + f) * kHeadDim + lane % 4 * 8;
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         uint32_t o[32];
         tmem_ld32(o_col + 32 * b, o);
         tmem_wait_ld();
-        if (real) {
-          if (g.part < 0) {
-            // (32-byte stores: whole sectors)
+        if (g.part < 0) {
+          uint32_t z[4][4];  // [quarter][word], then [row][word]
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t z[8];
+          for (int f = 0; f < 16; ++f)
+            z[f / 4][f % 4] = pack_bf16x2(__uint_as_float(o[dim(2 * f)]) * inv, __uint_as_float(o[dim(2 * f + 1)]) * inv);
 #pragma unroll
-              for (int f = 0; f < 8; ++f)
-                z[f] = pack_bf16x2(__uint_as_float(o[dim(16 * e + 2 * f)]) * inv,
-                                   __uint_as_float(o[dim(16 * e + 2 * f + 1)]) * inv);
-              st_global_v8(a.o + at * kHeadDim + 32 * b + 16 * e, z);
+          for (int d = 1; d < 4; d *= 2) {
+            const bool upper = lane & d;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              if (f & d) continue;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? z[f][w] : z[f + d][w], d);
+                if (upper)
+                  z[f][w] = got;
+                else
+                  z[f + d][w] = got;
+              }
             }
-          } else {
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t z[8];
+          for (int f = 0; f < 4; ++f)
+            if (reals >> ((lane & ~3) + f) & 1)
+              *reinterpret_cast<uint4*>(a.o + to[f] + 32 * b) = make_uint4(z[f][0], z[f][1], z[f][2], z[f][3]);
+        } else if (real) {
 #pragma unroll
-              for (int f = 0; f < 8; ++f) z[f] = __float_as_uint(__uint_as_float(o[dim(8 * e + f)]) * inv);
-              // [8 columns][row]: a warp's stores lie side by side
-              st_global_v8(part + ((4 * b + e) * kUnitRows + 128 * t + row) * 8, z);
-            }
+          for (int e = 0; e < 4; ++e) {
+            uint32_t z[8];
+#pragma unroll
+            for (int f = 0; f < 8; ++f) z[f] = __float_as_uint(__uint_as_float(o[dim(8 * e + f)]) * inv);
+            // [8 columns][row]: a warp's stores lie side by side
+            st_global_v8(part + ((4 * b + e) * kUnitRows + 128 * t + row) * 8, z);
           }
         }
       }
