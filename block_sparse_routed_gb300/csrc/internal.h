@@ -254,7 +254,8 @@ struct ChunkMaps {
 };
 cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScratch& ws, int ctas,
                                cudaStream_t s);
-cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
+                              cudaStream_t s);
 
 // Tensor map of a row-major 2-D array of `elem`-byte elements, box
 // [box_rows, 128 bytes], 128-byte swizzle, zeros past the last row.

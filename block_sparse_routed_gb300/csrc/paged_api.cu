@@ -252,7 +252,8 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   if (!maps) return SA_ECUDA;
   // no more CTAs than units times the key tiles of the longest context that the table can hold
   const int64_t units = p->seqs + (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile;
-  const int64_t most = units * p->H * ((int64_t(p->table_width) * p->page_size + tile - 1) / tile + 1);
+  const int64_t tiles = (int64_t(p->table_width) * p->page_size + tile - 1) / tile;
+  const int64_t most = units * p->H * (tiles + 1);
   int ctas = (f.few ? 2 : 1) * multiprocessors();
   if (ctas <= 0) return SA_ECUDA;
   if (ctas > f.max_ctas) ctas = f.max_ctas;
@@ -260,5 +261,7 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   const cudaError_t e = f.few ? launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream)
                               : launch_paged_chunk(boxes, a, scratch, ctas, stream);
   if (cuda_failed(e)) return SA_ECUDA;
-  return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, stream)) ? SA_ECUDA : SA_OK;
+  // a dozen parts a unit and more (the chunks' parts have three key tiles at least)
+  const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
+  return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
 }

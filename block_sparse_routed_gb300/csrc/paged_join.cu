@@ -106,24 +106,31 @@ __global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const PagedAttnAr
 }
 
 // The form for chunks.  A warp takes 8 rows x 32 columns: the parts are read
-// 256 bytes, the output written 64 bytes at a time.
-__global__ void __launch_bounds__(32 * kWarps) join_chunk_kernel(const PagedAttnArgs a, const PagedScratch ws) {
+// 256 bytes, the output written 64 bytes at a time.  kGroups sets of warps
+// share the parts of a unit: where few units are cut into many parts they are
+// what keeps enough loads in flight (60 tokens over 30000 keys, 16 / 2 heads,
+// 38 parts a unit: 41 us with one set, 37 with four); with two or three parts
+// a unit they only wait (128 over 1000, 8 / 4 heads: 20.5 us with one, 24 with
+// four).
+template <int kGroups>
+__global__ void __launch_bounds__(32 * kWarps * kGroups)
+join_chunk_kernel(const PagedAttnArgs a, const PagedScratch ws) {
   constexpr int kRows = kPagedChunkRows;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % kWarps, group = threadIdx.x / (32 * kWarps);
   griddep_wait();
   const JoinDesc d = ws.join[blockIdx.x];
   join_status(a, ws);
-  if (d.pieces == 0) return;
+  if (d.pieces == 0 || blockIdx.y * 8 >= d.rows) return;
   // warp: columns 32 w ..; lane: row, 8 columns
   const int row = blockIdx.y * 8 + lane % 8, chunk = warp * 4 + lane / 8;
-  if (row >= d.rows) return;
+  if (kGroups == 1 && row >= d.rows) return;  // (else they load what nobody wrote, and write nothing)
   // Four parts at a time, references, sums and values by one round of loads.
   float m = -INFINITY, l = 0.f;
   float o[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll 1
-  for (int i0 = 0; i0 < d.pieces; i0 += 4) {
+  for (int i0 = 4 * group; i0 < d.pieces; i0 += 4 * kGroups) {
     float2 ml[4];
     float4 x[4], y[4];
 #pragma unroll
@@ -157,6 +164,41 @@ __global__ void __launch_bounds__(32 * kWarps) join_chunk_kernel(const PagedAttn
       o[7] += w * y[u].w;
     }
   }
+  if constexpr (kGroups > 1) {
+    __shared__ float2 s_ml[kGroups - 1][32 * kWarps];
+    __shared__ float4 s_o[kGroups - 1][2][32 * kWarps];
+    const int at = threadIdx.x % (32 * kWarps);
+    if (group > 0) {
+      s_ml[group - 1][at] = make_float2(m, l);
+      s_o[group - 1][0][at] = make_float4(o[0], o[1], o[2], o[3]);
+      s_o[group - 1][1][at] = make_float4(o[4], o[5], o[6], o[7]);
+    }
+    __syncthreads();
+    if (group > 0) return;
+    const float own = m;
+#pragma unroll
+    for (int k = 0; k < kGroups - 1; ++k) m = fmaxf(m, s_ml[k][at].x);
+    const float f = own == -INFINITY ? 0.f : ex2_approx(own - m);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float2 ml = s_ml[k][at];
+      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+      const float4 x = s_o[k][0][at], y = s_o[k][1][at];
+      l += w * ml.y;
+      o[0] += w * x.x;
+      o[1] += w * x.y;
+      o[2] += w * x.z;
+      o[3] += w * x.w;
+      o[4] += w * y.x;
+      o[5] += w * y.y;
+      o[6] += w * y.z;
+      o[7] += w * y.w;
+    }
+  }
+  if (kGroups > 1 && row >= d.rows) return;
   const int rho = d.rho0 + row, i = div_group(a, rho);
   const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
   const float inv = join_inverse(l);
@@ -169,10 +211,13 @@ __global__ void __launch_bounds__(32 * kWarps) join_chunk_kernel(const PagedAttn
 
 }  // namespace
 
-cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s) {
+cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
+                              cudaStream_t s) {
   if (row_tile <= kPagedFewRows)
     return launch_dependent(join_few_kernel, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile);
-  return launch_dependent(join_chunk_kernel, dim3(ctas, kPagedChunkRows / 8), dim3(32 * kWarps), 0, s, a, ws);
+  const dim3 grid(ctas, kPagedChunkRows / 8);
+  if (many_parts) return launch_dependent(join_chunk_kernel<4>, grid, dim3(32 * kWarps * 4), 0, s, a, ws);
+  return launch_dependent(join_chunk_kernel<1>, grid, dim3(32 * kWarps), 0, s, a, ws);
 }
 
 }  // namespace sa
