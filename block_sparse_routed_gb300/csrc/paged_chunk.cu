@@ -326,6 +326,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
   };
   // K's slot of the CTA's x-th key tile is 2x, V's 2x + 1 of one sequence.
   constexpr int kSlots = C::kSlots;
+  // What the producer loads into: the ring, or the staged codes.
+  constexpr int kBufs = kKind ? kStageSlots : kSlots;
+  constexpr int kFull = kKind ? BAR_SGFULL : BAR_FULL, kEmpty = kKind ? BAR_SGEMPTY : BAR_EMPTY;
+  int q = 0;  // producer: tiles of K or V so far
   bool ok = true;
 
   if (warp < 4) setmaxnreg_dec<C::kRegsControl>();
@@ -338,10 +342,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     walk_begin<Line>(a, w, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
-    int q = 0, buf = 0, round = 0;  // tiles of K or V so far, the next one's slot and use of it
+    int buf = 0, round = 0;  // the next tile's slot and use of it
     const uint32_t elect = elect_one();
-    constexpr int kBufs = kKind ? kStageSlots : kSlots;
-    constexpr int kFull = kKind ? BAR_SGFULL : BAR_FULL, kEmpty = kKind ? BAR_SGEMPTY : BAR_EMPTY;
     auto next_buf = [&] {
       ++q;
       if (++buf == kBufs) {
@@ -433,11 +435,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       }
     }
     bad = __any_sync(0xFFFFFFFFu, bad);
-    if (!ok) {
-      *s_abort = 1;
-      // copies in flight land before the CTA ends (bounded)
-      for (int x = max(0, q - kBufs); x < q; ++x) drain(kFull + x % kBufs, x / kBufs);
-    }
+    if (!ok) *s_abort = 1;
     if (lane == 0) {
       ws.join[blockIdx.x] = join;
       if (bad) *s_bad = 1;
@@ -832,7 +830,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       x += g.nt;
       y += g.nt;
     }
-    if (!ok) *s_abort = 1;
+    if (!ok) {
+      tmem_wait_st();  // stores in flight complete before tensor memory is freed
+      *s_abort = 1;
+    }
   } else if constexpr (kKind != 0) {
     // ------------------------------------------------------------ widening
     setmaxnreg_dec<C::kRegsConvert>();
@@ -840,14 +841,14 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     // of slots, the same slots always: they see every phase of their barriers).
     static_assert(kSlots % 2 == 0 && kStageSlots % 2 == 0, "slots of the widening warps");
     const int kv = (warp - 12) / 2;
-    int q = kv;
+    int x = kv;
     for (int k = 0; ok; ++k) {
       Segment g;
       ok = next_seg(k, g);
       if (!ok || !g.valid) break;
-      for (int j = 0; j < g.nt; ++j, q += 2) {
-        const int b = q % kStageSlots, slot = q % kSlots;
-        ok = all_wait2(BAR_SGFULL + b, q / kStageSlots, BAR_EMPTY + slot, q >= kSlots ? q / kSlots - 1 : -1);
+      for (int j = 0; j < g.nt; ++j, x += 2) {
+        const int b = x % kStageSlots, slot = x % kSlots;
+        ok = all_wait2(BAR_SGFULL + b, x / kStageSlots, BAR_EMPTY + slot, x >= kSlots ? x / kSlots - 1 : -1);
         if (!ok) break;
         const int key0 = (g.t0 + j) * kTileKeys;
         const uint32_t src = sbase + C::kOffStage + b * kStageBytes, dst = sbase + C::kOffRing + slot * kSlotBytes;
@@ -936,6 +937,11 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Where a warp has given up, nobody may have waited for the last loads: they
+  // land before the CTA ends (bounded).  Only here is it known: the producer
+  // may have issued all its loads before another warp's wait fails.
+  if (warp == 0 && *s_abort)
+    for (int x = max(0, q - kBufs); x < q; ++x) drain(kFull + x % kBufs, x / kBufs);
   if (warp == 1) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0) ws.cta_status[blockIdx.x] = *s_abort ? 5 /* SA_ETIMEOUT */ : (*s_bad ? kPagedInvalid : 0);
   griddep_launch_dependents();

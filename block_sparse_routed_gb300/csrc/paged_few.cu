@@ -224,6 +224,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   // takes the fewest registers).
   const float inv_group = 1.0f / static_cast<float>(a.group);
   auto token_of = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
+  int seq = 0, steps = 0;  // producer: stages and descriptions so far
 
   if (warp == C::kConsumers) {
     // ------------------------------------------------------------ producer
@@ -238,7 +239,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     JoinDesc join;
     join.pieces = 0;
     bool ok = true;
-    int stage = 0, seq = 0;
+    int stage = 0;
     const int per_page = min(c.page_size, kTileKeys);        // keys of a tile in one page
     const int tile_pages = kTileKeys / per_page;
     const uint32_t elect = elect_one();
@@ -279,6 +280,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         segs[k % kSegs] = g;
         mbar_arrive(bar(BAR_SFULL + k % kSegs));
       }
+      ++steps;
       if (!g.valid) break;
       entry = checked(entry);
       for (int t = g.t0; t < g.t0 + g.nt; ++t) {
@@ -329,13 +331,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       }
     }
     bad = __any_sync(0xFFFFFFFFu, bad);
-    if (!ok) {
-      *s_abort = 1;
-      // copies in flight land before the CTA ends (bounded)
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      for (int q = max(0, seq - C::kStages); q < seq; ++q)
-        mbar_wait(bar(BAR_FULL + q % C::kStages), (q / C::kStages) & 1, kWaitLimitNs);
-    }
+    if (!ok) *s_abort = 1;
     if (lane == 0) {
       ws.join[blockIdx.x] = join;
       if (bad) *s_bad = 1;
@@ -729,6 +725,15 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (!ok) *s_abort = 1;
   }
   __syncthreads();
+  // Where a warp has given up, nobody may have waited for the last loads: they
+  // land before the CTA ends (bounded).  Only here is it known: the producer
+  // may have issued all its loads before another warp's wait fails.
+  if (warp == C::kConsumers && *s_abort) {
+    for (int k = max(0, steps - kSegs); k < steps; ++k)
+      mbar_wait(bar(BAR_SFULL + k % kSegs), (k / kSegs) & 1, kWaitLimitNs);
+    for (int q = max(0, seq - C::kStages); q < seq; ++q)
+      mbar_wait(bar(BAR_FULL + q % C::kStages), (q / C::kStages) & 1, kWaitLimitNs);
+  }
   if (threadIdx.x == 0) ws.cta_status[blockIdx.x] = *s_abort ? 5 /* SA_ETIMEOUT */ : (*s_bad ? kPagedInvalid : 0);
   griddep_launch_dependents();
 }
