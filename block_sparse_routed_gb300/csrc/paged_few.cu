@@ -629,7 +629,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
         for (int d = kRows; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) l += ml[i].x == -INFINITY ? 0.f : ml[i].y * ex2_approx(ml[i].x - m);
+        for (int i = 0; i < kSteps; ++i)  // (a warp without a reference has the sum 0, or NaN if its logits are)
+          l += ml[i].x == -INFINITY ? ml[i].y : ml[i].y * ex2_approx(ml[i].x - m);
 #pragma unroll
         for (int d = kRows; d < 32; d *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
         if (lane < kRows) s_row[lane] = make_float2(m, l);

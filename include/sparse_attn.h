@@ -420,7 +420,8 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, 
  *   o     BF16 [rows, Hq, 128], contiguous, 32-byte aligned; zeros for a row
  *         that sees no key
  *   lse   optional (may be NULL) float32 [rows, Hq]: natural logarithm of the
- *         sum of exp(logit), -inf for a row that sees no key
+ *         sum of exp(logit), -inf for a row that sees no key, NaN for one
+ *         that sees a logit which is NaN
  *   ws    workspace of sparse_attn_paged_ws_bytes(p) bytes: the status word
  *         in the first 256, then scratch of this call
  * Cached values behind kv_len, or below the window of every row, are never

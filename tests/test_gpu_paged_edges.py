@@ -63,3 +63,89 @@ def test_copies_in_flight_of_a_call_that_gives_up(bsr, kind, lens, news, H, Hq):
         assert bsr.sparse_attn_last_device_status(ws) == 0
         assert torch.equal(o, o2) and torch.equal(lse, l2)
     assert bsr.SA_ETIMEOUT in statuses
+
+
+# ---- values that are not finite
+
+def check_odd(b, q, o, lse, causal=True, window=0):
+    """Every row as the float64 oracle has it: NaN and infinities where it has
+    them, what is finite within the bounds."""
+    og, lg = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    q64 = q.double().cpu().numpy()
+    finite = []
+    for s, n in enumerate(b.lens):
+        if not b.news[s]:
+            continue
+        rows, pos = (list(x) for x in zip(*OP.positions(b.starts, b.lens, s)))
+        k, v = OP.gather(b.k64, b.table_np, s, n), OP.gather(b.v64, b.table_np, s, n)
+        with np.errstate(invalid="ignore", over="ignore"):
+            ro, rl, mass, reach = OP.paged_attention(q64[rows], k, v, pos, n, causal, window)
+            fine = np.isfinite(ro)
+            assert np.array_equal(np.isnan(ro), np.isnan(og[rows])), s
+            assert np.array_equal(ro[np.isinf(ro)], og[rows][np.isinf(ro)]), s
+            ds = (2 * 128 + 8) * U * np.where(np.isfinite(reach), reach, 0)
+            tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 4 * ds + 2.0 ** -21 + 2 * (n + 64) * U)[..., None] * mass
+            assert np.all(np.abs(og[rows] - ro)[fine] <= tol[fine]), s
+            assert np.array_equal(np.isnan(rl), np.isnan(lg[rows])), s
+            assert np.array_equal(rl == -np.inf, lg[rows] == -np.inf), s
+            tl = ds + 2 * (n + 64) * U + 2.0 ** -21 + 4 * U * np.abs(rl)
+            known = np.isfinite(rl)
+            assert np.all(np.abs(lg[rows] - rl)[known] <= tl[known]), s
+        finite.append(fine.reshape(-1))
+    finite = np.concatenate(finite)
+    return finite
+
+
+def set_nan(b, what, s, j):
+    """Key or value of token j of sequence s is NaN (BF16: one dimension of it)."""
+    pg, sl = b.table_np[s, j // b.page], j % b.page
+    t, t64, e = (b.k_pages, b.k64, b.k_exp) if what == "k" else (b.v_pages, b.v64, b.v_exp)
+    if b.kind == "e4m3":
+        e[pg, :, sl] = 255
+        t64[pg, :, sl] = math.nan
+    else:
+        t[pg, :, sl, 17] = math.nan
+        t64[pg, :, sl, 17] = math.nan
+
+
+@KINDS
+@pytest.mark.parametrize("lens,news,H,Hq,window", [
+    ([65, 17, 161], [1, 1, 1], 2, 8, 0),         # the newest key is alone in its sixteen
+    ([161, 33], [4, 3], 1, 4, 0),                # 12 to 16 packed rows
+    ([3000, 81], [1, 1], 1, 4, 16),              # it is alone in the window's last sixteen
+    ([81, 161], [70, 90], 1, 2, 0),              # chunks: alone in its key tile
+    ([500, 161], [60, 1], 1, 4, 1),              # every row sees one key
+])
+def test_a_nan_key_alone_among_the_keys_of_a_warp(bsr, kind, lens, news, H, Hq, window):
+    b = Batch(lens, news, H, 64, kind, seed=3)
+    for s, n in enumerate(lens):
+        set_nan(b, "k", s, n - 1)
+    q, o, lse = run_attention(bsr, b, Hq, window=window)
+    check_odd(b, q, o, lse, True, window)
+    assert lse.isnan().any()
+
+
+def run_with(bsr, b, q, **kw):
+    ws = bsr.paged_workspace(q, b.k_pages, b.table, max(b.news))
+    o, lse = bsr.paged_attn(q, *b.where, max_new=max(b.news), **b.exps, ws=ws, **kw)
+    assert bsr.sparse_attn_last_device_status(ws) == 0
+    return o, lse
+
+
+@KINDS
+@pytest.mark.parametrize("lens,news,H,Hq", [
+    ([40, 5], [1, 1], 1, 4),                     # one part
+    ([9505, 100], [1, 1], 2, 8),                 # cut into many and joined
+    ([9505, 100], [4, 2], 1, 4),
+    ([100, 70], [60, 30], 1, 2),
+    ([9505, 100], [150, 40], 1, 4),
+])
+def test_a_nan_in_a_query_row(bsr, kind, lens, news, H, Hq):
+    """One head of one row has a NaN: its output and its log-sum-exp are NaN
+    (-inf would say that it sees no key), and no other's."""
+    b = Batch(lens, news, H, 64, kind, seed=3)
+    q = (torch.randn((b.rows, Hq, 128), generator=torch.Generator().manual_seed(5)).bfloat16() * 2).cuda()
+    q[0, 1, 77] = math.nan
+    o, lse = run_with(bsr, b, q)
+    check_odd(b, q, o, lse)
+    assert lse.isnan().sum() == 1 and o.isnan().sum() == 128
