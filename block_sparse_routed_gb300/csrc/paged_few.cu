@@ -550,7 +550,8 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           for (int e = 0; e < 4; ++e) {
             const float x = ex2_approx(s[n][e] - (ref[n][e & 1] == -INFINITY ? 0.f : ref[n][e & 1]));
             sum[n][e & 1] += x;
-            y[e] = kKind == 0 ? x : (x == 0.f ? 0.f : x * vs[e / 2]);  // (a hidden key's scale may be NaN)
+            // (a hidden key's scale may be NaN; that of a key which is seen counts whatever its probability)
+            y[e] = kKind == 0 ? x : (s[n][e] == -INFINITY ? 0.f : x * vs[e / 2]);
           }
           p[n][0] = transpose8(pack_bf16x2(y[0], y[1]));
           p[n][1] = transpose8(pack_bf16x2(y[2], y[3]));

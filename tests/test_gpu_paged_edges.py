@@ -149,3 +149,28 @@ def test_a_nan_in_a_query_row(bsr, kind, lens, news, H, Hq):
     o, lse = run_with(bsr, b, q)
     check_odd(b, q, o, lse)
     assert lse.isnan().sum() == 1 and o.isnan().sum() == 128
+
+
+@KINDS
+@pytest.mark.parametrize("news", [1, 3, 40])
+def test_a_nan_value_whose_probability_vanishes(bsr, kind, news):
+    """0 * NaN is NaN: a NaN that a row sees is not lost where its key's
+    probability is below every number of 32 bits."""
+    n = 200
+    b = Batch([n], [news], 1, 64, kind, seed=3)
+    q = torch.ones((news, 4, 128), dtype=torch.bfloat16, device="cuda")
+    # token 0: logit -40 * sqrt(128) = -452, the others' near 0
+    pg = b.table_np[0, 0]
+    if kind == "bf16":
+        b.k_pages[pg, 0, 0] = -40.0
+    else:
+        b.k_pages.view(torch.uint8)[pg, 0, 0] = 0xF8  # -256
+        b.k_exp[pg, 0, 0] = 127 - 2
+    b.k64[pg, 0, 0] = -40.0 if kind == "bf16" else -64.0
+    set_nan(b, "v", 0, 0)
+    o, lse = run_with(bsr, b, q)
+    if kind == "bf16":
+        assert o[:, :, 17].isnan().all() and o.isnan().sum() == news * 4
+    else:
+        assert o.isnan().all()
+    assert lse.isfinite().all()
