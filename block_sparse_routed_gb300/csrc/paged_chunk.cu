@@ -77,7 +77,11 @@ constexpr uint32_t kQBytes = 32768;      // of a tile: 2 column halves x [128 ro
 constexpr int kSegs = 2;
 constexpr int kStageSlots = 4;           // staged code tiles (E4M3): [80 keys x 128 B]
 constexpr uint32_t kStageBytes = kTileKeys * 128;
-constexpr float kRescaleLog2 = 32.0f;
+// The reference follows a row's maximum only when that passes it, and then by
+// this much more (log2), so that O is seldom rescaled.  Probabilities relative
+// to it are at most 1: a sum of them times values overflows only where the one
+// relative to the maximum itself would.
+constexpr float kLead = 8.0f;
 // Key tiles of a CTA at least, while there are any.  300 tokens over 600 keys,
 // 8 / 4 heads, E4M3: 22.6 us with 2 or 3, 24.6 with 4, 26.5 with 6; 20 over
 // 8000, 8 / 1 heads, where the parts are to be joined: 46 with 1, 31 with 2.
@@ -668,11 +672,9 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_SREAD + t));
-        // The reference follows the row's maximum only when that has passed it
-        // by 2^32 (p <= 2^32 leaves FP32 room): O is seldom rescaled.
         const float mx = max80(s) * c2;  // (scale > 0)
         const float prev = ref;
-        if (prev == -INFINITY || mx > prev + kRescaleLog2) ref = fmaxf(prev, mx);
+        if (mx > prev) ref = mx + kLead;
         const bool moved = prev != -INFINITY && ref != prev;
         const float neg = ref == -INFINITY ? 0.f : -ref;
         const uint64_t c2x = f2(c2, c2), negx = f2(neg, neg);

@@ -26,9 +26,12 @@
 // largest magnitude to 2^14 (what lies 2^29 below that is lost, far below the
 // FP32 sum's own rounding).  V: BF16, since a probability times its key's
 // scale can leave FP16's range; a word's codes c0..c3 are two dimensions of two keys,
-// and exponent and fraction shifted into place, times 2^120, give the pairs
+// and exponent and fraction shifted into place, times a power of two, give the pairs
 // (c0, c2) and (c1, c3) without a byte permutation.  A key's scale is a power
-// of two: K's multiplies the logit, V's the probability.
+// of two: K's multiplies the logit, V's the probability.  So that the latter
+// stays in BF16's normal range as far down as can be, probabilities are 2^7
+// times what they are in the BF16 kind, and V's codes 2^-7 times: a key of
+// probability p keeps all 8 bits of it for scales down to 2^-126 / p.
 //
 // Two CTAs an SM: four consumer warps and three stages of 32 KB, or, for up
 // to eight rows over E4M3 pages, where the widening takes more instructions
@@ -61,13 +64,19 @@ constexpr int kKeyShift = 6;  // 64 keys a stage
 constexpr int kTileKeys = kPagedFewKeys;
 static_assert(kTileKeys == 1 << kKeyShift, "");
 constexpr uint32_t kQRow = 272;  // bytes of a row of Q in shared memory (256 and padding: other banks for each row)
-constexpr float kRescaleLog2 = 8.0f;
+// The reference follows a row's maximum only when that passes it, and then by
+// this much more (log2), so that O is seldom rescaled.  Probabilities relative
+// to it are at most 1: a sum of them times values overflows only where the one
+// relative to the maximum itself would.
+constexpr float kLead = 7.0f;
 // A unit's beginning (its Q) and end (joining the warps), in stages.
 constexpr int kOverBf16 = 2, kOverE4m3 = 3;
 constexpr uint32_t kRegionBytes = 4096;  // of the merge area: 8 rows x 128 floats
 
 template <int kKind, int kN>
 struct Cfg {
+  // Probabilities reach 2^kTop: what V's codes are short of (E4M3).
+  static constexpr float kTop = kKind == 0 ? 0.0f : 7.0f;
   static constexpr int kGroups = kKind == 1 && kN == 1 ? 2 : 1;  // of four consumer warps, on stages in turn
   static constexpr int kConsumers = 4 * kGroups;
   static constexpr int kThreads = 32 * (kConsumers + 1);
@@ -144,17 +153,17 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 // Codes (c0, c2) and (c1, c3) of a word as BF16 pairs: the seven magnitude
 // bits land on BF16's exponent and upper fraction as the value times 2^-120
-// (subnormal codes as subnormals).
-__device__ __forceinline__ uint32_t times_2_120(uint32_t v) {
+// (subnormal codes as subnormals); what is returned is the value times 2^-7.
+__device__ __forceinline__ uint32_t times_2_113(uint32_t v) {
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x7B807B80u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x78007800u));
   return d;
 }
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-  return times_2_120(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u));
+  return times_2_113(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u));
 }
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
-  return times_2_120(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u));
+  return times_2_113(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u));
 }
 // Codes (c0, c1) and (c2, c3) as FP16 pairs.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -525,17 +534,16 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               if (key < lo[n][e & 1] || key >= hi[n][e & 1]) s[n][e] = -INFINITY;
             }
           }
-          // The reference follows the maximum only when some key passes it by
-          // 2^8 (p <= 256 keeps the sums far inside FP32): the lanes need not
-          // agree on a maximum before that.
+          // The lanes need not agree on a maximum before some key passes the
+          // reference (by 2^kTop).
           float mx[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
-          if (__any_sync(0xFFFFFFFFu, mx[0] > ref[n][0] + kRescaleLog2 || mx[1] > ref[n][1] + kRescaleLog2)) {
+          if (__any_sync(0xFFFFFFFFu, mx[0] > ref[n][0] + C::kTop || mx[1] > ref[n][1] + C::kTop)) {
             float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
               for (int d = 4; d < 32; d *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], d));
-              const float to = mx[e] > ref[n][e] + kRescaleLog2 ? mx[e] : ref[n][e];
+              const float to = mx[e] > ref[n][e] + C::kTop ? mx[e] + (kLead - C::kTop) : ref[n][e];
               f[e] = to == ref[n][e] ? 1.f : ex2_approx(ref[n][e] - to);  // the first keys: 2^-inf = 0
               ref[n][e] = to;
               sum[n][e] *= f[e];
@@ -614,6 +622,10 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) sum[n][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][e], d);
+          if constexpr (kKind != 0) {  // relative to the reference that the outputs have
+            ref[n][e] += C::kTop;
+            sum[n][e] *= 1.0f / 128;
+          }
           if (u == 0) s_ml[warp * kRows + 8 * n + 2 * t4 + e] = make_float2(ref[n][e], sum[n][e]);
         }
       ok = !bar_any<kWorkers>(!ok || *s_abort != 0);

@@ -426,6 +426,10 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, 
  *         in the first 256, then scratch of this call
  * Cached values behind kv_len, or below the window of every row, are never
  * used, whatever they are.
+ * Logits and sums are FP32.  A row's probabilities are taken relative to a
+ * reference that is never below its largest logit so far: o is finite where
+ * sum exp(logit - largest) |v| stays under 2^128, and a key 2^118 times less
+ * probable than the most probable one may count as 0.
  * Errors: as sparse_attn_cache_write, and SA_EINVAL for Hq not a multiple of
  * H, causal not 0 or 1, window < 0 or with causal = 0, scale not positive and finite, o
  * not 32-byte or lse not 4-byte aligned, a short workspace.

@@ -174,3 +174,54 @@ def test_a_nan_value_whose_probability_vanishes(bsr, kind, news):
     else:
         assert o.isnan().all()
     assert lse.isfinite().all()
+
+
+# ---- the ends of the formats' ranges
+
+class Filled:
+    """One sequence in a cache that cache_write has filled with the rows k, v
+    [n, H, 128]; k64, v64 are what it then holds."""
+
+    def __init__(self, bsr, k, v, news, page=64, kind="bf16"):
+        n, H, _ = k.shape
+        i32 = dict(dtype=torch.int32, device="cuda")
+        pages = -(-n // page)
+        self.cache = bsr.paged_cache(pages, H, page, kind)
+        self.exps = dict(k_exp=self.cache[2], v_exp=self.cache[3])
+        self.table = torch.randperm(pages, generator=torch.Generator().manual_seed(n)).to(torch.int32)[None].cuda()
+        self.kv_len, self.n, self.news = torch.tensor([n], **i32), n, news
+        self.row_start = torch.tensor([0, news], **i32)
+        all_rows = torch.tensor([0, n], **i32)
+        bsr.cache_write(k.bfloat16().cuda(), v.bfloat16().cuda(), *self.cache[:2], self.table, all_rows, self.kv_len,
+                        **self.exps)
+        back = bsr.cache_read(*self.cache[:2], self.table, all_rows, self.kv_len, rows=n, **self.exps)
+        self.k64, self.v64 = (t.double().cpu().numpy() for t in back)
+
+    def attend(self, bsr, q, **kw):
+        return bsr.paged_attn(q, *self.cache[:2], self.table, self.row_start, self.kv_len, **self.exps, **kw)
+
+    def check(self, q, o, lse, **kw):
+        ro, rl, mass, reach = OP.paged_attention(q.double().cpu().numpy(), self.k64, self.v64,
+                                                 list(range(self.n - self.news, self.n)), self.n, **kw)
+        assert np.isfinite(ro).all()
+        ds = (2 * 128 + 8) * U * reach
+        tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 4 * ds + 2.0 ** -21 + 2 * (self.n + 64) * U)[..., None] * mass
+        assert np.all(np.abs(o.double().cpu().numpy() - ro) <= tol)
+        assert np.all(np.abs(lse.double().cpu().numpy() - rl) <= ds + 2 * (self.n + 64) * U + 2.0 ** -21 + 4 * U * np.abs(rl))
+
+
+@KINDS
+@pytest.mark.parametrize("news", [1, 4, 40, 300])
+@pytest.mark.parametrize("slope", [0.004, 0.02])
+def test_large_values_under_rising_logits(bsr, kind, news, slope):
+    """Values near 2^122 and logits that rise from key to key by 0.065 or 0.33
+    (base 2): at the end of the walk sum 2^(x_j - max) is at most 23, so that
+    sum 2^(x_j - max) |v_j| stays under 2^127, and the result must be finite
+    however far the running reference lags."""
+    n, H = 1500, 64 if news < 16 else 1  # (64 heads: a block walks several key tiles)
+    k = (slope * torch.arange(n, dtype=torch.float32))[:, None, None].expand(n, H, 128)
+    g = torch.Generator().manual_seed(1)
+    v = (0.5 + 0.5 * torch.rand((n, 1, 128), generator=g)).expand(n, H, 128) * 2.0 ** 122
+    f = Filled(bsr, k, v, news, kind=kind)
+    q = torch.ones((news, 4 * H, 128), dtype=torch.bfloat16, device="cuda")
+    f.check(q, *f.attend(bsr, q))
