@@ -23,8 +23,10 @@
 //
 // E4M3 (exact in both products).  K: two cvt make four FP16 values of a word;
 // Q is held in FP16 too, each row scaled by a power of two that brings its
-// largest magnitude to 2^14 (what lies 2^29 below that is lost, far below the
-// FP32 sum's own rounding).  V: BF16, since a probability times its key's
+// largest magnitude to 2^13 or 2^14: exact down to 2^-30 of that (FP16's
+// subnormals hold BF16's 8 bits from 2^-17 on); smaller ones lose bits and
+// vanish below 2^-38 of it, which shows only where a key is 0 in every
+// dimension that is larger.  V: BF16, since a probability times its key's
 // scale can leave FP16's range; a word's codes c0..c3 are two dimensions of two keys,
 // and exponent and fraction shifted into place, times a power of two, give the pairs
 // (c0, c2) and (c1, c3) without a byte permutation.  A key's scale is a power
@@ -176,6 +178,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
@@ -353,7 +357,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     float2* s_row = s_ml + 8 * 16;                                  // [row]: of all warps
     int64_t* s_at = reinterpret_cast<int64_t*>(s_row + 16);         // [row]: where its output goes
     float* s_inv = reinterpret_cast<float*>(s_at + 16);             // [row]: its factor
-    float* s_qinv = s_inv + 16;                                     // [row]: 2^-e of its Q
+    float* s_qinv = s_inv + 16;                                     // [row]: 2^(-e / 2) of its Q
     const float c2 = a.scale * 1.4426950408889634f;
     // ldmatrix rows: lane l gives row l % 8 of matrix l / 8.  K: (keys 0-7,
     // chunk i), (8-15, i), (0-7, i + 1), (8-15, i + 1); V the same in the
@@ -388,22 +392,20 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const uint32_t q0 = lds_b32(at + 8 * lane), q1 = lds_b32(at + 8 * lane + 4);
           const uint32_t m2 = __vmaxu2(q0 & 0x7FFF7FFFu, q1 & 0x7FFF7FFFu);
           const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(m2 >> 16, m2 & 0xFFFFu));
-          // largest magnitude 2^(E - 127): times 2^(141 - E), at most 2^127
-          const int e = min(127, 141 - static_cast<int>(m >> 7));
-          const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          // largest magnitude 2^(E - 127): times 2^(141 - E) or half of it (e is even), at most 2^126
+          const int e = min(126, (141 - static_cast<int>(m >> 7)) & ~1);
+          const float f = pow2(e);
           const uint32_t to = at + lane / 4 * 32 + lane % 4 * 4;
           sts_b32(to, pack_f16x2(bf_lo(q0) * f, bf_hi(q0) * f));
           sts_b32(to + 16, pack_f16x2(bf_lo(q1) * f, bf_hi(q1) * f));
-          // 2^-e, a subnormal number for e = 127
-          if (lane == 0)
-            s_qinv[row] = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          if (lane == 0) s_qinv[row] = pow2(-e / 2);
         }
         bar_all<kWorkers>();
       }
       // Q as the second operand: row u of each tile, dimensions 2t, 2t + 1
       // and 2t + 8, 2t + 9 of 16
       uint32_t qf[kN][8][2];
-      float qinv[kN][2];  // E4M3: undoes the scaling of rows 2t, 2t + 1
+      float qinv[kN][2];  // E4M3: its square undoes the scaling of rows 2t, 2t + 1
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
 #pragma unroll
@@ -492,12 +494,18 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
           }
         }
-        float ks[2], vs[2];
+        // A key's scale as two factors of half its exponent, as Q's: the
+        // product of one of each is a number, whatever the two scales are, and
+        // a logit leaves FP32's range on the way only if it does in the end.
+        float ks[2][2];
+        float vs[2];
         if constexpr (kKind != 0) {
           const uint8_t* ex = base + C::kOffExp + stage * C::kExp + 16 * quarter + u;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            ks[e] = exp_scale(ex[8 * e]) * c2;
+            const int k = ex[8 * e], half = k >> 1;
+            ks[e][0] = pow2(half - 64);
+            ks[e][1] = (k - 1u < 254u ? pow2(k - half - 63) : exp_scale(k)) * c2;
             vs[e] = exp_scale(ex[kTileKeys + 8 * e]);
           }
         }
@@ -524,8 +532,10 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         for (int n = 0; n < kN; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[n][e] *= kKind == 0 ? c2 : qinv[n][e & 1];
-            if constexpr (kKind != 0) s[n][e] *= ks[e / 2];
+            if constexpr (kKind == 0)
+              s[n][e] *= c2;
+            else
+              s[n][e] = s[n][e] * (qinv[n][e & 1] * ks[e / 2][0]) * (qinv[n][e & 1] * ks[e / 2][1]);
           }
           if (cut) {
 #pragma unroll

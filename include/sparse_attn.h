@@ -430,6 +430,8 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const void* k_pages, 
  * reference that is never below its largest logit so far: o is finite where
  * sum exp(logit - largest) |v| stays under 2^128, and a key 2^118 times less
  * probable than the most probable one may count as 0.
+ * For few rows over E4M3 pages, elements of a query head's row below 2^-30 of
+ * its largest one lose bits.
  * Errors: as sparse_attn_cache_write, and SA_EINVAL for Hq not a multiple of
  * H, causal not 0 or 1, window < 0 or with causal = 0, scale not positive and finite, o
  * not 32-byte or lse not 4-byte aligned, a short workspace.

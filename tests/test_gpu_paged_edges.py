@@ -225,3 +225,18 @@ def test_large_values_under_rising_logits(bsr, kind, news, slope):
     f = Filled(bsr, k, v, news, kind=kind)
     q = torch.ones((news, 4 * H, 128), dtype=torch.bfloat16, device="cuda")
     f.check(q, *f.attend(bsr, q))
+
+
+@KINDS
+@pytest.mark.parametrize("news", [1, 4, 40])
+@pytest.mark.parametrize("qe,ke", [(120, -117), (-117, 120), (60, -58), (0, 0)])
+def test_logits_of_large_queries_and_small_keys(bsr, kind, news, qe, ke):
+    """Q near 2^120 and K near 2^-117 and the reverse: their products are
+    ordinary numbers, whatever the order in which scales are applied."""
+    n = 333
+    g = torch.Generator().manual_seed(2)
+    k = torch.randn((n, 1, 128), generator=g) * 2.0 ** ke
+    v = torch.randn((n, 1, 128), generator=g)
+    f = Filled(bsr, k, v, news, kind=kind)
+    q = ((0.25 + torch.rand((news, 4, 128), generator=g)) * 2.0 ** (qe - 2)).bfloat16().cuda()
+    f.check(q, *f.attend(bsr, q))
