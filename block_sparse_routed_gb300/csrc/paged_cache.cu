@@ -63,6 +63,40 @@ __device__ __forceinline__ int64_t slot_of(const PagedArgs& c, int r, int lane, 
   return (static_cast<int64_t>(page) * c.H << c.page_shift) + (pos & (c.page_size - 1));
 }
 
+// Eight codes (BF16 pairs scaled by 2^-e already).
+__device__ __forceinline__ uint2 to_codes(const uint32_t (&v)[4]) {
+  uint16_t half[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(half[k])
+        : "f"(__uint_as_float(v[k] & 0xFFFF0000u)), "f"(__uint_as_float(v[k] << 16)));
+  return make_uint2(half[0] | (static_cast<uint32_t>(half[1]) << 16), half[2] | (static_cast<uint32_t>(half[3]) << 16));
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t v;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(a), "r"(b));
+  return v;
+}
+
+// From 248 * 2^120 on, the nearest code would stand for 256 * 2^120, which is
+// no BF16 number: such elements take 240's, like the largest that round to it.
+// Only rows of the exponent 120 have them.  One thread writes such a row once
+// more, after the barrier behind its first writing: in the kernel's main path
+// a test for it took 2 to 4 us of 67 (9505 tokens of 56 heads).
+constexpr int kLargestExp = 247;
+__device__ __noinline__ void rewrite_largest(const uint16_t* src, uint8_t* dst) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    const uint4 x = ld_once(src + 8 * i);
+    uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = bf16x2_mul(__vminu2(v[k] & 0x7FFF7FFFu, 0x7F777F77u) | (v[k] & 0x80008000u), (254 - kLargestExp) * 0x00800080u);
+    *reinterpret_cast<uint2*>(dst + 8 * i) = to_codes(v);
+  }
+}
+
 template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c, const CacheRows rows, int blocks_h) {
   if (blockIdx.x == 0) paged_check_all(c);
@@ -117,19 +151,9 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c
       const int e = finite ? max(1, static_cast<int>((m + 31) >> 7) - 8) : 255;
       // times 2^(127 - e), exact in BF16; NaN makes every code of the row one
       const uint32_t inv = finite ? (254 - e) * 0x00800080u : 0x7FFF7FFFu;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint16_t half[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t v;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(w[k]), "r"(inv));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-            : "=h"(half[k])
-            : "f"(__uint_as_float(v & 0xFFFF0000u)), "f"(__uint_as_float(v << 16)));
-      }
-      if (real)
-        *reinterpret_cast<uint2*>(pages + row * 128 + sub * 8) =
-            make_uint2(half[0] | (static_cast<uint32_t>(half[1]) << 16), half[2] | (static_cast<uint32_t>(half[3]) << 16));
+      const uint32_t v[4] = {bf16x2_mul(x[i].x, inv), bf16x2_mul(x[i].y, inv), bf16x2_mul(x[i].z, inv),
+                             bf16x2_mul(x[i].w, inv)};
+      if (real) *reinterpret_cast<uint2*>(pages + row * 128 + sub * 8) = to_codes(v);
       if (sub == 0) s_exp[is_v][i][warp] = static_cast<uint8_t>(e);
     }
   }
@@ -138,8 +162,17 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const PagedArgs c
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * kHeads * kTile; i += kThreads) {
       const int t = i % kTile, h = i / kTile % kHeads, v = i / (kTile * kHeads);
-      if (s_slot[t] >= 0 && h0 + h < c.H)
-        (v ? c.v_exp : c.k_exp)[s_slot[t] + (static_cast<int64_t>(h0 + h) << c.page_shift)] = s_exp[v][h][t];
+      if (s_slot[t] >= 0 && h0 + h < c.H) {
+        const int64_t row = s_slot[t] + (static_cast<int64_t>(h0 + h) << c.page_shift);
+        const uint8_t e = s_exp[v][h][t];
+        (v ? c.v_exp : c.k_exp)[row] = e;
+        if (e == kLargestExp) {
+          const int r1 = r - warp + t;
+          rewrite_largest(v ? rows.v + r1 * rows.v_token + (h0 + h) * rows.v_head
+                            : rows.k + r1 * rows.k_token + (h0 + h) * rows.k_head,
+                          (v ? c.v_pages : c.k_pages) + row * 128);
+        }
+      }
     }
   }
 }

@@ -328,12 +328,12 @@ sa_status sparse_attn_spark_reblock(const sa_reblock_params* p, const void* x, i
  *                  even, and k_exp, v_exp uint8 [pages, H, page_size] hold
  *                  e + 127.  Scaling by 2^e is exact both ways, so the
  *                  code's own rounding is the only one, and what a code
- *                  stands for is a BF16 value (it is infinite where rounding
- *                  to 4 bits passes the largest one).  A row that holds a NaN
- *                  or an infinity has the exponent byte 255 and NaN codes:
- *                  all of it stands for NaN.  (NaN codes under another
- *                  exponent byte, which cache_write never makes, are +-480
- *                  to paged_fwd.)
+ *                  stands for is a BF16 value, a finite one (for e = 120 the
+ *                  largest code used is 240's: 256 * 2^120 would not be).  A
+ *                  row that holds a NaN or an infinity has the exponent byte
+ *                  255 and NaN codes: all of it stands for NaN.  (NaN codes
+ *                  under another exponent byte, which cache_write never makes,
+ *                  are +-480 to paged_fwd.)
  * Batch (device memory, int32, read by every call).  Sequence s < seqs has
  *   kv_len[s] tokens; token j is in slot j % page_size of page
  *   table[s * table_stride + j / page_size].  The rows row_start[s] ..

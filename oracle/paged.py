@@ -38,12 +38,13 @@ def quantise_row(bits: np.ndarray):
     while amax > 448.0 * 2.0 ** e:
         e += 1
     vals = e4m3_values()[:127]  # the magnitudes, ascending with the code
+    vals = vals[vals * 2.0 ** e <= 255 * 2.0 ** 120]  # that stand for a finite BF16 value
     codes = np.empty(x.shape, dtype=np.uint8)
     for i, v in enumerate(x):
         a = abs(v) * 2.0 ** -e
         hi = int(np.searchsorted(vals, a))  # vals[hi - 1] < a <= vals[hi]
         lo = max(hi - 1, 0)
-        hi = min(hi, 126)
+        hi = min(hi, len(vals) - 1)
         dl, dh = a - vals[lo], vals[hi] - a
         c = lo if dl < dh or (dl == dh and lo % 2 == 0) else hi
         codes[i] = c | (128 if np.signbit(v) else 0)

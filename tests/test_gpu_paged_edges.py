@@ -240,3 +240,52 @@ def test_logits_of_large_queries_and_small_keys(bsr, kind, news, qe, ke):
     f = Filled(bsr, k, v, news, kind=kind)
     q = ((0.25 + torch.rand((news, 4, 128), generator=g)) * 2.0 ** (qe - 2)).bfloat16().cuda()
     f.check(q, *f.attend(bsr, q))
+
+
+@pytest.mark.parametrize("H", [1, 3, 8])
+def test_the_largest_values_stay_finite(bsr, H):
+    """256 * 2^120 is no BF16 number: what would round to it takes 240 * 2^120,
+    which is at most half a step (2^-4) off."""
+    n = 20
+    x = torch.randn((n, H, 128), generator=torch.Generator().manual_seed(3))
+    top = [3.3895e38, 3.31e38, 248 * 2.0 ** 120, 247 * 2.0 ** 120, 3.2e38, 2.0 ** 127, 2.0 ** 120]
+    for i, t in enumerate(top):
+        x[i, i % H] *= t / 4
+        x[i, i % H, 5:9] = torch.tensor([t, -t, t / 2, -t / 3])
+    x[8, 0, 3], x[8, 0, 4] = math.inf, 3.3895e38
+    x[9, 0, 3], x[9, 0, 4] = math.nan, 3.3895e38
+    x = x.clamp(-3.3895e38, 3.3895e38).where(x.isfinite(), x).bfloat16()
+    b = Batch([n], [n], H, 16, "e4m3")
+    xc = x.cuda()
+    bsr.cache_write(xc, xc, *b.where, **b.exps)
+    for j in range(n):
+        pg, sl = b.table_np[0, j // 16], j % 16
+        for h in range(H):
+            want, byte = OP.quantise_row(bits(x[j, h]))
+            for t, e in ((b.k_pages, b.k_exp), (b.v_pages, b.v_exp)):
+                code = t.view(torch.uint8)[pg, h, sl].cpu().numpy()
+                assert e[pg, h, sl].item() == byte
+                assert np.all((code == want) | ((code & 127 == 127) & (want & 127 == 127))), (j, h)
+    k, _ = bsr.cache_read(*b.where, rows=n, **b.exps)
+    k, x = k.double().cpu(), x.double()
+    fine = x.isfinite().all(-1)
+    assert k[fine].isfinite().all() and k[~fine].isnan().all()
+    err, amax = (k - x).abs()[fine], x.abs().amax(-1, keepdim=True).expand_as(x)[fine]
+    # half a step, or half of the smallest step of a row whose largest code is 240 or more
+    assert (err <= torch.maximum(2.0 ** -4 * x.abs()[fine], 2.0 ** -10 * amax / 224)).all()
+
+
+@KINDS
+@pytest.mark.parametrize("news", [1, 4, 40, 300])
+def test_the_largest_values_reach_only_the_rows_that_see_them(bsr, kind, news):
+    """Values of 3.39e38 in the newest tokens: rows that do not see them have
+    the results of a cache without, the others finite ones."""
+    n = 400
+    g = torch.Generator().manual_seed(4)
+    k, v = torch.randn((n, 1, 128), generator=g), torch.randn((n, 1, 128), generator=g)
+    for j in (n - 1, n - 1 - news // 2):
+        v[j, 0, 10:20] = 3.3895e38
+        v[j, 0, 20:30] = -3.3895e38
+    f = Filled(bsr, k, v, news, kind=kind)
+    q = torch.randn((news, 4, 128), generator=g).bfloat16().cuda()
+    f.check(q, *f.attend(bsr, q))

@@ -1,0 +1,30 @@
+"""The paged cache without a GPU: the ends of the E4M3 format's range and the
+Python layer's checks of its arguments."""
+
+import numpy as np
+import pytest
+
+import oracle as O
+from oracle import paged as OP
+
+
+# ---- the oracle
+
+@pytest.mark.parametrize("amax,code", [
+    (255 * 2.0 ** 120, 0x77),  # BF16's largest: 240 * 2^120, since 256 * 2^120 is not finite
+    (248 * 2.0 ** 120, 0x77),
+    (247 * 2.0 ** 120, 0x77),
+    (232 * 2.0 ** 120, 0x76),  # half way between 224 and 240: even
+    (224 * 2.0 ** 120, 0x7E),  # 448 * 2^119
+    (2.0 ** 127, 0x78),        # 256 * 2^119
+])
+def test_codes_stand_for_finite_values(amax, code):
+    bits = np.zeros(128, dtype=np.uint16)
+    bits[7] = int(np.array([amax], dtype=np.float32).view(np.uint32)[0]) >> 16
+    bits[9] = bits[7] | 0x8000
+    codes, byte = OP.quantise_row(bits)
+    assert codes[7] == code and codes[9] == code | 128 and byte == (247 if code < 0x7E and amax > 2.0 ** 127 else 246)
+    back = OP.dequantise(codes[None], np.array([byte]))[0]
+    ref = O.decode_bf16(bits)
+    assert np.all(np.abs(back) <= 255 * 2.0 ** 120)
+    assert np.all(np.abs(back - ref) <= 2.0 ** -4 * np.abs(ref))
