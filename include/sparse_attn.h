@@ -331,9 +331,12 @@ sa_status sparse_attn_spark_reblock(const sa_reblock_params* p, const void* x, i
  *                  stands for is a BF16 value, a finite one (for e = 120 the
  *                  largest code used is 240's: 256 * 2^120 would not be).  A
  *                  row that holds a NaN or an infinity has the exponent byte
- *                  255 and NaN codes: all of it stands for NaN.  (NaN codes
- *                  under another exponent byte, which cache_write never makes,
- *                  are +-480 to paged_fwd.)
+ *                  255 and NaN codes: all of it stands for NaN.  Two things
+ *                  that cache_write never makes stand for nothing certain: a
+ *                  NaN code under another exponent byte (to paged_fwd it is a
+ *                  NaN or 480, by the form that a call takes) and a code that
+ *                  with its exponent byte is past the largest BF16 value
+ *                  (outputs of that sequence are unspecified).
  * Batch (device memory, int32, read by every call).  Sequence s < seqs has
  *   kv_len[s] tokens; token j is in slot j % page_size of page
  *   table[s * table_stride + j / page_size].  The rows row_start[s] ..

@@ -289,3 +289,30 @@ def test_the_largest_values_reach_only_the_rows_that_see_them(bsr, kind, news):
     f = Filled(bsr, k, v, news, kind=kind)
     q = torch.randn((news, 4, 128), generator=g).bfloat16().cuda()
     f.check(q, *f.attend(bsr, q))
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("news", [1, 3, 40])
+def test_nan_codes_under_a_finite_exponent(bsr, what, news):
+    """A foreign code 127 in the newest token: NaN or 480 times its scale to
+    the rows that see it, nothing to the others, in either form."""
+    n = 100
+    b = Batch([n, 70], [news, 1], 1, 64, "e4m3", seed=3)
+    q = torch.randn((b.rows, 4, 128), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    base, _ = run_with(bsr, b, q)
+    pages, p64, exp = (b.k_pages, b.k64, b.k_exp) if what == "k" else (b.v_pages, b.v64, b.v_exp)
+    pg, sl = b.table_np[0, (n - 1) // 64], (n - 1) % 64
+    pages.view(torch.uint8)[pg, 0, sl, 9] = 127
+    exp[pg, 0, sl] = 127
+    p64[pg, 0, sl] = OP.dequantise(pages.view(torch.uint8)[pg, 0, sl].cpu().numpy()[None], np.array([127]))[0]
+    p64[pg, 0, sl, 9] = 480.0
+    o, _ = run_with(bsr, b, q)
+    last = np.array([news - 1])
+    others = np.setdiff1d(np.arange(b.rows), last)
+    assert torch.equal(o[others], base[others])
+    k, v = OP.gather(b.k64, b.table_np, 0, n), OP.gather(b.v64, b.table_np, 0, n)
+    ro, _, mass, reach = OP.paged_attention(q.double().cpu().numpy()[last], k, v, [n - 1], n)
+    got = o.double().cpu().numpy()[last]
+    ds = (2 * 128 + 8) * U * reach
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 4 * ds + 2.0 ** -21 + 2 * (n + 64) * U)[..., None] * mass
+    assert np.all(np.isnan(got) | (np.abs(got - ro) <= tol))
