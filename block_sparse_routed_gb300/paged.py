@@ -45,6 +45,10 @@ def _env():
 @functools.lru_cache(maxsize=4096)
 def _params(*fields):
     """(C parameters, a reference to them) of a call's sizes: a plain function of numbers."""
+    for (name, kind), x in zip(SaPagedParams._fields_[1:], fields):
+        bits = 8 * ctypes.sizeof(kind) - 1
+        if kind is not ctypes.c_float and not -(1 << bits) <= x < 1 << bits:  # (ctypes would cut it)
+            raise ValueError(f"{name}: {x} is out of range")
     p = SaPagedParams(_native.SA_ABI_VERSION, *fields)
     return p, ctypes.byref(p)
 
@@ -257,6 +261,8 @@ def paged_attn(q, k_pages, v_pages, table, row_start, kv_len, max_new=None, caus
         raise ValueError("q's heads must be a multiple of the cache's")
     if window < 0 or (window and not causal):
         raise ValueError("window: 0, or a positive number with causal=True")
+    if window > 0x7FFFFFFF:  # more tokens than a sequence can have
+        window = 0x7FFFFFFF
     max_new = n if max_new is None or max_new > n else max_new
     if max_new < 0:
         raise ValueError("max_new must not be negative")

@@ -316,3 +316,15 @@ def test_nan_codes_under_a_finite_exponent(bsr, what, news):
     ds = (2 * 128 + 8) * U * reach
     tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 4 * ds + 2.0 ** -21 + 2 * (n + 64) * U)[..., None] * mass
     assert np.all(np.isnan(got) | (np.abs(got - ro) <= tol))
+
+
+# ---- arguments and streams
+
+@pytest.mark.parametrize("news", [1, 40])
+def test_a_window_past_32_bits_is_all_keys(bsr, news):
+    b = Batch([300, 70], [news, 1], 1, 64, seed=3)
+    q = torch.randn((b.rows, 4, 128), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    want, lse = run_with(bsr, b, q)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 + 1, 10 ** 30):
+        o, l2 = run_with(bsr, b, q, window=window)
+        assert torch.equal(o, want) and torch.equal(l2, lse), window

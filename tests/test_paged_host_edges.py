@@ -28,3 +28,30 @@ def test_codes_stand_for_finite_values(amax, code):
     ref = O.decode_bf16(bits)
     assert np.all(np.abs(back) <= 255 * 2.0 ** 120)
     assert np.all(np.abs(back - ref) <= 2.0 ** -4 * np.abs(ref))
+
+
+# ---- the Python layer
+
+FIELDS = dict(kind=0, pages=10, H=2, page_size=64, D=128, seqs=3, table_width=4, table_stride=4, rows=7, max_new=7,
+              Hq=4, causal=1, window=0, scale=0.1, at=512, ah=128, bt=512, bh=128)
+
+
+@pytest.mark.parametrize("name", [n for n in FIELDS if n not in ("scale",)])
+@pytest.mark.parametrize("value", [2 ** 63, -2 ** 63 - 1, 2 ** 64 + 16])
+def test_numbers_that_the_structure_cannot_hold_are_refused(name, value):
+    """ctypes would take them modulo 2^32 (2^64)."""
+    from block_sparse_routed_gb300 import paged
+
+    with pytest.raises(ValueError, match="range"):
+        paged._params(*dict(FIELDS, **{name: value}).values())
+
+
+@pytest.mark.parametrize("name", [n for n in FIELDS if n not in ("scale", "table_stride", "at", "ah", "bt", "bh")])
+def test_numbers_past_32_bits_are_refused_where_the_structure_has_32(name):
+    from block_sparse_routed_gb300 import paged
+
+    for value in (2 ** 31, 2 ** 32 + 16, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="range"):
+            paged._params(*dict(FIELDS, **{name: value}).values())
+    p, _ = paged._params(*dict(FIELDS, at=2 ** 40, table_stride=2 ** 33).values())
+    assert p.a_token_stride == 2 ** 40 and p.table_stride == 2 ** 33
