@@ -89,9 +89,9 @@ def _cache(env, k_pages, v_pages, k_exp, v_exp):
     if not k_pages.is_contiguous() or not v_pages.is_contiguous() or v_pages.get_device() != dev:
         raise ValueError("k_pages and v_pages must be contiguous and on one device")
     if kind:
-        n = shape[0] * shape[1] * shape[2]
+        rows = shape[:3]
         for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-            if t is None or t.dtype is not env[3] or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+            if t is None or t.dtype is not env[3] or t.shape != rows or not t.is_contiguous() or t.get_device() != dev:
                 raise ValueError(f"{name}: contiguous uint8 [pages, H, page_size] on the cache's device required")
     elif k_exp is not None or v_exp is not None:
         raise ValueError("a bfloat16 cache has no exponents")
@@ -137,9 +137,11 @@ def _rows(env, t, name, dev):
     return n, h, ts, hs
 
 
-def _given(t, name, n, dtype, dev):
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: contiguous {dtype} tensor with {n} elements on the cache's device required")
+def _given(t, name, shape, dtype, dev):
+    """Checks an output of the given shape (a leading 1 is allowed, as in the rows)."""
+    if (t.dtype is not dtype or (t.shape != shape and t.shape != (1, *shape)) or not t.is_contiguous()
+            or t.get_device() != dev):
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on the cache's device required")
     return t
 
 
@@ -202,9 +204,8 @@ def cache_read(k_pages, v_pages, table, row_start, kv_len, rows=None, k_exp=None
         fresh = [env[0].empty((rows, H, 128), dtype=env[1], device=k_pages.device) for t in (k, v) if t is None]
         new = iter(fresh)
         k, v = (t if t is not None else next(new) for t in (k, v))
-    n = rows * H * 128
-    _given(k, "k", n, env[1], dev)
-    _given(v, "v", n, env[1], dev)
+    _given(k, "k", (rows, H, 128), env[1], dev)
+    _given(v, "v", (rows, H, 128), env[1], dev)
     _, p = _params(kind, pages, H, ps, d, seqs, width, outer, rows, rows, H, 1, 0, 1.0, 0, 0, 0, 0)
     _call(env, "sparse_attn_cache_read", dev, stream, fresh, (
         p, k_pages.data_ptr(), v_pages.data_ptr(), k_exp.data_ptr() if kind else None,
@@ -271,12 +272,12 @@ def paged_attn(q, k_pages, v_pages, table, row_start, kv_len, max_new=None, caus
         o = env[0].empty((n, hq, 128), dtype=env[1], device=k_pages.device)
         fresh.append(o)
     else:
-        _given(o, "o", n * hq * 128, env[1], dev)
+        _given(o, "o", (n, hq, 128), env[1], dev)
     if lse is None:
         lse = env[0].empty((n, hq), dtype=env[0].float32, device=k_pages.device)
         fresh.append(lse)
     else:
-        _given(lse, "lse", n * hq, env[0].float32, dev)
+        _given(lse, "lse", (n, hq), env[0].float32, dev)
     fields = (kind, pages, H, ps, d, seqs, width, outer, n, max_new, hq, 1 if causal else 0, window,
               SCALE if scale is None else scale, qt, qh, 0, 0)
     if ws is None:

@@ -328,3 +328,30 @@ def test_a_window_past_32_bits_is_all_keys(bsr, news):
     for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 + 1, 10 ** 30):
         o, l2 = run_with(bsr, b, q, window=window)
         assert torch.equal(o, want) and torch.equal(l2, lse), window
+
+
+def test_tensors_of_another_shape_are_refused(bsr):
+    b = Batch([200, 90], [4, 1], 2, 64, "e4m3", seed=4)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    q = torch.randn((b.rows, 4, 128), **bf)
+    for o in (torch.empty((4, b.rows, 128), **bf), torch.empty(b.rows * 512, **bf), torch.empty((b.rows, 512), **bf)):
+        with pytest.raises(ValueError, match="o:"):
+            bsr.paged_attn(q, *b.where, **b.exps, o=o)
+    for lse in (torch.empty((4, b.rows), device="cuda"), torch.empty(4 * b.rows, device="cuda")):
+        with pytest.raises(ValueError, match="lse"):
+            bsr.paged_attn(q, *b.where, **b.exps, lse=lse)
+    for name in ("k", "v"):
+        with pytest.raises(ValueError, match=name):
+            bsr.cache_read(*b.where, **b.exps, rows=b.rows, **{name: torch.empty((2, b.rows, 128), **bf)})
+    for name in ("k_exp", "v_exp"):
+        exps = dict(b.exps, **{name: b.exps[name].reshape(2, -1, 64)})
+        with pytest.raises(ValueError, match=name):
+            bsr.paged_attn(q, *b.where, **exps)
+    # rows, outputs and a leading 1
+    o, lse = bsr.paged_attn(q, *b.where, **b.exps)
+    o1, l1 = bsr.paged_attn(q[None], *b.where, **b.exps, o=torch.empty((1, b.rows, 4, 128), **bf),
+                            lse=torch.empty((1, b.rows, 4), device="cuda"))
+    assert torch.equal(o1[0], o) and torch.equal(l1[0], lse)
+    k, v = bsr.cache_read(*b.where, **b.exps, rows=b.rows)
+    k1, _ = bsr.cache_read(*b.where, **b.exps, k=torch.empty((1, b.rows, 2, 128), **bf), v=torch.empty_like(v))
+    assert torch.equal(k1[0], k)

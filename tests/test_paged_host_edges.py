@@ -55,3 +55,18 @@ def test_numbers_past_32_bits_are_refused_where_the_structure_has_32(name):
             paged._params(*dict(FIELDS, **{name: value}).values())
     p, _ = paged._params(*dict(FIELDS, at=2 ** 40, table_stride=2 ** 33).values())
     assert p.a_token_stride == 2 ** 40 and p.table_stride == 2 ** 33
+
+
+def test_an_output_of_another_shape_is_refused():
+    """As many elements in another order are not the output."""
+    torch = pytest.importorskip("torch")
+    from block_sparse_routed_gb300 import paged
+
+    f32 = torch.float32
+    for shape in ((3, 4), (1, 3, 4)):
+        t = torch.zeros(shape)
+        assert paged._given(t, "lse", (3, 4), f32, -1) is t
+    for t in (torch.zeros(4, 3), torch.zeros(12), torch.zeros(3, 1, 4), torch.zeros(4, 3).t(), torch.zeros(2, 3, 4),
+              torch.zeros(3, 4, dtype=torch.float64), torch.zeros(6, 4)[::2]):
+        with pytest.raises(ValueError, match="lse"):
+            paged._given(t, "lse", (3, 4), f32, -1)
