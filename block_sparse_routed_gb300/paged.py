@@ -151,16 +151,23 @@ def _scratch(env, ws, dev, least):
     return ws.data_ptr()
 
 
-def _call(env, name, dev, stream, fresh, args):
-    """Runs a C entry point on ``stream`` (default: the device's current one).
-    ``fresh``: tensors allocated here, kept for the stream that uses them."""
-    if stream is None:
-        raw = env[6](dev)
-    else:
-        raw = stream.cuda_stream
-        if fresh and raw != env[6](dev):
-            for t in fresh:
-                t.record_stream(stream)
+def _new(env, stream, like, shape, dtype):
+    """A tensor that a call on ``stream`` fills.  On another stream than the
+    current one it comes from that stream's pool (what the current stream has
+    freed may still be in use there), and is kept for the current one, where
+    the caller may use it."""
+    if stream is None or stream.cuda_stream == env[6](like.get_device()):
+        return env[0].empty(shape, dtype=dtype, device=like.device)
+    here = env[0].cuda.current_stream(like.device)
+    with env[0].cuda.stream(stream):
+        t = env[0].empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(here)
+    return t
+
+
+def _call(env, name, dev, stream, args):
+    """Runs a C entry point on ``stream`` (default: the device's current one)."""
+    raw = env[6](dev) if stream is None else stream.cuda_stream
     fn = getattr(env[5], name)
     if env[7]() == dev:
         st = fn(*args, raw or None)
@@ -182,7 +189,7 @@ def cache_write(k, v, k_pages, v_pages, table, row_start, kv_len, k_exp=None, v_
     if n != nv or h != H or hv != H:
         raise ValueError("k and v must both be [rows, H, 128] with the cache's H")
     _, p = _params(kind, pages, H, ps, d, seqs, width, outer, n, n, H, 1, 0, 1.0, kt, kh, vt, vh)
-    _call(env, "sparse_attn_cache_write", dev, stream, (), (
+    _call(env, "sparse_attn_cache_write", dev, stream, (
         p, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_exp.data_ptr() if kind else None,
         v_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(),
         None if ws is None else _scratch(env, ws, dev, 256)))
@@ -199,15 +206,10 @@ def cache_read(k_pages, v_pages, table, row_start, kv_len, rows=None, k_exp=None
         if k is None:
             raise ValueError("give rows, or k and v")
         rows = _rows(env, k, "k", dev)[0]
-    fresh = []
-    if k is None or v is None:
-        fresh = [env[0].empty((rows, H, 128), dtype=env[1], device=k_pages.device) for t in (k, v) if t is None]
-        new = iter(fresh)
-        k, v = (t if t is not None else next(new) for t in (k, v))
-    _given(k, "k", (rows, H, 128), env[1], dev)
-    _given(v, "v", (rows, H, 128), env[1], dev)
+    k, v = (_new(env, stream, k_pages, (rows, H, 128), env[1]) if t is None
+            else _given(t, name, (rows, H, 128), env[1], dev) for t, name in ((k, "k"), (v, "v")))
     _, p = _params(kind, pages, H, ps, d, seqs, width, outer, rows, rows, H, 1, 0, 1.0, 0, 0, 0, 0)
-    _call(env, "sparse_attn_cache_read", dev, stream, fresh, (
+    _call(env, "sparse_attn_cache_read", dev, stream, (
         p, k_pages.data_ptr(), v_pages.data_ptr(), k_exp.data_ptr() if kind else None,
         v_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(), k.data_ptr(),
         v.data_ptr(), None if ws is None else _scratch(env, ws, dev, 256)))
@@ -267,24 +269,20 @@ def paged_attn(q, k_pages, v_pages, table, row_start, kv_len, max_new=None, caus
     max_new = n if max_new is None or max_new > n else max_new
     if max_new < 0:
         raise ValueError("max_new must not be negative")
-    fresh = []
     if o is None:
-        o = env[0].empty((n, hq, 128), dtype=env[1], device=k_pages.device)
-        fresh.append(o)
+        o = _new(env, stream, k_pages, (n, hq, 128), env[1])
     else:
         _given(o, "o", (n, hq, 128), env[1], dev)
     if lse is None:
-        lse = env[0].empty((n, hq), dtype=env[0].float32, device=k_pages.device)
-        fresh.append(lse)
+        lse = _new(env, stream, k_pages, (n, hq), env[0].float32)
     else:
         _given(lse, "lse", (n, hq), env[0].float32, dev)
     fields = (kind, pages, H, ps, d, seqs, width, outer, n, max_new, hq, 1 if causal else 0, window,
               SCALE if scale is None else scale, qt, qh, 0, 0)
     if ws is None:
-        ws = env[0].empty(_ws_bytes(*fields), dtype=env[3], device=k_pages.device)
-        fresh.append(ws)
+        ws = _new(env, stream, k_pages, (_ws_bytes(*fields),), env[3])
     _, p = _params(*fields)
-    _call(env, "sparse_attn_paged_fwd", dev, stream, fresh, (
+    _call(env, "sparse_attn_paged_fwd", dev, stream, (
         p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_exp.data_ptr() if kind else None,
         v_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(), o.data_ptr(),
         lse.data_ptr(), _scratch(env, ws, dev, 0), ws.numel()))

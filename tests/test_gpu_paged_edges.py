@@ -355,3 +355,101 @@ def test_tensors_of_another_shape_are_refused(bsr):
     k, v = bsr.cache_read(*b.where, **b.exps, rows=b.rows)
     k1, _ = bsr.cache_read(*b.where, **b.exps, k=torch.empty((1, b.rows, 2, 128), **bf), v=torch.empty_like(v))
     assert torch.equal(k1[0], k)
+
+
+def written_late(sizes):
+    """Tensors of the current stream's pool that are given back at once, with
+    writes to them that come late."""
+    ts = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in sizes]
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for t in ts:
+        t.fill_(7)
+
+
+@pytest.mark.parametrize("call", ["attn", "read"])
+def test_what_a_call_on_another_stream_allocates_is_that_streams(bsr, call):
+    """Memory that the current stream has freed may still be written there: a
+    call on another stream, whose inputs alone are ready, must not get it."""
+    b = Batch([300, 70], [40, 1], 2, 64, seed=9)
+    q = torch.randn((b.rows, 4, 128), device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+
+    def run(**kw):
+        if call == "attn":
+            return bsr.paged_attn(q, *b.where, **kw)
+        return bsr.cache_read(*b.where, rows=b.rows, **kw)
+
+    want = run()
+    sizes = [(t.shape, t.dtype) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    if call == "attn":
+        sizes.append(((bsr.paged_ws_bytes(q, b.k_pages, b.table),), torch.uint8))
+    written_late(sizes)
+    got = run(stream=side)
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("call", ["attn", "read"])
+def test_outputs_of_a_call_on_another_stream_may_be_used_here(bsr, call):
+    """They are used on the current stream, which waits for the other, and
+    dropped: the next call on the other stream must not get their memory while
+    that use is under way."""
+    b = Batch([300, 70], [40, 1], 2, 64, seed=9)
+    q1, q2 = (torch.randn((b.rows, 4, 128), device="cuda").bfloat16() for _ in range(2))
+    k2 = torch.roll(b.k_pages, 1, 0).contiguous()
+    side = torch.cuda.Stream()
+
+    def run(i, **kw):
+        if call == "attn":
+            return bsr.paged_attn((q1, q2)[i], *b.where, **kw)
+        return bsr.cache_read((b.k_pages, k2)[i], *b.where[1:], rows=b.rows, **kw)
+
+    want = run(0)[0].clone()
+    torch.cuda.synchronize()
+    out = run(0, stream=side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(20_000_000)
+    kept = out.clone()
+    del out
+    run(1, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want)
+
+
+def test_a_stream_of_the_default_kind_and_the_current_one(bsr):
+    b = Batch([300, 70], [40, 1], 2, 64, seed=9)
+    q = torch.randn((b.rows, 4, 128), device="cuda").bfloat16()
+    want, lse = bsr.paged_attn(q, *b.where)
+    for stream in (torch.cuda.current_stream(), torch.cuda.default_stream()):
+        o, l2 = bsr.paged_attn(q, *b.where, stream=stream)
+        assert torch.equal(o, want) and torch.equal(l2, lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # and the default one from another
+        o, l2 = bsr.paged_attn(q, *b.where, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(l2, lse)
+
+
+def test_a_captured_call_on_another_stream(bsr):
+    """A branch of a captured graph: outputs and workspace come from the
+    graph's memory."""
+    b = Batch([300, 70], [40, 1], 2, 64, seed=9)
+    q = torch.randn((b.rows, 4, 128), device="cuda").bfloat16()
+    want, _ = bsr.paged_attn(q, *b.where)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        o, _ = bsr.paged_attn(q, *b.where, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        twice = o * 2
+    for _ in range(3):
+        o.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(twice, want * 2)
