@@ -108,7 +108,8 @@ enum {
   BAR_UEMPTY = 28,   // +slot: every role is done with the descriptor
   BAR_DRAIN = 30,    // the S issuer's MMAs drained (abort)
   BAR_DRAIN2 = 31,   // the PV issuer's MMAs drained (abort)
-  NUM_BARS = 32
+  BAR_END = 32,      // +issuer (2): MMAs drained at the CTA's end (abort)
+  NUM_BARS = 34
 };
 static_assert(NUM_BARS * 8 <= 512, "barrier area");
 
@@ -257,6 +258,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   uint32_t* tslot = reinterpret_cast<uint32_t*>(base + kOffMisc);
   volatile int32_t* s_abort = reinterpret_cast<volatile int32_t*>(base + kOffMisc + 16);
   volatile int32_t* s_status = reinterpret_cast<volatile int32_t*>(base + kOffMisc + 24);
+  int32_t* s_loads = reinterpret_cast<int32_t*>(base + kOffMisc + 32);  // K and V tiles, Q tiles that the producer has loaded
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * i; };
   constexpr uint64_t lim = kProbeOnce ? 0 : kWaitLimitNs;  // pipeline waits (drains: kWaitLimitNs)
   auto ent_buf = [&](int slot) { return reinterpret_cast<int32_t*>(base + kOffEnt + 4u * kMaxEnt * slot); };
@@ -592,7 +594,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tma_prefetch_desc(&tm_ak);
         tma_prefetch_desc(&tm_av);
       }
-      int seq = 0;
+      int seq = 0, units = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int slot = k & 1;
@@ -606,6 +608,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_arrive_expect_tx(bar(BAR_QFULL + slot), kQBytes);
         tma_load_2d(sQ, &tm_q, bar(BAR_QFULL + slot), xq, d.row0);
         tma_load_2d(sQ + 16384, &tm_q, bar(BAR_QFULL + slot), xq + 64, d.row0);
+        units = k + 1;
         // Load order (the MMA issuers consume in the same order): K0, K1,
         // K2, then per step j: V_j, K_{j+3}.
         // kind 0: K (or summary keys), kind 1: V (or summary values)
@@ -650,6 +653,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int q = max(0, seq - kSlots); q < seq; ++q)
           mbar_wait(bar(BAR_FULL + q % kSlots), (q / kSlots) & 1, kWaitLimitNs);
       }
+      s_loads[0] = seq;
+      s_loads[1] = units;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S issuer
@@ -1054,6 +1059,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       G += n;
     }
     if (!ok) {
+      tmem_wait_st();  // stores in flight complete before tensor memory is freed
       *s_abort = 1;
       set_status(a.status, 5 /* SA_ETIMEOUT */);
     }
@@ -1062,6 +1068,22 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*s_abort) {
+    // Where a warp has given up, or the lists were refused, a role that was
+    // through by then has waited for nothing: its copies land and its MMAs
+    // complete before the CTA ends (bounded).
+    if (warp == 0 && lane == 0) {
+      for (int q = max(0, s_loads[0] - kSlots); q < s_loads[0]; ++q)
+        mbar_wait(bar(BAR_FULL + q % kSlots), (q / kSlots) & 1, kWaitLimitNs);
+      for (int k = max(0, s_loads[1] - 2); k < s_loads[1]; ++k)
+        mbar_wait(bar(BAR_QFULL + (k & 1)), (k >> 1) & 1, kWaitLimitNs);
+    }
+    if ((warp == 1 || warp == 3) && lane == 0) {
+      umma_commit(bar(BAR_END + warp / 2));
+      mbar_wait(bar(BAR_END + warp / 2), 0, kWaitLimitNs);
+    }
+    __syncthreads();
+  }
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
