@@ -261,7 +261,7 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   const cudaError_t e = f.few ? launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream)
                               : launch_paged_chunk(boxes, a, scratch, ctas, stream);
   if (cuda_failed(e)) return SA_ECUDA;
-  // a dozen parts a unit and more (the chunks' parts have three key tiles at least)
+  // a dozen parts a unit and more (an estimate: the chunks' parts have the places of three key tiles at least)
   const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
   return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
 }

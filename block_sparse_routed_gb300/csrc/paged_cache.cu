@@ -10,9 +10,10 @@
 // its page; in cache_read they have to.
 //
 // Measured (a copy reaches 6.78 TB/s): writing 9505 tokens of 56 heads as E4M3
-// 69 us, 5.94 TB/s (four tokens a warp instead of one: slower); reading
+// 68 us, 6.0 TB/s (four tokens a warp instead of one: slower); reading
 // 67608 tokens of 24 heads back 186 us, 6.72 TB/s; one token of 32 sequences
-// and 8 heads 5.3 us, a launch and two dependent look-ups.
+// and 8 heads 5.3 us alone and 3.2 among others, a launch and two dependent
+// look-ups.
 #include <cstdint>
 
 #include "internal.h"

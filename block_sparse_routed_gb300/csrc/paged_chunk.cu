@@ -47,10 +47,11 @@
 // fills the instruction cache, and what is not in it costs about 100 cycles
 // for every eight instructions.
 //
-// Measured (tensor rate of the visible pairs):
-//   2048 new of 33792, 40 / 8 heads, causal, BF16    950 us  1447 TFLOP/s
-//   8704 of 8704, 24 / 24 heads, causal, BF16        348 us  1338
-//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  324 us  1110
+// Measured (graphs of four calls, with the joining kernel; tensor rate of the
+// visible pairs; the first by the chip's power, 936 to 974 us from run to run):
+//   2048 new of 33792, 40 / 8 heads, causal, BF16    960 us  1431 TFLOP/s
+//   8704 of 8704, 24 / 24 heads, causal, BF16        344 us  1353
+//   1320 new of 9505, 56 / 56 heads, all keys, E4M3  322 us  1117
 // (a cuBLAS product of 8192^3 reaches 1949 alone and 1723 for seconds).
 //
 // Tensor memory: O of tile 0 and 1 in columns [0, 128), [128, 256); S of
@@ -82,7 +83,9 @@ constexpr uint32_t kStageBytes = kTileKeys * 128;
 // to it are at most 1: a sum of them times values overflows only where the one
 // relative to the maximum itself would.
 constexpr float kLead = 8.0f;
-// Key tiles of a CTA at least, while there are any.  300 tokens over 600 keys,
+// The line's places of a CTA are those of this many key tiles at least, while
+// there are any.  (A unit's beginning has places too, so the first CTAs of a
+// unit may have fewer tiles, or none.)  300 tokens over 600 keys,
 // 8 / 4 heads, E4M3: 22.6 us with 2 or 3, 24.6 with 4, 26.5 with 6; 20 over
 // 8000, 8 / 1 heads, where the parts are to be joined: 46 with 1, 31 with 2.
 constexpr int kMinTiles = 3;

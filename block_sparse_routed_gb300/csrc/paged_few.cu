@@ -42,15 +42,16 @@
 // 366 us against 229 for 64 sequences of 8704 keys.)
 //
 // Measured (bytes of the cached keys a second; a copy reaches 6.78 TB/s):
-//   64 sequences of 512 to 33792 keys, 40 / 8 heads, BF16, one new   239 us  6.76 TB/s
-//   96 of them, 56 / 8 heads, E4M3, one new                          269 us  6.23
+//   64 sequences of 512 to 33792 keys, 40 / 8 heads, BF16, one new   238 us  6.79 TB/s
+//   96 of them, 56 / 8 heads, E4M3, one new                          268 us  6.25
 //   64 of 8704, 24 / 8 heads, four new (12 rows): BF16               348 us  6.56
 //                                                 E4M3               229 us  5.02
 // The last is bound by the instructions of the widening and of two products.
 // Small calls are bound by what comes once: about 2 us until the line is
 // walked, 1.5 us for joining the warps, and the
 // joining kernel (16 sequences of 300 to 8704 keys, window 4096, 24 / 8 heads,
-// E4M3, four new: 29.6 us, of which the keys' bytes are 10).  Code that runs
+// E4M3, four new: 25.4 us in a graph of such calls, of which the keys' bytes
+// are 10).  Code that runs
 // once is fetched as it runs, about 100 cycles for every eight instructions,
 // so a unit's beginning and end are kept short.
 #include <cstdint>

@@ -18,6 +18,13 @@ what a call does for positions below 0, and what is checked on the device.
 Nothing here waits for the GPU.  With ``ws`` (a workspace of
 ``paged_workspace``, or 256 bytes for the two copies)
 ``sparse_attn_last_device_status(ws)`` tells what the device found wrong.
+Without it nobody learns that a sequence was refused (more rows than
+``max_new``, a page out of range) or that a call gave up, and outputs that the
+call allocated hold in those rows what the memory held before.
+
+``stream``: another stream than the current one waits for nothing by itself;
+what the call allocates comes from that stream's memory and may be used on the
+current stream once this has waited for the other.
 """
 
 from __future__ import annotations
