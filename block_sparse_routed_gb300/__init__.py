@@ -17,6 +17,8 @@ Two calls, backed by hand-written CUDA kernels in a C-ABI library:
 * ``cache_write`` / ``cache_read`` / ``paged_attn``: a paged key/value cache of
   many sequences (BF16, or E4M3 with a scale a row) and attention of new
   tokens over it (``paged.py``).
+* ``cache_weigh`` / ``cache_evict``: the attention weight that its keys
+  received, and eviction of those that received little (``eviction.py``).
 * ``spark_reblock``: Spark's token reblocking, a per-head permutation of the
   tokens into 64-token blocks by a landmark tree, and its inverse.
 
@@ -36,6 +38,7 @@ from ._native import (  # noqa: F401
     SA_ETIMEOUT,
     SA_EUNSUPPORTED,
     SA_OK,
+    SaEvictParams,
     SaPagedParams,
     SaParams,
     SaReblockParams,
@@ -46,6 +49,11 @@ from ._native import (  # noqa: F401
     sparse_attn_status_string,
 )
 
+from .eviction import (  # noqa: F401
+    cache_evict,
+    cache_weigh,
+    cache_weights,
+)
 from .paged import (  # noqa: F401
     cache_read,
     cache_write,
@@ -58,7 +66,10 @@ from .paged import (  # noqa: F401
 __all__ = [
     "Params",
     "SparseAttnError",
+    "cache_evict",
     "cache_read",
+    "cache_weigh",
+    "cache_weights",
     "cache_write",
     "load_library",
     "paged_attn",

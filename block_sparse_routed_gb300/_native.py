@@ -43,6 +43,9 @@ ENTRY_POINTS = (
     "sparse_attn_cache_read",
     "sparse_attn_paged_ws_bytes",
     "sparse_attn_paged_fwd",
+    "sparse_attn_weigh_ws_bytes",
+    "sparse_attn_cache_weigh",
+    "sparse_attn_cache_evict",
     "sparse_attn_last_device_status",
     "sparse_attn_set_single_probe_waits",
     "sparse_attn_last_cuda_error",
@@ -127,6 +130,16 @@ class SaPagedParams(ctypes.Structure):
     ]
 
 
+class SaEvictParams(ctypes.Structure):
+    _fields_ = [
+        ("keep", ctypes.c_int32),
+        ("first", ctypes.c_int32),
+        ("last", ctypes.c_int32),
+        ("to_width", ctypes.c_int32),
+        ("to_stride", ctypes.c_int64),
+    ]
+
+
 class SparseAttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = int(status)
@@ -189,6 +202,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sparse_attn_paged_ws_bytes.restype = ctypes.c_int
     lib.sparse_attn_paged_fwd.argtypes = [P(SaPagedParams)] + [vp] * 11 + [sz, vp]
     lib.sparse_attn_paged_fwd.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    lib.sparse_attn_weigh_ws_bytes.argtypes = [P(SaPagedParams), P(ctypes.c_uint64)]
+    lib.sparse_attn_weigh_ws_bytes.restype = ctypes.c_int
+    lib.sparse_attn_cache_weigh.argtypes = [P(SaPagedParams), i32, i32] + [vp] * 9 + [sz, vp]
+    lib.sparse_attn_cache_weigh.restype = ctypes.c_int
+    lib.sparse_attn_cache_evict.argtypes = [P(SaPagedParams), P(SaEvictParams)] + [vp] * 12
+    lib.sparse_attn_cache_evict.restype = ctypes.c_int
     lib.sparse_attn_status_string.argtypes = [ctypes.c_int]
     lib.sparse_attn_status_string.restype = ctypes.c_char_p
     _lib = lib

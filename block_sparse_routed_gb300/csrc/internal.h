@@ -207,6 +207,25 @@ struct PagedAttnArgs {
   uint64_t wait_limit;       // of a pipeline wait, ns (0, the testing hook: a single probe)
 };
 
+// Weights of cached keys [pages, H, page_size].
+struct WeighArgs {
+  PagedAttnArgs a;    // (its outputs and V are not used)
+  const float* lse;   // [rows, Hq]
+  float* weights;
+  int first;          // keys below are left as they are
+  int accumulate;     // 0: weights are set; 1: added to those of the tokens before the call's own
+};
+
+struct EvictArgs {
+  float* weights;
+  const int32_t* to_table;  // pages of the tokens that stay, or null: the sequence's first ones
+  int64_t to_stride;
+  int to_width;
+  int keep, first, last;
+  int32_t* kept;            // [seqs, H, keep]
+  int32_t* new_len;         // [seqs]
+};
+
 // What the joining kernel needs of the unit (a tile of packed rows of one
 // sequence and key head) that begins in a CTA's part of the work and does not
 // end there.
@@ -245,6 +264,8 @@ struct PagedForm {
 
 cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
+cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s);
+cudaError_t launch_evict(const PagedArgs& c, const EvictArgs& e, int sms, cudaStream_t s);
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
 // K's and V's maps of the form for chunks, of BF16 pages: boxes of 16 (i + 1)

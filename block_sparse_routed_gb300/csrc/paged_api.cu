@@ -83,6 +83,28 @@ PagedArgs paged_args(const sa_paged_params* p, const void* kp, const void* vp, c
   return c;
 }
 
+PagedAttnArgs attn_args(const sa_paged_params* p, const void* q, const PagedArgs& c, void* o, float* lse) {
+  PagedAttnArgs a;
+  a.c = c;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_token = p->a_token_stride;
+  a.q_head = p->a_head_stride;
+  a.Hq = p->Hq;
+  a.group = p->Hq / p->H;
+  // with 2^l >= group: m = ceil(2^(31 + l) / group) is off by less than 2^l / group, and x < 2^31
+  int l = 0;
+  while ((int64_t(1) << l) < a.group) ++l;
+  a.group_shift = 31 + l;
+  a.group_mul = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + a.group - 1) / a.group);
+  a.causal = p->causal;
+  a.window = p->window;
+  a.scale = p->scale;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.wait_limit = wait_limit_ns();
+  return a;
+}
+
 // The form that computes a call: by the most packed rows of one sequence and
 // key head, from the host's bound.
 PagedForm form_of(const sa_paged_params* p) {
@@ -211,24 +233,8 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   st = static_cast<sa_status>(device_status());
   if (st != SA_OK) return st;
   if (p->rows == 0 || p->seqs == 0) return clear_status(ws, stream);
-  PagedAttnArgs a;
-  a.c = paged_args(p, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, ws);
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_token = p->a_token_stride;
-  a.q_head = p->a_head_stride;
-  a.Hq = p->Hq;
-  a.group = p->Hq / p->H;
-  // with 2^l >= group: m = ceil(2^(31 + l) / group) is off by less than 2^l / group, and x < 2^31
-  int l = 0;
-  while ((int64_t(1) << l) < a.group) ++l;
-  a.group_shift = 31 + l;
-  a.group_mul = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + a.group - 1) / a.group);
-  a.causal = p->causal;
-  a.window = p->window;
-  a.scale = p->scale;
-  a.o = static_cast<uint16_t*>(o);
-  a.lse = lse;
-  a.wait_limit = wait_limit_ns();
+  const PagedAttnArgs a =
+      attn_args(p, q, paged_args(p, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, ws), o, lse);
   const PagedForm f = form_of(p);
   PagedScratch scratch;
   scratch_of(ws, f, &scratch);
@@ -264,4 +270,82 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   // a dozen parts a unit and more (an estimate: the chunks' parts have the places of three key tiles at least)
   const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
   return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
+}
+
+SA_API sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* out) {
+  if (out == nullptr) return SA_EINVAL;
+  const sa_status st = check_attn(p);
+  if (st != SA_OK) return st;
+  *out = kStatusBytes;
+  return SA_OK;
+}
+
+SA_API sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32_t accumulate, const void* q,
+                                         const float* lse, const void* k_pages, const uint8_t* k_exp,
+                                         const int32_t* table, const int32_t* row_start, const int32_t* kv_len,
+                                         float* weights, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  uint64_t need = 0;
+  sa_status st = sparse_attn_weigh_ws_bytes(p, &need);
+  if (st != SA_OK) return st;
+  if (bad_stride(p->a_token_stride) || bad_stride(p->a_head_stride)) return SA_EINVAL;
+  if (first < 0 || (accumulate != 0 && accumulate != 1)) return SA_EINVAL;
+  if (!ws || !weights || (p->rows > 0 && (!q || !lse))) return SA_EINVAL;
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(weights, 16)) return SA_EINVAL;
+  // (V is not read: K stands in for it)
+  st = check_pointers(p, k_pages, k_pages, k_exp, k_exp, table, row_start, kv_len, ws);
+  if (st != SA_OK) return st;
+  if (ws_bytes < need) return SA_EINVAL;
+  st = static_cast<sa_status>(device_status());
+  if (st != SA_OK) return st;
+  st = clear_status(ws, stream);
+  if (st != SA_OK || p->rows == 0 || p->seqs == 0) return st;
+  WeighArgs w;
+  w.a = attn_args(p, q, paged_args(p, k_pages, nullptr, k_exp, nullptr, table, row_start, kv_len, ws), nullptr, nullptr);
+  w.lse = lse;
+  w.weights = weights;
+  w.first = first;
+  w.accumulate = accumulate;
+  const int sms = multiprocessors();
+  if (sms <= 0) return SA_ECUDA;
+  const int64_t rows = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * w.a.group;
+  const int64_t tiles = (int64_t(p->table_width) * p->page_size + 15) / 16 * p->seqs * p->H;
+  if (tiles == 0 || rows == 0) return SA_OK;
+  return cuda_failed(launch_weigh(w, rows, sms, tiles, stream)) ? SA_ECUDA : SA_OK;
+}
+
+SA_API sa_status sparse_attn_cache_evict(const sa_paged_params* p, const sa_evict_params* e, void* k_pages,
+                                         void* v_pages, uint8_t* k_exp, uint8_t* v_exp, float* weights,
+                                         const int32_t* table, const int32_t* kv_len, const int32_t* to_table,
+                                         int32_t* kept, int32_t* new_len, void* ws, cudaStream_t stream) {
+  sa_status st = check_paged(p);
+  if (st != SA_OK) return st;
+  if (e == nullptr) return SA_EINVAL;
+  if (e->keep < 1 || e->first < 0 || e->last < 0 || int64_t(e->first) + e->last > e->keep) return SA_EINVAL;
+  if (to_table && (e->to_width < 0 || e->to_stride < 0)) return SA_EINVAL;
+  // (the blocks of a launch, and positions that a block's step passes)
+  if (int64_t(p->seqs) * p->H >= int64_t(1) << 27 || int64_t(p->table_width) * p->page_size > int64_t(1) << 30)
+    return SA_EUNSUPPORTED;
+  if (!weights || (p->seqs > 0 && (!kept || !new_len))) return SA_EINVAL;
+  if (!aligned(weights, 16) || !aligned(to_table, 4) || !aligned(kept, 4) || !aligned(new_len, 4)) return SA_EINVAL;
+  if (p->seqs > 0 && new_len == kv_len) return SA_EINVAL;  // lengths are read while new ones are written
+  st = check_pointers(p, k_pages, v_pages, k_exp, v_exp, table, k_pages /* no row_start */, kv_len, ws);
+  if (st != SA_OK) return st;
+  st = static_cast<sa_status>(device_status());
+  if (st != SA_OK) return st;
+  st = clear_status(ws, stream);
+  if (st != SA_OK || p->seqs == 0) return st;
+  const PagedArgs c = paged_args(p, k_pages, v_pages, k_exp, v_exp, table, nullptr, kv_len, ws);
+  EvictArgs a;
+  a.weights = weights;
+  a.to_table = to_table;
+  a.to_stride = e->to_stride;
+  a.to_width = e->to_width;
+  a.keep = e->keep;
+  a.first = e->first;
+  a.last = e->last;
+  a.kept = kept;
+  a.new_len = new_len;
+  const int sms = multiprocessors();
+  if (sms <= 0) return SA_ECUDA;
+  return cuda_failed(launch_evict(c, a, sms, stream)) ? SA_ECUDA : SA_OK;
 }

@@ -446,6 +446,83 @@ sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, const v
                                 void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * The attention weight that cached keys receive, by which
+ * sparse_attn_cache_evict chooses: for each key head h and key j >= first of a
+ * sequence with rows in the call,
+ *     w[j] = (what w[j] was, or 0) + sum exp(scale * (q . k_j) - lse)
+ * over the rows that see key j and the query heads that read key head h, in
+ * FP32.  What w[j] was counts with accumulate = 1 and only for tokens before
+ * the call's own rows; a token's own call, and every call with accumulate = 0,
+ * sets it.  Fields of `p`, batch, q and checks as in sparse_attn_paged_fwd
+ * (causal, window, scale as in the call that gave lse); V is not read.
+ *   lse      float32 [rows, Hq], contiguous: sparse_attn_paged_fwd's or
+ *            sparse_attn_prefix_fwd's of the same rows.  A row whose lse is
+ *            -inf counts nothing
+ *   weights  float32 [pages, H, page_size], contiguous, 16-byte aligned: the
+ *            weight of the token in a page's slot
+ *   first    keys at positions below it keep their weights (those that an
+ *            eviction keeps anyway, or a prefix that several sequences share)
+ *   accumulate  0 or 1
+ *   ws       workspace of sparse_attn_weigh_ws_bytes(p) bytes, the status word first
+ * With accumulate = 1 a key that no row sees is left as it was, with 0 it gets
+ * 0.  Sequences without rows are left as they were.  A page that stands in
+ * several rows of the table must lie below `first` in all of them but one;
+ * else its weights are those of one of them, or their sum.  Results do not
+ * depend on the order in which the device works.
+ * Errors: as sparse_attn_paged_fwd; SA_EINVAL also for first < 0, accumulate
+ * not 0 or 1, a null or misaligned lse or weights.
+ */
+sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* out);
+sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32_t accumulate, const void* q,
+                                  const float* lse, const void* k_pages, const uint8_t* k_exp,
+                                  const int32_t* table, const int32_t* row_start, const int32_t* kv_len,
+                                  float* weights, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Eviction: of every sequence with more than `keep` tokens each key head keeps
+ * `keep` of them: the first `first` and the last `last`, and of those between
+ * the ones with the largest weights (of equal ones the earlier; +0 and -0 are
+ * equal, NaN is above all).  The tokens that a head keeps move, in their
+ * order, to the positions 0 .. of the sequence: rows of K and V as they are,
+ * exponents, and weights.  Heads keep different tokens; what a position was is
+ * told by `kept`.  A sequence of at most `keep` tokens keeps all.
+ *   to_table  NULL: in place, the sequence's first pages.  Then no page that
+ *             holds a token at position `first` or later may stand in another
+ *             row of the table.  Else int32 table [seqs] rows of to_width
+ *             entries, to_stride apart: the pages that the tokens go to, none
+ *             of which holds a token of the call.  The old pages stay as they
+ *             were, and sequences that keep all are copied.
+ *   weights   float32 [pages, H, page_size], 16-byte aligned
+ *   kept      int32 [seqs, H, keep]: the former position of the token at
+ *             position i, -1 from the new length on
+ *   new_len   int32 [seqs]: min(kv_len, keep); must not be kv_len itself
+ *   ws        optional (may be NULL): 256 bytes whose first word takes the status
+ * Slots from the new length on are left as they were.  Later rows see kept
+ * tokens by their new positions (a window counts kept tokens).
+ * Of `p`, rows, max_new, Hq, causal, window, scale and the strides are not
+ * used.  Checked on the device: 0 <= kv_len[s] <= table_width * page_size, all
+ * pages of its tokens and of their destinations in [0, pages), room for them
+ * in to_width pages; else SA_EINVAL in the status word: nothing of that
+ * sequence moves, kept is -1 throughout and new_len is kv_len.
+ * Errors before launch: as sparse_attn_cache_write; SA_EINVAL also for keep <
+ * 1, first or last < 0, first + last > keep, a null or misaligned weights,
+ * kept or new_len, new_len == kv_len; SA_EUNSUPPORTED also for seqs * H >=
+ * 2^27, table_width * page_size > 2^30.
+ */
+typedef struct sa_evict_params {
+  int32_t keep;       /* tokens that a sequence may have after the call, >= 1   */
+  int32_t first;      /* tokens at its start that stay, >= 0                    */
+  int32_t last;       /* tokens at its end that stay, >= 0                      */
+  int32_t to_width;   /* entries of a row of to_table, >= 0                     */
+  int64_t to_stride;  /* elements between the rows of to_table, >= 0            */
+} sa_evict_params;
+
+sa_status sparse_attn_cache_evict(const sa_paged_params* p, const sa_evict_params* e, void* k_pages, void* v_pages,
+                                  uint8_t* k_exp, uint8_t* v_exp, float* weights, const int32_t* table,
+                                  const int32_t* kv_len, const int32_t* to_table, int32_t* kept, int32_t* new_len,
+                                  void* ws, cudaStream_t stream);
+
+/*
  * Reads the device status word of `ws` (written by the last plan or fwd
  * enqueued with it).  Synchronises `stream`.  SA_ECUDA if the copy fails.
  */

@@ -100,3 +100,40 @@ def paged_attention(q, k, v, pos, length, causal=True, window=0, scale=None):
             lse[i, h] = m + math.log(p.sum())
             reach[i, h] = abs(scale) * (np.abs(kk) @ np.abs(q[i, h])).max()
     return o, lse, mass, reach
+
+
+def received(q, lse, k, pos, length, causal=True, window=0, scale=None):
+    """Weight that the keys of one sequence receive, fp64: q [n, Hq, 128], lse
+    [n, Hq], k [length, H, 128], pos [n].
+
+    Returns (w, slack, count) [H, length]: w = sum exp(scale q.k - lse) over
+    the rows that see the key and the heads of its group; slack = the same sum
+    with each term times scale * sum_d |q_d k_d| + |lse|, for error bounds;
+    count = the number of terms."""
+    scale = 1 / math.sqrt(HEAD_DIM) if scale is None else scale
+    n, hq, _ = q.shape
+    h = k.shape[1]
+    w, slack, count = np.zeros((h, length)), np.zeros((h, length)), np.zeros((h, length), dtype=int)
+    for i in range(n):
+        lo, hi = visible(int(pos[i]), length, causal, window)
+        for head in range(hq):
+            if hi <= lo or lse[i, head] == -np.inf:
+                continue
+            kh = head // (hq // h)
+            p = np.exp(scale * (k[lo:hi, kh] @ q[i, head]) - lse[i, head])
+            w[kh, lo:hi] += p
+            slack[kh, lo:hi] += p * (scale * (np.abs(k[lo:hi, kh]) @ np.abs(q[i, head])) + abs(lse[i, head]))
+            count[kh, lo:hi] += 1
+    return w, slack, count
+
+
+def survivors(w, keep, first, last):
+    """Positions that one head keeps of tokens with the weights w [n]: the first
+    and last ones, and the largest of the others (of equal ones the earlier;
+    NaN is above all), ascending."""
+    n = len(w)
+    if n <= keep:
+        return list(range(n))
+    middle = range(first, n - last)
+    order = sorted(middle, key=lambda j: (0 if math.isnan(w[j]) else 1, 0.0 if math.isnan(w[j]) else -float(w[j]), j))
+    return sorted(list(range(first)) + order[:keep - first - last] + list(range(n - last, n)))
