@@ -17,6 +17,8 @@ Two calls, backed by hand-written CUDA kernels in a C-ABI library:
 * ``cache_write`` / ``cache_read`` / ``paged_attn``: a paged key/value cache of
   many sequences (BF16, or E4M3 with a scale a row) and attention of new
   tokens over it (``paged.py``).
+* ``prefix_attn``: the same attention where groups of sequences begin with the
+  same tokens, whose keys are then read once (``paged.py``).
 * ``cache_weigh`` / ``cache_evict``: the attention weight that its keys
   received, and eviction of those that received little (``eviction.py``).
 * ``spark_reblock``: Spark's token reblocking, a per-head permutation of the
@@ -61,6 +63,9 @@ from .paged import (  # noqa: F401
     paged_cache,
     paged_workspace,
     paged_ws_bytes,
+    prefix_attn,
+    prefix_workspace,
+    prefix_ws_bytes,
 )
 
 __all__ = [
@@ -76,6 +81,9 @@ __all__ = [
     "paged_cache",
     "paged_workspace",
     "paged_ws_bytes",
+    "prefix_attn",
+    "prefix_workspace",
+    "prefix_ws_bytes",
     "sparse_attn",
     "sparse_attn_fwd",
     "sparse_attn_last_device_status",

@@ -43,6 +43,8 @@ ENTRY_POINTS = (
     "sparse_attn_cache_read",
     "sparse_attn_paged_ws_bytes",
     "sparse_attn_paged_fwd",
+    "sparse_attn_prefix_ws_bytes",
+    "sparse_attn_prefix_fwd",
     "sparse_attn_weigh_ws_bytes",
     "sparse_attn_cache_weigh",
     "sparse_attn_cache_evict",
@@ -203,6 +205,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sparse_attn_paged_fwd.argtypes = [P(SaPagedParams)] + [vp] * 11 + [sz, vp]
     lib.sparse_attn_paged_fwd.restype = ctypes.c_int
     i32 = ctypes.c_int32
+    lib.sparse_attn_prefix_ws_bytes.argtypes = [P(SaPagedParams), i32, P(ctypes.c_uint64)]
+    lib.sparse_attn_prefix_ws_bytes.restype = ctypes.c_int
+    lib.sparse_attn_prefix_fwd.argtypes = [P(SaPagedParams), i32] + [vp] * 13 + [sz, vp]
+    lib.sparse_attn_prefix_fwd.restype = ctypes.c_int
     lib.sparse_attn_weigh_ws_bytes.argtypes = [P(SaPagedParams), P(ctypes.c_uint64)]
     lib.sparse_attn_weigh_ws_bytes.restype = ctypes.c_int
     lib.sparse_attn_cache_weigh.argtypes = [P(SaPagedParams), i32, i32] + [vp] * 9 + [sz, vp]

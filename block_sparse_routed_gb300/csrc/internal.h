@@ -194,6 +194,7 @@ struct CacheRows {
 };
 
 struct PagedAttnArgs {
+  static constexpr bool shared = false;
   PagedArgs c;
   const uint16_t* q;
   int64_t q_token, q_head;
@@ -205,6 +206,18 @@ struct PagedAttnArgs {
   uint16_t* o;               // BF16 [rows, Hq, 128]
   float* lse;                // [rows, Hq] or null
   uint64_t wait_limit;       // of a pipeline wait, ns (0, the testing hook: a single probe)
+};
+
+// Attention where groups of sequences share the whole pages of a prefix: each
+// row's result over the prefix and over its sequence's own keys, which
+// launch_shared_merge joins.
+struct SharedAttnArgs : PagedAttnArgs {
+  static constexpr bool shared = true;
+  int groups;
+  const int32_t* group_start;  // [groups + 1]
+  const int32_t* prefix_len;   // [groups]
+  float* sums;    // [2: prefix, own][16][rows * Hq][8]: FP32 sums relative to the reference, eight dimensions together
+  float2* refs;   // [2][rows * Hq]: reference in log2 units, sum
 };
 
 // Weights of cached keys [pages, H, page_size].
@@ -235,7 +248,8 @@ struct JoinDesc {
   int rho0;    // first packed row of the tile
   int rows;    // packed rows of the tile
   int h;
-  int pad[3];
+  int own;     // SharedAttnArgs: 0 over a prefix, 1 over own keys
+  int pad[2];
 };
 
 // Workspace of paged_fwd: the status words, then a word and a JoinDesc of each
@@ -277,6 +291,11 @@ cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, co
                                cudaStream_t s);
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
                               cudaStream_t s);
+// The same for rows that share prefixes: the chunks' kernel, its join, and the
+// join of the two results of each row.
+cudaError_t launch_shared_chunk(const ChunkMaps& maps, const SharedAttnArgs& a, const PagedScratch& ws, int ctas,
+                                cudaStream_t s);
+cudaError_t launch_shared_join(const SharedAttnArgs& a, const PagedScratch& ws, int ctas, bool many_parts, cudaStream_t s);
 
 // Tensor map of a row-major 2-D array of `elem`-byte elements, box
 // [box_rows, 128 bytes], 128-byte swizzle, zeros past the last row.

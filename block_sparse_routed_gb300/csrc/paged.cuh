@@ -22,6 +22,12 @@ struct PagedSeq {
   int len;   // cached tokens, the new ones among them
 };
 
+// One of the line's sequences where some share a prefix (SharedAttnArgs).
+struct SharedSeq : PagedSeq {
+  int row;    // of the table
+  int page0;  // first page (0: all keys are its own); -1: the keys are a prefix, and all rows of its group see all of them
+};
+
 __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& c, int s, bool& bad) {
   PagedSeq q;
   const int r0 = c.row_start[s], r1 = c.row_start[s + 1];
@@ -141,8 +147,86 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, const PagedSeq&
                           static_cast<uint32_t>(row_tile));
 }
 
-template <class Line>
-__device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const PagedSeq& q, int p) {
+// The sequences of a line: those of the batch, or, where some share a prefix,
+// the prefixes of the groups (the rows of all of a group's sequences over the
+// whole pages of its prefix) and then the sequences with their own keys.
+__device__ __forceinline__ int line_seqs(const PagedAttnArgs& a) { return a.c.seqs; }
+__device__ __forceinline__ PagedSeq line_seq(const PagedAttnArgs& a, int s, bool& bad) { return paged_seq(a.c, s, bad); }
+__device__ __forceinline__ bool line_causal(const PagedAttnArgs& a, const PagedSeq&) { return a.causal; }
+
+__device__ __forceinline__ int line_seqs(const SharedAttnArgs& a) { return a.groups + a.c.seqs; }
+__device__ __forceinline__ bool line_causal(const SharedAttnArgs& a, const SharedSeq& q) { return a.causal && q.page0 >= 0; }
+
+// Shared pages of group g (0 where it has less than two sequences), and its
+// sequences [s0, s1).
+__device__ __forceinline__ int shared_pages(const SharedAttnArgs& a, int g, int& s0, int& s1, bool& bad) {
+  s0 = a.group_start[g];
+  s1 = a.group_start[g + 1];
+  const int len = a.prefix_len[g];
+  bad = s0 < 0 || s1 < s0 || s1 > a.c.seqs || len < 0 || len > (static_cast<int64_t>(a.c.table_width) << a.c.page_shift);
+  return bad || s1 - s0 < 2 ? 0 : len >> a.c.page_shift;
+}
+
+// Shared pages of sequence s.
+__device__ __forceinline__ int shared_before(const SharedAttnArgs& a, int s, bool& bad) {
+  int lo = 0, hi = a.groups;  // groups that start at or before s: [0, lo), behind it: [hi, ..)
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (a.group_start[mid] <= s) lo = mid + 1;
+    else hi = mid;
+  }
+  bad = false;
+  if (lo == 0) return 0;
+  int s0, s1;
+  const int pages = shared_pages(a, lo - 1, s0, s1, bad);
+  return s < s1 ? pages : 0;
+}
+
+__device__ __forceinline__ SharedSeq line_seq(const SharedAttnArgs& a, int v, bool& bad) {
+  SharedSeq q;
+  q.row0 = q.n = q.len = q.row = 0;
+  q.page0 = -1;
+  if (v < a.groups) {
+    int s1;
+    const int pages = shared_pages(a, v, q.row, s1, bad);
+    if (pages > 0) {
+      const int r0 = a.c.row_start[q.row], r1 = a.c.row_start[s1];
+      bad = r0 < 0 || r1 < r0 || r1 > a.c.rows;
+      if (!bad) {
+        q.row0 = r0;
+        q.n = r1 - r0;
+        q.len = pages << a.c.page_shift;
+      }
+    }
+    return q;
+  }
+  bool wrong;
+  static_cast<PagedSeq&>(q) = paged_seq(a.c, v - a.groups, bad);
+  q.row = v - a.groups;
+  q.page0 = shared_before(a, q.row, wrong);
+  const int before = q.page0 << a.c.page_shift;
+  bad |= wrong || (before > 0 && q.len - q.n < before);
+  if (bad) q.n = 0;
+  q.len -= before;
+  return q;
+}
+
+// Where a row's result lies: `at` = row * Hq + head.
+__device__ __forceinline__ int64_t shared_ref(const SharedAttnArgs& a, int own, int64_t at) {
+  return own * (static_cast<int64_t>(a.c.rows) * a.Hq) + at;
+}
+__device__ __forceinline__ int64_t shared_sums(const SharedAttnArgs& a, int own, int chunk, int64_t at) {
+  return ((own * 16 + chunk) * (static_cast<int64_t>(a.c.rows) * a.Hq) + at) * 8;
+}
+
+// What a step's description says of its sequence besides: 1, or for a
+// SharedSeq 1 for a prefix, else 2 + its first page.
+__device__ __forceinline__ int line_kind(const PagedSeq&) { return 1; }
+__device__ __forceinline__ int line_kind(const SharedSeq& q) { return 2 + q.page0; }
+__device__ __forceinline__ int line_row(const PagedSeq&, int s) { return s; }
+__device__ __forceinline__ int line_row(const SharedSeq& q, int) { return q.row; }
+template <class Line, class Args, class Seq>
+__device__ __forceinline__ UnitKeys unit_keys(const Args& a, const Seq& q, int p) {
   constexpr int row_tile = Line::row_tile, key_tile = Line::key_tile;
   const int rows = q.n * a.group;
   int i0 = 0, i1 = q.n - 1;  // first and last new token of the tile
@@ -151,7 +235,7 @@ __device__ __forceinline__ UnitKeys unit_keys(const PagedAttnArgs& a, const Page
     i1 = div_group(a, min((p + 1) * row_tile, rows) - 1);
   }
   UnitKeys u;
-  u.hi = a.causal ? min(q.len, q.len - q.n + i1 + 1) : q.len;
+  u.hi = line_causal(a, q) ? min(q.len, q.len - q.n + i1 + 1) : q.len;
   u.lo = row_lo(a, q.len - q.n + i0);
   if (u.hi <= u.lo) u.lo = u.hi = 0;
   u.t0 = u.lo / static_cast<uint32_t>(key_tile);
@@ -184,14 +268,15 @@ __device__ __forceinline__ int64_t muldiv(int64_t x, int64_t y, int64_t z) {
 
 // Places of one head of the sequences base + lane, one a lane (0 past the
 // last).  Sequences of many row tiles are summed by the whole warp.
-template <class Line>
-__device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, int lane, bool& bad) {
+template <class Line, class Args>
+__device__ __forceinline__ int64_t lane_tiles(const Args& a, int base, int lane, bool& bad) {
+  using Seq = decltype(line_seq(a, 0, bad));
   const int s = base + lane;
-  PagedSeq q;
+  Seq q;
   q.n = q.len = 0;
-  if (s < a.c.seqs) {
+  if (s < line_seqs(a)) {
     bool b;
-    q = paged_seq(a.c, s, b);
+    q = line_seq(a, s, b);
     bad |= b;
   }
   if constexpr (Line::single) {
@@ -206,8 +291,9 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
     while (many) {
       const int src = __ffs(many) - 1;
       many &= many - 1;
-      PagedSeq r;
+      Seq r;
       r.row0 = 0;
+      if constexpr (Args::shared) r.page0 = __shfl_sync(0xFFFFFFFFu, q.page0, src);
       r.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
       r.len = __shfl_sync(0xFFFFFFFFu, q.len, src);
       const int n = __shfl_sync(0xFFFFFFFFu, tiles, src);
@@ -222,54 +308,56 @@ __device__ __forceinline__ int64_t lane_tiles(const PagedAttnArgs& a, int base, 
 }
 // The same for sequences behind the first 32, out of the way where it is long:
 // a small batch's time is that of fetching the code that it runs.
-template <class Line>
-__device__ __noinline__ int64_t far_call(const PagedAttnArgs& a, int base, bool& bad) {
+template <class Line, class Args>
+__device__ __noinline__ int64_t far_call(const Args& a, int base, bool& bad) {
   return lane_tiles<Line>(a, base, threadIdx.x % 32, bad);
 }
-template <class Line>
-__device__ __forceinline__ int64_t far_tiles(const PagedAttnArgs& a, int base, bool& bad) {
+template <class Line, class Args>
+__device__ __forceinline__ int64_t far_tiles(const Args& a, int base, bool& bad) {
   if constexpr (Line::single) return lane_tiles<Line>(a, base, threadIdx.x % 32, bad);
   else return far_call<Line>(a, base, bad);
 }
 
 // One step of a CTA: some key tiles of a unit.
 struct Segment {
-  int valid;       // 0: no more
+  int valid;       // 0: no more; else line_kind of the sequence
   int row0, n, len, h, rho0, rows;
   int lo, hi;      // keys that some row sees
   int all_lo, all_hi;  // keys that every row sees
   int t0, nt;      // key tiles of this step
   int part;        // -1: the unit's output; else the partial result's slot (0 or 1)
-  int s;
+  int s;           // row of the table
 };
 
 // Walks the steps of a CTA's part of the line (by a whole warp, all lanes
 // alike).
-struct LineWalk {
+template <class Seq>
+struct LineWalkOf {
   int64_t at, end, total;
   int ctas;     // CTAs with work: all, or fewer when tiles are few
   int s, h, p;
   int skip;     // places of the unit that earlier CTAs have
-  PagedSeq q;
+  Seq q;
   int tiles;    // row tiles of the sequence
 };
+using LineWalk = LineWalkOf<PagedSeq>;
 
-template <class Line>
-__device__ __forceinline__ void walk_seq(const PagedAttnArgs& a, LineWalk& w) {
+template <class Line, class Args, class Seq>
+__device__ __forceinline__ void walk_seq(const Args& a, LineWalkOf<Seq>& w) {
   bool bad;
-  w.q = paged_seq(a.c, w.s, bad);
+  w.q = line_seq(a, w.s, bad);
   w.tiles = row_tiles(a, w.q, Line::row_tile);
 }
 
 // Finds the part of CTA `cta` of `ctas`.  Sets `bad` when a sequence fails its
 // checks.
-template <class Line>
-__device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, int cta, int ctas, bool& bad) {
+template <class Line, class Args, class Seq>
+__device__ __forceinline__ void walk_begin(const Args& a, LineWalkOf<Seq>& w, int cta, int ctas, bool& bad) {
   const int lane = threadIdx.x % 32;
   const int64_t first = lane_tiles<Line>(a, 0, lane, bad);
   int64_t t = first;
 #pragma unroll 1
-  for (int base = 32; base < a.c.seqs; base += 32) t += far_tiles<Line>(a, base, bad);
+  for (int base = 32; base < line_seqs(a); base += 32) t += far_tiles<Line>(a, base, bad);
   w.total = warp_sum(t) * a.c.H;
   const int64_t most = (w.total + Line::min_places - 1) / Line::min_places;
   w.ctas = static_cast<int>(min(static_cast<int64_t>(ctas), most));
@@ -318,8 +406,8 @@ __device__ __forceinline__ void walk_begin(const PagedAttnArgs& a, LineWalk& w, 
 
 // The next step (valid = 0 at the end); `join` is filled when it leaves a
 // unit unfinished that it began.
-template <class Line>
-__device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w, int cta, JoinDesc& join) {
+template <class Line, class Args, class Seq>
+__device__ __forceinline__ Segment walk_next(const Args& a, LineWalkOf<Seq>& w, int cta, JoinDesc& join) {
   Segment g;
   g.valid = 0;
   while (w.at < w.end) {
@@ -337,19 +425,19 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
     const auto tiles_before = [&](int place) { return (max(0, place - Line::over) + u.each - 1) / u.each; };
     const int from = tiles_before(w.skip), to = tiles_before(w.skip + take);
     if (to > from) {
-      g.valid = 1;
+      g.valid = line_kind(w.q);
       g.row0 = w.q.row0;
       g.n = w.q.n;
       g.len = w.q.len;
       g.h = w.h;
-      g.s = w.s;
+      g.s = line_row(w.q, w.s);
       g.rho0 = w.p * Line::row_tile;
       g.rows = min(Line::row_tile, w.q.n * a.group - g.rho0);
       g.lo = u.lo;
       g.hi = u.hi;
       const int base = w.q.len - w.q.n;
       g.all_lo = row_lo(a, base + div_group(a, g.rho0 + g.rows - 1));
-      g.all_hi = a.causal ? min(w.q.len, base + div_group(a, g.rho0) + 1) : w.q.len;
+      g.all_hi = line_causal(a, w.q) ? min(w.q.len, base + div_group(a, g.rho0) + 1) : w.q.len;
       g.t0 = u.t0 + from;
       g.nt = to - from;
       g.part = from == 0 ? (to == u.nt ? -1 : 1) : 0;
@@ -361,6 +449,7 @@ __device__ __forceinline__ Segment walk_next(const PagedAttnArgs& a, LineWalk& w
         join.rho0 = g.rho0;
         join.rows = g.rows;
         join.h = g.h;
+        if constexpr (Args::shared) join.own = g.valid > 1;
       }
     }
     w.at += take;

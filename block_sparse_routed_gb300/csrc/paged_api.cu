@@ -149,6 +149,34 @@ uint64_t scratch_of(void* ws, const PagedForm& f, PagedScratch* out) {
   return off;
 }
 
+// K's and V's boxes of the form for chunks (BF16 pages).
+bool chunk_maps(const sa_paged_params* p, const void* k_pages, const void* v_pages, ChunkMaps* boxes) {
+  const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
+  bool ok = true;
+  if (p->kind == SA_CACHE_BF16)
+    for (int i = 0; 16 * i < kPagedChunkKeys && 16 * i < p->page_size; ++i)
+      ok = ok && make_map_groups(&boxes->m[0][i], k_pages, cached, 16 * (i + 1)) &&
+           make_map_groups(&boxes->m[1][i], v_pages, cached, 16 * (i + 1));
+  return ok;
+}
+
+// Whether a call with groups of sequences goes by them: its workspace, too.
+bool shares(const sa_paged_params* p, int32_t groups) { return groups > 0 && p->seqs > 1 && p->rows > 0; }
+
+PagedForm chunk_form() { return {kPagedChunkRows, kPagedChunkCtas, false}; }
+
+uint64_t shared_scratch_of(const sa_paged_params* p, void* ws, PagedScratch* scratch, SharedAttnArgs* a) {
+  uint64_t off = align256(scratch_of(ws, chunk_form(), scratch));
+  const uint64_t rows = uint64_t(p->rows) * p->Hq;
+  const uint64_t sums = off; off += align256(2 * rows * kHeadDim * 4);
+  const uint64_t refs = off; off += align256(2 * rows * 8);
+  if (a) {
+    a->sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sums);
+    a->refs = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + refs);
+  }
+  return off;
+}
+
 sa_status clear_status(void* ws, cudaStream_t stream) {
   if (ws && cuda_failed(cudaMemsetAsync(ws, 0, kStatusBytes, stream))) return SA_ECUDA;
   return SA_OK;
@@ -250,10 +278,8 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
              make_map_rows(&tv, v_pages, cached, kHeadDim, 1, box);
     else
       maps = make_map_groups(&tk, k_pages, cached, box) && make_map_groups(&tv, v_pages, cached, box);
-  } else if (p->kind == SA_CACHE_BF16) {
-    for (int i = 0; 16 * i < tile && 16 * i < p->page_size; ++i)
-      maps = maps && make_map_groups(&boxes.m[0][i], k_pages, cached, 16 * (i + 1)) &&
-             make_map_groups(&boxes.m[1][i], v_pages, cached, 16 * (i + 1));
+  } else {
+    maps = chunk_maps(p, k_pages, v_pages, &boxes);
   }
   if (!maps) return SA_ECUDA;
   // no more CTAs than units times the key tiles of the longest context that the table can hold
@@ -270,6 +296,59 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   // a dozen parts a unit and more (an estimate: the chunks' parts have the places of three key tiles at least)
   const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
   return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
+}
+
+SA_API sa_status sparse_attn_prefix_ws_bytes(const sa_paged_params* p, int32_t groups, uint64_t* out) {
+  if (out == nullptr) return SA_EINVAL;
+  const sa_status st = check_attn(p);
+  if (st != SA_OK) return st;
+  if (groups < 0 || p->window != 0) return SA_EINVAL;
+  *out = shares(p, groups) ? shared_scratch_of(p, nullptr, nullptr, nullptr) : scratch_of(nullptr, form_of(p), nullptr);
+  return SA_OK;
+}
+
+SA_API sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups, const void* q, const void* k_pages,
+                                        const void* v_pages, const uint8_t* k_exp, const uint8_t* v_exp,
+                                        const int32_t* table, const int32_t* row_start, const int32_t* kv_len,
+                                        const int32_t* group_start, const int32_t* prefix_len, void* o, float* lse,
+                                        void* ws, size_t ws_bytes, cudaStream_t stream) {
+  uint64_t need = 0;
+  sa_status st = sparse_attn_prefix_ws_bytes(p, groups, &need);
+  if (st != SA_OK) return st;
+  if (!group_start || (groups > 0 && !prefix_len)) return SA_EINVAL;
+  if (!aligned(group_start, 4) || !aligned(prefix_len, 4)) return SA_EINVAL;
+  if (!shares(p, groups))
+    return sparse_attn_paged_fwd(p, q, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, o, lse, ws, ws_bytes,
+                                 stream);
+  if (bad_stride(p->a_token_stride) || bad_stride(p->a_head_stride)) return SA_EINVAL;
+  if (!ws || !q || !o) return SA_EINVAL;
+  if (!aligned(q, 16) || !aligned(o, 32) || !aligned(lse, 4)) return SA_EINVAL;
+  st = check_pointers(p, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, ws);
+  if (st != SA_OK) return st;
+  if (ws_bytes < need) return SA_EINVAL;
+  st = static_cast<sa_status>(device_status());
+  if (st != SA_OK) return st;
+  SharedAttnArgs a;
+  static_cast<PagedAttnArgs&>(a) =
+      attn_args(p, q, paged_args(p, k_pages, v_pages, k_exp, v_exp, table, row_start, kv_len, ws), o, lse);
+  a.groups = groups;
+  a.group_start = group_start;
+  a.prefix_len = prefix_len;
+  PagedScratch scratch;
+  shared_scratch_of(p, ws, &scratch, &a);
+  ChunkMaps boxes{};
+  if (!chunk_maps(p, k_pages, v_pages, &boxes)) return SA_ECUDA;
+  // (as in sparse_attn_paged_fwd; every row is in a unit over its prefix, too)
+  const int64_t units = p->seqs + groups + 2 * ((int64_t(p->rows) * a.group + kPagedChunkRows - 1) / kPagedChunkRows);
+  const int64_t tiles = (int64_t(p->table_width) * p->page_size + kPagedChunkKeys - 1) / kPagedChunkKeys;
+  const int64_t most = units * p->H * (tiles + 1);
+  int ctas = multiprocessors();
+  if (ctas <= 0) return SA_ECUDA;
+  if (ctas > kPagedChunkCtas) ctas = kPagedChunkCtas;
+  if (most < ctas) ctas = static_cast<int>(most);
+  if (cuda_failed(launch_shared_chunk(boxes, a, scratch, ctas, stream))) return SA_ECUDA;
+  const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
+  return cuda_failed(launch_shared_join(a, scratch, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
 }
 
 SA_API sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* out) {

@@ -265,9 +265,9 @@ __device__ __noinline__ void odd_add(uint32_t o_col, const uint16_t* q, const ui
   }
 }
 
-template <int kKind>
+template <int kKind, class Args>
 __global__ void __launch_bounds__(Cfg<kKind>::kThreads, 1)
-paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a, const PagedScratch ws) {
+paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const Args a, const PagedScratch ws) {
   using C = Cfg<kKind>;
   const PagedArgs& c = a.c;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -332,6 +332,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
     if (lane == 0) mbar_arrive(bar(BAR_SEGEMPTY + k % kSegs));
     return true;
   };
+  // Where sequences share a prefix: the first page of a step's keys, and
+  // whether its rows see keys only up to their own.
+  auto first_page = [](const Segment& g) { return Args::shared ? max(0, g.valid - 2) : 0; };
+  auto causal = [&](const Segment& g) { return a.causal && (!Args::shared || g.valid > 1); };
   // K's slot of the CTA's x-th key tile is 2x, V's 2x + 1 of one sequence.
   constexpr int kSlots = C::kSlots;
   // What the producer loads into: the ring, or the staged codes.
@@ -343,8 +347,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (kKind == 0 && lane < 2 * min(kBoxes, c.page_size / kBoxKeys)) tma_prefetch_desc(&maps.m[lane % 2][lane / 2]);
-    LineWalk w;
     bool bad = false;
+    LineWalkOf<decltype(line_seq(a, 0, bad))> w;
     using Line = LineShape<kUnitRows, kTileKeys, C::kHalfPlaces, C::kFullPlaces, C::kOver, kMinTiles * C::kFullPlaces, false>;
     walk_begin<Line>(a, w, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
@@ -367,7 +371,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         mbar_arrive(bar(BAR_SEGFULL + k % kSegs));
       }
       if (!g.valid) break;
-      const int32_t* table = c.table + g.s * c.table_stride;
+      const int32_t* table = c.table + g.s * c.table_stride + first_page(g);
       const int p_lo = g.lo >> c.page_shift, p_hi = (g.hi + c.page_size - 1) >> c.page_shift;
       int have = -64, entry = 0;  // entry: page index have + lane
       for (int t = g.t0; t < g.t0 + g.nt && ok; ++t) {
@@ -633,7 +637,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       const int pos = g.len - g.n + i;
       // a row that does not exist has Q = 0: no mask, and no output
       const int lo = real ? row_lo(a, pos) : 0;
-      const int hi = real ? (a.causal ? min(g.len, pos + 1) : g.len) : 0x7FFFFFFF;
+      const int hi = real ? (causal(g) ? min(g.len, pos + 1) : g.len) : 0x7FFFFFFF;
       float ref = -INFINITY, l = 0.f;
       float whole = 1.f;  // NaN once the row has seen a value that is NaN as a whole
       // O starts as zeros (PV accumulates; the last unit's O has been read)
@@ -752,7 +756,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
               if constexpr (kKind != 0) {
                 if (see) whole = __uint_as_float(0x7FFFFFFFu);  // all of the value is NaN
               } else {
-                const int page = c.table[g.s * c.table_stride + (key >> c.page_shift)];
+                const int page = c.table[g.s * c.table_stride + first_page(g) + (key >> c.page_shift)];
                 if (page < 0 || page >= c.pages) continue;  // (reported by the producer)
                 odd_add(o_col,
                         a.q + static_cast<int64_t>(g.row0 + i) * a.q_token +
@@ -784,7 +788,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
       const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + (rho - i * a.group)
                                     : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows + 128 * t + row;
       float* part = ws.part + (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kUnitRows * kHeadDim;  // (g.part >= 0)
-      const float inv = (g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * whole;  // (NaN stays)
+      const float inv = (Args::shared || g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * whole;  // (NaN stays)
       // Output rows are Hq rows apart, and a store of one row a lane touches 32
       // lines: lanes 4 x .. 4 x + 3 exchange their rows' quarters of 64 bytes
       // first, so that each store has 8 rows of them.
@@ -797,7 +801,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
         uint32_t o[32];
         tmem_ld32(o_col + 32 * b, o);
         tmem_wait_ld();
-        if (g.part < 0) {
+        if (!Args::shared && g.part < 0) {
           uint32_t z[4][4];  // [quarter][word], then [row][word]
 #pragma unroll
           for (int f = 0; f < 16; ++f)
@@ -829,13 +833,18 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
 #pragma unroll
             for (int f = 0; f < 8; ++f) z[f] = __float_as_uint(__uint_as_float(o[dim(8 * e + f)]) * inv);
             // [8 columns][row]: a warp's stores lie side by side
-            st_global_v8(part + ((4 * b + e) * kUnitRows + 128 * t + row) * 8, z);
+            float* to = part + ((4 * b + e) * kUnitRows + 128 * t + row) * 8;
+            if constexpr (Args::shared)
+              if (g.part < 0) to = a.sums + shared_sums(a, g.valid > 1, 4 * b + e, at);
+            st_global_v8(to, z);
           }
         }
       }
       if (real) {
         if (g.part >= 0)
           ws.ml[at] = make_float2(ref, l);
+        else if constexpr (Args::shared)
+          a.refs[shared_ref(a, g.valid > 1, at)] = make_float2(ref, l);
         else if (a.lse)
           a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
       }
@@ -961,10 +970,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const PagedAttnArgs a
   griddep_launch_dependents();
 }
 
-template <int kKind>
-cudaError_t launch(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScratch& ws, int ctas, cudaStream_t s) {
+template <int kKind, class Args>
+cudaError_t launch(const ChunkMaps& maps, const Args& a, const PagedScratch& ws, int ctas, cudaStream_t s) {
   using C = Cfg<kKind>;
-  auto* kern = paged_chunk_kernel<kKind>;
+  auto* kern = paged_chunk_kernel<kKind, Args>;
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
@@ -989,6 +998,11 @@ cudaError_t launch(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScr
 
 cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, const PagedScratch& ws, int ctas,
                                cudaStream_t s) {
+  return a.c.kind == 0 ? launch<0>(maps, a, ws, ctas, s) : launch<1>(maps, a, ws, ctas, s);
+}
+
+cudaError_t launch_shared_chunk(const ChunkMaps& maps, const SharedAttnArgs& a, const PagedScratch& ws, int ctas,
+                                cudaStream_t s) {
   return a.c.kind == 0 ? launch<0>(maps, a, ws, ctas, s) : launch<1>(maps, a, ws, ctas, s);
 }
 

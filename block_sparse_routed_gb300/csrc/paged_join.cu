@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const PagedAttnAr
 // 38 parts a unit: 41 us with one set, 37 with four); with two or three parts
 // a unit they only wait (128 over 1000, 8 / 4 heads: 20.5 us with one, 24 with
 // four).
-template <int kGroups>
+template <int kGroups, class Args>
 __global__ void __launch_bounds__(32 * kWarps * kGroups)
-join_chunk_kernel(const PagedAttnArgs a, const PagedScratch ws) {
+join_chunk_kernel(const Args a, const PagedScratch ws) {
   constexpr int kRows = kPagedChunkRows;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % kWarps, group = threadIdx.x / (32 * kWarps);
   griddep_wait();
@@ -201,6 +201,13 @@ join_chunk_kernel(const PagedAttnArgs a, const PagedScratch ws) {
   if (kGroups > 1 && row >= d.rows) return;
   const int rho = d.rho0 + row, i = div_group(a, rho);
   const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
+  if constexpr (Args::shared) {
+    float4* to = reinterpret_cast<float4*>(a.sums + shared_sums(a, d.own, chunk, at));
+    to[0] = make_float4(o[0], o[1], o[2], o[3]);
+    to[1] = make_float4(o[4], o[5], o[6], o[7]);
+    if (chunk == 0) a.refs[shared_ref(a, d.own, at)] = make_float2(m, l);
+    return;
+  }
   const float inv = join_inverse(l);
   uint32_t z[4];
 #pragma unroll
@@ -209,15 +216,62 @@ join_chunk_kernel(const PagedAttnArgs a, const PagedScratch ws) {
   if (a.lse && chunk == 0) a.lse[at] = join_lse(m, l);
 }
 
+// Rows over their group's prefix and over their own keys: one result.  A block
+// takes a row of the batch; a warp 8 heads x 4 of the 16 times 8 dimensions.
+__global__ void __launch_bounds__(32 * kWarps) shared_merge_kernel(const SharedAttnArgs a) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, r = blockIdx.x;
+  griddep_wait();
+  const int s = paged_find(a.c, r, lane);
+  if (s < 0) return;
+  bool bad;
+  const SharedSeq q = line_seq(a, a.groups + s, bad);
+  if (bad || r < q.row0 || r >= q.row0 + q.n) return;  // (a sequence that is refused, or none)
+  for (int x = warp; x < (a.Hq + 7) / 8 * 4; x += kWarps) {
+    const int head = x / 4 * 8 + lane % 8, chunk = x % 4 * 4 + lane / 8;
+    if (head >= a.Hq) continue;
+    const int64_t at = static_cast<int64_t>(r) * a.Hq + head;
+    const float2 own = a.refs[shared_ref(a, 1, at)];
+    const float4* from = reinterpret_cast<const float4*>(a.sums + shared_sums(a, 1, chunk, at));
+    float4 u = from[0], v = from[1];
+    float m = own.x, l = own.y;
+    if (q.page0 > 0) {
+      const float2 pre = a.refs[shared_ref(a, 0, at)];
+      const float4* other = reinterpret_cast<const float4*>(a.sums + shared_sums(a, 0, chunk, at));
+      const float4 y = other[0], z = other[1];
+      m = fmaxf(own.x, pre.x);
+      const float f = own.x == -INFINITY ? 0.f : ex2_approx(own.x - m);
+      const float g = pre.x == -INFINITY ? 0.f : ex2_approx(pre.x - m);
+      // (a part without a reference has the sum 0, or NaN if its logits are)
+      l = (own.x == -INFINITY ? own.y : f * own.y) + (pre.x == -INFINITY ? pre.y : g * pre.y);
+      u = make_float4(f * u.x + g * y.x, f * u.y + g * y.y, f * u.z + g * y.z, f * u.w + g * y.w);
+      v = make_float4(f * v.x + g * z.x, f * v.y + g * z.y, f * v.z + g * z.z, f * v.w + g * z.w);
+    }
+    const float inv = join_inverse(l);
+    reinterpret_cast<uint4*>(a.o + at * kHeadDim)[chunk] =
+        make_uint4(pack_bf16x2(u.x * inv, u.y * inv), pack_bf16x2(u.z * inv, u.w * inv),
+                   pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    if (a.lse && chunk == 0) a.lse[at] = join_lse(m, l);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_shared_join(const SharedAttnArgs& a, const PagedScratch& ws, int ctas, bool many_parts, cudaStream_t s) {
+  const dim3 grid(ctas, kPagedChunkRows / 8);
+  const cudaError_t e =
+      many_parts ? launch_dependent(join_chunk_kernel<4, SharedAttnArgs>, grid, dim3(32 * kWarps * 4), 0, s, a, ws)
+                 : launch_dependent(join_chunk_kernel<1, SharedAttnArgs>, grid, dim3(32 * kWarps), 0, s, a, ws);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(shared_merge_kernel, dim3(a.c.rows), dim3(32 * kWarps), 0, s, a);
+}
 
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
                               cudaStream_t s) {
   if (row_tile <= kPagedFewRows)
     return launch_dependent(join_few_kernel, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile);
   const dim3 grid(ctas, kPagedChunkRows / 8);
-  if (many_parts) return launch_dependent(join_chunk_kernel<4>, grid, dim3(32 * kWarps * 4), 0, s, a, ws);
-  return launch_dependent(join_chunk_kernel<1>, grid, dim3(32 * kWarps), 0, s, a, ws);
+  if (many_parts) return launch_dependent(join_chunk_kernel<4, PagedAttnArgs>, grid, dim3(32 * kWarps * 4), 0, s, a, ws);
+  return launch_dependent(join_chunk_kernel<1, PagedAttnArgs>, grid, dim3(32 * kWarps), 0, s, a, ws);
 }
 
 }  // namespace sa

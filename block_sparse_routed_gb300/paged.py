@@ -13,7 +13,8 @@ what a call does for positions below 0, and what is checked on the device.
 * ``cache_write``: rows of K and V into the cache;
 * ``cache_read``: the inverse, the packed BF16 tensors of ``sparse_attn``;
 * ``paged_attn``: attention of rows of Q over the cache, for chunks of new
-  tokens and for single ones.
+  tokens and for single ones;
+* ``prefix_attn``: the same where groups of sequences share a prefix.
 
 Nothing here waits for the GPU.  With ``ws`` (a workspace of
 ``paged_workspace``, or 256 bytes for the two copies)
@@ -293,4 +294,84 @@ def paged_attn(q, k_pages, v_pages, table, row_start, kv_len, max_new=None, caus
         p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_exp.data_ptr() if kind else None,
         v_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(), o.data_ptr(),
         lse.data_ptr(), _scratch(env, ws, dev, 0), ws.numel()))
+    return o, lse
+
+
+def _groups(env, group_start, prefix_len, dev):
+    """Checks the groups; returns their number."""
+    for t, name in ((group_start, "group_start"), (prefix_len, "prefix_len")):
+        if t.dtype is not env[4] or t.dim() != 1 or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name}: contiguous int32 vector on the cache's device required")
+    if group_start.numel() != prefix_len.numel() + 1:
+        raise ValueError("group_start must be [groups + 1] and prefix_len [groups]")
+    return prefix_len.numel()
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefix_ws_bytes(groups, *fields):
+    """Bytes of a call's workspace: a plain function of numbers."""
+    out = ctypes.c_uint64(0)
+    st = _native.load_library().sparse_attn_prefix_ws_bytes(_params(*fields)[1], groups, ctypes.byref(out))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_prefix_ws_bytes")
+    return int(out.value)
+
+
+def prefix_ws_bytes(q, k_pages, table, group_start, max_new=None):
+    """Bytes of the workspace of ``prefix_attn`` calls of these sizes."""
+    env = _env()
+    n, hq, _, _ = _rows(env, q, "q", q.get_device())
+    pages, H, ps, d = k_pages.shape
+    if hq < 1 or H < 1 or hq % H:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    max_new = n if max_new is None else min(int(max_new), n)
+    return _prefix_ws_bytes(group_start.numel() - 1, 1 if k_pages.dtype is env[2] else 0, pages, H, ps, d, table.shape[0],
+                            table.shape[1], 0, n, max_new, hq, 1, 0, 1.0, 0, 0, 0, 0)
+
+
+def prefix_workspace(q, k_pages, table, group_start, max_new=None):
+    """A workspace for ``prefix_attn`` calls of these sizes, as ``paged_workspace``."""
+    return _env()[0].empty(prefix_ws_bytes(q, k_pages, table, group_start, max_new), dtype=_env()[3], device=k_pages.device)
+
+
+def prefix_attn(q, k_pages, v_pages, table, row_start, kv_len, group_start, prefix_len, max_new=None, causal=True,
+                scale=None, k_exp=None, v_exp=None, o=None, lse=None, ws=None, stream=None):
+    """``paged_attn`` for a batch in which groups of sequences begin with the
+    same tokens, whose keys are read once for all rows of the group.
+
+    ``group_start`` (int32 [groups + 1], ascending) and ``prefix_len`` (int32
+    [groups]), on the GPU: the sequences group_start[g] .. group_start[g + 1] - 1
+    begin with the same prefix_len[g] tokens.  Those in whole pages are read
+    once, from the pages of the group's first sequence, which the others' rows
+    of ``table`` name too; all others by each sequence's own row.  A sequence's
+    rows must lie behind the shared pages.  There is no window.
+
+    Returns (o, lse) as ``paged_attn``, equal up to the order of sums."""
+    env = _env()
+    kind, (pages, H, ps, d), dev = _cache(env, k_pages, v_pages, k_exp, v_exp)
+    seqs, width, outer = _batch(env, table, row_start, kv_len, dev)
+    groups = _groups(env, group_start, prefix_len, dev)
+    n, hq, qt, qh = _rows(env, q, "q", dev)
+    if hq < 1 or H < 1 or hq % H:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    max_new = n if max_new is None or max_new > n else max_new
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    if o is None:
+        o = _new(env, stream, k_pages, (n, hq, 128), env[1])
+    else:
+        _given(o, "o", (n, hq, 128), env[1], dev)
+    if lse is None:
+        lse = _new(env, stream, k_pages, (n, hq), env[0].float32)
+    else:
+        _given(lse, "lse", (n, hq), env[0].float32, dev)
+    fields = (kind, pages, H, ps, d, seqs, width, outer, n, max_new, hq, 1 if causal else 0, 0,
+              SCALE if scale is None else scale, qt, qh, 0, 0)
+    if ws is None:
+        ws = _new(env, stream, k_pages, (_prefix_ws_bytes(groups, *fields),), env[3])
+    _, p = _params(*fields)
+    _call(env, "sparse_attn_prefix_fwd", dev, stream, (
+        p, groups, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_exp.data_ptr() if kind else None,
+        v_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(),
+        group_start.data_ptr(), prefix_len.data_ptr(), o.data_ptr(), lse.data_ptr(), _scratch(env, ws, dev, 0), ws.numel()))
     return o, lse

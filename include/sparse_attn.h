@@ -446,6 +446,41 @@ sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, const v
                                 void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * The same attention for a batch in which groups of sequences begin with the
+ * same tokens (one instruction before many questions, several continuations of
+ * one clip): the keys of a prefix are read and multiplied once for all rows of
+ * its group, and joined with each row's own keys in one softmax.
+ *   groups       groups, >= 0
+ *   group_start  int32 [groups + 1], device memory, ascending: group g is the
+ *                sequences group_start[g] .. group_start[g + 1] - 1 (others
+ *                share nothing)
+ *   prefix_len   int32 [groups], device memory: the first prefix_len[g] tokens
+ *                of all sequences of group g are the same.  Those in whole
+ *                pages are read once, from the pages of the group's first
+ *                sequence, which the others' table rows name too (or pages
+ *                that hold the same); the rest of them, as all other tokens,
+ *                by each sequence's own row.  A group of one sequence shares
+ *                nothing
+ * Everything else is as in sparse_attn_paged_fwd, and so is the result, up to
+ * the order of sums.  window must be 0.
+ *   ws  workspace of sparse_attn_prefix_ws_bytes(p, groups) bytes (1040 for
+ *       each row and query head, besides those of sparse_attn_paged_fwd)
+ * Checked on the device besides: 0 <= group_start[g] <= group_start[g + 1] <=
+ * seqs, 0 <= prefix_len[g] <= table_width * page_size, and that a sequence's
+ * own rows lie behind its group's whole shared pages; else SA_EINVAL in the
+ * status word, and the outputs of the group, or of the sequence, are
+ * unspecified.
+ * Errors: as sparse_attn_paged_fwd; SA_EINVAL also for groups < 0, window not
+ * 0, a null or misaligned group_start, or prefix_len with groups > 0.
+ */
+sa_status sparse_attn_prefix_ws_bytes(const sa_paged_params* p, int32_t groups, uint64_t* out);
+sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups, const void* q, const void* k_pages,
+                                 const void* v_pages, const uint8_t* k_exp, const uint8_t* v_exp,
+                                 const int32_t* table, const int32_t* row_start, const int32_t* kv_len,
+                                 const int32_t* group_start, const int32_t* prefix_len, void* o, float* lse,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * The attention weight that cached keys receive, by which
  * sparse_attn_cache_evict chooses: for each key head h and key j >= first of a
  * sequence with rows in the call,
