@@ -55,6 +55,7 @@ from .eviction import (  # noqa: F401
     cache_evict,
     cache_weigh,
     cache_weights,
+    weigh_workspace,
 )
 from .paged import (  # noqa: F401
     cache_read,
@@ -95,6 +96,7 @@ __all__ = [
     "spark_reweight",
     "spark_reblock",
     "sparse_attn_spark_fwd",
+    "weigh_workspace",
 ]
 
 

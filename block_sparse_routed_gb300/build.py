@@ -20,7 +20,7 @@ LIB_NAME = "libsparse_attn.so"
 LIB_PATH = os.path.join(OUT, LIB_NAME)
 SOURCES = ["api.cu", "plan_kernels.cu", "attn_kernel.cu", "plan_static.cu", "spark_reweight.cu", "reblock.cu",
            "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_chunk.cu", "paged_join.cu", "paged_weigh.cu",
-           "paged_evict.cu"]
+           "paged_weigh_chunk.cu", "paged_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-lineinfo",

@@ -229,6 +229,23 @@ struct WeighArgs {
   int accumulate;     // 0: weights are set; 1: added to those of the tokens before the call's own
 };
 
+// What the join needs of the unit (keys of one sequence and head) that begins
+// in a CTA's part of the work and does not end there.
+struct WeighJoin {
+  int pieces;  // 0: none
+  int s, h, key0;
+  int lo, hi;  // keys whose weight is written
+  int fresh;   // weights of keys below are added to
+  int pad;
+};
+constexpr int kWeighKeys = 256;  // keys of a unit of the form for chunks
+constexpr int kWeighCtas = 160;  // most CTAs of it
+struct WeighScratch {
+  int32_t* cta_status;  // [ctas]
+  WeighJoin* join;      // [ctas]
+  float* part;          // [ctas][2][keys]
+};
+
 struct EvictArgs {
   float* weights;
   const int32_t* to_table;  // pages of the tokens that stay, or null: the sequence's first ones
@@ -279,6 +296,7 @@ struct PagedForm {
 cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s);
+cudaError_t launch_weigh_chunk(const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s);
 cudaError_t launch_evict(const PagedArgs& c, const EvictArgs& e, int sms, cudaStream_t s);
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);

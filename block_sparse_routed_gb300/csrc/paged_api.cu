@@ -177,6 +177,26 @@ uint64_t shared_scratch_of(const sa_paged_params* p, void* ws, PagedScratch* scr
   return off;
 }
 
+// Whether weights are taken by the form for few rows: as form_of.
+bool weighs_few(const sa_paged_params* p) {
+  return int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H) <= kPagedFewRows;
+}
+
+uint64_t weigh_scratch_of(const sa_paged_params* p, void* ws, WeighScratch* out) {
+  if (weighs_few(p)) return kStatusBytes;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint64_t off = kStatusBytes;
+  const uint64_t status = off; off += align256(kWeighCtas * 4);
+  const uint64_t join = off;   off += align256(kWeighCtas * sizeof(WeighJoin));
+  const uint64_t part = off;   off += kWeighCtas * 2 * kWeighKeys * 4;
+  if (out) {
+    out->cta_status = reinterpret_cast<int32_t*>(w + status);
+    out->join = reinterpret_cast<WeighJoin*>(w + join);
+    out->part = reinterpret_cast<float*>(w + part);
+  }
+  return off;
+}
+
 sa_status clear_status(void* ws, cudaStream_t stream) {
   if (ws && cuda_failed(cudaMemsetAsync(ws, 0, kStatusBytes, stream))) return SA_ECUDA;
   return SA_OK;
@@ -355,7 +375,7 @@ SA_API sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* 
   if (out == nullptr) return SA_EINVAL;
   const sa_status st = check_attn(p);
   if (st != SA_OK) return st;
-  *out = kStatusBytes;
+  *out = weigh_scratch_of(p, nullptr, nullptr);
   return SA_OK;
 }
 
@@ -376,8 +396,12 @@ SA_API sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first
   if (ws_bytes < need) return SA_EINVAL;
   st = static_cast<sa_status>(device_status());
   if (st != SA_OK) return st;
-  st = clear_status(ws, stream);
-  if (st != SA_OK || p->rows == 0 || p->seqs == 0) return st;
+  const int64_t longest = int64_t(p->table_width) * p->page_size;
+  const bool few = weighs_few(p);
+  if (few || p->rows == 0 || p->seqs == 0) {
+    st = clear_status(ws, stream);
+    if (st != SA_OK || p->rows == 0 || p->seqs == 0) return st;
+  }
   WeighArgs w;
   w.a = attn_args(p, q, paged_args(p, k_pages, nullptr, k_exp, nullptr, table, row_start, kv_len, ws), nullptr, nullptr);
   w.lse = lse;
@@ -386,10 +410,20 @@ SA_API sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first
   w.accumulate = accumulate;
   const int sms = multiprocessors();
   if (sms <= 0) return SA_ECUDA;
-  const int64_t rows = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * w.a.group;
-  const int64_t tiles = (int64_t(p->table_width) * p->page_size + 15) / 16 * p->seqs * p->H;
-  if (tiles == 0 || rows == 0) return SA_OK;
-  return cuda_failed(launch_weigh(w, rows, sms, tiles, stream)) ? SA_ECUDA : SA_OK;
+  if (few) {
+    const int64_t rows = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * w.a.group;
+    const int64_t tiles = (longest + 15) / 16 * p->seqs * p->H;
+    // (at least one block: it reports what is wrong with the batch)
+    return cuda_failed(launch_weigh(w, rows, sms, tiles > 0 ? tiles : 1, stream)) ? SA_ECUDA : SA_OK;
+  }
+  WeighScratch scratch;
+  weigh_scratch_of(p, ws, &scratch);
+  // no more CTAs than key blocks times steps that the call can have
+  const int64_t blocks = (longest / kWeighKeys + 2) * p->seqs * p->H;
+  const int64_t most = blocks * (int64_t(p->rows) * w.a.group / 96 + 2);
+  int ctas = sms > kWeighCtas ? kWeighCtas : sms;
+  if (most < ctas) ctas = static_cast<int>(most);
+  return cuda_failed(launch_weigh_chunk(w, scratch, ctas, stream)) ? SA_ECUDA : SA_OK;
 }
 
 SA_API sa_status sparse_attn_cache_evict(const sa_paged_params* p, const sa_evict_params* e, void* k_pages,

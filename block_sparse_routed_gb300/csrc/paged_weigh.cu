@@ -117,8 +117,7 @@ struct Rows {
   }
 };
 
-// kLoop: more packed rows than 8 kN.
-template <int kKind, int kN, bool kLoop>
+template <int kKind, int kN>  // kN: tiles of eight rows
 __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
   const PagedAttnArgs& a = w.a;
   const PagedArgs& c = a.c;
@@ -211,9 +210,8 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
     float old = 0.f;
     if (write && w.accumulate && key < q.len - q.n) old = *to;
     float sum[2] = {0.f, 0.f};
-    const int all = q.n * a.group;
-    for (int rho0 = 0; rho0 < all; rho0 += 8 * kN) {
-      if (kLoop || fresh) rows.load(w, q, h, rho0, lane);
+    {
+      if (fresh) rows.load(w, q, h, 0, lane);
       fresh = false;
       float d[kN][4];
 #pragma unroll
@@ -247,7 +245,6 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
           const float p = ex2_approx(fmaf(d[n][e], scale[e / 2], rows.neg[n][e & 1]));
           if (j >= rows.lo[n][e & 1] && j < rows.hi[n][e & 1]) sum[e / 2] += p;
         }
-      if (!kLoop) break;
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -258,9 +255,9 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
   }
 }
 
-template <int kKind, int kN, bool kLoop>
+template <int kKind, int kN>
 cudaError_t launch(const WeighArgs& w, int ctas, cudaStream_t s) {
-  weigh_kernel<kKind, kN, kLoop><<<ctas, 32 * kWarps, 0, s>>>(w);
+  weigh_kernel<kKind, kN><<<ctas, 32 * kWarps, 0, s>>>(w);
   return cudaGetLastError();
 }
 
@@ -270,9 +267,8 @@ cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_
   int64_t ctas = (key_tiles + kWarps - 1) / kWarps;
   if (ctas > 6 * sms) ctas = 6 * sms;
   const int n = static_cast<int>(ctas);
-  if (w.a.c.kind == 0)
-    return rows <= 8 ? launch<0, 1, false>(w, n, s) : rows <= 16 ? launch<0, 2, false>(w, n, s) : launch<0, 2, true>(w, n, s);
-  return rows <= 8 ? launch<1, 1, false>(w, n, s) : rows <= 16 ? launch<1, 2, false>(w, n, s) : launch<1, 2, true>(w, n, s);
+  if (w.a.c.kind == 0) return rows <= 8 ? launch<0, 1>(w, n, s) : launch<0, 2>(w, n, s);
+  return rows <= 8 ? launch<1, 1>(w, n, s) : launch<1, 2>(w, n, s);
 }
 
 }  // namespace sa

@@ -23,7 +23,7 @@ import ctypes
 import functools
 
 from . import _native
-from ._native import SaEvictParams
+from ._native import SA_OK, SaEvictParams, SparseAttnError
 from .paged import SCALE, _batch, _cache, _call, _env, _given, _new, _params, _rows, _scratch
 
 _INT32 = 0x7FFFFFFF
@@ -41,6 +41,29 @@ def _weights(env, weights, shape, dev):
             or weights.get_device() != dev):
         raise ValueError("weights: contiguous float32 [pages, H, page_size] on the cache's device required")
     return weights.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _weigh_ws_bytes(*fields):
+    """Bytes of a call's workspace: a plain function of numbers."""
+    out = ctypes.c_uint64(0)
+    st = _native.load_library().sparse_attn_weigh_ws_bytes(_params(*fields)[1], ctypes.byref(out))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_weigh_ws_bytes")
+    return int(out.value)
+
+
+def weigh_workspace(q, k_pages, table, max_new=None):
+    """A workspace for ``cache_weigh`` calls of these sizes, as ``paged_workspace``."""
+    env = _env()
+    n, hq, _, _ = _rows(env, q, "q", q.get_device())
+    pages, H, ps, d = k_pages.shape
+    if hq < 1 or H < 1 or hq % H:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    max_new = n if max_new is None else min(int(max_new), n)
+    size = _weigh_ws_bytes(1 if k_pages.dtype is env[2] else 0, pages, H, ps, d, table.shape[0], table.shape[1], 0, n, max_new,
+                           hq, 1, 0, 1.0, 0, 0, 0, 0)
+    return env[0].empty(size, dtype=env[3], device=k_pages.device)
 
 
 def cache_weigh(q, lse, weights, k_pages, table, row_start, kv_len, max_new=None, causal=True, window=0, scale=None,
@@ -66,10 +89,11 @@ def cache_weigh(q, lse, weights, k_pages, table, row_start, kv_len, max_new=None
         raise ValueError("max_new must not be negative")
     _given(lse, "lse", (n, hq), env[0].float32, dev)
     w = _weights(env, weights, (pages, H, ps), dev)
-    _, p = _params(kind, pages, H, ps, d, seqs, width, outer, n, max_new, hq, 1 if causal else 0, min(window, _INT32),
-                   SCALE if scale is None else scale, qt, qh, 0, 0)
+    fields = (kind, pages, H, ps, d, seqs, width, outer, n, max_new, hq, 1 if causal else 0, min(window, _INT32),
+              SCALE if scale is None else scale, qt, qh, 0, 0)
     if ws is None:
-        ws = _new(env, stream, k_pages, (256,), env[3])
+        ws = _new(env, stream, k_pages, (_weigh_ws_bytes(*fields),), env[3])
+    _, p = _params(*fields)
     _call(env, "sparse_attn_cache_weigh", dev, stream, (
         p, min(first, _INT32), 1 if accumulate else 0, q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(),
         k_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(), w,
