@@ -179,6 +179,26 @@ bool sa::make_map_groups(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool sa::make_map_heads(CUtensorMap* m, const void* ptr, int tokens, int H, int group, int64_t token_stride,
+                        int64_t head_stride, int box_tokens, int box_heads) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  // a stride of a single element is any; rows that overlap (expanded tensors) have no map
+  if (group * H == 1) head_stride = kHeadDim;
+  if (tokens == 1) token_stride = head_stride * group * H;
+  if (head_stride < kHeadDim || token_stride < kHeadDim) return false;
+  const cuuint64_t lim = cuuint64_t(1) << 40;
+  cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(group), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(head_stride) * 2 * group,
+                           static_cast<cuuint64_t>(token_stride) * 2};
+  if (strides[0] >= lim || strides[1] >= lim || strides[2] >= lim) return false;
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), 1, static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // [T rows, H*128 columns] view of a BF16 [T, H, 128] tensor.

@@ -227,6 +227,9 @@ struct WeighArgs {
   float* weights;
   int first;          // keys below are left as they are
   int accumulate;     // 0: weights are set; 1: added to those of the tokens before the call's own
+  // the form for chunks: a step's rows are `tokens` tokens of `heads` heads, of
+  // which a group has `slices`; boxes: the tensor map of Q can be used
+  int tokens, heads, slices, boxes;
 };
 
 // What the join needs of the unit (keys of one sequence and head) that begins
@@ -296,7 +299,7 @@ struct PagedForm {
 cudaError_t launch_cache_write(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_cache_read(const PagedArgs& c, const CacheRows& r, cudaStream_t s);
 cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s);
-cudaError_t launch_weigh_chunk(const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s);
+cudaError_t launch_weigh_chunk(WeighArgs w, const WeighScratch& ws, int ctas, cudaStream_t s);
 cudaError_t launch_evict(const PagedArgs& c, const EvictArgs& e, int sms, cudaStream_t s);
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s);
@@ -323,6 +326,13 @@ bool make_map_rows(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols
 // halves][8 rows][64 columns]: a box is box_rows rows, written as one 1 KB
 // block (8 rows x 128 bytes, 128-byte swizzle) for each half of each 8 rows.
 bool make_map_groups(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows);
+
+// Tensor map of BF16 rows of 128 at token * token_stride + head * head_stride
+// (elements), heads in groups: [tokens][H][group][128]; a box is 64 columns of
+// `box_heads` heads of one group and `box_tokens` tokens, 128-byte swizzle,
+// zeros past a group's last head.  False where strides allow no map.
+bool make_map_heads(CUtensorMap* m, const void* ptr, int tokens, int H, int group, int64_t token_stride,
+                    int64_t head_stride, int box_tokens, int box_heads);
 
 size_t route_topk_smem_bytes(const Geometry& g);
 size_t attention_smem_bytes();

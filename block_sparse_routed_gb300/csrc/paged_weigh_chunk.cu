@@ -17,9 +17,12 @@
 // The line of all steps of all units is cut into equal parts, one a CTA; a
 // unit that a cut divides is joined from its parts in order by a second kernel.
 //
-// Warps: 0-2 gather Q (a group of any size, any strides), 32 rows each; 3
-// walks the line and issues the products; 4-7 and 8-11 are the keys of tile 0
-// and 1: they load the next unit's keys into registers while the present one's
+// Warps: 0 and 1 bring the rows of Q, a box of whole tokens a step (and gather,
+// 48 rows each, what is no whole box: a sequence's last rows, strides that no
+// box has); 2 and 3 issue the products of tile 1 and 0 (an issue takes about
+// 48 cycles, as long as the product: one warp for both came to 1000 cycles a
+// step), and 3 walks the line; 4-7 and 8-11 are the keys of tile 0 and 1.
+// They bring the next unit's keys into shared memory while the present one's
 // rows pass, widen codes, and write them to tensor memory.
 //
 // Tensor memory: K of tile t in columns [64 t, + 64); scores of tile t, every
@@ -36,7 +39,7 @@ namespace {
 
 constexpr int kKeys = kWeighKeys;  // of a unit
 constexpr int kRows = 96;          // packed rows of a step
-constexpr int kStages = 4;
+constexpr int kStages = 6, kAhead = 2;
 constexpr int kSegs = 3;
 constexpr uint32_t kHalfBytes = kRows * 128;  // of a stage: 64 dimensions of its rows
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
@@ -44,30 +47,37 @@ constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr int kOver = 3;
 constexpr int kMinPlaces = 4;
 
-constexpr int kThreads = 384;
+constexpr int kKeyWarps = 8;
+constexpr int kThreads = 32 * (4 + kKeyWarps);
 // Registers after the split: their sum over warpgroups stays within the
 // launch allocation (384 x 168).
 constexpr uint32_t kRegsLaunch = 168, kRegsControl = 88, kRegsKeys = 208;
 static_assert(kRegsControl + 2 * kRegsKeys <= 3 * kRegsLaunch, "");
 
-// Shared memory, from a 1024-byte boundary.
-constexpr uint32_t kOffNeg = kStages * kStageBytes;          // [stages][rows]: -L
-constexpr uint32_t kOffPos = kOffNeg + kStages * kRows * 4;  // [stages][rows]: position
-constexpr uint32_t kOffSeg = kOffPos + kStages * kRows * 4;
+// Shared memory, from a 1024-byte boundary.  -L and positions of a step's rows
+// stay twice as long as the rows: the keys' warps release scores, not rows, and
+// are then at most two steps behind the products.
+constexpr int kNegs = 2 * kStages;
+constexpr uint32_t kOffKeys = kStages * kStageBytes;         // the next unit's keys, as they lie in the cache
+constexpr uint32_t kOffNeg = kOffKeys + kKeys * 256;         // [negs][rows]: -L
+constexpr uint32_t kOffPos = kOffNeg + kNegs * kRows * 4;    // [negs][rows]: position
+constexpr uint32_t kOffSeg = kOffPos + kNegs * kRows * 4;
 constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
-constexpr uint32_t kOffMisc = kOffBar + 256;
+constexpr uint32_t kOffMisc = kOffBar + 512;
 constexpr uint32_t kSmem = kOffMisc + 64 + 1024;
+static_assert(kSmem <= 232448, "shared memory");
 
 enum {
-  BAR_QFULL = 0,    // +stage (4): 96 lanes' copies and 3 warps
-  BAR_QEMPTY = 4,   // +stage: the products and 8 warps of keys
-  BAR_SFULL = 8,    // +2 tile, + every other step
-  BAR_SEMPTY = 12,
-  BAR_KREADY = 16,  // +tile
-  BAR_SEGFULL = 18, // +segment (3)
-  BAR_SEGEMPTY = 21,
-  BAR_DRAIN = 24,
-  NUM_BARS = 25
+  BAR_QFULL = 0,     // +stage (6): warps 0 and 1, and the box
+  BAR_QEMPTY = 8,    // +stage: both tiles' products
+  BAR_SFULL = 16,    // +2 tile, + every other step: the products, and that the step's -L are there
+  BAR_SEMPTY = 20,
+  BAR_KREADY = 24,   // +tile
+  BAR_DONE = 26,     // the warps of tile 1 are through with a unit
+  BAR_SEGFULL = 28,  // +segment (3)
+  BAR_SEGEMPTY = 31,
+  BAR_DRAIN = 34,    // +tile
+  NUM_BARS = 36
 };
 
 // One step of the walk: some steps of a unit.
@@ -76,8 +86,8 @@ struct Work {
   int row0, n, len, h, s;
   int key0;    // first key of the unit
   int lo, hi;  // its keys whose weight is written
-  int rho0;    // first packed row
-  int end;     // past the last
+  int i0, i1;  // tokens of the unit's rows
+  int j0;      // first of its steps
   int steps;
   int part;    // -1: the unit's weights; else the partial sums' slot (0 or 1)
 };
@@ -85,7 +95,7 @@ static_assert(sizeof(Work) <= 64, "");
 
 struct Unit {
   int lo, hi;      // keys whose weight is written
-  int rho0, rows;  // packed rows that see some of them
+  int i0, i1;      // tokens whose rows see some of them
   int steps, places;
 };
 
@@ -110,9 +120,9 @@ __device__ __forceinline__ Unit unit_of(const WeighArgs& w, const PagedSeq& q, i
     i0 = min(max(u.lo - base, 0), q.n);
     if (w.a.window) i1 = static_cast<int>(min(int64_t(q.n), max(int64_t(i0), int64_t(u.hi) - 1 + w.a.window - base)));
   }
-  u.rho0 = i0 * w.a.group;
-  u.rows = (i1 - i0) * w.a.group;
-  u.steps = max(1, (u.rows + kRows - 1) / kRows);
+  u.i0 = i0;
+  u.i1 = i1;
+  u.steps = max(1, (i1 - i0 + w.tokens - 1) / w.tokens) * w.slices;
   u.places = u.steps + kOver;
   return u;
 }
@@ -258,8 +268,9 @@ __device__ __forceinline__ Work walk_step(const WeighArgs& w, Walk& k, WeighJoin
       g.key0 = (k.lo / kKeys + k.b) * kKeys;
       g.lo = u.lo;
       g.hi = u.hi;
-      g.rho0 = u.rho0 + from * kRows;
-      g.end = u.rho0 + u.rows;
+      g.i0 = u.i0;
+      g.i1 = u.i1;
+      g.j0 = from;
       g.steps = to - from;
       g.part = from == 0 ? (to == u.steps ? -1 : 1) : 0;
       if (g.part == 1) {  // the CTA that holds the unit's last place
@@ -303,11 +314,6 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void lds_f2x2(uint64_t& a, uint64_t& b, uint32_t addr) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
@@ -315,17 +321,19 @@ __device__ __forceinline__ void lds_i4(int (&v)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
-// A key in registers: its row as it lies in the cache, and where its weight is.
-template <int kKind>
-struct Key {
-  uint4 x[kKind == 0 ? 16 : 8];
-  uint32_t exp;
-  float old;
-  int64_t at;  // of the weight; -1: none is written
-};
+__device__ __forceinline__ void sts_f1(uint32_t addr, float a) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
 
 template <int kKind>
-__global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const WeighArgs w, const WeighScratch ws) {
+__global__ void __launch_bounds__(kThreads, 1)
+weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, const WeighScratch ws) {
   const PagedAttnArgs& a = w.a;
   const PagedArgs& c = a.c;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -337,24 +345,34 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const WeighArg
   int32_t* s_bad = reinterpret_cast<int32_t*>(base + kOffMisc + 4);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(base + kOffMisc + 8);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  // A step's rows: `tokens` tokens of `heads` heads (a slice of the group).
+  const int step_rows = w.tokens * w.heads;
 
+  // Rows of a stage that no step has are zeros throughout.
+  for (int i = step_rows * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
+    for (int st = 0; st < 2 * kStages; ++st)
+      *reinterpret_cast<uint4*>(base + st * kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (threadIdx.x == 0) {
     *s_abort = 0;
     *s_bad = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(BAR_QFULL + i), 3);
-      mbar_init(bar(BAR_QEMPTY + i), 9);
+      mbar_init(bar(BAR_QFULL + i), 2);
+      mbar_init(bar(BAR_QEMPTY + i), 2);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(BAR_SFULL + i), 1);
+      mbar_init(bar(BAR_SFULL + i), 2);
       mbar_init(bar(BAR_SEMPTY + i), 4);
     }
-    for (int t = 0; t < 2; ++t) mbar_init(bar(BAR_KREADY + t), 4);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(BAR_KREADY + t), 4);
+      mbar_init(bar(BAR_DRAIN + t), 1);
+    }
+    mbar_init(bar(BAR_DONE), 4);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(BAR_SEGFULL + i), 1);
-      mbar_init(bar(BAR_SEGEMPTY + i), 11);
+      mbar_init(bar(BAR_SEGEMPTY + i), 3 + kKeyWarps);
     }
-    mbar_init(bar(BAR_DRAIN), 1);
     fence_barrier_init();
   }
   if (warp == 3) {
@@ -381,123 +399,200 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const WeighArg
   bool ok = true;
 
   if (warp < 4) setmaxnreg_dec<kRegsControl>();
-  if (warp < 3) {
+  if (warp < 2) {
     // ------------------------------------------------------------ rows of Q
-    int x = 0;  // steps so far
-    int pending = -1;  // the step whose copies are under way
-    auto publish = [&](int step) {  // its copies have landed
+    if (warp == 0 && lane == 0 && w.boxes) tma_prefetch_desc(&tm_q);
+    // A lane has row lane of the warp's 48, and half of the lanes a second one,
+    // 32 behind it; their lse come a step ahead.
+    struct Row {
+      int at, tok, head;  // of the step
+      int i, sub;         // token, and head of the group
+      bool real;
+      float l;
+    } row[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      row[e].at = 48 * warp + 32 * e + lane;
+      row[e].tok = row[e].at / w.heads;
+      row[e].head = row[e].at - row[e].tok * w.heads;
+    }
+    auto rows_at = [&](const Work& g, int j) {
+      const int tile = w.slices == 1 ? g.j0 + j : (g.j0 + j) / w.slices;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        Row& r = row[e];
+        r.sub = (g.j0 + j - tile * w.slices) * w.heads + r.head;
+        r.i = g.i0 + tile * w.tokens + r.tok;
+        r.real = (e == 0 || lane < 16) && r.at < step_rows && r.i < g.i1 && r.sub < a.group;
+        r.l = -INFINITY;
+        if (r.real) r.l = __ldg(w.lse + static_cast<int64_t>(g.row0 + r.i) * a.Hq + g.h * a.group + r.sub);
+      }
+    };
+    const uint32_t elect = elect_one();
+    int x = 0, done = 0;  // steps so far; those whose copies have landed, or are a box's
+    auto publish = [&](int to) {
+      if (done >= to) return;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_QFULL + step % kStages));
+      for (; done < to; ++done)
+        if (lane == 0) mbar_arrive(bar(BAR_QFULL + done % kStages));
     };
-    for (int k = 0; ok; ++k) {
-      Work g;
-      ok = next_seg(k, g);
-      if (!ok || !g.valid) break;
-      for (int j = 0; j < g.steps; ++j, ++x) {
-        const int st = x % kStages;
-        ok = x < kStages || all_wait(BAR_QEMPTY + st, x / kStages - 1);
-        if (!ok) break;
-        const int r = 32 * warp + lane, rho = g.rho0 + j * kRows + r;
-        const bool real = rho < g.end;
-        const int i = div_group(a, rho), e = rho - i * a.group;
-        const uint16_t* mine = a.q;
-        float neg = -INFINITY;
-        if (real) {
-          mine += static_cast<int64_t>(g.row0 + i) * a.q_token + static_cast<int64_t>(g.h * a.group + e) * a.q_head;
-          const float l = __ldg(w.lse + static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + e);
-          if (l != -INFINITY) neg = -l * 1.4426950408889634f;
+    auto flush = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      publish(x);
+    };
+    Work g;
+    int k = 0, j = 0;
+    ok = next_seg(0, g);
+    if (ok && g.valid) rows_at(g, 0);
+    while (ok && g.valid) {
+      const int st = x % kStages, ng = x % kNegs;
+      ok = x < kStages || all_wait(BAR_QEMPTY + st, x / kStages - 1);
+      if (!ok) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const Row& r = row[e];
+        if (e == 1 && lane >= 16) break;
+        sts_f1(sbase + kOffNeg + (ng * kRows + r.at) * 4, r.l == -INFINITY ? -INFINITY : -r.l * 1.4426950408889634f);
+        *reinterpret_cast<int*>(base + kOffPos + (ng * kRows + r.at) * 4) = r.real ? g.len - g.n + r.i : -0x40000000;
+      }
+      const int first = __shfl_sync(0xFFFFFFFFu, row[0].i - row[0].tok, 0);  // token of the step's first row
+      if (w.boxes && first + w.tokens <= g.i1) {
+        __syncwarp();
+        if (warp == 0 && elect) {
+          mbar_arrive_expect_tx(bar(BAR_QFULL + st), 2 * step_rows * 128);
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            tma_load_4d(sbase + st * kStageBytes + half * kHalfBytes, &tm_q, bar(BAR_QFULL + st), half * 64,
+                        row[0].sub - row[0].head, g.h, g.row0 + first);
+        } else if (warp != 0 && lane == 0) {
+          mbar_arrive(bar(BAR_QFULL + st));
         }
-        const uint32_t to = sbase + st * kStageBytes + (lane % 16 / 8) * kHalfBytes;
-#pragma unroll 8
-        for (int y = 0; y < 32; y += 2) {
-          const int row = y + lane / 16;
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(mine), row));
-          const bool is = g.rho0 + j * kRows + 32 * warp + row < g.end;
-          cp_async16(to + (32 * warp + row) * 128 + ((lane ^ row) & 7) * 16, src + (is ? lane % 16 * 8 : 0), is);
+        if (done < x) flush();
+        done = ++x;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Row& r = row[e];
+          const uint16_t* src0 = a.q;
+          if (r.real) src0 += static_cast<int64_t>(g.row0 + r.i) * a.q_token + static_cast<int64_t>(g.h * a.group + r.sub) * a.q_head;
+          const uint32_t to = sbase + st * kStageBytes + (lane % 16 / 8) * kHalfBytes + (48 * warp + 32 * e) * 128;
+          const unsigned reals = __ballot_sync(0xFFFFFFFFu, r.real);
+#pragma unroll 4
+          for (int y = 0; y < (e ? 16 : 32); y += 2) {
+            const int z = y + lane / 16;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src0), z));
+            const bool is = reals >> z & 1;
+            cp_async16(to + z * 128 + ((lane ^ z) & 7) * 16, src + (is ? lane % 16 * 8 : 0), is);
+          }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        *reinterpret_cast<float*>(base + kOffNeg + (st * kRows + r) * 4) = neg;
-        *reinterpret_cast<int*>(base + kOffPos + (st * kRows + r) * 4) = real ? g.len - g.n + i : -0x40000000;
-        if (pending >= 0) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          publish(pending);
+        ++x;
+        if (x - done > kAhead) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+          publish(x - kAhead);
         }
-        pending = x;
       }
+      if (++j == g.steps) {
+        j = 0;
+        ++k;
+        // The next description may come only once the products of these steps are under way.
+        if (done < x && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar(BAR_SEGFULL + k % kSegs), (k / kSegs) & 1))) flush();
+        ok = next_seg(k, g);
+        if (!ok) break;
+      }
+      if (g.valid) rows_at(g, j);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (ok && pending >= 0) publish(pending);
+    if (ok) publish(x);
     if (!ok) *s_abort = 1;
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ the line, and the products
+    if (lane == 0 && warp == 0) *reinterpret_cast<int32_t*>(base + kOffMisc + 12) = x;
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ products of tile t; warp 3 walks the line
+    const int t = 3 - warp;
     Walk walk;
-    bool bad = false;
-    walk_start(w, walk, bad);
     WeighJoin join;
-    join.pieces = 0;
-    const uint32_t id = idesc_bf16(128, kRows, false, false);
-    auto off = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4); };
-    const uint32_t elect = elect_one();
-    auto give = [&](int k, const Work& g) -> bool {
+    Work g;
+    bool bad = false;
+    int k = 0;  // descriptions so far
+    auto give = [&]() -> bool {  // the next one, to the others
+      g = walk_step(w, walk, join);
       if (k >= kSegs && !all_wait(BAR_SEGEMPTY + k % kSegs, k / kSegs - 1)) return false;
       if (lane == 0) {
         segs[k % kSegs] = g;
         mbar_arrive(bar(BAR_SEGFULL + k % kSegs));
       }
       __syncwarp();
+      ++k;
       return true;
     };
-    int x = 0;            // steps so far
-    int y0 = 0, y1 = 0;   // of tile 0 and 1
-    int u0 = 0, u1 = 0;   // units of them
+    if (t == 0) {
+      walk_start(w, walk, bad);
+      join.pieces = 0;
+      ok = give();
+    } else {
+      ok = next_seg(k++, g);
+    }
+    const uint32_t id = idesc_bf16(128, (step_rows + 15) / 16 * 16, false, false);
+    auto off = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4); };
+    const uint32_t elect = elect_one();
+    int st = 0, phase = 0;  // the next step's stage
+    int y = 0, u = 0;       // steps and units of the tile
     bool issued = false;
-    Work g = walk_step(w, walk, join);
-    ok = give(0, g);
-    for (int k = 0; ok && g.valid; ++k) {
-      const Work next = walk_step(w, walk, join);
-      ok = give(k + 1, next);
-      const int tiles = g.hi > g.key0 + 128 ? 2 : 1;
-      ok = ok && all_wait(BAR_KREADY, u0) && (tiles < 2 || all_wait(BAR_KREADY + 1, u1));
-      ++u0;
-      if (tiles == 2) ++u1;
+    while (ok && g.valid) {
+      const int steps = g.steps;
+      const bool mine = g.hi > g.key0 + 128 * t;
+      ok = t == 0 ? give() : next_seg(k++, g);  // (g is the next unit's from here on)
+      if (!ok) break;
+      if (mine) {
+        ok = all_wait(BAR_KREADY + t, u++);
+      } else if (u > 0) {
+        // The tile has a pause, in which its warps could be more than two steps
+        // behind: they are through with their last unit before the rows' -L
+        // are written over.
+        ok = all_wait(BAR_DONE, u - 1);
+      }
 #pragma unroll 1
-      for (int j = 0; j < g.steps && ok; ++j, ++x) {
-        const int st = x % kStages;
-        ok = all_wait(BAR_QFULL + st, x / kStages);
+      for (int j = 0; j < steps && ok; ++j) {
+        ok = all_wait(BAR_QFULL + st, phase);
         if (!ok) break;
-        const uint64_t qs = sdesc_sw128(sbase + st * kStageBytes, 16, 1024);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t >= tiles) break;
-          const int y = t ? y1 : y0, s = 2 * t + (y & 1);
+        if (mine) {
+          const int s = 2 * t + (y & 1);
           ok = y < 2 || all_wait(BAR_SEMPTY + s, y / 2 - 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + 128 + kRows * s;
+          const uint64_t qs = sdesc_sw128(sbase + st * kStageBytes, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) umma_ts_elect(d, tmem + 64 * t + 8 * kk, qs + off(kk), id, kk > 0 ? 1u : 0u, elect);
           if (elect) {
             umma_commit(bar(BAR_SFULL + s));
-            if (t + 1 == tiles) umma_commit(bar(BAR_QEMPTY + st));
+            mbar_arrive(bar(BAR_SFULL + s));
+            umma_commit(bar(BAR_QEMPTY + st));
           }
-          __syncwarp();
           issued = true;
+          ++y;
+        } else if (elect) {
+          mbar_arrive(bar(BAR_QEMPTY + st));
         }
-        ++y0;
-        if (tiles == 2) ++y1;
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
-      g = next;
     }
     if (!ok) *s_abort = 1;
     if (elect && issued) {  // products in flight complete before the CTA ends
-      umma_commit(bar(BAR_DRAIN));
-      mbar_wait(bar(BAR_DRAIN), 0, kWaitLimitNs);
+      umma_commit(bar(BAR_DRAIN + t));
+      mbar_wait(bar(BAR_DRAIN + t), 0, kWaitLimitNs);
     }
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) {
-      ws.join[blockIdx.x] = join;
-      if (bad) *s_bad = 1;
+    if (t == 0) {
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (lane == 0) {
+        ws.join[blockIdx.x] = join;
+        if (bad) *s_bad = 1;
+      }
     }
   } else {
     // ------------------------------------------------------------ keys of tile t
@@ -509,165 +604,170 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const WeighArg
     const float c2 = a.scale * 1.4426950408889634f;
     const uint64_t c2x = f2(c2, c2);
     auto has = [&](const Work& g) { return g.valid && g.hi > g.key0 + 128 * t; };
+    // The next unit's key comes into shared memory (a thread's own row, its 16-byte
+    // chunks in another order in every row for the banks' sake).
+    constexpr int kRow = kKind == 0 ? 256 : 128, kChunks = kRow / 16;
+    uint32_t exp = 0;
+    float next_old = 0.f;
+    int64_t next_at = -1;  // of its weight; -1: none is written
+    const uint32_t mine = sbase + kOffKeys + (t * 128 + row) * kRow;
     auto load = [&](const Work& g) {
-      Key<kKind> key;
-      key.at = -1;
-      key.old = 0.f;
-      key.exp = 0;
-#pragma unroll
-      for (auto& v : key.x) v = make_uint4(0, 0, 0, 0);
+      next_at = -1;
+      next_old = 0.f;
+      exp = 0;
       const int j = g.key0 + 128 * t + row;
-      if (!has(g) || j < g.lo || j >= g.hi) return key;
-      const int page = __ldg(c.table + g.s * c.table_stride + (j >> c.page_shift));
-      if (page < 0 || page >= c.pages) {
-        *s_bad = 1;
-        return key;
+      if (has(g) && j >= g.lo && j < g.hi) {
+        const int page = __ldg(c.table + g.s * c.table_stride + (j >> c.page_shift));
+        if (page < 0 || page >= c.pages)
+          *s_bad = 1;
+        else
+          next_at = ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (j & (c.page_size - 1));
       }
-      key.at = ((static_cast<int64_t>(page) * c.H + g.h) << c.page_shift) + (j & (c.page_size - 1));
-      const uint8_t* src = c.k_pages + key.at * (kKind == 0 ? 256 : 128);
+      const bool is = next_at >= 0;
+      const uint8_t* src = c.k_pages + (is ? next_at * kRow : 0);
 #pragma unroll
-      for (int e = 0; e < (kKind == 0 ? 16 : 8); ++e) key.x[e] = ld_once(src + 16 * e);
-      if constexpr (kKind != 0) key.exp = __ldg(c.k_exp + key.at);
-      if (w.accumulate && j < g.len - g.n) key.old = w.weights[key.at];
-      return key;
+      for (int e = 0; e < kChunks; ++e) cp_async16(mine + (e ^ (row % 8)) * 16, src + (is ? 16 * e : 0), is);
+      if (is) {
+        if constexpr (kKind != 0) exp = __ldg(c.k_exp + next_at);
+        if (w.accumulate && j < g.len - g.n) next_old = w.weights[next_at];
+      }
     };
-    // The key's row in BF16 into tensor memory.
-    auto store = [&](const Key<kKind>& key) {
-      uint32_t z[2][32];
-      if constexpr (kKind == 0) {
+    // The key in BF16 into tensor memory, 32 columns at a time.
+    auto store = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      // codes land as the value times 2^-120; two factors, of 2^120 and the row's scale
+      const uint32_t e1 = min(exp, 134u), two = exp == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
+      const uint32_t more = (exp == 255 ? 127u : exp - e1 + 127) * 0x00800080u;
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        uint32_t z[32];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          z[e / 8][e % 8 * 4] = key.x[e].x;
-          z[e / 8][e % 8 * 4 + 1] = key.x[e].y;
-          z[e / 8][e % 8 * 4 + 2] = key.x[e].z;
-          z[e / 8][e % 8 * 4 + 3] = key.x[e].w;
-        }
-      } else {
-        // codes land as the value times 2^-120; two factors, of 2^120 and the row's scale
-        const uint32_t e1 = min(key.exp, 134u), two = key.exp == 255 ? 0x7FFF7FFFu : (e1 + 120) * 0x00800080u;
-        const uint32_t more = (key.exp == 255 ? 127u : key.exp - e1 + 127) * 0x00800080u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t in[4] = {key.x[e].x, key.x[e].y, key.x[e].z, key.x[e].w};
+        for (int e = 0; e < kChunks / 2; ++e) {
+          uint32_t in[4];
+          lds_i4(reinterpret_cast<int(&)[4]>(in), mine + ((b * (kChunks / 2) + e) ^ (row % 8)) * 16);
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             const uint32_t v = in[f];
-            const uint32_t even = bf16x2_mul(bf16x2_mul(((v * 16) & 0x07F007F0u) | ((v * 256) & 0x80008000u), two), more);
-            const uint32_t odd = bf16x2_mul(bf16x2_mul(((v >> 4) & 0x07F007F0u) | (v & 0x80008000u), two), more);
-            z[e / 4][e % 4 * 8 + 2 * f] = __byte_perm(even, odd, 0x5410);
-            z[e / 4][e % 4 * 8 + 2 * f + 1] = __byte_perm(even, odd, 0x7632);
+            if constexpr (kKind == 0) {
+              z[4 * e + f] = v;
+            } else {
+              const uint32_t even = bf16x2_mul(bf16x2_mul(((v * 16) & 0x07F007F0u) | ((v * 256) & 0x80008000u), two), more);
+              const uint32_t odd = bf16x2_mul(bf16x2_mul(((v >> 4) & 0x07F007F0u) | (v & 0x80008000u), two), more);
+              z[8 * e + 2 * f] = __byte_perm(even, odd, 0x5410);
+              z[8 * e + 2 * f + 1] = __byte_perm(even, odd, 0x7632);
+            }
           }
         }
+        tmem_st32(k_col + 32 * b, z);
       }
-      tmem_st32(k_col, z[0]);
-      tmem_st32(k_col + 32, z[1]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_KREADY + t));
     };
-    int x = 0, y = 0;  // steps of the CTA, and of the tile
+    int y = 0, ng = 0;  // steps of the tile; place of the next step's -L
     Work g, next;
-    ok = next_seg(0, g);
-    Key<kKind> key;
     int64_t at = -1;
     float old = 0.f;
+    ok = next_seg(0, g);
     if (ok) {
-      key = load(g);
-      if (has(g)) store(key);
-      at = key.at;
-      old = key.old;
+      load(g);
+      if (has(g)) store();
+      at = next_at;
+      old = next_old;
     }
     for (int k = 0; ok && g.valid; ++k) {
       ok = next_seg(k + 1, next);
       if (!ok) break;
-      key = load(next);
-      const bool mine = has(g);
-      float sum = 0.f;
-      uint64_t acc[4];
+      load(next);
+      if (!has(g)) {
+        ng = (ng + g.steps) % kNegs;
+        if (has(next)) store();
+      } else {
+        const int j0 = g.key0 + 128 * t + row;
+        // Steps [0, e0) and [e1, ..) have rows that miss some key of the unit.
+        int e0 = 0, e1 = g.j0 + g.steps;
+        if (a.causal) {
+          const int64_t p0 = g.len - g.n + g.i0;  // position of the unit's first row
+          e0 = static_cast<int>((max(int64_t(0), g.hi - 1 - p0) + w.tokens - 1) / w.tokens) * w.slices;
+          if (a.window) {
+            const int64_t far = g.lo + int64_t(a.window) + 1 - p0;  // tokens until one misses the unit's first key
+            e1 = static_cast<int>(min(int64_t(e1), far <= w.tokens ? 0 : (far - 1) / w.tokens * w.slices));
+          }
+        }
+        uint64_t acc[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) acc[b] = f2(0.f, 0.f);
-      const int j0 = g.key0 + 128 * t + row;
+        for (int b = 0; b < 4; ++b) acc[b] = f2(0.f, 0.f);
 #pragma unroll 1
-      for (int j = 0; j < g.steps; ++j, ++x) {
-        const int st = x % kStages;
-        ok = all_wait(BAR_QFULL + st, x / kStages);
-        if (!ok) break;
-        if (mine) {
+        for (int j = 0; j < g.steps; ++j, ++y) {
           const int s = 2 * t + (y & 1);
+          const uint32_t col = tmem + lane_addr + 128 + kRows * s;
+          const uint32_t negs = sbase + kOffNeg + ng * (kRows * 4);
+          ng = ng + 1 == kNegs ? 0 : ng + 1;
           ok = all_wait(BAR_SFULL + s, y / 2);
           if (!ok) break;
           tc_fence_after();
-          // the unit's last scores are there: the tile's K may be the next unit's
-          if (j + 1 == g.steps && has(next)) store(key);
-          ++y;
-          // does some row of the step miss some key of the unit?
-          bool edge = false;
-          if (a.causal) {
-            const int rho = g.rho0 + j * kRows, base_pos = g.len - g.n;
-            edge = base_pos + div_group(a, rho) < g.hi - 1 ||
-                   (a.window && static_cast<int64_t>(base_pos + div_group(a, min(rho + kRows, g.end) - 1)) - a.window >= g.lo);
-          }
-          const uint32_t col = tmem + lane_addr + 128 + kRows * s, negs = sbase + kOffNeg + st * kRows * 4,
-                         poss = sbase + kOffPos + st * kRows * 4;
-          uint32_t z[kRows / 32][32];
+          if (g.j0 + j < e0 || g.j0 + j >= e1) {
+            // masked in place: a second copy of the sums, with the mask in it,
+            // is not in the instruction cache
+#pragma unroll 1
+            for (int b = 0; b < kRows; b += 8) {
+              uint32_t v[8];
+              int pos[8];
+              tmem_ld8(col + b, v);
+              lds_i4(*reinterpret_cast<int(*)[4]>(&pos[0]), negs + kOffPos - kOffNeg + 4 * b);
+              lds_i4(*reinterpret_cast<int(*)[4]>(&pos[4]), negs + kOffPos - kOffNeg + 4 * b + 16);
+              tmem_wait_ld();
 #pragma unroll
-          for (int b = 0; b < kRows / 32; ++b) tmem_ld32(col + 32 * b, z[b]);
+              for (int e = 0; e < 8; ++e)
+                if (j0 > pos[e] || (a.window && j0 <= pos[e] - a.window)) v[e] = __float_as_uint(-INFINITY);
+              tmem_st8(col + b, v);
+            }
+            tmem_wait_st();
+          }
+          uint32_t z[kRows];
+#pragma unroll
+          for (int b = 0; b < kRows; b += 32) tmem_ld32(col + b, *reinterpret_cast<uint32_t(*)[32]>(&z[b]));
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + s));
-          if (!edge) {
+          // no product reads the unit's keys any more
+          if (j + 1 == g.steps && has(next)) store();
 #pragma unroll
-            for (int b = 0; b < kRows / 4; ++b) {
+          for (int b = 0; b < kRows; b += 32) {
+            if (b >= step_rows) break;  // (no such rows)
+#pragma unroll
+            for (int e = b; e < b + 32; e += 4) {
               uint64_t n0, n1;
-              lds_f2x2(n0, n1, negs + 16 * b);
-              const uint32_t* v = &z[b / 8][b % 8 * 4];
+              lds_f2x2(n0, n1, negs + 4 * e);
               float p0, p1, p2, p3;
-              unf2(ffma2(f2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2x, n0), p0, p1);
-              unf2(ffma2(f2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2x, n1), p2, p3);
-              acc[2 * (b & 1)] = fadd2(acc[2 * (b & 1)], f2(ex2_approx(p0), ex2_approx(p1)));
-              acc[2 * (b & 1) + 1] = fadd2(acc[2 * (b & 1) + 1], f2(ex2_approx(p2), ex2_approx(p3)));
-            }
-          } else {
-#pragma unroll
-            for (int b = 0; b < kRows / 4; ++b) {
-              uint64_t n0, n1;
-              int pos[4];
-              lds_f2x2(n0, n1, negs + 16 * b);
-              lds_i4(pos, poss + 16 * b);
-              const uint32_t* v = &z[b / 8][b % 8 * 4];
-              float p[4];
-              unf2(ffma2(f2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2x, n0), p[0], p[1]);
-              unf2(ffma2(f2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2x, n1), p[2], p[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                p[e] = j0 <= pos[e] && (!a.window || j0 > pos[e] - a.window) ? ex2_approx(p[e]) : 0.f;
-              acc[0] = fadd2(acc[0], f2(p[0], p[1]));
-              acc[1] = fadd2(acc[1], f2(p[2], p[3]));
+              unf2(ffma2(f2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])), c2x, n0), p0, p1);
+              unf2(ffma2(f2(__uint_as_float(z[e + 2]), __uint_as_float(z[e + 3])), c2x, n1), p2, p3);
+              acc[e / 2 % 4] = fadd2(acc[e / 2 % 4], f2(ex2_approx(p0), ex2_approx(p1)));
+              acc[e / 2 % 4 + 1] = fadd2(acc[e / 2 % 4 + 1], f2(ex2_approx(p2), ex2_approx(p3)));
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_QEMPTY + st));
-      }
-      if (!ok) break;
-      if (mine) {
+        if (!ok) break;
         float p, q;
         unf2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), p, q);
-        sum = p + q;
+        const float sum = p + q;
+        if (t == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BAR_DONE));
+        }
         if (g.part >= 0)
           ws.part[(static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kKeys + 128 * t + row] = sum;
         else if (at >= 0)
           w.weights[at] = old + sum;
-      } else if (has(next)) {
-        store(key);
       }
-      at = key.at;
-      old = key.old;
+      at = next_at;
+      old = next_old;
       g = next;
     }
     if (!ok) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
       tmem_wait_st();
       *s_abort = 1;
     }
@@ -676,6 +776,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_chunk_kernel(const WeighArg
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Where a warp has given up, nobody may have waited for the last boxes: they
+  // land before the CTA ends (bounded; a stage without a box may not fill).
+  if (warp == 0 && *s_abort) {
+    const int n = *reinterpret_cast<volatile int32_t*>(base + kOffMisc + 12);
+    for (int x = max(0, n - kStages); x < n; ++x) mbar_wait(bar(BAR_QFULL + x % kStages), (x / kStages) & 1, kWaitLimitNs / 100);
+  }
   if (warp == 3) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0) ws.cta_status[blockIdx.x] = *s_abort ? 5 /* SA_ETIMEOUT */ : (*s_bad ? kPagedInvalid : 0);
   griddep_launch_dependents();
@@ -705,7 +811,7 @@ __global__ void __launch_bounds__(kKeys) weigh_join_kernel(const WeighArgs w, co
 }
 
 template <int kKind>
-cudaError_t launch(const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tm_q, const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s) {
   auto* kern = weigh_chunk_kernel<kKind>;
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kern), kSmem);
@@ -722,7 +828,7 @@ cudaError_t launch(const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStr
     known.store(regs, std::memory_order_relaxed);
   }
   if (regs * 3 < static_cast<int>(kRegsControl + 2 * kRegsKeys)) return cudaErrorInvalidConfiguration;
-  kern<<<ctas, kThreads, kSmem, s>>>(w, ws);
+  kern<<<ctas, kThreads, kSmem, s>>>(tm_q, w, ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(weigh_join_kernel, dim3(ctas), dim3(kKeys), 0, s, w, ws);
@@ -730,8 +836,14 @@ cudaError_t launch(const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStr
 
 }  // namespace
 
-cudaError_t launch_weigh_chunk(const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s) {
-  return w.a.c.kind == 0 ? launch<0>(w, ws, ctas, s) : launch<1>(w, ws, ctas, s);
+cudaError_t launch_weigh_chunk(WeighArgs w, const WeighScratch& ws, int ctas, cudaStream_t s) {
+  const PagedAttnArgs& a = w.a;
+  w.heads = a.group < kRows ? a.group : kRows;
+  w.tokens = kRows / w.heads;
+  w.slices = (a.group + w.heads - 1) / w.heads;
+  CUtensorMap tm_q{};
+  w.boxes = make_map_heads(&tm_q, a.q, a.c.rows, a.c.H, a.group, a.q_token, a.q_head, w.tokens, w.heads);
+  return a.c.kind == 0 ? launch<0>(tm_q, w, ws, ctas, s) : launch<1>(tm_q, w, ws, ctas, s);
 }
 
 }  // namespace sa

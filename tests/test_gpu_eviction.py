@@ -113,6 +113,31 @@ def test_weights_of_a_long_context(bsr, kind, news, Hq):
     run_weigh(bsr, b, Hq)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,news,H,Hq,window", [([2600], [40], 24, 24, 0),        # many units a block, one step each
+                                                   ([5200], [700], 8, 24, 0),        # many, of many steps
+                                                   ([3000, 2000], [900, 1], 6, 30, 1000)])
+def test_weights_of_many_units(bsr, kind, lens, news, H, Hq, window):
+    b = Batch(lens, news, H, 64, kind, seed=15)
+    q, lse, w = run_weigh(bsr, b, Hq, window=window, check=False)
+    # a few keys of a few heads
+    before = fresh_weights(b).cpu().numpy()
+    q64, l64, got = q.double().cpu().numpy(), lse.double().cpu().numpy(), w.cpu().numpy()
+    g = Hq // H
+    for s, n in enumerate(lens):
+        rows = [r for r, _ in OP.positions(b.starts, lens, s)]
+        pos = [p for _, p in OP.positions(b.starts, lens, s)]
+        k = OP.gather(b.k64, b.table_np, s, n)
+        for h in (0, H // 2, H - 1):
+            r, slack, count = OP.received(q64[rows][:, h * g:(h + 1) * g], l64[rows][:, h * g:(h + 1) * g], k[:, h:h + 1], pos, n,
+                                          True, window)
+            j = np.arange(n)
+            at = (b.table_np[s, j // 64], h, j % 64)
+            want = np.where(j < n - len(rows), before[at], 0) + r[0]
+            tol = 2 * 264 * U * slack[0] + 2.0 ** -21 * r[0] + (count[0] + 8) * U * want + count[0] * 2.0 ** -126
+            assert np.all(np.abs(got[at] - want) <= tol), (s, h)
+
+
 def test_weights_of_strided_queries_and_scales(bsr):
     b = Batch([200, 90], [70, 1], 2, 64, seed=4)
     x = torch.randn((b.rows, 3, 4, 136), device="cuda").bfloat16()
