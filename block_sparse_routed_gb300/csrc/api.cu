@@ -199,6 +199,18 @@ bool sa::make_map_heads(CUtensorMap* m, const void* ptr, int tokens, int H, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool sa::make_map_heads16(CUtensorMap* m, const void* ptr, int tokens, int H, int group, int box_tokens, int box_heads) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {8, static_cast<cuuint64_t>(group), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[3] = {16, static_cast<cuuint64_t>(group) * 16, static_cast<cuuint64_t>(group) * H * 16};
+  cuuint32_t box[4] = {8, static_cast<cuuint32_t>(box_heads), 1, static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // [T rows, H*128 columns] view of a BF16 [T, H, 128] tensor.

@@ -247,6 +247,7 @@ struct WeighScratch {
   int32_t* cta_status;  // [ctas]
   WeighJoin* join;      // [ctas]
   float* part;          // [ctas][2][keys]
+  uint4* shift;         // [rows, Hq]: -lse / scale as three BF16 parts, and zeros
 };
 
 struct EvictArgs {
@@ -333,6 +334,9 @@ bool make_map_groups(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t bo
 // zeros past a group's last head.  False where strides allow no map.
 bool make_map_heads(CUtensorMap* m, const void* ptr, int tokens, int H, int group, int64_t token_stride,
                     int64_t head_stride, int box_tokens, int box_heads);
+
+// The same of 16 bytes a head, contiguous [tokens, H * group], no swizzle.
+bool make_map_heads16(CUtensorMap* m, const void* ptr, int tokens, int H, int group, int box_tokens, int box_heads);
 
 size_t route_topk_smem_bytes(const Geometry& g);
 size_t attention_smem_bytes();

@@ -189,7 +189,9 @@ uint64_t weigh_scratch_of(const sa_paged_params* p, void* ws, WeighScratch* out)
   const uint64_t status = off; off += align256(kWeighCtas * 4);
   const uint64_t join = off;   off += align256(kWeighCtas * sizeof(WeighJoin));
   const uint64_t part = off;   off += kWeighCtas * 2 * kWeighKeys * 4;
+  const uint64_t shift = off;  off += uint64_t(p->rows) * p->Hq * 16;
   if (out) {
+    out->shift = reinterpret_cast<uint4*>(w + shift);
     out->cta_status = reinterpret_cast<int32_t*>(w + status);
     out->join = reinterpret_cast<WeighJoin*>(w + join);
     out->part = reinterpret_cast<float*>(w + part);

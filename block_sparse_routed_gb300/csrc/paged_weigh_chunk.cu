@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kKeys = kWeighKeys;  // of a unit
 constexpr int kRows = 96;          // packed rows of a step
-constexpr int kStages = 6, kAhead = 2;
+constexpr int kStages = 5, kAhead = 2;
 constexpr int kSegs = 3;
 constexpr uint32_t kHalfBytes = kRows * 128;  // of a stage: 64 dimensions of its rows
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
@@ -54,31 +54,37 @@ constexpr int kThreads = 32 * (4 + kKeyWarps);
 constexpr uint32_t kRegsLaunch = 168, kRegsControl = 88, kRegsKeys = 208;
 static_assert(kRegsControl + 2 * kRegsKeys <= 3 * kRegsLaunch, "");
 
-// Shared memory, from a 1024-byte boundary.  -L and positions of a step's rows
-// stay twice as long as the rows: the keys' warps release scores, not rows, and
-// are then at most two steps behind the products.
-constexpr int kNegs = 2 * kStages;
-constexpr uint32_t kOffKeys = kStages * kStageBytes;         // the next unit's keys, as they lie in the cache
-constexpr uint32_t kOffNeg = kOffKeys + kKeys * 256;         // [negs][rows]: -L
-constexpr uint32_t kOffPos = kOffNeg + kNegs * kRows * 4;    // [negs][rows]: position
-constexpr uint32_t kOffSeg = kOffPos + kNegs * kRows * 4;
+// Shared memory, from a 1024-byte boundary.  The ninth blocks are laid out
+// without a swizzle: 8 rows x 16 bytes together, eight rows after eight, and
+// the second 16 bytes of all rows behind the first.
+constexpr uint32_t kOnesBytes = 128 * 32, kShiftBytes = kRows * 32;
+constexpr uint32_t kOffKeys = kStages * kStageBytes;            // the next unit's keys, as they lie in the cache
+constexpr uint32_t kOffOnes = kOffKeys + kKeys * 256;           // the ninth block of the keys
+constexpr uint32_t kOffShift = kOffOnes + kOnesBytes;           // [stages]: of the rows
+constexpr uint32_t kOffTok = kOffShift + kStages * kShiftBytes; // [rows]: token of a step's row
+constexpr uint32_t kOffSeg = kOffTok + kRows * 4;
 constexpr uint32_t kOffBar = kOffSeg + kSegs * 64;
 constexpr uint32_t kOffMisc = kOffBar + 512;
 constexpr uint32_t kSmem = kOffMisc + 64 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
 
 enum {
-  BAR_QFULL = 0,     // +stage (6): warps 0 and 1, and the box
+  BAR_QFULL = 0,     // +stage (5): warps 0 and 1, and the box
   BAR_QEMPTY = 8,    // +stage: both tiles' products
-  BAR_SFULL = 16,    // +2 tile, + every other step: the products, and that the step's -L are there
+  BAR_SFULL = 16,    // +2 tile, + every other step
   BAR_SEMPTY = 20,
   BAR_KREADY = 24,   // +tile
-  BAR_DONE = 26,     // the warps of tile 1 are through with a unit
-  BAR_SEGFULL = 28,  // +segment (3)
-  BAR_SEGEMPTY = 31,
-  BAR_DRAIN = 34,    // +tile
-  NUM_BARS = 36
+  BAR_SEGFULL = 26,  // +segment (3)
+  BAR_SEGEMPTY = 29,
+  BAR_DRAIN = 32,    // +tile
+  NUM_BARS = 34
 };
+
+// A matrix descriptor of a ninth block: no swizzle; 16 bytes on, and 8 rows on.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t next16, uint32_t next8) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(next16 >> 4) << 16 |
+         static_cast<uint64_t>(next8 >> 4) << 32 | 1ull << 46;
+}
 
 // One step of the walk: some steps of a unit.
 struct Work {
@@ -299,9 +305,9 @@ __device__ __forceinline__ uint64_t f2(float lo, float hi) {
 __device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
@@ -314,26 +320,17 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ void lds_f2x2(uint64_t& a, uint64_t& b, uint32_t addr) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+__device__ __forceinline__ float bf16_of(float x) {  // rounded to BF16
+  return __uint_as_float(pack_bf16x2(0.f, x) & 0xFFFF0000u);
 }
 __device__ __forceinline__ void lds_i4(int (&v)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
-__device__ __forceinline__ void sts_f1(uint32_t addr, float a) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-}
-
 template <int kKind>
 __global__ void __launch_bounds__(kThreads, 1)
-weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, const WeighScratch ws) {
+weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_shift,
+                   const WeighArgs w, const WeighScratch ws) {
   const PagedAttnArgs& a = w.a;
   const PagedArgs& c = a.c;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -348,10 +345,19 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
   // A step's rows: `tokens` tokens of `heads` heads (a slice of the group).
   const int step_rows = w.tokens * w.heads;
 
+  auto shift_at = [&](int st, int row) { return reinterpret_cast<uint4*>(base + kOffShift + st * kShiftBytes + row * 16); };
+  const uint4 kNothing = make_uint4(0x0000FF80u, 0, 0, 0);  // -infinity: a row that counts nothing
+
   // Rows of a stage that no step has are zeros throughout.
   for (int i = step_rows * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
     for (int st = 0; st < 2 * kStages; ++st)
       *reinterpret_cast<uint4*>(base + st * kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+  // The ninth blocks: three ones in each key; zeros but for a row's three parts.
+  for (int i = threadIdx.x; i < static_cast<int>((kOnesBytes + kStages * kShiftBytes) / 16); i += kThreads)
+    *reinterpret_cast<uint4*>(base + kOffOnes + i * 16) = 
+        i < 128 ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < kStages * kRows; i += kThreads) *shift_at(i / kRows, i % kRows) = kNothing;
+  if (threadIdx.x < kRows) *reinterpret_cast<int*>(base + kOffTok + threadIdx.x * 4) = threadIdx.x / w.heads;
   fence_proxy_async_smem();
   if (threadIdx.x == 0) {
     *s_abort = 0;
@@ -361,14 +367,13 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
       mbar_init(bar(BAR_QEMPTY + i), 2);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(BAR_SFULL + i), 2);
+      mbar_init(bar(BAR_SFULL + i), 1);
       mbar_init(bar(BAR_SEMPTY + i), 4);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(BAR_KREADY + t), 4);
       mbar_init(bar(BAR_DRAIN + t), 1);
     }
-    mbar_init(bar(BAR_DONE), 4);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(BAR_SEGFULL + i), 1);
       mbar_init(bar(BAR_SEGEMPTY + i), 3 + kKeyWarps);
@@ -400,36 +405,14 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
 
   if (warp < 4) setmaxnreg_dec<kRegsControl>();
   if (warp < 2) {
-    // ------------------------------------------------------------ rows of Q
-    if (warp == 0 && lane == 0 && w.boxes) tma_prefetch_desc(&tm_q);
-    // A lane has row lane of the warp's 48, and half of the lanes a second one,
-    // 32 behind it; their lse come a step ahead.
-    struct Row {
-      int at, tok, head;  // of the step
-      int i, sub;         // token, and head of the group
-      bool real;
-      float l;
-    } row[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      row[e].at = 48 * warp + 32 * e + lane;
-      row[e].tok = row[e].at / w.heads;
-      row[e].head = row[e].at - row[e].tok * w.heads;
+    // ------------------------------------------------------------ rows
+    if (warp == 0 && lane == 0 && w.boxes) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_shift);
     }
-    auto rows_at = [&](const Work& g, int j) {
-      const int tile = w.slices == 1 ? g.j0 + j : (g.j0 + j) / w.slices;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        Row& r = row[e];
-        r.sub = (g.j0 + j - tile * w.slices) * w.heads + r.head;
-        r.i = g.i0 + tile * w.tokens + r.tok;
-        r.real = (e == 0 || lane < 16) && r.at < step_rows && r.i < g.i1 && r.sub < a.group;
-        r.l = -INFINITY;
-        if (r.real) r.l = __ldg(w.lse + static_cast<int64_t>(g.row0 + r.i) * a.Hq + g.h * a.group + r.sub);
-      }
-    };
+    griddep_wait();  // the rows' ninth blocks
     const uint32_t elect = elect_one();
-    int x = 0, done = 0;  // steps so far; those whose copies have landed, or are a box's
+    int x = 0, done = 0;  // steps so far; those whose copies have landed, or are boxes
     auto publish = [&](int to) {
       if (done >= to) return;
       fence_proxy_async_smem();
@@ -444,40 +427,42 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
     Work g;
     int k = 0, j = 0;
     ok = next_seg(0, g);
-    if (ok && g.valid) rows_at(g, 0);
     while (ok && g.valid) {
-      const int st = x % kStages, ng = x % kNegs;
+      const int st = x % kStages;
       ok = x < kStages || all_wait(BAR_QEMPTY + st, x / kStages - 1);
       if (!ok) break;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const Row& r = row[e];
-        if (e == 1 && lane >= 16) break;
-        sts_f1(sbase + kOffNeg + (ng * kRows + r.at) * 4, r.l == -INFINITY ? -INFINITY : -r.l * 1.4426950408889634f);
-        *reinterpret_cast<int*>(base + kOffPos + (ng * kRows + r.at) * 4) = r.real ? g.len - g.n + r.i : -0x40000000;
-      }
-      const int first = __shfl_sync(0xFFFFFFFFu, row[0].i - row[0].tok, 0);  // token of the step's first row
-      if (w.boxes && first + w.tokens <= g.i1) {
-        __syncwarp();
+      const int tile = w.slices == 1 ? g.j0 + j : (g.j0 + j) / w.slices, slice = g.j0 + j - tile * w.slices;
+      const int first = g.i0 + tile * w.tokens;  // token of the step's first row
+      if (w.boxes && first + w.tokens <= g.i1 && (slice + 1) * w.heads <= a.group) {
         if (warp == 0 && elect) {
-          mbar_arrive_expect_tx(bar(BAR_QFULL + st), 2 * step_rows * 128);
+          mbar_arrive_expect_tx(bar(BAR_QFULL + st), step_rows * (2 * 128 + 16));
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             tma_load_4d(sbase + st * kStageBytes + half * kHalfBytes, &tm_q, bar(BAR_QFULL + st), half * 64,
-                        row[0].sub - row[0].head, g.h, g.row0 + first);
+                        slice * w.heads, g.h, g.row0 + first);
+          tma_load_4d(sbase + kOffShift + st * kShiftBytes, &tm_shift, bar(BAR_QFULL + st), 0, slice * w.heads, g.h,
+                      g.row0 + first);
         } else if (warp != 0 && lane == 0) {
           mbar_arrive(bar(BAR_QFULL + st));
         }
+        __syncwarp();
         if (done < x) flush();
         done = ++x;
       } else {
-#pragma unroll
+        // a lane has row lane of the warp's 48, and half of the lanes a second one, 32 behind it
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-          const Row& r = row[e];
+          const int at = 48 * warp + 32 * e + lane, tok = at / w.heads, i = first + tok, sub = slice * w.heads + at - tok * w.heads;
+          const bool real = (e == 0 || lane < 16) && at < step_rows && i < g.i1 && sub < a.group;
           const uint16_t* src0 = a.q;
-          if (r.real) src0 += static_cast<int64_t>(g.row0 + r.i) * a.q_token + static_cast<int64_t>(g.h * a.group + r.sub) * a.q_head;
+          if (real) {
+            src0 += static_cast<int64_t>(g.row0 + i) * a.q_token + static_cast<int64_t>(g.h * a.group + sub) * a.q_head;
+            cp_async16(smem_u32(shift_at(st, at)), ws.shift + static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + sub, true);
+          } else if (e == 0 || lane < 16) {
+            *shift_at(st, at) = kNothing;
+          }
           const uint32_t to = sbase + st * kStageBytes + (lane % 16 / 8) * kHalfBytes + (48 * warp + 32 * e) * 128;
-          const unsigned reals = __ballot_sync(0xFFFFFFFFu, r.real);
+          const unsigned reals = __ballot_sync(0xFFFFFFFFu, real);
 #pragma unroll 4
           for (int y = 0; y < (e ? 16 : 32); y += 2) {
             const int z = y + lane / 16;
@@ -499,9 +484,7 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
         // The next description may come only once the products of these steps are under way.
         if (done < x && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar(BAR_SEGFULL + k % kSegs), (k / kSegs) & 1))) flush();
         ok = next_seg(k, g);
-        if (!ok) break;
       }
-      if (g.valid) rows_at(g, j);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (ok) publish(x);
@@ -533,8 +516,10 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
     } else {
       ok = next_seg(k++, g);
     }
-    const uint32_t id = idesc_bf16(128, (step_rows + 15) / 16 * 16, false, false);
+    // (whole thirds: what is no row counts nothing)
+    const uint32_t id = idesc_bf16(128, (step_rows + 31) / 32 * 32, false, false);
     auto off = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4); };
+    const uint64_t ones = sdesc_plain(sbase + kOffOnes, 128 * 16, 128);
     const uint32_t elect = elect_one();
     int st = 0, phase = 0;  // the next step's stage
     int y = 0, u = 0;       // steps and units of the tile
@@ -544,14 +529,7 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
       const bool mine = g.hi > g.key0 + 128 * t;
       ok = t == 0 ? give() : next_seg(k++, g);  // (g is the next unit's from here on)
       if (!ok) break;
-      if (mine) {
-        ok = all_wait(BAR_KREADY + t, u++);
-      } else if (u > 0) {
-        // The tile has a pause, in which its warps could be more than two steps
-        // behind: they are through with their last unit before the rows' -L
-        // are written over.
-        ok = all_wait(BAR_DONE, u - 1);
-      }
+      if (mine) ok = all_wait(BAR_KREADY + t, u++);
 #pragma unroll 1
       for (int j = 0; j < steps && ok; ++j) {
         ok = all_wait(BAR_QFULL + st, phase);
@@ -565,9 +543,9 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
           const uint64_t qs = sdesc_sw128(sbase + st * kStageBytes, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) umma_ts_elect(d, tmem + 64 * t + 8 * kk, qs + off(kk), id, kk > 0 ? 1u : 0u, elect);
+          umma_ss_elect(d, ones, sdesc_plain(sbase + kOffShift + st * kShiftBytes, kRows * 16, 128), id, 1u, elect);
           if (elect) {
             umma_commit(bar(BAR_SFULL + s));
-            mbar_arrive(bar(BAR_SFULL + s));
             umma_commit(bar(BAR_QEMPTY + st));
           }
           issued = true;
@@ -665,7 +643,7 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_KREADY + t));
     };
-    int y = 0, ng = 0;  // steps of the tile; place of the next step's -L
+    int y = 0;  // steps of the tile
     Work g, next;
     int64_t at = -1;
     float old = 0.f;
@@ -681,7 +659,6 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
       if (!ok) break;
       load(next);
       if (!has(g)) {
-        ng = (ng + g.steps) % kNegs;
         if (has(next)) store();
       } else {
         const int j0 = g.key0 + 128 * t + row;
@@ -698,65 +675,74 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
         uint64_t acc[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) acc[b] = f2(0.f, 0.f);
-#pragma unroll 1
-        for (int j = 0; j < g.steps; ++j, ++y) {
+        uint32_t z[kRows / 32][32];
+        // The scores of the unit's step j are there; the first third of them is on its way.
+        auto arrived = [&](int j) -> bool {
           const int s = 2 * t + (y & 1);
-          const uint32_t col = tmem + lane_addr + 128 + kRows * s;
-          const uint32_t negs = sbase + kOffNeg + ng * (kRows * 4);
-          ng = ng + 1 == kNegs ? 0 : ng + 1;
-          ok = all_wait(BAR_SFULL + s, y / 2);
-          if (!ok) break;
+          if (!all_wait(BAR_SFULL + s, y / 2)) return false;
           tc_fence_after();
+          const uint32_t col = tmem + lane_addr + 128 + kRows * s;
           if (g.j0 + j < e0 || g.j0 + j >= e1) {
             // masked in place: a second copy of the sums, with the mask in it,
-            // is not in the instruction cache
+            // is not in the instruction cache (1002 us against 846 for the long chunk)
+            const int tile = w.slices == 1 ? g.j0 + j : (g.j0 + j) / w.slices;
+            const int p0 = g.len - g.n + g.i0 + tile * w.tokens, k0 = j0 - lane;  // the step's first row, the warp's first key
 #pragma unroll 1
-            for (int b = 0; b < kRows; b += 8) {
-              uint32_t v[8];
-              int pos[8];
-              tmem_ld8(col + b, v);
-              lds_i4(*reinterpret_cast<int(*)[4]>(&pos[0]), negs + kOffPos - kOffNeg + 4 * b);
-              lds_i4(*reinterpret_cast<int(*)[4]>(&pos[4]), negs + kOffPos - kOffNeg + 4 * b + 16);
-              tmem_wait_ld();
+            for (int b = 0; b < kRows; b += 16) {
+              int tok[16];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (j0 > pos[e] || (a.window && j0 <= pos[e] - a.window)) v[e] = __float_as_uint(-INFINITY);
-              tmem_st8(col + b, v);
+              for (int e = 0; e < 16; e += 4) lds_i4(*reinterpret_cast<int(*)[4]>(&tok[e]), sbase + kOffTok + 4 * (b + e));
+              const int pa = p0 + tok[0], pz = p0 + tok[15];
+              if (k0 + 31 <= pa && (!a.window || k0 > pz - a.window)) continue;  // all are seen
+              uint32_t v[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(-INFINITY);
+              if (k0 <= pz && (!a.window || k0 + 31 > pa - a.window)) {  // some are
+                tmem_ld16(col + b, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (j0 > p0 + tok[e] || (a.window && j0 <= p0 + tok[e] - a.window)) v[e] = __float_as_uint(-INFINITY);
+              }
+              tmem_st16(col + b, v);
             }
             tmem_wait_st();
           }
-          uint32_t z[kRows];
+          tmem_ld32(col, z[0]);
+          // no product reads the unit's keys any more
+          if (j + 1 == g.steps && has(next)) store();
+          return true;
+        };
+        ok = arrived(0);
+#pragma unroll 1
+        for (int j = 0; ok && j < g.steps; ++j) {
+          const int s = 2 * t + (y & 1);
+          auto add = [&](const uint32_t(&v)[32]) {
 #pragma unroll
-          for (int b = 0; b < kRows; b += 32) tmem_ld32(col + b, *reinterpret_cast<uint32_t(*)[32]>(&z[b]));
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              unf2(fmul2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x), p0, p1);
+              acc[e / 2 % 4] = fadd2(acc[e / 2 % 4], f2(ex2_approx(p0), ex2_approx(p1)));
+            }
+          };
+          tmem_wait_ld();
+#pragma unroll
+          for (int b = 1; b < kRows / 32; ++b) tmem_ld32(tmem + lane_addr + 128 + kRows * s + 32 * b, z[b]);
+          add(z[0]);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + s));
-          // no product reads the unit's keys any more
-          if (j + 1 == g.steps && has(next)) store();
-#pragma unroll
-          for (int b = 0; b < kRows; b += 32) {
-            if (b >= step_rows) break;  // (no such rows)
-#pragma unroll
-            for (int e = b; e < b + 32; e += 4) {
-              uint64_t n0, n1;
-              lds_f2x2(n0, n1, negs + 4 * e);
-              float p0, p1, p2, p3;
-              unf2(ffma2(f2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])), c2x, n0), p0, p1);
-              unf2(ffma2(f2(__uint_as_float(z[e + 2]), __uint_as_float(z[e + 3])), c2x, n1), p2, p3);
-              acc[e / 2 % 4] = fadd2(acc[e / 2 % 4], f2(ex2_approx(p0), ex2_approx(p1)));
-              acc[e / 2 % 4 + 1] = fadd2(acc[e / 2 % 4 + 1], f2(ex2_approx(p2), ex2_approx(p3)));
-            }
-          }
+          if (step_rows > 32) add(z[1]);
+          ++y;
+          // the next step's first third comes while this one's last is added
+          if (j + 1 < g.steps) ok = arrived(j + 1);
+          if (step_rows > 64) add(z[2]);
         }
         if (!ok) break;
         float p, q;
         unf2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), p, q);
         const float sum = p + q;
-        if (t == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_DONE));
-        }
         if (g.part >= 0)
           ws.part[(static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kKeys + 128 * t + row] = sum;
         else if (at >= 0)
@@ -787,6 +773,18 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const WeighArgs w, 
   griddep_launch_dependents();
 }
 
+// The rows' ninth blocks: -lse / scale = hi + mid + lo in BF16.
+__global__ void __launch_bounds__(256) weigh_shift_kernel(const WeighArgs w, const WeighScratch ws) {
+  griddep_launch_dependents();
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= static_cast<int64_t>(w.a.c.rows) * w.a.Hq) return;
+  const float l = w.lse[at];
+  const float v = l == -INFINITY ? -INFINITY : -l / w.a.scale;
+  const float hi = bf16_of(v);
+  const float mid = isfinite(hi) ? bf16_of(v - hi) : 0.f, lo = isfinite(hi) ? v - hi - mid : 0.f;
+  ws.shift[at] = make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0, 0);
+}
+
 // The units that a cut divided, their parts in order; and the call's status.
 __global__ void __launch_bounds__(kKeys) weigh_join_kernel(const WeighArgs w, const WeighScratch ws) {
   griddep_wait();
@@ -811,7 +809,7 @@ __global__ void __launch_bounds__(kKeys) weigh_join_kernel(const WeighArgs w, co
 }
 
 template <int kKind>
-cudaError_t launch(const CUtensorMap& tm_q, const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_shift, const WeighArgs& w, const WeighScratch& ws, int ctas, cudaStream_t s) {
   auto* kern = weigh_chunk_kernel<kKind>;
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kern), kSmem);
@@ -828,8 +826,11 @@ cudaError_t launch(const CUtensorMap& tm_q, const WeighArgs& w, const WeighScrat
     known.store(regs, std::memory_order_relaxed);
   }
   if (regs * 3 < static_cast<int>(kRegsControl + 2 * kRegsKeys)) return cudaErrorInvalidConfiguration;
-  kern<<<ctas, kThreads, kSmem, s>>>(tm_q, w, ws);
+  const int64_t all = static_cast<int64_t>(w.a.c.rows) * w.a.Hq;
+  weigh_shift_kernel<<<static_cast<unsigned>((all + 255) / 256), 256, 0, s>>>(w, ws);
   e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(ctas), dim3(kThreads), kSmem, s, tm_q, tm_shift, w, ws);
   if (e != cudaSuccess) return e;
   return launch_dependent(weigh_join_kernel, dim3(ctas), dim3(kKeys), 0, s, w, ws);
 }
@@ -841,9 +842,10 @@ cudaError_t launch_weigh_chunk(WeighArgs w, const WeighScratch& ws, int ctas, cu
   w.heads = a.group < kRows ? a.group : kRows;
   w.tokens = kRows / w.heads;
   w.slices = (a.group + w.heads - 1) / w.heads;
-  CUtensorMap tm_q{};
-  w.boxes = make_map_heads(&tm_q, a.q, a.c.rows, a.c.H, a.group, a.q_token, a.q_head, w.tokens, w.heads);
-  return a.c.kind == 0 ? launch<0>(tm_q, w, ws, ctas, s) : launch<1>(tm_q, w, ws, ctas, s);
+  CUtensorMap tm_q{}, tm_shift{};
+  w.boxes = make_map_heads(&tm_q, a.q, a.c.rows, a.c.H, a.group, a.q_token, a.q_head, w.tokens, w.heads) &&
+            make_map_heads16(&tm_shift, ws.shift, a.c.rows, a.c.H, a.group, w.tokens, w.heads);
+  return a.c.kind == 0 ? launch<0>(tm_q, tm_shift, w, ws, ctas, s) : launch<1>(tm_q, tm_shift, w, ws, ctas, s);
 }
 
 }  // namespace sa
