@@ -517,7 +517,7 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       ok = next_seg(k++, g);
     }
     // (whole thirds: what is no row counts nothing)
-    const uint32_t id = idesc_bf16(128, (step_rows + 31) / 32 * 32, false, false);
+    const uint32_t id = idesc_bf16(128, kRows, false, false);
     auto off = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4); };
     const uint64_t ones = sdesc_plain(sbase + kOffOnes, 128 * 16, 128);
     const uint32_t elect = elect_one();
@@ -676,7 +676,7 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
         for (int b = 0; b < 4; ++b) acc[b] = f2(0.f, 0.f);
         uint32_t z[kRows / 32][32];
-        // The scores of the unit's step j are there; the first third of them is on its way.
+        // The scores of the unit's step j are there, and on their way.
         auto arrived = [&](int j) -> bool {
           const int s = 2 * t + (y & 1);
           if (!all_wait(BAR_SFULL + s, y / 2)) return false;
@@ -708,36 +708,30 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tmem_wait_st();
           }
-          tmem_ld32(col, z[0]);
+#pragma unroll
+          for (int b = 0; b < kRows / 32; ++b) tmem_ld32(col + 32 * b, z[b]);
           // no product reads the unit's keys any more
           if (j + 1 == g.steps && has(next)) store();
           return true;
         };
-        ok = arrived(0);
 #pragma unroll 1
-        for (int j = 0; ok && j < g.steps; ++j) {
-          const int s = 2 * t + (y & 1);
-          auto add = [&](const uint32_t(&v)[32]) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              unf2(fmul2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x), p0, p1);
-              acc[e / 2 % 4] = fadd2(acc[e / 2 % 4], f2(ex2_approx(p0), ex2_approx(p1)));
-            }
-          };
-          tmem_wait_ld();
-#pragma unroll
-          for (int b = 1; b < kRows / 32; ++b) tmem_ld32(tmem + lane_addr + 128 + kRows * s + 32 * b, z[b]);
-          add(z[0]);
+        for (int j = 0; j < g.steps; ++j) {
+          ok = arrived(j);
+          if (!ok) break;
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + s));
-          if (step_rows > 32) add(z[1]);
+          if (lane == 0) mbar_arrive(bar(BAR_SEMPTY + 2 * t + (y & 1)));
           ++y;
-          // the next step's first third comes while this one's last is added
-          if (j + 1 < g.steps) ok = arrived(j + 1);
-          if (step_rows > 64) add(z[2]);
+#pragma unroll
+          for (int b = 0; b < kRows / 32; ++b) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              unf2(fmul2(f2(__uint_as_float(z[b][e]), __uint_as_float(z[b][e + 1])), c2x), p0, p1);
+              acc[e / 2 % 4] = fadd2(acc[e / 2 % 4], f2(ex2_approx(p0), ex2_approx(p1)));
+            }
+          }
         }
         if (!ok) break;
         float p, q;
