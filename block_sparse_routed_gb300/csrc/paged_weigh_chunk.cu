@@ -9,21 +9,39 @@
 // at a time.  A thread has a key: it reads the key's scores of 96 rows, and
 // adds up their exponentials in registers.  Nothing passes between threads.
 //
-// Keys in tensor memory, because shared memory would not feed them: of a step
-// (two tiles, 96 rows) products read Q there twice, 2 x 24 KB, and the copies
-// write 24 KB, 560 cycles at 128 bytes a cycle, against 768 of the tensor
+// A row's lse belongs to a column, which all threads read: from shared memory
+// that is 768 cycles a step.  So the products subtract it, in a ninth block of
+// 16 dimensions: 1 in the keys, and in the rows -lse / scale as three BF16
+// parts, which hold all of its 24 bits (604 -> 580 us for 2048 rows that see all
+// of 33792 keys).  A kernel in front makes the rows' blocks (made by the warps
+// that bring the rows, these were what the rest waited for: 580 -> 555).
+//
+// Keys are in tensor memory because shared memory would not feed both operands:
+// of a step (two tiles, 96 rows) products read Q there twice, 2 x 24 KB, and the
+// copies write 24 KB, 560 cycles at 128 bytes a cycle, against 864 of the tensor
 // pipe; with the keys in shared memory it would be 1060.
 //
+// What bounds it is the warps of keys: a step takes them 1400 cycles.  The
+// exponentials are 768 of a scheduler's two warps, but a warp alone takes 650 for
+// its own (their latency), reading 96 columns of tensor memory 240, and waiting
+// for them and releasing them 200.  Three tiles with one place for their scores
+// take 2115 cycles a step, 16 warps of 48 columns each 1650 for two tiles, a
+// loop that reads ahead in thirds 1440, one of 32 columns 1640: tried, not kept.
+//
 // The line of all steps of all units is cut into equal parts, one a CTA; a
-// unit that a cut divides is joined from its parts in order by a second kernel.
+// unit that a cut divides is joined from its parts in order by another kernel.
 //
 // Warps: 0 and 1 bring the rows of Q, a box of whole tokens a step (and gather,
 // 48 rows each, what is no whole box: a sequence's last rows, strides that no
-// box has); 2 and 3 issue the products of tile 1 and 0 (an issue takes about
-// 48 cycles, as long as the product: one warp for both came to 1000 cycles a
-// step), and 3 walks the line; 4-7 and 8-11 are the keys of tile 0 and 1.
-// They bring the next unit's keys into shared memory while the present one's
-// rows pass, widen codes, and write them to tensor memory.
+// box has); 2 and 3 issue the products of tile 1 and 0 (one warp for both: 556
+// against 538 us), and 3 walks the line; 4-7 and 8-11 are the keys of tile 0
+// and 1.  They bring the next unit's keys into shared memory while the present
+// one's rows pass, widen codes, and write them to tensor memory.
+//
+// Measured (graphs of four calls; tensor rate of the visible pairs):
+//   2048 new of 33792, 40 / 8 heads, causal, BF16      570 us  1206 TFLOP/s
+//   8704 of 8704, 24 / 24 heads, causal, BF16          212 us  1096
+//   64 each of 8 sequences, 24 / 24 heads, E4M3         71 us  (1.3 TB/s: units of one step)
 //
 // Tensor memory: K of tile t in columns [64 t, + 64); scores of tile t, every
 // other step, in [128 + 96 (2 t + b), + 96).
@@ -352,11 +370,12 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   for (int i = step_rows * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
     for (int st = 0; st < 2 * kStages; ++st)
       *reinterpret_cast<uint4*>(base + st * kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
-  // The ninth blocks: three ones in each key; zeros but for a row's three parts.
-  for (int i = threadIdx.x; i < static_cast<int>((kOnesBytes + kStages * kShiftBytes) / 16); i += kThreads)
-    *reinterpret_cast<uint4*>(base + kOffOnes + i * 16) = 
-        i < 128 ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < kStages * kRows; i += kThreads) *shift_at(i / kRows, i % kRows) = kNothing;
+  // The ninth blocks: three ones in each key; nothing yet in the rows.
+  for (int i = threadIdx.x; i < static_cast<int>((kOnesBytes + kStages * kShiftBytes) / 16); i += kThreads) {
+    const bool ones = i < 128, row = i >= 256 && (i - 256) % (2 * kRows) < kRows;
+    *reinterpret_cast<uint4*>(base + kOffOnes + i * 16) =
+        ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : row ? kNothing : make_uint4(0, 0, 0, 0);
+  }
   if (threadIdx.x < kRows) *reinterpret_cast<int*>(base + kOffTok + threadIdx.x * 4) = threadIdx.x / w.heads;
   fence_proxy_async_smem();
   if (threadIdx.x == 0) {
