@@ -14,7 +14,7 @@
 namespace sa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kBlocks = 4;  // blocks an SM
 constexpr int kTileKeys = 16;  // keys of a warp's tile: inside one page
 
 // Keys of sequence q whose weight the call writes.
@@ -117,8 +117,21 @@ struct Rows {
   }
 };
 
+// A tile of 16 keys: keys u and u + 8 of the lanes of a row.
+template <int kKind>
+struct Tile {
+  uint4 x[2][kKind == 0 ? 4 : 2];
+  float scale[2];  // of their logits
+  float old;       // the weight that this lane writes
+  int64_t row0;    // first row of the cache; -1: not to be looked at
+  int key0, lo, hi;
+  bool fresh;      // the first of its unit
+  PagedSeq q;
+  int h;
+};
+
 template <int kKind, int kN>  // kN: tiles of eight rows
-__global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const WeighArgs w) {
   const PagedAttnArgs& a = w.a;
   const PagedArgs& c = a.c;
   const int lane = threadIdx.x % 32, u = lane / 4, t4 = lane % 4;
@@ -126,11 +139,10 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
   const int worker = blockIdx.x * kWarps + threadIdx.x / 32, workers = gridDim.x * kWarps;
   // The line of all tiles, in the order (sequence, head, tile), in equal parts.
   PagedSeq q;
-  int64_t total = 0;
+  const int first_tiles = lane_tiles16(w, lane, q);  // of the first 32 sequences
+  int64_t total = first_tiles;
 #pragma unroll 1
-  for (int base = 0; base < c.seqs; base += 32) {
-    total += lane_tiles16(w, base + lane, q);
-  }
+  for (int base = 32; base < c.seqs; base += 32) total += lane_tiles16(w, base + lane, q);
   total = warp_sum(total) * c.H;
   int64_t at = muldiv(worker, total, workers);
   const int64_t end = muldiv(worker + 1, total, workers);
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
     int64_t left = at;
 #pragma unroll 1
     for (int base = 0;; base += 32) {
-      const int64_t mine = static_cast<int64_t>(lane_tiles16(w, base + lane, q)) * c.H;
+      const int64_t mine = static_cast<int64_t>(base ? lane_tiles16(w, base + lane, q) : first_tiles) * c.H;
       const int64_t upto = warp_scan(mine, lane);
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
       if (hit) {
@@ -158,11 +170,12 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
     t = static_cast<int>(left - static_cast<int64_t>(h) * nt);
   }
   KeySpan k = key_span(w, q);
-  Rows<kKind, kN> rows;
-  bool fresh = true;  // the unit's rows are to be loaded
+  bool fresh = true;
   int have = -1, entry = 0;  // table entries 32 have + lane
   const float c2 = a.scale * 1.4426950408889634f;
-  for (; at < end; ++at, ++t) {
+  constexpr int kRow = kKind == 0 ? 256 : 128, kLoads = kKind == 0 ? 4 : 2;
+  // The next tile of the part, its loads under way.
+  auto fetch = [&](Tile<kKind>& n) {
     if (t == k.nt) {
       t = 0;
       fresh = true;
@@ -171,57 +184,68 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
         have = -1;
         do {
           bool bad;
-          if (++s >= c.seqs) return;
+          if (++s >= c.seqs) {
+            n.row0 = -1;
+            return;
+          }
           q = paged_seq(c, s, bad);
           k = key_span(w, q);
         } while (k.nt == 0);
       }
     }
-    const int key0 = (k.t0 + t) * kTileKeys;
-    const int pi = key0 >> c.page_shift;
+    n.key0 = (k.t0 + t) * kTileKeys;
+    n.lo = k.lo;
+    n.hi = k.hi;
+    n.fresh = fresh;
+    n.q = q;
+    n.h = h;
+    fresh = false;
+    ++t;
+    const int pi = n.key0 >> c.page_shift;
     if (pi / 32 != have) {
       have = pi / 32;
       const int e = have * 32 + lane;
-      entry = e << c.page_shift < k.hi && ((e + 1) << c.page_shift) > k.lo ? __ldg(c.table + s * c.table_stride + e) : 0;
+      entry = (static_cast<int64_t>(e) << c.page_shift) < k.hi && (static_cast<int64_t>(e + 1) << c.page_shift) > k.lo
+                  ? __ldg(c.table + s * c.table_stride + e) : 0;
     }
     const int page = __shfl_sync(0xFFFFFFFFu, entry, pi % 32);
+    n.row0 = -1;
     if (page < 0 || page >= c.pages) {
       if (lane == 0) paged_fail(c);
-      continue;
+      return;
     }
-    const int64_t row0 = ((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (key0 & (c.page_size - 1));
-    // K as the first operand: keys u and u + 8
-    uint4 x[2][kKind == 0 ? 4 : 2];
-    constexpr int kRow = kKind == 0 ? 256 : 128;
+    n.row0 = ((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (n.key0 & (c.page_size - 1));
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int i = 0; i < (kKind == 0 ? 4 : 2); ++i)
-        x[e][i] = ld_stream(c.k_pages + (row0 + u + 8 * e) * kRow + 16 * (t4 + 4 * i));
-    float scale[2] = {c2, c2};
-    if constexpr (kKind != 0) {
+      for (int i = 0; i < kLoads; ++i) n.x[e][i] = ld_stream(c.k_pages + (n.row0 + u + 8 * e) * kRow + 16 * (t4 + 4 * i));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) scale[e] = exp_scale(__ldg(c.k_exp + row0 + u + 8 * e)) * (128.0f * c2);
-    }
+    for (int e = 0; e < 2; ++e) n.scale[e] = kKind == 0 ? c2 : exp_scale(__ldg(c.k_exp + n.row0 + u + 8 * e)) * (128.0f * c2);
     // lanes t = 0 and 1 of each four write keys u and u + 8
-    const int key = key0 + u + 8 * t4;
-    const bool write = t4 < 2 && key >= k.lo && key < k.hi;
-    float* to = w.weights + row0 + u + 8 * t4;
-    float old = 0.f;
-    if (write && w.accumulate && key < q.len - q.n) old = *to;
-    float sum[2] = {0.f, 0.f};
-    {
-      if (fresh) rows.load(w, q, h, 0, lane);
-      fresh = false;
+    const int key = n.key0 + u + 8 * t4;
+    n.old = 0.f;
+    if (t4 < 2 && key >= k.lo && key < q.len - q.n && w.accumulate) n.old = w.weights[n.row0 + u + 8 * t4];
+  };
+  Rows<kKind, kN> rows;
+  bool need = false;  // the unit's rows are to be loaded
+  Tile<kKind> now, next;
+  fetch(now);
+#pragma unroll 1
+  for (; at < end; ++at) {
+    if (at + 1 < end) fetch(next);
+    need |= now.fresh;
+    if (now.row0 >= 0) {
+      if (need) rows.load(w, now.q, now.h, 0, lane);
+      need = false;
       float d[kN][4];
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
 #pragma unroll
-      for (int i = 0; i < (kKind == 0 ? 4 : 2); ++i) {
-        const uint32_t k0[4] = {x[0][i].x, x[0][i].y, x[0][i].z, x[0][i].w};
-        const uint32_t k1[4] = {x[1][i].x, x[1][i].y, x[1][i].z, x[1][i].w};
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t k0[4] = {now.x[0][i].x, now.x[0][i].y, now.x[0][i].z, now.x[0][i].w};
+        const uint32_t k1[4] = {now.x[1][i].x, now.x[1][i].y, now.x[1][i].z, now.x[1][i].w};
         if constexpr (kKind == 0) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
@@ -237,21 +261,24 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs w) {
           }
         }
       }
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // key u + 8 (e / 2), row 2 t + e % 2
-          const int j = key0 + u + 8 * (e / 2);
-          const float p = ex2_approx(fmaf(d[n][e], scale[e / 2], rows.neg[n][e & 1]));
+          const int j = now.key0 + u + 8 * (e / 2);
+          const float p = ex2_approx(fmaf(d[n][e], now.scale[e / 2], rows.neg[n][e & 1]));
           if (j >= rows.lo[n][e & 1] && j < rows.hi[n][e & 1]) sum[e / 2] += p;
         }
-    }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
-      sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
+      for (int e = 0; e < 2; ++e) {
+        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
+        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
+      }
+      const int key = now.key0 + u + 8 * t4;
+      if (t4 < 2 && key >= now.lo && key < now.hi) w.weights[now.row0 + u + 8 * t4] = now.old + (t4 ? sum[1] : sum[0]);
     }
-    if (write) *to = old + (t4 ? sum[1] : sum[0]);
+    now = next;
   }
 }
 
@@ -265,7 +292,7 @@ cudaError_t launch(const WeighArgs& w, int ctas, cudaStream_t s) {
 
 cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s) {
   int64_t ctas = (key_tiles + kWarps - 1) / kWarps;
-  if (ctas > 6 * sms) ctas = 6 * sms;
+  if (ctas > kBlocks * sms) ctas = kBlocks * sms;
   const int n = static_cast<int>(ctas);
   if (w.a.c.kind == 0) return rows <= 8 ? launch<0, 1>(w, n, s) : launch<0, 2>(w, n, s);
   return rows <= 8 ? launch<1, 1>(w, n, s) : launch<1, 2>(w, n, s);
