@@ -4,7 +4,26 @@
 //            2^(x_rj - L_r),   x_rj = scale log2(e) (q_r . k_j),  L_r = log2(e) lse_r
 //
 // A key's weight depends on its own K alone, so whoever has a key adds up all
-// rows for it: nothing is joined, and no atomics change an order.
+// rows for it: nothing is joined, and no atomics change an order.  This is the
+// form for few rows (at most 16 packed rows a sequence and key head).
+//
+// Bound by memory: K once (256 bytes a key and head, 129 in the E4M3 kind), the
+// weight read and written.  The line of all tiles of 16 keys is cut into equal
+// parts, one a warp, however ragged the batch is; warps share nothing, so a call
+// is a launch, a walk of the line and as many tiles as a warp has.  K goes from
+// memory into the registers of mma.sync m16n8k16 as its first operand (the
+// order of dimensions inside a product is free), a tile while the last one is
+// multiplied.
+//
+// Measured:
+//   64 sequences of 512 to 33792 keys, 40 / 8 heads, BF16, one new   129 us  6.47 TB/s
+//                                                    E4M3             79 us  5.48
+//   64 of 8704, 24 / 8 heads, four new (12 rows): BF16               186 us  6.32
+//                                                 E4M3               129 us  4.76
+//   one of 1152, 8 / 2 heads, BF16                                   6.4 us  (latency)
+// Without the loads ahead the first takes 153 us; in E4M3 what a tile costs
+// besides its bytes counts: finding the next one from the last (113 -> 89 us)
+// and codes as FP16 instead of BF16.  Two tiles ahead: no better (registers).
 #include <cstdint>
 
 #include "internal.h"
@@ -14,7 +33,10 @@
 namespace sa {
 namespace {
 
-constexpr int kWarps = 4, kBlocks = 4;  // blocks an SM
+constexpr int kWarps = 4;
+// Blocks an SM: what the registers of so many rows allow without spills.
+template <int kN>
+constexpr int kBlocks = kN == 1 ? 4 : 3;
 constexpr int kTileKeys = 16;  // keys of a warp's tile: inside one page
 
 // Keys of sequence q whose weight the call writes.
@@ -52,27 +74,38 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                : "l"(p));
   return v;
 }
-// Codes (c0, c2) and (c1, c3) of a word as BF16 pairs, times 2^-7.
-__device__ __forceinline__ uint32_t times_2_113(uint32_t v) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x78007800u));
-  return d;
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-  return times_2_113(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u));
+// Codes (c0, c1) and (c2, c3) as FP16 pairs.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
-  return times_2_113(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u));
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
 }
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // Rows of Q: as the second operand of K Q^T, 8 kN of them.  A lane has row
 // lane / 4 of each eight, and 16-byte chunks lane % 4 + 4 i of it, as of K's
 // rows: the order of dimensions inside a product is free as long as both have
 // the same.
+// E4M3: K's codes become FP16 (two instructions for four), and so does Q, each row
+// scaled by the even power of two that brings its largest magnitude to 2^13 or
+// 2^14 or just below: exact down to 2^-30 of that.
 template <int kKind, int kN>
 struct Rows {
   uint32_t q[kN][8][2];
   float neg[kN][2];        // -L of rows 2 t, 2 t + 1 of each eight (-inf: counts nothing)
+  float undo[kN][2];       // E4M3: their squares undo the rows' scaling
   int lo[kN][2], hi[kN][2];  // keys that they see
 
   __device__ __forceinline__ void load(const WeighArgs& w, const PagedSeq& s, int h, int rho0, int lane) {
@@ -84,23 +117,42 @@ struct Rows {
       const int i = div_group(a, rho);
       const uint16_t* src = a.q + static_cast<int64_t>(s.row0 + i) * a.q_token +
                             static_cast<int64_t>(h * a.group + rho - i * a.group) * a.q_head;
+      uint4 x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (kKind == 0) {
-          if (rho < rows) x = __ldg(reinterpret_cast<const uint4*>(src + 8 * (t4 + 4 * e)));
-          q[n][2 * e][0] = x.x;
-          q[n][2 * e][1] = x.y;
-          q[n][2 * e + 1][0] = x.z;
-          q[n][2 * e + 1][1] = x.w;
-        } else {
-          // 16 codes of K are 32 bytes here; a word's codes are taken as (c0, c2), (c1, c3)
-          if (rho < rows) x = __ldg(reinterpret_cast<const uint4*>(src + 16 * (t4 + 4 * (e / 2)) + 8 * (e % 2)));
-          q[n][2 * e][0] = __byte_perm(x.x, x.y, 0x5410);
-          q[n][2 * e][1] = __byte_perm(x.x, x.y, 0x7632);
-          q[n][2 * e + 1][0] = __byte_perm(x.z, x.w, 0x5410);
-          q[n][2 * e + 1][1] = __byte_perm(x.z, x.w, 0x7632);
+        x[e] = make_uint4(0, 0, 0, 0);
+        // (16 codes of K are 32 bytes here)
+        const int at = kKind == 0 ? 8 * (t4 + 4 * e) : 16 * (t4 + 4 * (e / 2)) + 8 * (e % 2);
+        if (rho < rows) x[e] = __ldg(reinterpret_cast<const uint4*>(src + at));
+      }
+      if constexpr (kKind != 0) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[e].x & 0x7FFF7FFFu, x[e].y & 0x7FFF7FFFu),
+                                   __vmaxu2(x[e].z & 0x7FFF7FFFu, x[e].w & 0x7FFF7FFFu)));
+        m = max(m >> 16, m & 0xFFFFu);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        // largest magnitude 2^(E - 127): times 2^(141 - E) or half of it, at most 2^126
+        const int e2 = min(126, (141 - static_cast<int>(m >> 7)) & ~1);
+        const float f = pow2(e2), back = pow2(-e2 / 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t* v = reinterpret_cast<uint32_t*>(&x[e]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = pack_f16x2(__uint_as_float(v[k] << 16) * f, __uint_as_float(v[k] & 0xFFFF0000u) * f);
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) undo[n][e] = __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t4 + e));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q[n][2 * e][0] = x[e].x;
+        q[n][2 * e][1] = x[e].y;
+        q[n][2 * e + 1][0] = x[e].z;
+        q[n][2 * e + 1][1] = x[e].w;
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -121,17 +173,17 @@ struct Rows {
 template <int kKind>
 struct Tile {
   uint4 x[2][kKind == 0 ? 4 : 2];
-  float scale[2];  // of their logits
+  uint32_t exp[2];  // E4M3: their exponents
   float old;       // the weight that this lane writes
   int64_t row0;    // first row of the cache; -1: not to be looked at
-  int key0, lo, hi;
+  int key0, lo, hi;  // of the tile, and keys of its unit whose weight is written
   bool fresh;      // the first of its unit
   PagedSeq q;
   int h;
 };
 
 template <int kKind, int kN>  // kN: tiles of eight rows
-__global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const WeighArgs w) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks<kN>) weigh_kernel(const WeighArgs w) {
   const PagedAttnArgs& a = w.a;
   const PagedArgs& c = a.c;
   const int lane = threadIdx.x % 32, u = lane / 4, t4 = lane % 4;
@@ -174,8 +226,36 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const Weigh
   int have = -1, entry = 0;  // table entries 32 have + lane
   const float c2 = a.scale * 1.4426950408889634f;
   constexpr int kRow = kKind == 0 ? 256 : 128, kLoads = kKind == 0 ? 4 : 2;
+  auto load = [&](Tile<kKind>& n, int64_t from) {
+    n.row0 = from;
+    n.lo = k.lo;
+    n.hi = k.hi;
+    n.q = q;
+    n.h = h;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) n.x[e][i] = ld_stream(c.k_pages + (from + u + 8 * e) * kRow + 16 * (t4 + 4 * i));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) n.exp[e] = kKind == 0 ? 0u : __ldg(c.k_exp + from + u + 8 * e);
+    // lanes t = 0 and 1 of each four write keys u and u + 8
+    const int key = n.key0 + u + 8 * t4;
+    n.old = 0.f;
+    if (t4 < 2 && key >= k.lo && key < q.len - q.n && w.accumulate) n.old = w.weights[from + u + 8 * t4];
+  };
   // The next tile of the part, its loads under way.
+  int64_t row0 = -1;
+  int more = 0;  // tiles of the same page and unit that follow
   auto fetch = [&](Tile<kKind>& n) {
+    if (more > 0 && row0 >= 0) {
+      --more;
+      ++t;
+      row0 += kTileKeys;
+      n.key0 = (k.t0 + t - 1) * kTileKeys;
+      n.fresh = false;
+      load(n, row0);
+      return;
+    }
     if (t == k.nt) {
       t = 0;
       fresh = true;
@@ -194,11 +274,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const Weigh
       }
     }
     n.key0 = (k.t0 + t) * kTileKeys;
-    n.lo = k.lo;
-    n.hi = k.hi;
+    more = min(k.nt - t, (c.page_size - (n.key0 & (c.page_size - 1))) / kTileKeys) - 1;
     n.fresh = fresh;
-    n.q = q;
-    n.h = h;
     fresh = false;
     ++t;
     const int pi = n.key0 >> c.page_shift;
@@ -209,30 +286,22 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const Weigh
                   ? __ldg(c.table + s * c.table_stride + e) : 0;
     }
     const int page = __shfl_sync(0xFFFFFFFFu, entry, pi % 32);
-    n.row0 = -1;
+    row0 = n.row0 = -1;
     if (page < 0 || page >= c.pages) {
       if (lane == 0) paged_fail(c);
       return;
     }
-    n.row0 = ((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (n.key0 & (c.page_size - 1));
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) n.x[e][i] = ld_stream(c.k_pages + (n.row0 + u + 8 * e) * kRow + 16 * (t4 + 4 * i));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) n.scale[e] = kKind == 0 ? c2 : exp_scale(__ldg(c.k_exp + n.row0 + u + 8 * e)) * (128.0f * c2);
-    // lanes t = 0 and 1 of each four write keys u and u + 8
-    const int key = n.key0 + u + 8 * t4;
-    n.old = 0.f;
-    if (t4 < 2 && key >= k.lo && key < q.len - q.n && w.accumulate) n.old = w.weights[n.row0 + u + 8 * t4];
+    row0 = ((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (n.key0 & (c.page_size - 1));
+    load(n, row0);
   };
   Rows<kKind, kN> rows;
   bool need = false;  // the unit's rows are to be loaded
-  Tile<kKind> now, next;
-  fetch(now);
+  Tile<kKind> tiles[2];
+  fetch(tiles[0]);
+  Tile<kKind>& now = tiles[0];
 #pragma unroll 1
   for (; at < end; ++at) {
-    if (at + 1 < end) fetch(next);
+    if (at + 1 < end) fetch(tiles[1]);
     need |= now.fresh;
     if (now.row0 >= 0) {
       if (need) rows.load(w, now.q, now.h, 0, lane);
@@ -255,10 +324,23 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const Weigh
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t e0 = codes_even(k0[e]), o0 = codes_odd(k0[e]), e1 = codes_even(k1[e]), o1 = codes_odd(k1[e]);
+            uint32_t l0, h0, l1, h1;
+            codes_f16(k0[e], l0, h0);
+            codes_f16(k1[e], l1, h1);
 #pragma unroll
-            for (int n = 0; n < kN; ++n) mma_bf16(d[n], e0, e1, o0, o1, rows.q[n][4 * i + e][0], rows.q[n][4 * i + e][1]);
+            for (int n = 0; n < kN; ++n) mma_f16(d[n], l0, l1, h0, h1, rows.q[n][4 * i + e][0], rows.q[n][4 * i + e][1]);
           }
+        }
+      }
+      // A key's scale as two factors of half its exponent, as Q's: the product
+      // of one of each is a number, whatever the two scales are.
+      float ks[2][2] = {};
+      if constexpr (kKind != 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int x = now.exp[e], half = x >> 1;
+          ks[e][0] = pow2(half - 64);
+          ks[e][1] = (x - 1u < 254u ? pow2(x - half - 63) : exp_scale(x)) * c2;
         }
       }
       float sum[2] = {0.f, 0.f};
@@ -267,7 +349,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const Weigh
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // key u + 8 (e / 2), row 2 t + e % 2
           const int j = now.key0 + u + 8 * (e / 2);
-          const float p = ex2_approx(fmaf(d[n][e], now.scale[e / 2], rows.neg[n][e & 1]));
+          float x = d[n][e], f = c2;
+          if constexpr (kKind != 0) {
+            x *= rows.undo[n][e & 1] * ks[e / 2][0];
+            f = rows.undo[n][e & 1] * ks[e / 2][1];
+          }
+          const float p = ex2_approx(fmaf(x, f, rows.neg[n][e & 1]));
           if (j >= rows.lo[n][e & 1] && j < rows.hi[n][e & 1]) sum[e / 2] += p;
         }
 #pragma unroll
@@ -278,24 +365,23 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) weigh_kernel(const Weigh
       const int key = now.key0 + u + 8 * t4;
       if (t4 < 2 && key >= now.lo && key < now.hi) w.weights[now.row0 + u + 8 * t4] = now.old + (t4 ? sum[1] : sum[0]);
     }
-    now = next;
+    tiles[0] = tiles[1];
   }
 }
 
 template <int kKind, int kN>
-cudaError_t launch(const WeighArgs& w, int ctas, cudaStream_t s) {
-  weigh_kernel<kKind, kN><<<ctas, 32 * kWarps, 0, s>>>(w);
+cudaError_t launch(const WeighArgs& w, int sms, int64_t ctas, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(kBlocks<kN>) * sms;
+  weigh_kernel<kKind, kN><<<static_cast<unsigned>(ctas < most ? ctas : most), 32 * kWarps, 0, s>>>(w);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s) {
-  int64_t ctas = (key_tiles + kWarps - 1) / kWarps;
-  if (ctas > kBlocks * sms) ctas = kBlocks * sms;
-  const int n = static_cast<int>(ctas);
-  if (w.a.c.kind == 0) return rows <= 8 ? launch<0, 1>(w, n, s) : launch<0, 2>(w, n, s);
-  return rows <= 8 ? launch<1, 1>(w, n, s) : launch<1, 2>(w, n, s);
+  const int64_t ctas = (key_tiles + kWarps - 1) / kWarps;
+  if (w.a.c.kind == 0) return rows <= 8 ? launch<0, 1>(w, sms, ctas, s) : launch<0, 2>(w, sms, ctas, s);
+  return rows <= 8 ? launch<1, 1>(w, sms, ctas, s) : launch<1, 2>(w, sms, ctas, s);
 }
 
 }  // namespace sa

@@ -502,8 +502,11 @@ sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups, const
  * With accumulate = 1 a key that no row sees is left as it was, with 0 it gets
  * 0.  Sequences without rows are left as they were.  A page that stands in
  * several rows of the table must lie below `first` in all of them but one;
- * else its weights are those of one of them, or their sum.  Results do not
- * depend on the order in which the device works.
+ * else its weights are unspecified.  Results do not depend on the order in
+ * which the device works.
+ * For few rows over E4M3 pages, elements of a query head's row below 2^-30 of
+ * its largest one lose bits; for more rows lse / scale is formed in FP32, and
+ * a row counts nothing where that is past 2^127.
  * Errors: as sparse_attn_paged_fwd; SA_EINVAL also for first < 0, accumulate
  * not 0 or 1, a null or misaligned lse or weights.
  */
