@@ -213,6 +213,7 @@ struct PagedAttnArgs {
 // launch_shared_merge joins.
 struct SharedAttnArgs : PagedAttnArgs {
   static constexpr bool shared = true;
+  int parts;      // of the line: 1 the prefixes, 2 the sequences with their own keys, 3 both
   int groups;
   const int32_t* group_start;  // [groups + 1]
   const int32_t* prefix_len;   // [groups]
@@ -313,11 +314,15 @@ cudaError_t launch_paged_chunk(const ChunkMaps& maps, const PagedAttnArgs& a, co
                                cudaStream_t s);
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
                               cudaStream_t s);
-// The same for rows that share prefixes: the chunks' kernel, its join, and the
-// join of the two results of each row.
+// The same for rows that share prefixes (a.parts), and the join of a row's two
+// results.  behind: the stream's previous kernel may still run (the other part).
 cudaError_t launch_shared_chunk(const ChunkMaps& maps, const SharedAttnArgs& a, const PagedScratch& ws, int ctas,
                                 cudaStream_t s);
-cudaError_t launch_shared_join(const SharedAttnArgs& a, const PagedScratch& ws, int ctas, bool many_parts, cudaStream_t s);
+cudaError_t launch_shared_few(const CUtensorMap& tk, const CUtensorMap& tv, const SharedAttnArgs& a, const PagedScratch& ws,
+                              int row_tile, int ctas, bool behind, cudaStream_t s);
+cudaError_t launch_shared_join(const SharedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
+                               bool first, cudaStream_t s);
+cudaError_t launch_shared_merge(const SharedAttnArgs& a, cudaStream_t s);
 
 // Tensor map of a row-major 2-D array of `elem`-byte elements, box
 // [box_rows, 128 bytes], 128-byte swizzle, zeros past the last row.

@@ -154,7 +154,9 @@ __device__ __forceinline__ int line_seqs(const PagedAttnArgs& a) { return a.c.se
 __device__ __forceinline__ PagedSeq line_seq(const PagedAttnArgs& a, int s, bool& bad) { return paged_seq(a.c, s, bad); }
 __device__ __forceinline__ bool line_causal(const PagedAttnArgs& a, const PagedSeq&) { return a.causal; }
 
-__device__ __forceinline__ int line_seqs(const SharedAttnArgs& a) { return a.groups + a.c.seqs; }
+__device__ __forceinline__ int line_seqs(const SharedAttnArgs& a) {
+  return (a.parts & 1 ? a.groups : 0) + (a.parts & 2 ? a.c.seqs : 0);
+}
 __device__ __forceinline__ bool line_causal(const SharedAttnArgs& a, const SharedSeq& q) { return a.causal && q.page0 >= 0; }
 
 // Shared pages of group g (0 where it has less than two sequences), and its
@@ -186,6 +188,7 @@ __device__ __forceinline__ SharedSeq line_seq(const SharedAttnArgs& a, int v, bo
   SharedSeq q;
   q.row0 = q.n = q.len = q.row = 0;
   q.page0 = -1;
+  if (!(a.parts & 1)) v += a.groups;
   if (v < a.groups) {
     int s1;
     const int pages = shared_pages(a, v, q.row, s1, bad);

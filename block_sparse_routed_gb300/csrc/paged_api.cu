@@ -165,16 +165,63 @@ bool shares(const sa_paged_params* p, int32_t groups) { return groups > 0 && p->
 
 PagedForm chunk_form() { return {kPagedChunkRows, kPagedChunkCtas, false}; }
 
-uint64_t shared_scratch_of(const sa_paged_params* p, void* ws, PagedScratch* scratch, SharedAttnArgs* a) {
-  uint64_t off = align256(scratch_of(ws, chunk_form(), scratch));
+// How a call with groups is computed: the prefixes, and the sequences with
+// their own keys, by the form for few rows where those have at most 16 (two
+// tiles of them) in each, else by that for chunks; by one launch where both
+// take the same.
+//   Own keys: 64 sequences of 64 to 2048 tokens, 5 rows: chunks NNN us
+struct SharedForms {
+  bool few_prefix, few_own;
+  int row_tile;  // of the form for few rows
+};
+SharedForms shared_forms(const sa_paged_params* p) {
+  const int64_t group = p->Hq / p->H, all = p->rows * group, own = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * group;
+  SharedForms f;
+  f.few_prefix = all <= kPagedFewRows;
+  f.few_own = own <= 2 * kPagedFewRows;
+  f.row_tile = (f.few_prefix ? all : own) <= 8 ? 8 : kPagedFewRows;
+  return f;
+}
+
+uint64_t shared_scratch_of(const sa_paged_params* p, void* ws, PagedScratch* chunk, PagedScratch* few, SharedAttnArgs* a) {
+  const SharedForms f = shared_forms(p);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint64_t off = kStatusBytes;  // (of which each part below has its own, not used)
+  if (!f.few_prefix) off += align256(scratch_of(w + off, chunk_form(), chunk));
+  if (f.few_own) off += align256(scratch_of(w + off, {f.row_tile, kPagedFewCtas, true}, few));
   const uint64_t rows = uint64_t(p->rows) * p->Hq;
   const uint64_t sums = off; off += align256(2 * rows * kHeadDim * 4);
   const uint64_t refs = off; off += align256(2 * rows * 8);
   if (a) {
-    a->sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sums);
-    a->refs = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + refs);
+    a->sums = reinterpret_cast<float*>(w + sums);
+    a->refs = reinterpret_cast<float2*>(w + refs);
   }
   return off;
+}
+
+// Maps of the form for few rows: a box holds the keys of a page that fall into a tile.
+bool few_maps(const sa_paged_params* p, const void* k_pages, const void* v_pages, CUtensorMap* tk, CUtensorMap* tv) {
+  const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
+  const uint32_t box = p->page_size < kPagedFewKeys ? p->page_size : kPagedFewKeys;
+  if (p->kind == SA_CACHE_E4M3)
+    return make_map_rows(tk, k_pages, cached, kHeadDim, 1, box) && make_map_rows(tv, v_pages, cached, kHeadDim, 1, box);
+  return make_map_groups(tk, k_pages, cached, box) && make_map_groups(tv, v_pages, cached, box);
+}
+
+// CTAs of a form for `seqs` sequences whose packed rows fill `full` tiles: no
+// more than units times the key tiles of the longest context that the table can
+// hold (0: the device could not be asked).  many_parts: a dozen parts a unit and
+// more (an estimate: the chunks' parts have the places of three key tiles at least).
+int form_ctas(const sa_paged_params* p, const PagedForm& f, int64_t seqs, int64_t full, bool* many_parts) {
+  const int tile = f.few ? kPagedFewKeys : kPagedChunkKeys;
+  const int64_t units = seqs + full;
+  const int64_t tiles = (int64_t(p->table_width) * p->page_size + tile - 1) / tile;
+  const int64_t most = units * p->H * (tiles + 1);
+  int ctas = (f.few ? 2 : 1) * multiprocessors();
+  if (ctas > f.max_ctas) ctas = f.max_ctas;
+  if (most < ctas) ctas = static_cast<int>(most);
+  *many_parts = units * p->H * 12 < ctas && tiles >= 48;
+  return ctas;
 }
 
 // Whether weights are taken by the form for few rows: as form_of.
@@ -288,35 +335,15 @@ SA_API sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, 
   const PagedForm f = form_of(p);
   PagedScratch scratch;
   scratch_of(ws, f, &scratch);
-  const uint64_t cached = uint64_t(p->pages) * p->H * p->page_size;
-  const int tile = f.few ? kPagedFewKeys : kPagedChunkKeys;
   CUtensorMap tk, tv;
   ChunkMaps boxes{};
-  bool maps = true;
-  if (f.few) {  // a box holds the keys of a page that fall into a tile
-    const uint32_t box = p->page_size < tile ? p->page_size : tile;
-    if (p->kind == SA_CACHE_E4M3)
-      maps = make_map_rows(&tk, k_pages, cached, kHeadDim, 1, box) &&
-             make_map_rows(&tv, v_pages, cached, kHeadDim, 1, box);
-    else
-      maps = make_map_groups(&tk, k_pages, cached, box) && make_map_groups(&tv, v_pages, cached, box);
-  } else {
-    maps = chunk_maps(p, k_pages, v_pages, &boxes);
-  }
-  if (!maps) return SA_ECUDA;
-  // no more CTAs than units times the key tiles of the longest context that the table can hold
-  const int64_t units = p->seqs + (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile;
-  const int64_t tiles = (int64_t(p->table_width) * p->page_size + tile - 1) / tile;
-  const int64_t most = units * p->H * (tiles + 1);
-  int ctas = (f.few ? 2 : 1) * multiprocessors();
+  if (!(f.few ? few_maps(p, k_pages, v_pages, &tk, &tv) : chunk_maps(p, k_pages, v_pages, &boxes))) return SA_ECUDA;
+  bool many_parts;
+  const int ctas = form_ctas(p, f, p->seqs, (int64_t(p->rows) * a.group + f.row_tile - 1) / f.row_tile, &many_parts);
   if (ctas <= 0) return SA_ECUDA;
-  if (ctas > f.max_ctas) ctas = f.max_ctas;
-  if (most < ctas) ctas = static_cast<int>(most);
   const cudaError_t e = f.few ? launch_paged_few(tk, tv, a, scratch, f.row_tile, ctas, stream)
                               : launch_paged_chunk(boxes, a, scratch, ctas, stream);
   if (cuda_failed(e)) return SA_ECUDA;
-  // a dozen parts a unit and more (an estimate: the chunks' parts have the places of three key tiles at least)
-  const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
   return cuda_failed(launch_paged_join(a, scratch, f.row_tile, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
 }
 
@@ -325,7 +352,7 @@ SA_API sa_status sparse_attn_prefix_ws_bytes(const sa_paged_params* p, int32_t g
   const sa_status st = check_attn(p);
   if (st != SA_OK) return st;
   if (groups < 0 || p->window != 0) return SA_EINVAL;
-  *out = shares(p, groups) ? shared_scratch_of(p, nullptr, nullptr, nullptr) : scratch_of(nullptr, form_of(p), nullptr);
+  *out = shares(p, groups) ? shared_scratch_of(p, nullptr, nullptr, nullptr, nullptr) : scratch_of(nullptr, form_of(p), nullptr);
   return SA_OK;
 }
 
@@ -356,21 +383,37 @@ SA_API sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups
   a.groups = groups;
   a.group_start = group_start;
   a.prefix_len = prefix_len;
-  PagedScratch scratch;
-  shared_scratch_of(p, ws, &scratch, &a);
+  PagedScratch chunk, few;
+  shared_scratch_of(p, ws, &chunk, &few, &a);
+  const SharedForms f = shared_forms(p);
+  const int64_t rows = int64_t(p->rows) * a.group;
+  const PagedForm few_form = {f.row_tile, kPagedFewCtas, true};
+  CUtensorMap tk, tv;
   ChunkMaps boxes{};
-  if (!chunk_maps(p, k_pages, v_pages, &boxes)) return SA_ECUDA;
-  // (as in sparse_attn_paged_fwd; every row is in a unit over its prefix, too)
-  const int64_t units = p->seqs + groups + 2 * ((int64_t(p->rows) * a.group + kPagedChunkRows - 1) / kPagedChunkRows);
-  const int64_t tiles = (int64_t(p->table_width) * p->page_size + kPagedChunkKeys - 1) / kPagedChunkKeys;
-  const int64_t most = units * p->H * (tiles + 1);
-  int ctas = multiprocessors();
-  if (ctas <= 0) return SA_ECUDA;
-  if (ctas > kPagedChunkCtas) ctas = kPagedChunkCtas;
-  if (most < ctas) ctas = static_cast<int>(most);
-  if (cuda_failed(launch_shared_chunk(boxes, a, scratch, ctas, stream))) return SA_ECUDA;
-  const bool many_parts = units * p->H * 12 < ctas && tiles >= 48;
-  return cuda_failed(launch_shared_join(a, scratch, ctas, many_parts, stream)) ? SA_ECUDA : SA_OK;
+  if (f.few_own && !few_maps(p, k_pages, v_pages, &tk, &tv)) return SA_ECUDA;
+  if (!f.few_prefix && !chunk_maps(p, k_pages, v_pages, &boxes)) return SA_ECUDA;
+  // (every row is in a unit over its prefix, and in one over its own keys)
+  bool many = false, many_few = false;
+  int ctas = 0, few_ctas = 0;
+  a.parts = f.few_own ? 1 : 3;
+  if (!f.few_prefix) {
+    const int64_t full = (rows + kPagedChunkRows - 1) / kPagedChunkRows;
+    ctas = form_ctas(p, chunk_form(), groups + (f.few_own ? 0 : p->seqs), (f.few_own ? 1 : 2) * full, &many);
+    if (ctas <= 0 || cuda_failed(launch_shared_chunk(boxes, a, chunk, ctas, stream))) return SA_ECUDA;
+  }
+  SharedAttnArgs own = a;
+  own.parts = f.few_prefix ? 3 : 2;
+  if (f.few_own) {
+    const int64_t full = (rows + f.row_tile - 1) / f.row_tile;
+    few_ctas = form_ctas(p, few_form, p->seqs + (f.few_prefix ? groups : 0), 2 * full, &many_few);
+    if (few_ctas <= 0 || cuda_failed(launch_shared_few(tk, tv, own, few, f.row_tile, few_ctas, !f.few_prefix, stream)))
+      return SA_ECUDA;
+  }
+  if (!f.few_prefix && cuda_failed(launch_shared_join(a, chunk, kPagedChunkRows, ctas, many, true, stream))) return SA_ECUDA;
+  if (f.few_own && cuda_failed(launch_shared_join(own, few, f.row_tile, few_ctas, many_few, f.few_prefix, stream)))
+    return SA_ECUDA;
+  a.parts = 3;
+  return cuda_failed(launch_shared_merge(a, stream)) ? SA_ECUDA : SA_OK;
 }
 
 SA_API sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* out) {

@@ -202,10 +202,10 @@ __device__ __forceinline__ void bar_all() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
-template <int kKind, int kN>  // kN: tiles of eight rows
+template <int kKind, int kN, class Args>  // kN: tiles of eight rows
 __global__ void __launch_bounds__(Cfg<kKind, kN>::kThreads, 2)
 paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const PagedAttnArgs a, const PagedScratch ws) {
+                 const Args a, const PagedScratch ws) {
   using C = Cfg<kKind, kN>;
   constexpr int kRows = 8 * kN, kSegs = C::kSegs;
   constexpr int kWorkers = 32 * C::kConsumers;
@@ -234,8 +234,14 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     fence_barrier_init();
   }
   __syncthreads();
-  // Token of a packed row: there are at most 16, so FP32 divides exactly (and
-  // takes the fewest registers).
+  // Where sequences share a prefix: the first page of a step's keys, whether its
+  // rows see keys only up to their own, and its first packed row (a sequence and
+  // key head may have several tiles of rows there).
+  auto first_page = [](const Segment& g) { return Args::shared ? max(0, g.valid - 2) : 0; };
+  auto causal = [&](const Segment& g) { return a.causal && (!Args::shared || g.valid > 1); };
+  auto first_row = [](const Segment& g) { return Args::shared ? g.rho0 : 0; };
+  // Token of a packed row: there are few, so FP32 divides exactly (and takes the
+  // fewest registers).
   const float inv_group = 1.0f / static_cast<float>(a.group);
   auto token_of = [&](int row) { return static_cast<int>((static_cast<float>(row) + 0.5f) * inv_group); };
   int seq = 0, steps = 0;  // producer: stages and descriptions so far
@@ -246,9 +252,9 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    LineWalk w;
     bool bad = false;
-    using Line = LineShape<kRows, kTileKeys, 1, 1, kKind == 0 ? kOverBf16 : kOverE4m3, 1, true>;
+    LineWalkOf<decltype(line_seq(a, 0, bad))> w;
+    using Line = LineShape<kRows, kTileKeys, 1, 1, kKind == 0 ? kOverBf16 : kOverE4m3, 1, !Args::shared>;
     walk_begin<Line>(a, w, blockIdx.x, gridDim.x, bad);
     JoinDesc join;
     join.pieces = 0;
@@ -266,7 +272,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       // is under way while Q's are issued)
       const int p_lo = g.lo >> c.page_shift, p_hi = (g.hi + c.page_size - 1) >> c.page_shift;
       int have = g.valid ? (g.t0 << kKeyShift >> c.page_shift) / 32 : 0;  // entry: page index 32 * have + lane
-      const int32_t* table = c.table + (g.valid ? g.s * c.table_stride : 0);
+      const int32_t* table = c.table + (g.valid ? g.s * c.table_stride + first_page(g) : 0);
       auto fetch = [&] {
         const int at = have * 32 + lane;
         return at >= p_lo && at < p_hi ? __ldg(table + at) : 0;
@@ -277,15 +283,15 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         return wrong ? -1 : e;
       };
       int entry = 0;
-      if (g.valid) {  // (a unit is one row tile here: rho0 is 0)
+      if (g.valid) {  // (without shared prefixes a unit is one row tile)
         entry = fetch();
 #pragma unroll
         for (int x = 0; x < kRows / 2; ++x) {
-          const int row = 2 * x + lane / 16, i = token_of(row);
+          const int row = 2 * x + lane / 16, rho = first_row(g) + row, i = token_of(rho);
           const uint16_t* src = a.q;
           if (row < g.rows)
             src += static_cast<int64_t>(g.row0 + i) * a.q_token +
-                   static_cast<int64_t>(g.h * a.group + row - i * a.group) * a.q_head + lane % 16 * 8;
+                   static_cast<int64_t>(g.h * a.group + rho - i * a.group) * a.q_head + lane % 16 * 8;
           cp_async16(sbase + C::kOffQ + k % kSegs * C::kQBytes + row * kQRow + lane % 16 * 16, src, row < g.rows);
         }
       }
@@ -432,9 +438,9 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = 8 * n + 2 * t4 + e;
-          const int pos = g.len - g.n + token_of(row);
+          const int pos = g.len - g.n + token_of(first_row(g) + row);
           lo[n][e] = row < g.rows ? row_lo(a, pos) : 0;
-          hi[n][e] = row < g.rows ? (a.causal ? min(g.len, pos + 1) : g.len) : 0;
+          hi[n][e] = row < g.rows ? (causal(g) ? min(g.len, pos + 1) : g.len) : 0;
         }
       float acc[kN][8][4], ref[kN][2], sum[kN][2];
 #pragma unroll
@@ -669,14 +675,16 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // (the last warp's turn comes last: meanwhile, what concerns whole rows)
         if (n == 0 && warp == C::kConsumers - 1 && lane < kRows) {
           const float2 ml = s_row[lane];
-          const int i = token_of(lane);
+          const int rho = first_row(g) + lane, i = token_of(rho);
           const bool real = lane < g.rows;
-          const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + lane - i * a.group
+          const int64_t at = g.part < 0 ? static_cast<int64_t>(g.row0 + i) * a.Hq + g.h * a.group + rho - i * a.group
                                         : (static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kRows + lane;
-          s_at[lane] = real ? at * kHeadDim : -1;
-          s_inv[lane] = g.part >= 0 ? 1.f : ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y);  // (NaN stays)
+          s_at[lane] = real ? (Args::shared && g.part < 0 ? at : at * kHeadDim) : -1;
+          s_inv[lane] = Args::shared || g.part >= 0 ? 1.f : ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y);  // (NaN stays)
           if (real && g.part >= 0) ws.ml[at] = ml;
-          if (real && g.part < 0 && a.lse)
+          if constexpr (Args::shared)
+            if (real && g.part < 0) a.refs[shared_ref(a, g.valid > 1, at)] = ml;
+          if (!Args::shared && real && g.part < 0 && a.lse)
             a.lse[at] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
         }
         // The outputs, in the accumulators' own order (a float4 of 16
@@ -728,6 +736,13 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           auto put = [&](int e, int d, float lo, float hi) {
             const int64_t to = (e ? at[1] : at[0]) + d;
             if ((e ? at[1] : at[0]) < 0) return;  // no such row
+            if constexpr (Args::shared) {
+              if (g.part < 0) {
+                *reinterpret_cast<float2*>(a.sums + shared_sums(a, g.valid > 1, d / 8, e ? at[1] : at[0]) + d % 8) =
+                    make_float2(lo, hi);
+                return;
+              }
+            }
             if (g.part < 0)
               *reinterpret_cast<uint32_t*>(a.o + to) = pack_bf16x2(lo, hi);
             else
@@ -761,26 +776,40 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   }
   if (threadIdx.x == 0) ws.cta_status[blockIdx.x] = *s_abort ? 5 /* SA_ETIMEOUT */ : (*s_bad ? kPagedInvalid : 0);
   griddep_launch_dependents();
+  if constexpr (Args::shared) griddep_wait();  // (the prefixes' kernel has ended when this one has)
 }
 
-template <int kKind, int kN>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, const PagedScratch& ws,
-                   int ctas, cudaStream_t s) {
+template <int kKind, int kN, class Args>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a, const PagedScratch& ws, int ctas,
+                   bool behind, cudaStream_t s) {
   using C = Cfg<kKind, kN>;
+  auto* kern = paged_few_kernel<kKind, kN, Args>;
   static SmemOnce once;
-  const cudaError_t e = once.set(reinterpret_cast<const void*>(paged_few_kernel<kKind, kN>), C::kSmem);
+  const cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
-  paged_few_kernel<kKind, kN><<<ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a, ws);
+  if (behind) return launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, s, tk, tv, a, ws);
+  kern<<<ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a, ws);
   return cudaGetLastError();
+}
+
+template <class Args>
+cudaError_t launch_form(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a, const PagedScratch& ws, int row_tile,
+                        int ctas, bool behind, cudaStream_t s) {
+  if (a.c.kind == 0)
+    return row_tile == 8 ? launch<0, 1>(tk, tv, a, ws, ctas, behind, s) : launch<0, 2>(tk, tv, a, ws, ctas, behind, s);
+  return row_tile == 8 ? launch<1, 1>(tk, tv, a, ws, ctas, behind, s) : launch<1, 2>(tk, tv, a, ws, ctas, behind, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                              const PagedScratch& ws, int row_tile, int ctas, cudaStream_t s) {
-  if (a.c.kind == 0)
-    return row_tile == 8 ? launch<0, 1>(tk, tv, a, ws, ctas, s) : launch<0, 2>(tk, tv, a, ws, ctas, s);
-  return row_tile == 8 ? launch<1, 1>(tk, tv, a, ws, ctas, s) : launch<1, 2>(tk, tv, a, ws, ctas, s);
+  return launch_form(tk, tv, a, ws, row_tile, ctas, false, s);
+}
+
+cudaError_t launch_shared_few(const CUtensorMap& tk, const CUtensorMap& tv, const SharedAttnArgs& a, const PagedScratch& ws,
+                              int row_tile, int ctas, bool behind, cudaStream_t s) {
+  return launch_form(tk, tv, a, ws, row_tile, ctas, behind, s);
 }
 
 }  // namespace sa

@@ -17,12 +17,14 @@ namespace {
 
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ void join_status(const PagedAttnArgs& a, const PagedScratch& ws) {
+// (of a call's second join: with what the first one found)
+template <class Args>
+__device__ __forceinline__ void join_status(const Args& a, const PagedScratch& ws, bool first = true) {
   if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= 32) return;
   int st = 0;
   for (int i = threadIdx.x; i < gridDim.x; i += 32) st = max(st, ws.cta_status[i]);
   st = __reduce_max_sync(0xFFFFFFFFu, st);
-  if (threadIdx.x == 0) *a.c.status = st;
+  if (threadIdx.x == 0) *a.c.status = first ? st : max(st, *a.c.status);
 }
 
 // Row of the i-th part of the unit that begins in CTA blockIdx.x.
@@ -40,12 +42,12 @@ __device__ __forceinline__ float join_lse(float m, float l) {
 
 // The form for few rows.  A block takes a row; its warps share the parts (one
 // long context alone on the GPU has 150 of them), four columns a lane.
-__global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const PagedAttnArgs a, const PagedScratch ws,
-                                                               int row_tile) {
+template <class Args>
+__global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const Args a, const PagedScratch ws, int row_tile, bool first) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row = blockIdx.y;
   griddep_wait();
   const JoinDesc d = ws.join[blockIdx.x];
-  join_status(a, ws);
+  join_status(a, ws, first);
   if (d.pieces == 0 || row >= d.rows) return;
   // The references of 32 parts, one a lane, give the maximum so far; then the
   // parts themselves, relative to it.
@@ -99,6 +101,11 @@ __global__ void __launch_bounds__(32 * kWarps) join_few_kernel(const PagedAttnAr
   }
   const int rho = d.rho0 + row, i = div_group(a, rho);
   const int64_t at = static_cast<int64_t>(d.row0 + i) * a.Hq + d.h * a.group + rho - i * a.group;
+  if constexpr (Args::shared) {
+    *reinterpret_cast<float4*>(a.sums + shared_sums(a, d.own, lane / 2, at) + lane % 2 * 4) = o;
+    if (lane == 0) a.refs[shared_ref(a, d.own, at)] = make_float2(m, l);
+    return;
+  }
   const float inv = join_inverse(l);
   reinterpret_cast<uint2*>(a.o + at * kHeadDim)[lane] =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -256,19 +263,25 @@ __global__ void __launch_bounds__(32 * kWarps) shared_merge_kernel(const SharedA
 
 }  // namespace
 
-cudaError_t launch_shared_join(const SharedAttnArgs& a, const PagedScratch& ws, int ctas, bool many_parts, cudaStream_t s) {
+cudaError_t launch_shared_join(const SharedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
+                               bool first, cudaStream_t s) {
+  if (row_tile <= kPagedFewRows)
+    return launch_dependent(join_few_kernel<SharedAttnArgs>, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile,
+                            first);
   const dim3 grid(ctas, kPagedChunkRows / 8);
-  const cudaError_t e =
-      many_parts ? launch_dependent(join_chunk_kernel<4, SharedAttnArgs>, grid, dim3(32 * kWarps * 4), 0, s, a, ws)
-                 : launch_dependent(join_chunk_kernel<1, SharedAttnArgs>, grid, dim3(32 * kWarps), 0, s, a, ws);
-  if (e != cudaSuccess) return e;
+  if (many_parts)
+    return launch_dependent(join_chunk_kernel<4, SharedAttnArgs>, grid, dim3(32 * kWarps * 4), 0, s, a, ws);
+  return launch_dependent(join_chunk_kernel<1, SharedAttnArgs>, grid, dim3(32 * kWarps), 0, s, a, ws);
+}
+
+cudaError_t launch_shared_merge(const SharedAttnArgs& a, cudaStream_t s) {
   return launch_dependent(shared_merge_kernel, dim3(a.c.rows), dim3(32 * kWarps), 0, s, a);
 }
 
 cudaError_t launch_paged_join(const PagedAttnArgs& a, const PagedScratch& ws, int row_tile, int ctas, bool many_parts,
                               cudaStream_t s) {
   if (row_tile <= kPagedFewRows)
-    return launch_dependent(join_few_kernel, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile);
+    return launch_dependent(join_few_kernel<PagedAttnArgs>, dim3(ctas, row_tile), dim3(32 * kWarps), 0, s, a, ws, row_tile, true);
   const dim3 grid(ctas, kPagedChunkRows / 8);
   if (many_parts) return launch_dependent(join_chunk_kernel<4, PagedAttnArgs>, grid, dim3(32 * kWarps * 4), 0, s, a, ws);
   return launch_dependent(join_chunk_kernel<1, PagedAttnArgs>, grid, dim3(32 * kWarps), 0, s, a, ws);
