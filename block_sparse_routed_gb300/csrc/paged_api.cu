@@ -165,11 +165,13 @@ bool shares(const sa_paged_params* p, int32_t groups) { return groups > 0 && p->
 
 PagedForm chunk_form() { return {kPagedChunkRows, kPagedChunkCtas, false}; }
 
-// How a call with groups is computed: the prefixes, and the sequences with
-// their own keys, by the form for few rows where those have at most 16 (two
-// tiles of them) in each, else by that for chunks; by one launch where both
-// take the same.
-//   Own keys: 64 sequences of 64 to 2048 tokens, 5 rows: chunks NNN us
+// How a call with groups is computed: all of it by the form for few rows where
+// all rows of a key head fit into its tile; else by the form for chunks, in one
+// launch, but for own keys of few rows in E4M3, which that form widens for 256
+// rows: two tiles of the form for few rows are faster there.  64 sequences
+// behind 4096 tokens, with 1000 to 1500 own ones, 40 / 8 heads, own keys by
+// chunks and by few rows: BF16, 5 rows 86 and 99 us, 20 rows 92 and 122; E4M3, 20
+// rows 121 and 104; 32 sequences of 4096 to 8704, E4M3, 5 rows 180 and 114.
 struct SharedForms {
   bool few_prefix, few_own;
   int row_tile;  // of the form for few rows
@@ -178,7 +180,7 @@ SharedForms shared_forms(const sa_paged_params* p) {
   const int64_t group = p->Hq / p->H, all = p->rows * group, own = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * group;
   SharedForms f;
   f.few_prefix = all <= kPagedFewRows;
-  f.few_own = own <= 2 * kPagedFewRows;
+  f.few_own = f.few_prefix || (p->kind == SA_CACHE_E4M3 && own <= 2 * kPagedFewRows);
   f.row_tile = (f.few_prefix ? all : own) <= 8 ? 8 : kPagedFewRows;
   return f;
 }
