@@ -422,6 +422,8 @@ SA_API sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* 
   if (out == nullptr) return SA_EINVAL;
   const sa_status st = check_attn(p);
   if (st != SA_OK) return st;
+  // (lse / scale, which the form for chunks subtracts, and its parts are numbers then)
+  if (p->scale < 0x1p-100f || p->scale > 0x1p100f) return SA_EUNSUPPORTED;
   *out = weigh_scratch_of(p, nullptr, nullptr);
   return SA_OK;
 }
@@ -483,7 +485,7 @@ SA_API sa_status sparse_attn_cache_evict(const sa_paged_params* p, const sa_evic
   if (e->keep < 1 || e->first < 0 || e->last < 0 || int64_t(e->first) + e->last > e->keep) return SA_EINVAL;
   if (to_table && (e->to_width < 0 || e->to_stride < 0)) return SA_EINVAL;
   // (the blocks of a launch, and positions that a block's step passes)
-  if (int64_t(p->seqs) * p->H >= int64_t(1) << 27 || int64_t(p->table_width) * p->page_size > int64_t(1) << 30)
+  if (e->keep > 1 << 30 || int64_t(p->seqs) * p->H >= int64_t(1) << 27 || int64_t(p->table_width) * p->page_size > int64_t(1) << 30)
     return SA_EUNSUPPORTED;
   if (!weights || (p->seqs > 0 && (!kept || !new_len))) return SA_EINVAL;
   if (!aligned(weights, 16) || !aligned(to_table, 4) || !aligned(kept, 4) || !aligned(new_len, 4)) return SA_EINVAL;

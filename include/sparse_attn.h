@@ -505,10 +505,10 @@ sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups, const
  * else its weights are unspecified.  Results do not depend on the order in
  * which the device works.
  * For few rows over E4M3 pages, elements of a query head's row below 2^-30 of
- * its largest one lose bits; for more rows lse / scale is formed in FP32, and
- * a row counts nothing where that is past 2^127.
+ * its largest one lose bits.
  * Errors: as sparse_attn_paged_fwd; SA_EINVAL also for first < 0, accumulate
- * not 0 or 1, a null or misaligned lse or weights.
+ * not 0 or 1, a null or misaligned lse or weights; SA_EUNSUPPORTED also for a
+ * scale outside [2^-100, 2^100].
  */
 sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* out);
 sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32_t accumulate, const void* q,
@@ -544,8 +544,8 @@ sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32
  * sequence moves, kept is -1 throughout and new_len is kv_len.
  * Errors before launch: as sparse_attn_cache_write; SA_EINVAL also for keep <
  * 1, first or last < 0, first + last > keep, a null or misaligned weights,
- * kept or new_len, new_len == kv_len; SA_EUNSUPPORTED also for seqs * H >=
- * 2^27, table_width * page_size > 2^30.
+ * kept or new_len, new_len == kv_len; SA_EUNSUPPORTED also for keep > 2^30,
+ * seqs * H >= 2^27, table_width * page_size > 2^30.
  */
 typedef struct sa_evict_params {
   int32_t keep;       /* tokens that a sequence may have after the call, >= 1   */

@@ -483,3 +483,108 @@ def test_a_bounded_cache_in_use(bsr, kind):
                     assert ws[gone].max() <= ws[chosen].min() * (1 + 1e-4)  # 150 steps of 2^-13 at most
                     held[s][h] = [held[s][h][j] for j in mine]
     assert int(kl[0]) < 150
+
+
+# ---- waits, graphs, streams
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_wait_that_gives_up_is_reported(bsr, kind):
+    from block_sparse_routed_gb300 import _native
+
+    b = Batch([2900, 70], [300, 1], 2, 64, kind, seed=9)
+    q, lse, w = run_weigh(bsr, b, 8, check=False)
+    ws = bsr.weigh_workspace(q, b.k_pages, b.table, 300)
+    call = lambda w: bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len, max_new=300, k_exp=b.k_exp, ws=ws)  # noqa: E731
+    prev = _native.sparse_attn_set_single_probe_waits(True)
+    try:
+        statuses = []
+        for _ in range(5):  # a single probe almost surely comes too early
+            call(fresh_weights(b))
+            statuses.append(bsr.sparse_attn_last_device_status(ws))
+            if statuses[-1] == bsr.SA_ETIMEOUT:
+                break
+    finally:
+        _native.sparse_attn_set_single_probe_waits(bool(prev))
+    assert bsr.SA_ETIMEOUT in statuses
+    w2 = fresh_weights(b)
+    call(w2)
+    assert bsr.sparse_attn_last_device_status(ws) == 0 and torch.equal(w, w2)
+
+
+@pytest.mark.parametrize("news,keep", [(1, 100), (40, 5000)])
+def test_captured(bsr, news, keep):
+    """Attention, weights and eviction in one graph, replayed on new lengths."""
+    b = Batch([9000, 300], [news, 1], 2, 64, "e4m3", seed=9)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn((b.rows, 8, 128), generator=g).bfloat16().cuda()
+    start = [t.clone() for t in (b.k_pages.view(torch.uint8), b.v_pages.view(torch.uint8), b.k_exp, b.v_exp)] + [fresh_weights(b)]
+    state = [t.clone() for t in start]
+    o, lse = torch.zeros_like(q), torch.zeros((b.rows, 8), device="cuda")
+    kept = torch.zeros((2, 2, keep), dtype=torch.int32, device="cuda")
+    new_len = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws, ws2 = bsr.paged_workspace(q, b.k_pages, b.table, news), bsr.weigh_workspace(q, b.k_pages, b.table, news)
+
+    def step():
+        k, v = state[0].view(torch.float8_e4m3fn), state[1].view(torch.float8_e4m3fn)
+        bsr.paged_attn(q, k, v, b.table, b.row_start, b.kv_len, max_new=news, k_exp=state[2], v_exp=state[3], o=o, lse=lse, ws=ws)
+        bsr.cache_weigh(q, lse, state[4], k, b.table, b.row_start, b.kv_len, max_new=news, k_exp=state[2], ws=ws2)
+        bsr.cache_evict(k, v, state[4], b.table, b.kv_len, keep, first=2, last=50, k_exp=state[2], v_exp=state[3], kept=kept, new_len=new_len)
+
+    def reset():
+        for t, x in zip(state, start):
+            t.copy_(x)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens in ([9000, 300], [4999, 123]):
+        b.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        reset()
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (*state, o, lse, kept, new_len)]
+        for _ in range(2):
+            reset()
+            kept.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(want, (*state, o, lse, kept, new_len)))
+        assert new_len.tolist() == [min(n, keep) for n in lens]
+
+
+def test_two_streams_at_once(bsr):
+    """Calls on two streams, each with workspaces of its own, give what they give alone."""
+    cases = []
+    for seed, news in ((1, 300), (2, 200)):
+        b = Batch([4000, 200], [news, 1], 4, 64, "bf16", seed=seed)
+        q = torch.randn((b.rows, 8, 128), device="cuda").bfloat16()
+        _, lse = bsr.paged_attn(q, *b.where)
+        w = fresh_weights(b)
+        bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len)
+        cases.append((b, q, lse, w))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        out = []
+        for s, (b, q, lse, _) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                w = fresh_weights(b)
+                bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len)
+                k, v = b.k_pages.clone(), b.v_pages.clone()
+                kept, _ = bsr.cache_evict(k, v, w.clone(), b.table, b.kv_len, 1000, first=4, last=4)
+                out.append((w, kept))
+        torch.cuda.synchronize()
+        for (w, kept), (b, _, _, want) in zip(out, cases):
+            assert torch.equal(w, want)
+            j = np.arange(4000)
+            for h in range(4):
+                assert kept[0, h].tolist() == OP.survivors(want.cpu().numpy()[b.table_np[0, j // 64], h, j % 64], 1000, 4, 4)
+
+
+@pytest.mark.parametrize("H,Hq,news", [(1, 1, 1200), (1, 100, 30), (2, 192, 5), (1, 97, 40), (7, 49, 90)])
+def test_weights_of_odd_groups(bsr, H, Hq, news):
+    """Groups that leave rows of a step unused, and groups wider than a step."""
+    b = Batch([1300, 50], [news, 3], H, 32, "bf16", seed=21)
+    run_weigh(bsr, b, Hq)
