@@ -244,6 +244,7 @@ struct WeighJoin {
 };
 constexpr int kWeighKeys = 256;  // keys of a unit of the form for chunks
 constexpr int kWeighCtas = 160;  // most CTAs of it
+constexpr int kWeighFewRows = 128;  // most packed rows that paged_weigh.cu takes
 struct WeighScratch {
   int32_t* cta_status;  // [ctas]
   WeighJoin* join;      // [ctas]

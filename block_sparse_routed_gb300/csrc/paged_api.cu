@@ -226,9 +226,9 @@ int form_ctas(const sa_paged_params* p, const PagedForm& f, int64_t seqs, int64_
   return ctas;
 }
 
-// Whether weights are taken by the form for few rows: as form_of.
+// Whether weights are taken by the form for few rows (both measured in paged_weigh.cu).
 bool weighs_few(const sa_paged_params* p) {
-  return int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H) <= kPagedFewRows;
+  return int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H) <= kWeighFewRows;
 }
 
 uint64_t weigh_scratch_of(const sa_paged_params* p, void* ws, WeighScratch* out) {

@@ -5,7 +5,8 @@
 //
 // A key's weight depends on its own K alone, so whoever has a key adds up all
 // rows for it: nothing is joined, and no atomics change an order.  This is the
-// form for few rows (at most 16 packed rows a sequence and key head).
+// form for few rows (at most 128 packed rows a sequence and key head), in two
+// kernels: rows in registers up to 16, in shared memory above.
 //
 // Bound by memory: K once (256 bytes a key and head, 129 in the E4M3 kind), the
 // weight read and written.  The line of all tiles of 16 keys is cut into equal
@@ -369,6 +370,302 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<kN>) weigh_kernel(const W
   }
 }
 
+// ---- 17 to 128 packed rows a sequence and key head
+//
+// The same products, with more rows than a warp's registers hold: a block takes a
+// part of the line, the rows of its unit lie in shared memory (in the order of a
+// lane's reads), and each warp multiplies every fourth tile with all of them.  A tile
+// costs what its rows cost, and rows differ from sequence to sequence, so the line
+// is measured in that.
+// Bound by mma.sync where there are 64 rows (about three quarters of its rate), by
+// memory where there are few.  Eight sequences, 24 heads, up to so many rows each,
+// here and by the form of paged_weigh_chunk.cu, which multiplies six times as fast
+// but has to fill and drain 256 keys for however many rows come:
+//   rows   keys            E4M3            BF16
+//     17   1152          16 /  30 us     18 /  34 us
+//     17   17408         98 / 269       143 / 338
+//     64   1152          25 /  30        25 /  35
+//     64   17408        135 / 278       162 / 345
+//    128   17408        173 / 282       181 / 361
+// (a uniform 128 rows come near the other form; it takes what is above).  Two tiles
+// a warp (54 against 46 us for eight sequences of 1152 to 8704 keys, 64 heads' rows)
+// and two accumulators a product (no change) did not help: loads of rows did, all
+// under way at once and behind the first keys' (46 -> 43 us).
+constexpr int kMidRow = 320;   // bytes of a row: other banks for the next one
+constexpr int kMidBlocks = 4;  // blocks an SM
+
+template <int kRows>  // at most so many rows
+struct MidRows {
+  alignas(16) uint8_t q[kRows * kMidRow];
+  float4 use[kRows / 2];  // of a pair of rows: -L (-inf: counts nothing); E4M3: the roots of what undoes their scaling
+  int pos[kRows];         // positions
+};
+
+// The rows of unit (q, h), by the whole block: half a warp has a row at a time, and
+// eight of them are on their way before the first is looked at.
+template <int kKind, int kRows>
+__device__ __forceinline__ void mid_rows(const WeighArgs& w, const PagedSeq& q, int h, MidRows<kRows>& m) {
+  const PagedAttnArgs& a = w.a;
+  constexpr int kTurns = 8;
+  static_assert(kRows % (kTurns * 8) == 0 && 2 * kWarps == 8, "a turn is eight rows");
+  const int rows = q.n * a.group, lane = threadIdx.x % 32, sub = lane % 16;
+#pragma unroll 1
+  for (int r0 = 0; r0 < kRows; r0 += kTurns * 8) {
+    if (r0 >= rows) break;
+    uint4 x[kTurns];
+    float l[kTurns];
+#pragma unroll
+    for (int n = 0; n < kTurns; ++n) {
+      // (past the last: the last again, counting nothing)
+      const int rho = r0 + 8 * n + threadIdx.x / 16, real = min(rho, rows - 1), i = div_group(a, real), e = real - i * a.group;
+      x[n] = make_uint4(0, 0, 0, 0);
+      l[n] = INFINITY;
+      if (r0 + 8 * n < rows)
+        x[n] = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(q.row0 + i) * a.q_token +
+                                                    static_cast<int64_t>(h * a.group + e) * a.q_head + sub * 8));
+      if (rho < rows) l[n] = __ldg(w.lse + static_cast<int64_t>(q.row0 + i) * a.Hq + h * a.group + e);
+    }
+#pragma unroll
+    for (int n = 0; n < kTurns; ++n) {
+      const int rho = r0 + 8 * n + threadIdx.x / 16;
+      if (r0 + 8 * n >= rows) break;
+      int at = sub;
+      float* use = reinterpret_cast<float*>(m.use + rho / 2) + rho % 2;
+      if constexpr (kKind != 0) {  // (see Rows)
+        uint32_t z = __vmaxu2(__vmaxu2(x[n].x & 0x7FFF7FFFu, x[n].y & 0x7FFF7FFFu),
+                              __vmaxu2(x[n].z & 0x7FFF7FFFu, x[n].w & 0x7FFF7FFFu));
+        z = max(z >> 16, z & 0xFFFFu);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) z = max(z, __shfl_xor_sync(0xFFFFFFFFu, z, d));
+        const int e2 = min(126, (141 - static_cast<int>(z >> 7)) & ~1);
+        const float f = pow2(e2);
+        uint32_t* v = reinterpret_cast<uint32_t*>(&x[n]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = pack_f16x2(__uint_as_float(v[k] << 16) * f, __uint_as_float(v[k] & 0xFFFF0000u) * f);
+        if (sub == 0) use[2] = pow2(-e2 / 2);
+        // 16 codes of K are two of these: the first ones of the lanes t = 0 .. 3, then the second
+        at = (sub >> 3) * 8 + (sub & 1) * 4 + (sub >> 1 & 3);
+      }
+      *reinterpret_cast<uint4*>(m.q + rho * kMidRow + at * 16) = x[n];
+      if (sub == 0) {
+        use[0] = l[n] == -INFINITY ? -INFINITY : -l[n] * 1.4426950408889634f;
+        m.pos[rho] = q.len - q.n + div_group(a, min(rho, rows - 1));
+      }
+    }
+  }
+}
+
+using f2 = unsigned long long;  // two floats in a register pair
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// What a tile of a sequence costs, in units of eight rows' products (kTileCost: what
+// it costs beside them); the line is measured in it.
+constexpr int kTileCost = 4;
+__device__ __forceinline__ int tile_cost(const WeighArgs& w, const PagedSeq& q) { return kTileCost + (q.n * w.a.group + 7) / 8; }
+__device__ __forceinline__ int64_t lane_cost(const WeighArgs& w, int s, PagedSeq& q) {
+  const int nt = lane_tiles16(w, s, q);
+  return static_cast<int64_t>(nt) * tile_cost(w, q) * w.a.c.H;
+}
+
+template <int kKind, int kRows>
+__global__ void __launch_bounds__(32 * kWarps, kMidBlocks) weigh_mid_kernel(const WeighArgs w) {
+  const PagedAttnArgs& a = w.a;
+  const PagedArgs& c = a.c;
+  __shared__ MidRows<kRows> m;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, u = lane / 4, t4 = lane % 4;
+  if (blockIdx.x == 0) paged_check_all(c);
+  // The block's part of the line (every warp finds it for itself): the tiles that
+  // begin in it.
+  PagedSeq q;
+  const int64_t first = lane_cost(w, lane, q);  // of the first 32 sequences
+  int64_t total = first;
+#pragma unroll 1
+  for (int base = 32; base < c.seqs; base += 32) total += lane_cost(w, base + lane, q);
+  total = warp_sum(total);
+  int64_t left = muldiv(blockIdx.x, total, gridDim.x);
+  int64_t more = muldiv(static_cast<int64_t>(blockIdx.x) + 1, total, gridDim.x) - left;
+  if (more <= 0) return;
+  int s = 0;
+#pragma unroll 1
+  for (int base = 0;; base += 32) {
+    const int64_t mine = base ? lane_cost(w, base + lane, q) : first;
+    const int64_t upto = warp_scan(mine, lane);
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, upto > left);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      s = base + src;
+      left = __shfl_sync(0xFFFFFFFFu, left - (upto - mine), src);
+      break;
+    }
+    left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  bool bad;
+  q = paged_seq(c, s, bad);
+  KeySpan k = key_span(w, q);
+  int cost = tile_cost(w, q);
+  int64_t unit = static_cast<int64_t>(k.nt) * cost;
+  int h = static_cast<int>(muldiv(left, 1, unit));
+  left -= h * unit;
+  const float c2 = a.scale * 1.4426950408889634f;
+  constexpr int kRow = kKind == 0 ? 256 : 128, kLoads = kKind == 0 ? 4 : 2;
+  for (;;) {
+    const int t0 = static_cast<int>(muldiv(left + cost - 1, 1, cost));
+    const int t1 = left + more >= unit ? k.nt : static_cast<int>(muldiv(left + more + cost - 1, 1, cost));
+    if (t0 < t1) {
+      const int tiles = (q.n * a.group + 7) / 8;
+      // keys that all rows see
+      const int all_lo = row_lo(a, q.len - 1), all_hi = a.causal ? q.len - q.n + 1 : q.len;
+      const int32_t* table = c.table + s * c.table_stride;
+      int have = -1, entry = 0;  // table entries 32 have + lane
+      struct Keys {
+        uint4 x[2][kLoads];
+        uint32_t exp[2];
+        float old;
+        int64_t row0;  // -1: not to be looked at
+      } now, next;
+      auto fetch = [&](int t) {
+        const int key0 = (k.t0 + t) * kTileKeys, pi = key0 >> c.page_shift;
+        if (pi / 32 != have) {
+          have = pi / 32;
+          const int e = have * 32 + lane;
+          entry = (static_cast<int64_t>(e) << c.page_shift) < k.hi && (static_cast<int64_t>(e + 1) << c.page_shift) > k.lo ? __ldg(table + e) : 0;
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, entry, pi % 32);
+        next.row0 = -1;
+        if (page < 0 || page >= c.pages) {
+          if (lane == 0) paged_fail(c);
+          return;
+        }
+        next.row0 = ((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (key0 & (c.page_size - 1));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) next.x[e][i] = ld_stream(c.k_pages + (next.row0 + u + 8 * e) * kRow + 16 * (t4 + 4 * i));
+          next.exp[e] = kKind == 0 ? 0u : __ldg(c.k_exp + next.row0 + u + 8 * e);
+        }
+        const int key = key0 + u + 8 * t4;
+        next.old = 0.f;
+        if (t4 < 2 && key >= k.lo && key < q.len - q.n && w.accumulate) next.old = w.weights[next.row0 + u + 8 * t4];
+      };
+      if (t0 + warp < t1) fetch(t0 + warp);
+      __syncthreads();
+      mid_rows<kKind, kRows>(w, q, h, m);
+      __syncthreads();
+#pragma unroll 1
+      for (int t = t0 + warp; t < t1; t += kWarps) {
+        now = next;
+        if (t + kWarps < t1) fetch(t + kWarps);
+        if (now.row0 < 0) continue;
+        const int key0 = (k.t0 + t) * kTileKeys;
+        const bool edge = key0 < all_lo || key0 + kTileKeys > all_hi;
+        uint32_t f[2][16];  // E4M3: keys u and u + 8 in FP16
+        f2 ks[2][2];
+        if constexpr (kKind != 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+              const uint32_t v[4] = {now.x[e][i].x, now.x[e][i].y, now.x[e][i].z, now.x[e][i].w};
+#pragma unroll
+              for (int g = 0; g < 4; ++g) codes_f16(v[g], f[e][8 * i + 2 * g], f[e][8 * i + 2 * g + 1]);
+            }
+            const int x = now.exp[e], half = x >> 1;
+            const float near = pow2(half - 64), far = (x - 1u < 254u ? pow2(x - half - 63) : exp_scale(x)) * c2;
+            ks[e][0] = pair(near, near);
+            ks[e][1] = pair(far, far);
+          }
+        }
+        f2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll 2
+        for (int n = 0; n < tiles; ++n) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint4* rq = reinterpret_cast<const uint4*>(m.q + (8 * n + u) * kMidRow) + t4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 b = rq[4 * i];
+            if constexpr (kKind == 0) {
+              mma_bf16(d, now.x[0][i].x, now.x[1][i].x, now.x[0][i].y, now.x[1][i].y, b.x, b.y);
+              mma_bf16(d, now.x[0][i].z, now.x[1][i].z, now.x[0][i].w, now.x[1][i].w, b.z, b.w);
+            } else {
+              mma_f16(d, f[0][4 * i], f[1][4 * i], f[0][4 * i + 1], f[1][4 * i + 1], b.x, b.y);
+              mma_f16(d, f[0][4 * i + 2], f[1][4 * i + 2], f[0][4 * i + 3], f[1][4 * i + 3], b.z, b.w);
+            }
+          }
+          const float4 use = m.use[4 * n + t4];
+          const f2 neg = pair(use.x, use.y), undo = pair(use.z, use.w);
+          float p[2][2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // key u + 8 e, rows 2 t and 2 t + 1
+            f2 x = pair(d[2 * e], d[2 * e + 1]), g = pair(c2, c2);
+            if constexpr (kKind != 0) {
+              x = mul2(x, mul2(undo, ks[e][0]));
+              g = mul2(undo, ks[e][1]);
+            }
+            unpair(fma2(x, g, neg), p[e][0], p[e][1]);
+            p[e][0] = ex2_approx(p[e][0]);
+            p[e][1] = ex2_approx(p[e][1]);
+          }
+          if (edge) {
+            const int2 pos = *reinterpret_cast<const int2*>(&m.pos[8 * n + 2 * t4]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + u + 8 * (e / 2), at = e & 1 ? pos.y : pos.x;
+              if (key < row_lo(a, at) || (a.causal && key > at)) p[e / 2][e % 2] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sum[e] = add2(sum[e], pair(p[e][0], p[e][1]));
+        }
+        float all[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float lo, hi;
+          unpair(sum[e], lo, hi);
+          all[e] = lo + hi;
+          all[e] += __shfl_xor_sync(0xFFFFFFFFu, all[e], 1);
+          all[e] += __shfl_xor_sync(0xFFFFFFFFu, all[e], 2);
+        }
+        const int key = key0 + u + 8 * t4;
+        if (t4 < 2 && key >= k.lo && key < k.hi) w.weights[now.row0 + u + 8 * t4] = now.old + (t4 ? all[1] : all[0]);
+      }
+    }
+    more -= unit - left;  // on to the next unit
+    left = 0;
+    if (more <= 0) return;
+    if (++h == c.H) {
+      h = 0;
+      do {
+        if (++s >= c.seqs) return;
+        q = paged_seq(c, s, bad);
+        k = key_span(w, q);
+      } while (k.nt == 0);
+      cost = tile_cost(w, q);
+      unit = static_cast<int64_t>(k.nt) * cost;
+    }
+  }
+}
+
 template <int kKind, int kN>
 cudaError_t launch(const WeighArgs& w, int sms, int64_t ctas, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(kBlocks<kN>) * sms;
@@ -376,10 +673,19 @@ cudaError_t launch(const WeighArgs& w, int sms, int64_t ctas, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int kKind, int kRows>
+cudaError_t launch_mid(const WeighArgs& w, int sms, int64_t ctas, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(kMidBlocks) * sms;
+  weigh_mid_kernel<kKind, kRows><<<static_cast<unsigned>(ctas < most ? ctas : most), 32 * kWarps, 0, s>>>(w);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s) {
   const int64_t ctas = (key_tiles + kWarps - 1) / kWarps;
+  if (rows > 64) return w.a.c.kind == 0 ? launch_mid<0, 128>(w, sms, ctas, s) : launch_mid<1, 128>(w, sms, ctas, s);
+  if (rows > 16) return w.a.c.kind == 0 ? launch_mid<0, 64>(w, sms, ctas, s) : launch_mid<1, 64>(w, sms, ctas, s);
   if (w.a.c.kind == 0) return rows <= 8 ? launch<0, 1>(w, sms, ctas, s) : launch<0, 2>(w, sms, ctas, s);
   return rows <= 8 ? launch<1, 1>(w, sms, ctas, s) : launch<1, 2>(w, sms, ctas, s);
 }
