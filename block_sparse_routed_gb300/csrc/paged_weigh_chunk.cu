@@ -1,5 +1,5 @@
 // The attention weight that cached keys receive from chunks of rows (sm_103a):
-// more than 16 packed rows a sequence and key head, on tcgen05 tensor cores.
+// more than 128 packed rows a sequence and key head, on tcgen05 tensor cores.
 //
 //   w_j (+)= sum_r 2^(x_rj - L_r),   x_rj = scale log2(e) (q_r . k_j),  L_r = log2(e) lse_r
 //
@@ -41,7 +41,6 @@
 // Measured (graphs of four calls; tensor rate of the visible pairs):
 //   2048 new of 33792, 40 / 8 heads, causal, BF16      570 us  1206 TFLOP/s
 //   8704 of 8704, 24 / 24 heads, causal, BF16          212 us  1096
-//   64 each of 8 sequences, 24 / 24 heads, E4M3         71 us  (1.3 TB/s: units of one step)
 //
 // Tensor memory: K of tile t in columns [64 t, + 64); scores of tile t, every
 // other step, in [128 + 96 (2 t + b), + 96).
@@ -343,6 +342,37 @@ __device__ __forceinline__ float bf16_of(float x) {  // rounded to BF16
 }
 __device__ __forceinline__ void lds_i4(int (&v)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
+// A key's sum over the rows of a unit's steps, once more and one by one, where the
+// other one is not a number: an infinity in the key times the zeros of rows that
+// only fill a step is none, though each row's own product may be.
+__device__ __noinline__ float weigh_again(const WeighArgs& w, const Work& g, int key, const uint8_t* k) {
+  const PagedAttnArgs& a = w.a;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int j = g.j0; j < g.j0 + g.steps; ++j) {
+    const int tile = j / w.slices, e0 = (j - tile * w.slices) * w.heads, i0 = g.i0 + tile * w.tokens;
+#pragma unroll 1
+    for (int i = i0; i < min(i0 + w.tokens, g.i1); ++i) {
+      const int pos = g.len - g.n + i;
+      if ((a.causal && key > pos) || key < row_lo(a, pos)) continue;
+#pragma unroll 1
+      for (int e = e0; e < min(e0 + w.heads, a.group); ++e) {
+        const int64_t head = static_cast<int64_t>(g.h) * a.group + e;
+        const float l = w.lse[static_cast<int64_t>(g.row0 + i) * a.Hq + head];
+        if (l == -INFINITY) continue;
+        const uint16_t* q = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token + head * a.q_head;
+        float x = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < 128; ++d)
+          x = fmaf(__uint_as_float(static_cast<uint32_t>(q[d]) << 16),
+                   __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(k)[d]) << 16), x);
+        sum += ex2_approx((x * a.scale - l) * 1.4426950408889634f);
+      }
+    }
+  }
+  return sum;
 }
 
 template <int kKind>
@@ -755,7 +785,11 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!ok) break;
         float p, q;
         unf2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), p, q);
-        const float sum = p + q;
+        float sum = p + q;
+        if constexpr (kKind == 0) {
+          if (sum != sum && at >= 0) sum = weigh_again(w, g, j0, c.k_pages + at * kRow);
+          __syncwarp();
+        }
         if (g.part >= 0)
           ws.part[(static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kKeys + 128 * t + row] = sum;
         else if (at >= 0)

@@ -588,3 +588,28 @@ def test_weights_of_odd_groups(bsr, H, Hq, news):
     """Groups that leave rows of a step unused, and groups wider than a step."""
     b = Batch([1300, 50], [news, 3], H, 32, "bf16", seed=21)
     run_weigh(bsr, b, Hq)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [16, 17, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("H,group,causal,window", [(2, 1, True, 0), (1, 1, False, 0), (3, 1, True, 90)])
+def test_weights_by_rows(bsr, kind, news, H, group, causal, window):
+    """Around the numbers of rows at which the form changes; beside them sequences of other numbers."""
+    b = Batch([400, 700, 33, 140], [news, 1, 9, news // 2], H, 64, kind, seed=news, first_row=1, after=1)
+    run_weigh(bsr, b, H * group, causal=causal, window=window, accumulate=news % 2 == 0)
+
+
+@pytest.mark.parametrize("news", [1, 3, 11, 37, 64, 80])
+def test_an_infinite_key_that_all_rows_reject(bsr, news):
+    """Each row's logit is -inf there: it weighs nothing, whatever stands beside the rows."""
+    b = Batch([300, 90], [news, 1], 2, 64, seed=4)
+    q = torch.randn((b.rows, 4, 128), device="cuda").bfloat16()
+    q[:, :, 5] = -q[:, :, 5].abs() - 1
+    pg, sl = b.table_np[0, 2], 7  # token 135
+    b.k_pages[pg, 1, sl] = 0.5
+    b.k_pages[pg, 1, sl, 5] = math.inf
+    _, lse = bsr.paged_attn(q, *b.where)
+    assert lse.isfinite().all()
+    w = bsr.cache_weights(b.k_pages)
+    bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len, accumulate=False)
+    assert w.isfinite().all() and w[pg, 1, sl] == 0 and w[pg, 0, sl] > 0
