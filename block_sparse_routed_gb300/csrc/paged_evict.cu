@@ -368,28 +368,6 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
   }
 }
 
-// Launches `kern` in clusters of `blocks`; dependent: it may start while the
-// stream's previous kernel finishes (griddep_wait).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t units, int blocks, int threads, size_t smem, bool dependent,
-                            cudaStream_t s, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * blocks));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
-}
-
 template <int kKind, bool kAlone>
 cudaError_t launch(const PagedArgs& c, const EvictArgs& e, int64_t units, int blocks, int cache, cudaStream_t s) {
   using M = Move<kKind>;

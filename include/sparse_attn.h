@@ -573,7 +573,8 @@ sa_status sparse_attn_last_device_status(const void* ws, cudaStream_t stream, sa
  * MMAs in flight finish (those waits keep the 1 s limit), frees its tensor
  * memory and returns; the outputs of that call are invalid.  With `on`
  * nonzero, later launches by sparse_attn_fwd, sparse_attn_spark_fwd,
- * sparse_attn_fused and sparse_attn_paged_fwd are ones in which every pipeline
+ * sparse_attn_fused, sparse_attn_paged_fwd, sparse_attn_prefix_fwd and (its form
+ * for chunks) sparse_attn_cache_weigh are ones in which every pipeline
  * wait is a single probe, so that a call almost surely times out: it exists to
  * test that path.  Process-wide; returns the previous setting (0 or 1).
  * Host only: touches no device.
