@@ -437,12 +437,13 @@ SA_API sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first
   if (st != SA_OK) return st;
   if (bad_stride(p->a_token_stride) || bad_stride(p->a_head_stride)) return SA_EINVAL;
   if (first < 0 || (accumulate != 0 && accumulate != 1)) return SA_EINVAL;
-  if (!ws || !weights || (p->rows > 0 && (!q || !lse))) return SA_EINVAL;
+  const bool unreported = !ws && ws_bytes == 0 && need == kStatusBytes;
+  if ((!ws && !unreported) || !weights || (p->rows > 0 && (!q || !lse))) return SA_EINVAL;
   if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(weights, 16)) return SA_EINVAL;
   // (V is not read: K stands in for it)
   st = check_pointers(p, k_pages, k_pages, k_exp, k_exp, table, row_start, kv_len, ws);
   if (st != SA_OK) return st;
-  if (ws_bytes < need) return SA_EINVAL;
+  if (ws_bytes < need && !unreported) return SA_EINVAL;
   st = static_cast<sa_status>(device_status());
   if (st != SA_OK) return st;
   const int64_t longest = int64_t(p->table_width) * p->page_size;

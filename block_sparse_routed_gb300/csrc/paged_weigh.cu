@@ -17,11 +17,11 @@
 // multiplied.
 //
 // Measured:
-//   64 sequences of 512 to 33792 keys, 40 / 8 heads, BF16, one new   129 us  6.47 TB/s
+//   64 sequences of 512 to 33792 keys, 40 / 8 heads, BF16, one new   127 us  6.58 TB/s
 //                                                    E4M3             79 us  5.48
 //   64 of 8704, 24 / 8 heads, four new (12 rows): BF16               186 us  6.32
 //                                                 E4M3               129 us  4.76
-//   one of 1152, 8 / 2 heads, BF16                                   6.4 us  (latency)
+//   one of 1152, 8 / 2 heads, BF16                                   4.2 us  (latency; 6.4 with a status to clear)
 // Without the loads ahead the first takes 153 us; in E4M3 what a tile costs
 // besides its bytes counts: finding the next one from the last (113 -> 89 us)
 // and codes as FP16 instead of BF16.  Two tiles ahead: no better (registers).

@@ -27,6 +27,7 @@ from ._native import SA_OK, SaEvictParams, SparseAttnError
 from .paged import SCALE, _batch, _cache, _call, _env, _given, _new, _params, _rows, _scratch
 
 _INT32 = 0x7FFFFFFF
+_STATUS_BYTES = 256  # of a workspace, at its start
 
 
 def cache_weights(k_pages):
@@ -91,13 +92,18 @@ def cache_weigh(q, lse, weights, k_pages, table, row_start, kv_len, max_new=None
     w = _weights(env, weights, (pages, H, ps), dev)
     fields = (kind, pages, H, ps, d, seqs, width, outer, n, max_new, hq, 1 if causal else 0, min(window, _INT32),
               SCALE if scale is None else scale, qt, qh, 0, 0)
+    at = size = 0
     if ws is None:
-        ws = _new(env, stream, k_pages, (_weigh_ws_bytes(*fields),), env[3])
+        need = _weigh_ws_bytes(*fields)
+        if need > _STATUS_BYTES:
+            ws = _new(env, stream, k_pages, (need,), env[3])
+    if ws is not None:
+        at, size = _scratch(env, ws, dev, _STATUS_BYTES), ws.numel()
     _, p = _params(*fields)
     _call(env, "sparse_attn_cache_weigh", dev, stream, (
         p, min(first, _INT32), 1 if accumulate else 0, q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(),
         k_exp.data_ptr() if kind else None, table.data_ptr(), row_start.data_ptr(), kv_len.data_ptr(), w,
-        _scratch(env, ws, dev, 256), ws.numel()))
+        at or None, size))
     return weights
 
 

@@ -498,7 +498,9 @@ sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups, const
  *   first    keys at positions below it keep their weights (those that an
  *            eviction keeps anyway, or a prefix that several sequences share)
  *   accumulate  0 or 1
- *   ws       workspace of sparse_attn_weigh_ws_bytes(p) bytes, the status word first
+ *   ws       workspace of sparse_attn_weigh_ws_bytes(p) bytes, the status word first.
+ *            Where that is 256 (the status alone) it may be NULL with ws_bytes
+ *            0, as in sparse_attn_cache_write
  * With accumulate = 1 a key that no row sees is left as it was, with 0 it gets
  * 0.  Sequences without rows are left as they were.  A page that stands in
  * several rows of the table must lie below `first` in all of them but one;

@@ -613,3 +613,23 @@ def test_an_infinite_key_that_all_rows_reject(bsr, news):
     w = bsr.cache_weights(b.k_pages)
     bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len, accumulate=False)
     assert w.isfinite().all() and w[pg, 1, sl] == 0 and w[pg, 0, sl] > 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 20, 200])
+def test_weights_without_a_workspace(bsr, kind, news):
+    """The status goes unreported, and a bad sequence is left as it was all the same."""
+    b = Batch([300, 90, 50], [news, 1, 1], 2, 64, kind, seed=4)
+    q, lse, want = run_weigh(bsr, b, 4)
+    w = fresh_weights(b)
+    bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len, max_new=news, k_exp=b.k_exp)
+    assert torch.equal(w, want)
+    kl = b.kv_len.clone()
+    kl[1] = b.table.shape[1] * 64 + 1
+    w = fresh_weights(b)
+    bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, kl, max_new=news, k_exp=b.k_exp)
+    pages = b.table_np[1, :2]
+    assert torch.equal(w[pages], fresh_weights(b)[pages])
+    for s in (0, 2):
+        pages = b.table_np[s, : (b.lens[s] + 63) // 64]
+        assert torch.equal(w[pages], want[pages])
