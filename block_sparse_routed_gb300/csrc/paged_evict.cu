@@ -16,12 +16,16 @@
 // all loads of a round complete (a barrier of the cluster) before its stores,
 // which fill places below every source of the rounds that follow; so these are
 // loading already, two rounds ahead, and the barrier's time is that of the
-// last round's stores.
+// last round's stores.  Rounds whose places lie below all sources that the last
+// barrier has not covered need none: where a quarter stays that is all but a
+// few (67608 tokens to 16384 in 24 heads: 128 -> 104 us with the loads from
+// memory; 64 sequences of 8704 to 4096 in 8 heads, E4M3: 274 -> 230).  Moves to
+// other pages are a kernel of their own (113 -> 106 us for the first one below).
 //
-// Bound by memory where many units move to other pages, by the rounds' barriers
-// in place (a unit has one round at a time).  Measured:
-//   64 sequences of 1024 to 8704, 8 heads, E4M3, 2048 stay, to other pages   112 us  4.6 TB/s (75.7 at a copy's rate)
-//   one of 67608, 24 heads, BF16, 16384 stay, in place                       97 us  4.2      (60.8)
+// Bound by memory; by latency where there are few tokens (and by the choice, 30 us
+// of a long context's).  Measured:
+//   64 sequences of 1024 to 8704, 8 heads, E4M3, 2048 stay, to other pages   106 us  4.9 TB/s (75.7 at a copy's rate)
+//   one of 67608, 24 heads, BF16, 16384 stay, in place                      104 us  3.9      (60.8)
 //   one of 1152, 2 heads, BF16, 1024 stay, in place                          11.9 us  (four histograms, one after another)
 #include <cstdint>
 
@@ -237,14 +241,14 @@ struct Move {
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
 };
 
-template <int kKind, bool kAlone>  // kAlone: the cluster's first block chooses, else all
+template <int kKind, bool kAlone, bool kInPlace>  // kAlone: the cluster's first block chooses, else all
 __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, const EvictArgs e, int blocks, int cache) {
   using M = Move<kKind>;
   extern __shared__ __align__(128) uint8_t s_rows[];  // weights, then rows
   const int unit = blockIdx.x / blocks, rank = blockIdx.x % blocks;
   const int s = unit / c.H, h = unit % c.H;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const bool in_place = e.to_table == nullptr;
+  constexpr bool in_place = kInPlace;
   int32_t* kept = e.kept + static_cast<int64_t>(unit) * e.keep;
   const int32_t* from_table = c.table + s * c.table_stride;
   const int32_t* to_table = in_place ? from_table : e.to_table + s * e.to_stride;
@@ -337,6 +341,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
     }
     __syncwarp();  // the buffer is free
   };
+  // Places of round r lie below (r + 1) step.  Where the first token that the last
+  // barrier has not covered comes from behind them, none of their sources is
+  // still to be loaded, and the round's stores need no barrier of their own.
+  auto uncovered = [&](int round) {
+    const int i = (round + 1) * step;
+    return i < n ? kept[i] : 0x7FFFFFFF;
+  };
+  int limit = 0, covered = in_place ? uncovered(0) : 0;  // covered: what a barrier in iteration r makes of the limit
   // In iteration r the rows of round r have arrived, those of r + 1 and r + 2
   // are on their way, those of r - 1 go out while the cluster's blocks meet.
   Token before, now = lookup(0, position(0)), next = lookup(1, position(1)), after = lookup(2, position(2));
@@ -346,6 +358,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
   for (int r = 0; r <= rounds; ++r) {
     Token last = lookup(r + 3, pos);
     pos = position(r + 4);
+    bool meet = false;  // (the same for the whole cluster)
+    const int after_next = in_place ? uncovered(r + 1) : 0;
     if (r < rounds) {
       load(r + 2, after);
       cp_wait<2>();
@@ -356,11 +370,16 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(side), "r"(__float_as_uint(now.w)),
                      "r"(static_cast<uint32_t>(now.ke) | static_cast<uint32_t>(now.ve) << 8)
                      : "memory");
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        meet = limit < (r + 1) * step;
+        if (meet) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       }
     }
     if (r > 0) finish(r - 1, before);
-    if (r < rounds && in_place) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (meet) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      limit = covered;
+    }
+    covered = after_next;
     before = now;
     now = next;
     next = after;
@@ -368,10 +387,10 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
   }
 }
 
-template <int kKind, bool kAlone>
-cudaError_t launch(const PagedArgs& c, const EvictArgs& e, int64_t units, int blocks, int cache, cudaStream_t s) {
+template <int kKind, bool kAlone, bool kInPlace>
+cudaError_t launch_kernel(const PagedArgs& c, const EvictArgs& e, int64_t units, int blocks, int cache, cudaStream_t s) {
   using M = Move<kKind>;
-  auto* kern = evict_kernel<kKind, kAlone>;
+  auto* kern = evict_kernel<kKind, kAlone, kInPlace>;
   static SmemOnce once;
   const uint32_t weights = static_cast<uint32_t>(cache) * 4, bytes = M::kSmem > weights ? M::kSmem : weights;
   constexpr uint32_t most = M::kSmem > kSelCache * 4 ? M::kSmem : kSelCache * 4;
@@ -390,6 +409,12 @@ cudaError_t launch(const PagedArgs& c, const EvictArgs& e, int64_t units, int bl
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, c, e, blocks, cache);
+}
+
+template <int kKind, bool kAlone>
+cudaError_t launch(const PagedArgs& c, const EvictArgs& e, int64_t units, int blocks, int cache, cudaStream_t s) {
+  return e.to_table ? launch_kernel<kKind, kAlone, false>(c, e, units, blocks, cache, s)
+                    : launch_kernel<kKind, kAlone, true>(c, e, units, blocks, cache, s);
 }
 
 }  // namespace

@@ -633,3 +633,20 @@ def test_weights_without_a_workspace(bsr, kind, news):
     for s in (0, 2):
         pages = b.table_np[s, : (b.lens[s] + 63) // 64]
         assert torch.equal(w[pages], want[pages])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H", [2, 40])  # eight blocks a unit, and two
+@pytest.mark.parametrize("shape", ["rising", "falling", "hill", "valley", "steps", "late gap"])
+def test_eviction_in_place_of_uneven_gaps(bsr, kind, H, shape):
+    """Tokens that go stand together: places catch up with sources of other
+    rounds, or never do."""
+    n, keep = (9505, 5000) if H == 2 else (3000, 1700)
+    b, w = evict_case([n], H, 64, kind, seed=11)
+    x = np.arange(n) / n
+    level = {"rising": x, "falling": -x, "hill": -np.abs(x - 0.6), "valley": np.abs(x - 0.3), "steps": np.floor(x * 40) % 2,
+             "late gap": -(np.abs(x - 0.7) < 0.25).astype(float)}[shape]
+    j = np.arange(n)
+    for h in range(H):
+        w[b.table_np[0, j // 64], h, j % 64] = (level * (1 + h % 3) + 1e-3 * w[b.table_np[0, j // 64], h, j % 64]).astype(np.float32)
+    run_evict(bsr, b, w, keep, 4, 50)

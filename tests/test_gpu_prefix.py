@@ -295,3 +295,23 @@ def test_one_prompt_many_answers(bsr, kind):
                     assert mine[:P] == list(range(P)) and mine[-4:] == list(range(n - 4, n))
                     hist[s][h] = [hist[s][h][j] for j in mine]
     assert int(kl[0]) < P + 70
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news,H,group", [(1, 2, 17), (3, 2, 7), (4, 1, 6), (24, 2, 1), (3, 1, 8), (5, 1, 5), (1, 1, 33)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_own_rows_around_a_tile(bsr, kind, news, H, group, causal):
+    """17 to 24 rows of a sequence and key head (one tile in E4M3), fewer beside them, and one more."""
+    b = shared_batch([300, 64, 31, 700, 90, 5], [news, news, 1, news, 0, 2], [0, 3, 6], [320, 64], H, 32, kind, seed=news + group, first_row=1, after=1)
+    q, o, lse = run_prefix(bsr, b, H * group, causal=causal)
+    check_attention(b, q, o, lse, causal, filled=3.0)
+    q, o, lse = run_prefix(bsr, b, H * group, causal=causal, scale=2.5)
+    check_attention(b, q, o, lse, causal, scale=2.5, filled=3.0)
+
+
+@pytest.mark.parametrize("news,group", [(3, 7), (4, 6)])
+def test_long_own_keys_of_a_tile(bsr, news, group):
+    """Parts of a unit in many blocks."""
+    b = shared_batch([4000, 77, 5200], [news, 1, news], [0, 2], [640], 2, 64, "e4m3", seed=9)
+    q, o, lse = run_prefix(bsr, b, 2 * group)
+    check_attention(b, q, o, lse)
