@@ -37,6 +37,7 @@ namespace sa {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostBlocks = 8;  // of a unit
 // Weights that a block keeps in shared memory; the rest of a longer part is
 // read again (from the second-level cache).
 constexpr int kSelCache = 48 * 1024;
@@ -130,9 +131,11 @@ __device__ __forceinline__ void choose(const PagedArgs& c, const EvictArgs& e, i
     else __syncthreads();
     if (blocks > 1) {
       if (threadIdx.x < 256) {
-        uint32_t all = 0;
-#pragma unroll 4
-        for (int o = 0; o < blocks; ++o) all += cluster_word(&hist[threadIdx.x], o);
+        uint32_t of[kMostBlocks], all = 0;
+#pragma unroll
+        for (int o = 0; o < kMostBlocks; ++o) of[o] = o < blocks ? cluster_word(&hist[threadIdx.x], o) : 0u;
+#pragma unroll
+        for (int o = 0; o < kMostBlocks; ++o) all += of[o];
         s_all[threadIdx.x] = all;
       }
       __syncthreads();
@@ -205,9 +208,9 @@ __device__ __forceinline__ void choose(const PagedArgs& c, const EvictArgs& e, i
   if (blocks > 1) cluster_sync();
   else __syncthreads();
   int gt_before = s_warp[0][warp], eq_before = s_warp[1][warp];
-  for (int o = 0; o < rank; ++o) {
-    gt_before += cluster_word(&s_block[0], o);
-    eq_before += cluster_word(&s_block[1], o);
+  if (blocks > 1) {
+    gt_before += __reduce_add_sync(0xFFFFFFFFu, lane < rank ? cluster_word(&s_block[0], lane) : 0u);
+    eq_before += __reduce_add_sync(0xFFFFFFFFu, lane < rank ? cluster_word(&s_block[1], lane) : 0u);
   }
   // (read by others until the barrier behind the choice)
   int at = gt_before + min(eq_before, equals);
@@ -425,7 +428,7 @@ cudaError_t launch_evict(const PagedArgs& c, const EvictArgs& e, int sms, cudaSt
   // Two blocks an SM at most, of which a unit gets up to eight: 1152 tokens of 2
   // heads take 32 us with one, 21 with two, 16 with four and 12 with eight.
   int blocks = 1;
-  while (blocks < 8 && units * blocks <= sms) blocks *= 2;
+  while (blocks < kMostBlocks && units * blocks <= sms) blocks *= 2;
   // A choice by several blocks meets nine times: for 1152 tokens one block is
   // faster (12 us against 14), for 8704 eight are (28 against 31).
   const bool alone = blocks == 1 || longest <= 4096;
