@@ -18,14 +18,14 @@
 // loading already, two rounds ahead, and the barrier's time is that of the
 // last round's stores.  Rounds whose places lie below all sources that the last
 // barrier has not covered need none: where a quarter stays that is all but a
-// few (67608 tokens to 16384 in 24 heads: 128 -> 104 us with the loads from
-// memory; 64 sequences of 8704 to 4096 in 8 heads, E4M3: 274 -> 230).  Moves to
-// other pages are a kernel of their own (113 -> 106 us for the first one below).
+// few (67608 tokens to 16384 in 24 heads: 126 -> 99 us; 64 sequences of 8704 to
+// 4096 in 8 heads, E4M3: 274 -> 229).  Moves to other pages are a kernel of their
+// own (113 -> 106 us for the first one below).
 //
 // Bound by memory; by latency where there are few tokens (and by the choice, 30 us
 // of a long context's).  Measured:
 //   64 sequences of 1024 to 8704, 8 heads, E4M3, 2048 stay, to other pages   106 us  4.9 TB/s (75.7 at a copy's rate)
-//   one of 67608, 24 heads, BF16, 16384 stay, in place                      104 us  3.9      (60.8)
+//   one of 67608, 24 heads, BF16, 16384 stay, in place                       99 us  4.2      (60.8)
 //   one of 1152, 2 heads, BF16, 1024 stay, in place                          11.9 us  (four histograms, one after another)
 #include <cstdint>
 
@@ -348,21 +348,32 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
   // barrier has not covered comes from behind them, none of their sources is
   // still to be loaded, and the round's stores need no barrier of their own.
   auto uncovered = [&](int round) {
-    const int i = (round + 1) * step;
+    const int64_t i = static_cast<int64_t>(round + 1) * step;
     return i < n ? kept[i] : 0x7FFFFFFF;
   };
-  int limit = 0, covered = in_place ? uncovered(0) : 0;  // covered: what a barrier in iteration r makes of the limit
+  // (Of the first rounds they are in shared memory: a load in the loop would wait for
+  // the rows before it.  Later ones have a barrier each.)
+  __shared__ int s_limit[kThreads];
+  int limit = in_place ? uncovered(threadIdx.x) : 0;
   // In iteration r the rows of round r have arrived, those of r + 1 and r + 2
   // are on their way, those of r - 1 go out while the cluster's blocks meet.
   Token before, now = lookup(0, position(0)), next = lookup(1, position(1)), after = lookup(2, position(2));
   int pos = position(3);
   load(0, now);
   load(1, next);
+  if (in_place) {
+    s_limit[threadIdx.x] = limit;
+    limit = 0;
+    __syncthreads();
+  }
+  // (BF16: in a loop of one the rounds' registers change places, which waits for
+  // their loads: 134 against 124 us for what stays in place nearly as it is; E4M3:
+  // four are 97 against 76 us for the long context)
+#pragma unroll (kKind == 0 ? 4 : 1)
   for (int r = 0; r <= rounds; ++r) {
     Token last = lookup(r + 3, pos);
     pos = position(r + 4);
     bool meet = false;  // (the same for the whole cluster)
-    const int after_next = in_place ? uncovered(r + 1) : 0;
     if (r < rounds) {
       load(r + 2, after);
       cp_wait<2>();
@@ -373,16 +384,15 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const PagedArgs c, cons
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(side), "r"(__float_as_uint(now.w)),
                      "r"(static_cast<uint32_t>(now.ke) | static_cast<uint32_t>(now.ve) << 8)
                      : "memory");
-        meet = limit < (r + 1) * step;
+        meet = __any_sync(0xFFFFFFFFu, limit < (r + 1) * step);  // (a vote: the compiler knows that a warp agrees)
         if (meet) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       }
     }
     if (r > 0) finish(r - 1, before);
     if (meet) {
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      limit = covered;
+      limit = r < kThreads ? s_limit[r] : 0;
     }
-    covered = after_next;
     before = now;
     now = next;
     next = after;
