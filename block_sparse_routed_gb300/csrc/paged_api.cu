@@ -226,9 +226,12 @@ int form_ctas(const sa_paged_params* p, const PagedForm& f, int64_t seqs, int64_
   return ctas;
 }
 
-// Whether weights are taken by the form for few rows (both measured in paged_weigh.cu).
+// Whether weights are taken by the form for few rows (both measured in
+// paged_weigh.cu): what it costs goes with the rows that there are, what the form
+// for chunks costs with whole steps of 96.
 bool weighs_few(const sa_paged_params* p) {
-  return int64_t(p->max_new < p->rows ? p->max_new : p->rows) * (p->Hq / p->H) <= kWeighFewRows;
+  const int64_t group = p->Hq / p->H, most = int64_t(p->max_new < p->rows ? p->max_new : p->rows) * group;
+  return most <= 64 || (most <= kWeighFewRows && p->rows * group <= int64_t(80) * p->seqs);
 }
 
 uint64_t weigh_scratch_of(const sa_paged_params* p, void* ws, WeighScratch* out) {

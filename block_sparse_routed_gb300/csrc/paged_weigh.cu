@@ -387,10 +387,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks<kN>) weigh_kernel(const W
 //     64   1152          25 /  30        25 /  35
 //     64   17408        135 / 278       162 / 345
 //    128   17408        173 / 282       181 / 361
-// (a uniform 128 rows come near the other form; it takes what is above).  Two tiles
-// a warp (54 against 46 us for eight sequences of 1152 to 8704 keys, 64 heads' rows)
-// and two accumulators a product (no change) did not help: loads of rows did, all
-// under way at once and behind the first keys' (46 -> 43 us).
+// and as many rows each, over 17408 keys: 64 rows 208 / 282 and 209 / 364, 96 rows
+// 283 / 238 and 285 / 282, 128 rows 356 / 301 and 352 / 323 (so above 64 rows the
+// mean decides).  Two tiles a warp (54 against 46 us for eight sequences of 1152
+// to 8704 keys, up to 64 rows) and two accumulators a product (no change) did not
+// help: loads of rows did, all under way at once and behind the first keys' (46 ->
+// 43 us).
 constexpr int kMidRow = 320;   // bytes of a row: other banks for the next one
 constexpr int kMidBlocks = 4;  // blocks an SM
 
@@ -684,6 +686,7 @@ cudaError_t launch_mid(const WeighArgs& w, int sms, int64_t ctas, cudaStream_t s
 
 cudaError_t launch_weigh(const WeighArgs& w, int64_t rows, int sms, int64_t key_tiles, cudaStream_t s) {
   const int64_t ctas = (key_tiles + kWarps - 1) / kWarps;
+  static_assert(kWeighFewRows == 128, "the most rows of a kernel here");
   if (rows > 64) return w.a.c.kind == 0 ? launch_mid<0, 128>(w, sms, ctas, s) : launch_mid<1, 128>(w, sms, ctas, s);
   if (rows > 16) return w.a.c.kind == 0 ? launch_mid<0, 64>(w, sms, ctas, s) : launch_mid<1, 64>(w, sms, ctas, s);
   if (w.a.c.kind == 0) return rows <= 8 ? launch<0, 1>(w, sms, ctas, s) : launch<0, 2>(w, sms, ctas, s);

@@ -1,5 +1,5 @@
 // The attention weight that cached keys receive from chunks of rows (sm_103a):
-// more than 128 packed rows a sequence and key head, on tcgen05 tensor cores.
+// more than 128 packed rows (64, if most have many) a sequence and key head, on tcgen05 tensor cores.
 //
 //   w_j (+)= sum_r 2^(x_rj - L_r),   x_rj = scale log2(e) (q_r . k_j),  L_r = log2(e) lse_r
 //

@@ -650,3 +650,19 @@ def test_eviction_in_place_of_uneven_gaps(bsr, kind, H, shape):
     for h in range(H):
         w[b.table_np[0, j // 64], h, j % 64] = (level * (1 + h % 3) + 1e-3 * w[b.table_np[0, j // 64], h, j % 64]).astype(np.float32)
     run_evict(bsr, b, w, keep, 4, 50)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news,group", [(64, 1), (65, 1), (96, 1), (100, 1), (128, 1), (81, 1), (16, 7), (40, 2), (41, 2)])
+def test_weights_of_as_many_rows_each(bsr, kind, news, group):
+    """Where the mean number of rows decides on the form."""
+    b = Batch([400, 333, news], [news] * 3, 2, 64, kind, seed=news, first_row=1, after=1)
+    run_weigh(bsr, b, 2 * group, accumulate=news % 2 == 0)
+
+
+def test_a_workspace_follows_the_rows(bsr):
+    table = torch.zeros((8, 4), dtype=torch.int32, device="cuda")
+    k = bsr.paged_cache(16, 2, 64)[0]
+    size = lambda rows, max_new: bsr.weigh_workspace(torch.zeros((rows, 2, 128), dtype=torch.bfloat16, device="cuda"), k, table, max_new).numel()  # noqa: E731
+    assert size(8 * 64, 64) == size(8 * 80, 128) == 256
+    assert size(8 * 80 + 8, 128) > 256 and size(200, 200) > 256
