@@ -184,6 +184,18 @@ __device__ __forceinline__ int shared_before(const SharedAttnArgs& a, int s, boo
   return s < s1 ? pages : 0;
 }
 
+// The first sequence of [s0, s1) that has rows, where s0 has none: the last one
+// that starts at row r0, as s0 does.  (Empty slots' table rows may name any page.)
+__device__ __forceinline__ int first_with_rows(const SharedAttnArgs& a, int s0, int s1, int r0) {
+  int lo = s0, hi = s1 - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (a.c.row_start[mid] <= r0) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ SharedSeq line_seq(const SharedAttnArgs& a, int v, bool& bad) {
   SharedSeq q;
   q.row0 = q.n = q.len = q.row = 0;
@@ -193,9 +205,10 @@ __device__ __forceinline__ SharedSeq line_seq(const SharedAttnArgs& a, int v, bo
     int s1;
     const int pages = shared_pages(a, v, q.row, s1, bad);
     if (pages > 0) {
-      const int r0 = a.c.row_start[q.row], r1 = a.c.row_start[s1];
+      const int s0 = q.row, r0 = a.c.row_start[s0], r1 = a.c.row_start[s1], next = a.c.row_start[s0 + 1];
       bad = r0 < 0 || r1 < r0 || r1 > a.c.rows;
       if (!bad) {
+        if (next <= r0) q.row = first_with_rows(a, s0, s1, r0);
         q.row0 = r0;
         q.n = r1 - r0;
         q.len = pages << a.c.page_shift;
@@ -208,7 +221,7 @@ __device__ __forceinline__ SharedSeq line_seq(const SharedAttnArgs& a, int v, bo
   q.row = v - a.groups;
   q.page0 = shared_before(a, q.row, wrong);
   const int before = q.page0 << a.c.page_shift;
-  bad |= wrong || (before > 0 && q.len - q.n < before);
+  bad |= wrong || (before > 0 && q.n > 0 && q.len - q.n < before);
   if (bad) q.n = 0;
   q.len -= before;
   return q;

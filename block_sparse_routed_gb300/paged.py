@@ -342,9 +342,10 @@ def prefix_attn(q, k_pages, v_pages, table, row_start, kv_len, group_start, pref
     ``group_start`` (int32 [groups + 1], ascending) and ``prefix_len`` (int32
     [groups]), on the GPU: the sequences group_start[g] .. group_start[g + 1] - 1
     begin with the same prefix_len[g] tokens.  Those in whole pages are read
-    once, from the pages of the group's first sequence, which the others' rows
-    of ``table`` name too; all others by each sequence's own row.  A sequence's
-    rows must lie behind the shared pages.  There is no window.
+    once, from the pages of the group's first sequence that has rows, which the
+    others' rows of ``table`` name too; all others by each sequence's own row.  A
+    sequence's rows must lie behind the shared pages; of one without rows (an
+    empty slot) nothing has to agree with its group.  There is no window.
 
     Returns (o, lse) as ``paged_attn``, equal up to the order of sums."""
     env = _env()

@@ -457,10 +457,11 @@ sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, const v
  *   prefix_len   int32 [groups], device memory: the first prefix_len[g] tokens
  *                of all sequences of group g are the same.  Those in whole
  *                pages are read once, from the pages of the group's first
- *                sequence, which the others' table rows name too (or pages
- *                that hold the same); the rest of them, as all other tokens,
- *                by each sequence's own row.  A group of one sequence shares
- *                nothing
+ *                sequence that has rows, which the others' table rows name
+ *                too (or pages that hold the same); the rest of them, as all
+ *                other tokens, by each sequence's own row.  A group of one
+ *                sequence shares nothing; of one without rows, neither kv_len
+ *                nor the table's row has to agree with its group
  * Everything else is as in sparse_attn_paged_fwd, and so is the result, up to
  * the order of sums.  window must be 0.
  *   ws  workspace of sparse_attn_prefix_ws_bytes(p, groups) bytes (1040 for
