@@ -162,9 +162,11 @@ struct Rows {
         const bool real = r < rows;
         float l = INFINITY;
         if (real) l = __ldg(w.lse + static_cast<int64_t>(s.row0 + j) * a.Hq + h * a.group + r - j * a.group);
-        neg[n][e] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-        lo[n][e] = real ? row_lo(a, pos) : 0;
-        hi[n][e] = real ? (a.causal ? min(s.len, pos + 1) : s.len) : 0;
+        // (a row that counts nothing sees nothing here: its products may be NaN)
+        const bool counts = l != -INFINITY && real;
+        neg[n][e] = counts ? -l * 1.4426950408889634f : -INFINITY;
+        lo[n][e] = counts ? row_lo(a, pos) : 0;
+        hi[n][e] = counts ? (a.causal ? min(s.len, pos + 1) : s.len) : 0;
       }
     }
   }
@@ -400,17 +402,20 @@ template <int kRows>  // at most so many rows
 struct MidRows {
   alignas(16) uint8_t q[kRows * kMidRow];
   float4 use[kRows / 2];  // of a pair of rows: -L (-inf: counts nothing); E4M3: the roots of what undoes their scaling
-  int pos[kRows];         // positions
+  int pos[kRows];         // the last key that the row sees (-1: its lse is -infinity, it counts nothing)
 };
 
 // The rows of unit (q, h), by the whole block: half a warp has a row at a time, and
-// eight of them are on their way before the first is looked at.
+// eight of them are on their way before the first is looked at.  True where this
+// thread's rows have one that counts nothing: its products may be NaN and are to
+// be left out.
 template <int kKind, int kRows>
-__device__ __forceinline__ void mid_rows(const WeighArgs& w, const PagedSeq& q, int h, MidRows<kRows>& m) {
+__device__ __forceinline__ bool mid_rows(const WeighArgs& w, const PagedSeq& q, int h, MidRows<kRows>& m) {
   const PagedAttnArgs& a = w.a;
   constexpr int kTurns = 8;
   static_assert(kRows % (kTurns * 8) == 0 && 2 * kWarps == 8, "a turn is eight rows");
   const int rows = q.n * a.group, lane = threadIdx.x % 32, sub = lane % 16;
+  bool nothing = false;
 #pragma unroll 1
   for (int r0 = 0; r0 < kRows; r0 += kTurns * 8) {
     if (r0 >= rows) break;
@@ -431,6 +436,7 @@ __device__ __forceinline__ void mid_rows(const WeighArgs& w, const PagedSeq& q, 
     for (int n = 0; n < kTurns; ++n) {
       const int rho = r0 + 8 * n + threadIdx.x / 16;
       if (r0 + 8 * n >= rows) break;
+      nothing |= l[n] == -INFINITY;
       int at = sub;
       float* use = reinterpret_cast<float*>(m.use + rho / 2) + rho % 2;
       if constexpr (kKind != 0) {  // (see Rows)
@@ -452,10 +458,11 @@ __device__ __forceinline__ void mid_rows(const WeighArgs& w, const PagedSeq& q, 
       *reinterpret_cast<uint4*>(m.q + rho * kMidRow + at * 16) = x[n];
       if (sub == 0) {
         use[0] = l[n] == -INFINITY ? -INFINITY : -l[n] * 1.4426950408889634f;
-        m.pos[rho] = q.len - q.n + div_group(a, min(rho, rows - 1));
+        m.pos[rho] = rho >= rows || l[n] == -INFINITY ? -1 : a.causal ? q.len - q.n + div_group(a, rho) : 0x7FFFFFFF;
       }
     }
   }
+  return nothing;
 }
 
 using f2 = unsigned long long;  // two floats in a register pair
@@ -572,15 +579,14 @@ __global__ void __launch_bounds__(32 * kWarps, kMidBlocks) weigh_mid_kernel(cons
       };
       if (t0 + warp < t1) fetch(t0 + warp);
       __syncthreads();
-      mid_rows<kKind, kRows>(w, q, h, m);
-      __syncthreads();
+      const bool nothing = __syncthreads_or(mid_rows<kKind, kRows>(w, q, h, m));
 #pragma unroll 1
       for (int t = t0 + warp; t < t1; t += kWarps) {
         now = next;
         if (t + kWarps < t1) fetch(t + kWarps);
         if (now.row0 < 0) continue;
         const int key0 = (k.t0 + t) * kTileKeys;
-        const bool edge = key0 < all_lo || key0 + kTileKeys > all_hi;
+        const bool edge = key0 < all_lo || key0 + kTileKeys > all_hi || nothing;
         uint32_t f[2][16];  // E4M3: keys u and u + 8 in FP16
         f2 ks[2][2];
         if constexpr (kKind != 0) {
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(32 * kWarps, kMidBlocks) weigh_mid_kernel(cons
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + u + 8 * (e / 2), at = e & 1 ? pos.y : pos.x;
-              if (key < row_lo(a, at) || (a.causal && key > at)) p[e / 2][e % 2] = 0.f;
+              if (key < row_lo(a, at) || key > at) p[e / 2][e % 2] = 0.f;
             }
           }
 #pragma unroll

@@ -14,7 +14,9 @@
 // 16 dimensions: 1 in the keys, and in the rows -lse / scale as three BF16
 // parts, which hold all of its 24 bits (604 -> 580 us for 2048 rows that see all
 // of 33792 keys).  A kernel in front makes the rows' blocks (made by the warps
-// that bring the rows, these were what the rest waited for: 580 -> 555).
+// that bring the rows, these were what the rest waited for: 580 -> 555).  It marks
+// rows whose lse is -infinity, and who issues products writes zeros over them
+// first: such a row counts nothing, whatever it holds.
 //
 // Keys are in tensor memory because shared memory would not feed both operands:
 // of a step (two tiles, 96 rows) products read Q there twice, 2 x 24 KB, and the
@@ -340,13 +342,20 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float bf16_of(float x) {  // rounded to BF16
   return __uint_as_float(pack_bf16x2(0.f, x) & 0xFFFF0000u);
 }
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ void lds_i4(int (&v)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
 // A key's sum over the rows of a unit's steps, once more and one by one, where the
 // other one is not a number: an infinity in the key times the zeros of rows that
-// only fill a step is none, though each row's own product may be.
+// count nothing is none, though each row's own product may be.  (E4M3: a key that
+// is NaN as a whole, with only such rows.)
+template <int kKind>
 __device__ __noinline__ float weigh_again(const WeighArgs& w, const Work& g, int key, const uint8_t* k) {
   const PagedAttnArgs& a = w.a;
   float sum = 0.f;
@@ -362,6 +371,7 @@ __device__ __noinline__ float weigh_again(const WeighArgs& w, const Work& g, int
         const int64_t head = static_cast<int64_t>(g.h) * a.group + e;
         const float l = w.lse[static_cast<int64_t>(g.row0 + i) * a.Hq + head];
         if (l == -INFINITY) continue;
+        if constexpr (kKind != 0) return NAN;
         const uint16_t* q = a.q + static_cast<int64_t>(g.row0 + i) * a.q_token + head * a.q_head;
         float x = 0.f;
 #pragma unroll 4
@@ -570,6 +580,21 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto off = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4); };
     const uint64_t ones = sdesc_plain(sbase + kOffOnes, 128 * 16, 128);
     const uint32_t elect = elect_one();
+    // Zeros over a stage's marked rows (both warps that read it write the same).
+    auto blank_rows = [&](int st) {
+      uint32_t mark[kRows / 32], any = 0;
+#pragma unroll
+      for (int e = 0; e < kRows / 32; ++e) any |= mark[e] = lds_u32(smem_u32(shift_at(st, 32 * e + lane)) + 12);
+      if (!__any_sync(0xFFFFFFFFu, any)) return;
+#pragma unroll 1
+      for (int e = 0; e < kRows / 32; ++e)
+        for (unsigned m = __ballot_sync(0xFFFFFFFFu, e == 0 ? mark[0] : e == 1 ? mark[1] : mark[2]); m; m &= m - 1)
+          if (lane < 16)
+            *reinterpret_cast<uint4*>(base + st * kStageBytes + lane / 8 * kHalfBytes + (32 * e + __ffs(m) - 1) * 128 + lane % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
     int st = 0, phase = 0;  // the next step's stage
     int y = 0, u = 0;       // steps and units of the tile
     bool issued = false;
@@ -584,6 +609,7 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         ok = all_wait(BAR_QFULL + st, phase);
         if (!ok) break;
         if (mine) {
+          blank_rows(st);
           const int s = 2 * t + (y & 1);
           ok = y < 2 || all_wait(BAR_SEMPTY + s, y / 2 - 1);
           if (!ok) break;
@@ -787,9 +813,11 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         unf2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), p, q);
         float sum = p + q;
         if constexpr (kKind == 0) {
-          if (sum != sum && at >= 0) sum = weigh_again(w, g, j0, c.k_pages + at * kRow);
-          __syncwarp();
+          if (sum != sum && at >= 0) sum = weigh_again<kKind>(w, g, j0, c.k_pages + at * kRow);
+        } else {
+          if (sum != sum && at >= 0 && __ldg(c.k_exp + at) == 255) sum = weigh_again<kKind>(w, g, j0, nullptr);
         }
+        __syncwarp();
         if (g.part >= 0)
           ws.part[(static_cast<int64_t>(blockIdx.x) * 2 + g.part) * kKeys + 128 * t + row] = sum;
         else if (at >= 0)
@@ -820,7 +848,8 @@ weigh_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   griddep_launch_dependents();
 }
 
-// The rows' ninth blocks: -lse / scale = hi + mid + lo in BF16.
+// The rows' ninth blocks: -lse / scale = hi + mid + lo in BF16; and ones, which the
+// keys multiply by 0, as the mark of a row that counts nothing.
 __global__ void __launch_bounds__(256) weigh_shift_kernel(const WeighArgs w, const WeighScratch ws) {
   griddep_launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -829,7 +858,7 @@ __global__ void __launch_bounds__(256) weigh_shift_kernel(const WeighArgs w, con
   const float v = l == -INFINITY ? -INFINITY : -l / w.a.scale;
   const float hi = bf16_of(v);
   const float mid = isfinite(hi) ? bf16_of(v - hi) : 0.f, lo = isfinite(hi) ? v - hi - mid : 0.f;
-  ws.shift[at] = make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0, 0);
+  ws.shift[at] = make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0, l == -INFINITY ? 0x3F803F80u : 0u);
 }
 
 // The units that a cut divided, their parts in order; and the call's status.

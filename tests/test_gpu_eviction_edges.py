@@ -1,0 +1,73 @@
+"""Weights of cached keys at their edges: values that are not numbers, rows that
+count nothing."""
+
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from .test_gpu_eviction import check_weights, fresh_weights  # noqa: E402
+from .test_gpu_paged import Batch, bsr  # noqa: E402,F401
+
+FORMS = {"few": 3, "mid": 30, "chunk": 200}  # rows of the first sequence, 4 / 2 heads
+
+
+def form_batch(bsr, form, kind, seed=4):
+    """A batch that the form takes, its Q, lse and maximal number of rows."""
+    news = FORMS[form]
+    b = Batch([300, 90], [news, 1], 2, 64, kind, seed=seed)
+    q = torch.randn((b.rows, 4, 128), generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    assert (bsr.weigh_workspace(q, b.k_pages, b.table, news).numel() > 256) == (form == "chunk")
+    _, lse = bsr.paged_attn(q, *b.where, max_new=news, **b.exps)
+    return b, q, lse, news
+
+
+def weigh(bsr, b, q, lse, news, w=None, k=None, ke=None, **kw):
+    w = fresh_weights(b) if w is None else w
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    bsr.cache_weigh(q, lse, w, b.k_pages if k is None else k, b.table, b.row_start, b.kv_len, max_new=news,
+                    k_exp=b.k_exp if ke is None else ke, ws=ws, **kw)
+    assert bsr.sparse_attn_last_device_status(ws) == 0
+    return w
+
+
+def spoil(b, s, j, h, value):
+    """Copies of K and its exponents with one key that is not a number, or infinite."""
+    k, ke = b.k_pages.clone(), None if b.k_exp is None else b.k_exp.clone()
+    pg, sl = b.table_np[s, j // b.page], j % b.page
+    if ke is None:
+        k[pg, h, sl, 5] = value
+    else:
+        ke[pg, h, sl] = 255
+    return k, ke, (pg, h, sl)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_that_count_nothing_may_hold_anything(bsr, kind, form):
+    b, q, lse, news = form_batch(bsr, form, kind)
+    for r, h, value in ((0, 1, math.nan), (news // 2, 2, math.inf), (news - 1, 0, -math.inf), (news, 3, math.nan)):
+        q[r, h] = value
+        lse[r, h] = -math.inf
+    before = fresh_weights(b).cpu().numpy()
+    w = weigh(bsr, b, q, lse, news)
+    check_weights(b, q, lse, before, w, 0, True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_key_that_no_counting_row_sees(bsr, kind, form, value, causal):
+    """The last token, seen by the last row alone, whose lse says that it counts nothing."""
+    b, q, lse, news = form_batch(bsr, form, kind)
+    if causal:
+        lse[news - 1] = -math.inf
+    else:
+        lse[:news] = -math.inf
+    clean = weigh(bsr, b, q, lse, news, causal=causal)
+    k, ke, at = spoil(b, 0, 299, 1, value)
+    w = weigh(bsr, b, q, lse, news, k=k, ke=ke, causal=causal)
+    assert w[at] == 0 and torch.equal(w, clean)
