@@ -71,3 +71,49 @@ def test_a_key_that_no_counting_row_sees(bsr, kind, form, value, causal):
     k, ke, at = spoil(b, 0, 299, 1, value)
     w = weigh(bsr, b, q, lse, news, k=k, ke=ke, causal=causal)
     assert w[at] == 0 and torch.equal(w, clean)
+
+
+def microseconds(call):
+    best = math.inf
+    for _ in range(5):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        call()
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end) * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("what", ["lse", "row", "key"])
+def test_one_nan_in_a_chunk(bsr, kind, what):
+    """It reaches the keys that the row sees, or the rows that see the key, no
+    other sequence, and does not make the call longer by orders of magnitude."""
+    b = Batch([2900, 700], [300, 250], 2, 64, kind, seed=9)
+    q = torch.randn((b.rows, 8, 128), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    _, lse = bsr.paged_attn(q, *b.where, max_new=300, **b.exps)
+    clean = weigh(bsr, b, q, lse, 300)
+    k, ke = b.k_pages, b.k_exp
+    if what == "lse":
+        lse2, q2 = lse.clone(), q
+        lse2[280, 5] = math.nan  # key head 1
+    else:
+        q2 = q.clone()
+        if what == "row":
+            q2[280, 5, 77] = math.nan
+        else:
+            k, ke, _ = spoil(b, 0, 3, 1, math.nan)
+        _, lse2 = bsr.paged_attn(q2, k, *b.where[1:], max_new=300, k_exp=ke, v_exp=b.v_exp)
+    w = weigh(bsr, b, q2, lse2, 300, k=k, ke=ke)
+    seen = 2900 - 300 + 281 if what != "key" else 2900
+    bad = torch.zeros_like(w, dtype=torch.bool)
+    for j in range(seen):
+        bad[b.table_np[0, j // 64], 1, j % 64] = True
+    assert w[bad].isnan().all() and torch.equal(w[~bad], clean[~bad])
+    ws = bsr.weigh_workspace(q, b.k_pages, b.table, 300)
+    scratch = clean.clone()
+    call = lambda l, x, k, ke: bsr.cache_weigh(x, l, scratch, k, b.table, b.row_start, b.kv_len, max_new=300, k_exp=ke, ws=ws)  # noqa: E731
+    fine = microseconds(lambda: call(lse, q, b.k_pages, b.k_exp))
+    odd = microseconds(lambda: call(lse2, q2, k, ke))
+    assert odd < 20 * fine, (odd, fine)
