@@ -251,6 +251,16 @@ uint64_t weigh_scratch_of(const sa_paged_params* p, void* ws, WeighScratch* out)
   return off;
 }
 
+// Whether the n numbers from `out` on share one with `rows` rows of `width` numbers, `stride` apart.
+bool overlaps(const int32_t* out, int64_t n, const int32_t* in, int64_t rows, int64_t width, int64_t stride) {
+  if (!out || !in || n <= 0 || rows <= 0 || width <= 0) return false;
+  const int64_t at = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(in)) / 4;  // (both aligned)
+  if (at + n <= 0) return false;
+  // the last row that begins at or before `out` (none: -1), and the next one
+  const int64_t row = at < 0 ? -1 : stride == 0 || at / stride >= rows ? rows - 1 : at / stride;
+  return (row >= 0 && at < row * stride + width) || (row + 1 < rows && (row + 1) * stride < at + n);
+}
+
 sa_status clear_status(void* ws, cudaStream_t stream) {
   if (ws && cuda_failed(cudaMemsetAsync(ws, 0, kStatusBytes, stream))) return SA_ECUDA;
   return SA_OK;
@@ -493,7 +503,14 @@ SA_API sa_status sparse_attn_cache_evict(const sa_paged_params* p, const sa_evic
     return SA_EUNSUPPORTED;
   if (!weights || (p->seqs > 0 && (!kept || !new_len))) return SA_EINVAL;
   if (!aligned(weights, 16) || !aligned(to_table, 4) || !aligned(kept, 4) || !aligned(new_len, 4)) return SA_EINVAL;
-  if (p->seqs > 0 && new_len == kv_len) return SA_EINVAL;  // lengths are read while new ones are written
+  // Lengths and tables are read by all blocks while others write what was kept.
+  const int64_t all = int64_t(p->seqs) * p->H * e->keep;
+  if (overlaps(new_len, p->seqs, kv_len, 1, p->seqs, 0) || overlaps(kept, all, kv_len, 1, p->seqs, 0) ||
+      overlaps(kept, all, new_len, 1, p->seqs, 0) || overlaps(kept, all, table, p->seqs, p->table_width, p->table_stride) ||
+      overlaps(new_len, p->seqs, table, p->seqs, p->table_width, p->table_stride) ||
+      overlaps(kept, all, to_table, p->seqs, e->to_width, e->to_stride) ||
+      overlaps(new_len, p->seqs, to_table, p->seqs, e->to_width, e->to_stride))
+    return SA_EINVAL;
   st = check_pointers(p, k_pages, v_pages, k_exp, v_exp, table, k_pages /* no row_start */, kv_len, ws);
   if (st != SA_OK) return st;
   st = static_cast<sa_status>(device_status());

@@ -536,7 +536,8 @@ sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32
  *   weights   float32 [pages, H, page_size], 16-byte aligned
  *   kept      int32 [seqs, H, keep]: the former position of the token at
  *             position i, -1 from the new length on
- *   new_len   int32 [seqs]: min(kv_len, keep); must not be kv_len itself
+ *   new_len   int32 [seqs]: min(kv_len, keep)
+ * kept and new_len must not overlap each other, kv_len or a table.
  *   ws        optional (may be NULL): 256 bytes whose first word takes the status
  * Slots from the new length on are left as they were.  Later rows see kept
  * tokens by their new positions (a window counts kept tokens).
@@ -547,7 +548,7 @@ sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32
  * sequence moves, kept is -1 throughout and new_len is kv_len.
  * Errors before launch: as sparse_attn_cache_write; SA_EINVAL also for keep <
  * 1, first or last < 0, first + last > keep, a null or misaligned weights,
- * kept or new_len, new_len == kv_len; SA_EUNSUPPORTED also for keep > 2^30,
+ * kept or new_len, outputs that overlap as above; SA_EUNSUPPORTED also for keep > 2^30,
  * seqs * H >= 2^27, table_width * page_size > 2^30.
  */
 typedef struct sa_evict_params {
