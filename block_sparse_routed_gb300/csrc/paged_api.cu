@@ -435,8 +435,10 @@ SA_API sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* 
   if (out == nullptr) return SA_EINVAL;
   const sa_status st = check_attn(p);
   if (st != SA_OK) return st;
-  // (lse / scale, which the form for chunks subtracts, and its parts are numbers then)
-  if (p->scale < 0x1p-100f || p->scale > 0x1p100f) return SA_EUNSUPPORTED;
+  // (lse / scale, which the form for chunks subtracts, and its parts are numbers then; so is
+  // the half of a key's exponent that has scale in it in the forms for few rows, 2^64 at most
+  // without, and an E4M3 key of the largest values gives a row of zeros the logit 0)
+  if (p->scale < 0x1p-100f || p->scale > 0x1p60f) return SA_EUNSUPPORTED;
   *out = weigh_scratch_of(p, nullptr, nullptr);
   return SA_OK;
 }

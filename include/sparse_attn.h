@@ -511,7 +511,7 @@ sa_status sparse_attn_prefix_fwd(const sa_paged_params* p, int32_t groups, const
  * its largest one lose bits.
  * Errors: as sparse_attn_paged_fwd; SA_EINVAL also for first < 0, accumulate
  * not 0 or 1, a null or misaligned lse or weights; SA_EUNSUPPORTED also for a
- * scale outside [2^-100, 2^100].
+ * scale outside [2^-100, 2^60].
  */
 sa_status sparse_attn_weigh_ws_bytes(const sa_paged_params* p, uint64_t* out);
 sa_status sparse_attn_cache_weigh(const sa_paged_params* p, int32_t first, int32_t accumulate, const void* q,

@@ -1,8 +1,11 @@
-"""Outputs of an eviction that overlap what its blocks read, without a GPU."""
+"""Refusals of weights and eviction at their limits, without a GPU: outputs over
+what a launch's blocks read, scales past what the factors hold."""
+
+import ctypes
 
 import pytest
 
-from .test_eviction_host import E_FIELDS, _evict
+from .test_eviction_host import E_FIELDS, _evict, _weigh
 from .test_paged_host import _p, native  # noqa: F401
 
 # seqs 3, H 2, keep 5; a table of 3 rows of 4 entries, 100 apart; addresses that no path here may touch
@@ -41,3 +44,13 @@ def test_outputs_beside_inputs_are_not(native, kw):  # noqa: F811
     if torch.cuda.is_available():
         pytest.skip("the addresses are nobody's")
     assert call(native, **kw) != native.SA_EINVAL  # (but there is no device)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("e,fine", [(-101, False), (-100, True), (60, True), (61, False), (99, False), (120, False)])
+def test_scales(native, kind, e, fine):  # noqa: F811
+    p, out = _p(native, kind=kind, scale=2.0 ** e), ctypes.c_uint64()
+    want = native.SA_OK if fine else native.SA_EUNSUPPORTED
+    assert native.load_library().sparse_attn_weigh_ws_bytes(ctypes.byref(p), ctypes.byref(out)) == want
+    if not fine:
+        assert _weigh(native, p) == want

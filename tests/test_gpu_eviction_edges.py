@@ -3,13 +3,16 @@ count nothing."""
 
 import math
 
+import numpy as np
 import pytest
+
+from oracle import paged as OP
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from .test_gpu_eviction import check_weights, fresh_weights  # noqa: E402
-from .test_gpu_paged import Batch, bsr  # noqa: E402,F401
+from .test_gpu_paged import U, Batch, bsr  # noqa: E402,F401
 
 FORMS = {"few": 3, "mid": 30, "chunk": 200}  # rows of the first sequence, 4 / 2 heads
 
@@ -117,3 +120,37 @@ def test_one_nan_in_a_chunk(bsr, kind, what):
     fine = microseconds(lambda: call(lse, q, b.k_pages, b.k_exp))
     odd = microseconds(lambda: call(lse2, q2, k, ke))
     assert odd < 20 * fine, (odd, fine)
+
+
+def check_scaled(bsr, kind, news, qe, ke, se):
+    """Q near 2^qe (zeros below BF16's range), K near 2^ke, scale 2^se, lse by the oracle."""
+    n, scale = 333, 2.0 ** se
+    g = torch.Generator().manual_seed(2)
+    b = Batch([n], [news], 1, 64, kind, seed=3)
+    x = (torch.randn((n, 1, 128), generator=g) * 2.0 ** ke).bfloat16().cuda()
+    rs = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    bsr.cache_write(x, x, b.k_pages, b.v_pages, b.table, rs, b.kv_len, **b.exps)
+    k = bsr.cache_read(b.k_pages, b.v_pages, b.table, rs, b.kv_len, rows=n, **b.exps)[0].double().cpu().numpy()
+    q = ((0.25 + torch.rand((news, 4, 128), generator=g)) * 2.0 ** qe).bfloat16().cuda()
+    pos = list(range(n - news, n))
+    lse = torch.from_numpy(OP.paged_attention(q.double().cpu().numpy(), k, k, pos, n, scale=scale)[1]).float().cuda()
+    w = bsr.cache_weights(b.k_pages)
+    bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len, max_new=news, k_exp=b.k_exp, scale=scale)
+    got = torch.cat([w[p] for p in b.table[0].tolist()[:6]], 1)[:, :n].double().cpu().numpy()
+    ref, slack, count = OP.received(q.double().cpu().numpy(), lse.double().cpu().numpy(), k, pos, n, scale=scale)
+    assert np.all(np.abs(got - ref) <= 2 * 264 * U * slack + (2.0 ** -21 + (count + 8) * U) * ref + count * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 4, 20, 300])  # the two kernels for few rows, the one for more, chunks
+@pytest.mark.parametrize("qe,ke,se", [(120, -117, -5), (-117, 120, -5), (60, -58, -4), (50, 50, -100), (0, 100, -100), (100, 0, -100),
+                                      (-62, 0, 60), (0, -62, 60), (60, -120, 58)])
+def test_logits_of_large_and_small_factors(bsr, kind, news, qe, ke, se):
+    check_scaled(bsr, kind, news, qe, ke, se)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 4, 20, 300])
+@pytest.mark.parametrize("ke,se", [(0, 0), (119, 60), (119, -100), (-117, 60), (-117, -100)])
+def test_rows_of_zeros_weigh_all_keys_alike(bsr, kind, news, ke, se):
+    check_scaled(bsr, kind, news, -200, ke, se)
