@@ -1,5 +1,5 @@
-"""Weights of cached keys at their edges: values that are not numbers, rows that
-count nothing."""
+"""Weights and eviction at their edges: values that are not numbers, rows that
+count nothing, tables wider than their sequences."""
 
 import math
 
@@ -11,7 +11,7 @@ from oracle import paged as OP
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-from .test_gpu_eviction import check_weights, fresh_weights  # noqa: E402
+from .test_gpu_eviction import check_weights, evict_case, fresh_weights, run_evict  # noqa: E402
 from .test_gpu_paged import U, Batch, bsr  # noqa: E402,F401
 
 FORMS = {"few": 3, "mid": 30, "chunk": 200}  # rows of the first sequence, 4 / 2 heads
@@ -36,6 +36,18 @@ def weigh(bsr, b, q, lse, news, w=None, k=None, ke=None, **kw):
     return w
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_without_a_sum_in_every_form(bsr, kind, form):
+    """lse = -inf (a row that saw no key) and +inf."""
+    b, q, lse, news = form_batch(bsr, form, kind)
+    lse[0, 1], lse[b.rows - 1, 3] = -math.inf, math.inf
+    before = fresh_weights(b).cpu().numpy()
+    w = weigh(bsr, b, q, lse, news)
+    lse[lse == math.inf] = -math.inf  # to the oracle: no such row
+    check_weights(b, q, lse, before, w, 0, True)
+
+
 def spoil(b, s, j, h, value):
     """Copies of K and its exponents with one key that is not a number, or infinite."""
     k, ke = b.k_pages.clone(), None if b.k_exp is None else b.k_exp.clone()
@@ -45,6 +57,19 @@ def spoil(b, s, j, h, value):
     else:
         ke[pg, h, sl] = 255
     return k, ke, (pg, h, sl)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("j", [0, 135, 299])
+def test_a_key_that_is_nan_in_every_form(bsr, kind, form, j):
+    b, q, lse, news = form_batch(bsr, form, kind)
+    clean = weigh(bsr, b, q, lse, news)
+    k, ke, at = spoil(b, 0, j, 1, math.nan)
+    w = weigh(bsr, b, q, lse, news, k=k, ke=ke)
+    assert w[at].isnan()
+    w[at] = clean[at]
+    assert torch.equal(w, clean)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
@@ -120,6 +145,40 @@ def test_one_nan_in_a_chunk(bsr, kind, what):
     fine = microseconds(lambda: call(lse, q, b.k_pages, b.k_exp))
     odd = microseconds(lambda: call(lse2, q2, k, ke))
     assert odd < 20 * fine, (odd, fine)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_bad_pages_are_reported_by_the_form_for_chunks(bsr, kind):
+    b = Batch([300, 290], [200, 200], 2, 64, kind, seed=4)
+    q = torch.randn((b.rows, 4, 128), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    _, lse = bsr.paged_attn(q, *b.where, max_new=200, **b.exps)
+    clean = weigh(bsr, b, q, lse, 200)
+    ws = bsr.weigh_workspace(q, b.k_pages, b.table, 200)
+    assert ws.numel() > 256
+    for bad in (-1, b.pages, 2 ** 31 - 1, -2 ** 31):
+        t = b.table.clone()
+        t[0, 3] = bad
+        w = fresh_weights(b)
+        bsr.cache_weigh(q, lse, w, b.k_pages, t, b.row_start, b.kv_len, max_new=200, k_exp=b.k_exp, ws=ws)
+        assert bsr.sparse_attn_last_device_status(ws) == bsr.SA_EINVAL
+        lost = int(b.table_np[0, 3])
+        assert torch.equal(w[lost], fresh_weights(b)[lost])  # (nobody's row names it)
+        w[lost] = clean[lost]
+        assert torch.equal(w, clean)
+        bsr.cache_weigh(q, lse, w, b.k_pages, b.table, b.row_start, b.kv_len, max_new=200, k_exp=b.k_exp, ws=ws)
+        assert bsr.sparse_attn_last_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("to", [False, True])
+@pytest.mark.parametrize("lens,H,keep", [([1100, 300], 2, 700), ([700, 40, 333], 60, 200)])  # eight blocks a unit, and one
+def test_eviction_under_a_wide_table(bsr, kind, to, lens, H, keep):
+    """Entries past a sequence's pages are not looked at, however many there are."""
+    b, w = evict_case(lens, H, 64, kind, seed=3)
+    wide = torch.full((len(lens), 4096), -7, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    run_evict(bsr, b, w, keep, 4, 50, to)
 
 
 def check_scaled(bsr, kind, news, qe, ke, se):
