@@ -345,7 +345,9 @@ def prefix_attn(q, k_pages, v_pages, table, row_start, kv_len, group_start, pref
     once, from the pages of the group's first sequence that has rows, which the
     others' rows of ``table`` name too; all others by each sequence's own row.  A
     sequence's rows must lie behind the shared pages; of one without rows (an
-    empty slot) nothing has to agree with its group.  There is no window.
+    empty slot) nothing has to agree with its group.  There is no window.  A
+    batch of one sequence, or without rows, shares nothing: its groups are not
+    looked at.
 
     Returns (o, lse) as ``paged_attn``, equal up to the order of sums."""
     env = _env()

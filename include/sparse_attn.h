@@ -470,7 +470,8 @@ sa_status sparse_attn_paged_fwd(const sa_paged_params* p, const void* q, const v
  * seqs, 0 <= prefix_len[g] <= table_width * page_size, and that a sequence's
  * own rows lie behind its group's whole shared pages; else SA_EINVAL in the
  * status word, and the outputs of the group, or of the sequence, are
- * unspecified.
+ * unspecified.  Where seqs < 2 or rows is 0 nothing can be shared: the call is
+ * sparse_attn_paged_fwd's, and the groups are not looked at.
  * Errors: as sparse_attn_paged_fwd; SA_EINVAL also for groups < 0, window not
  * 0, a null or misaligned group_start, or prefix_len with groups > 0.
  */

@@ -110,3 +110,16 @@ def test_valid_calls_after_bad_groups(bsr, kind, news, bad):
     o, lse = bsr.prefix_attn(q, *b.where, gs, pl, max_new=news, **b.exps, ws=ws)
     assert bsr.sparse_attn_last_device_status(ws) == bsr.SA_OK
     check_attention(b, q, o, lse)
+
+
+@pytest.mark.parametrize("groups,prefix", [([0, 4], [64]), ([3, 1], [64]), ([0, 1], [-5]), ([0, 1], [64])])
+def test_one_sequence_shares_nothing(bsr, groups, prefix):
+    """Its groups are not looked at: the call is paged_attn's, bit for bit."""
+    b = Batch([200], [5], 2, 64, seed=4)
+    q = torch.randn((b.rows, 4, 128), device="cuda").bfloat16()
+    gs, pl = i32(*groups), i32(*prefix)
+    ws = bsr.prefix_workspace(q, b.k_pages, b.table, gs)
+    o, lse = bsr.prefix_attn(q, *b.where, gs, pl, ws=ws)
+    assert bsr.sparse_attn_last_device_status(ws) == bsr.SA_OK
+    o2, lse2 = bsr.paged_attn(q, *b.where)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
