@@ -22,10 +22,19 @@
 // 4096 in 8 heads, E4M3: 274 -> 229).  Moves to other pages are a kernel of their
 // own (113 -> 106 us for the first one below).
 //
+// Blocks a unit, the kernel and the shared memory for weights follow what the host
+// knows, the sequences, heads and the table's width, not the lengths.  Where a
+// block's part of the table's width is above 25600 tokens, the weights' memory leaves
+// one block an SM: under a table of 4096 entries the long context below takes 143 us
+// and the batch 125 (below, tables are as wide as the longest sequence).  Two
+// sequences over the budget among 64 have one block a head all the same: 47 us, and
+// 25 alone.
+//
 // Bound by memory; by latency where there are few tokens (and by the choice, 30 us
 // of a long context's).  Measured:
 //   64 sequences of 1024 to 8704, 8 heads, E4M3, 2048 stay, to other pages   106 us  4.9 TB/s (75.7 at a copy's rate)
-//   one of 67608, 24 heads, BF16, 16384 stay, in place                       99 us  4.2      (60.8)
+//   one of 67608, 24 heads, BF16, 16384 stay, in place                       98 us  4.2      (60.8)
+//                           E4M3                                             74 us  2.9      (31.4)
 //   one of 1152, 2 heads, BF16, 1024 stay, in place                          11.9 us  (four histograms, one after another)
 #include <cstdint>
 

@@ -35,7 +35,8 @@ namespace sa {
 namespace {
 
 constexpr int kWarps = 4;
-// Blocks an SM: what the registers of so many rows allow without spills.
+// Blocks an SM: what the registers of so many rows allow (BF16, up to eight rows:
+// with 86 bytes spilled).
 template <int kN>
 constexpr int kBlocks = kN == 1 ? 4 : 3;
 constexpr int kTileKeys = 16;  // keys of a warp's tile: inside one page

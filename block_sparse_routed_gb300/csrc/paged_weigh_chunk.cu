@@ -41,7 +41,8 @@
 // one's rows pass, widen codes, and write them to tensor memory.
 //
 // Measured (graphs of four calls; tensor rate of the visible pairs):
-//   2048 new of 33792, 40 / 8 heads, causal, BF16      570 us  1206 TFLOP/s
+//   2048 new of 33792, 40 / 8 heads, causal, BF16      573 us  1199 TFLOP/s
+//                                            E4M3      569 us  1208
 //   8704 of 8704, 24 / 24 heads, causal, BF16          212 us  1096
 //
 // Tensor memory: K of tile t in columns [64 t, + 64); scores of tile t, every
