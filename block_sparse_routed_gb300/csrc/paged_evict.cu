@@ -118,6 +118,11 @@ __device__ __forceinline__ void choose(const PagedArgs& c, const EvictArgs& e, i
   // the block's positions: [b0, b1), whole parts of 32 for each warp
   const int per_warp = (m + all_threads - 1) / all_threads * 32, per_block = per_warp * (threads / 32);
   const int b0 = min(static_cast<int64_t>(m), static_cast<int64_t>(rank) * per_block), b1 = min(static_cast<int64_t>(m), static_cast<int64_t>(b0) + per_block);
+  // Weights past the shared memory are read in every pass.  Where another sequence's
+  // moves change them meanwhile, on a page that the two must not share, more or fewer
+  // may stay than there is room for: whatever comes of it, places hold positions.
+  if (per_block > cache)
+    for (int i = first_thread; i < want; i += all_threads) kept[e.first + i] = e.first + i;
   const int32_t* table = c.table + s * c.table_stride;
   auto weight_at = [&](int i) {
     const int pos = e.first + i, page = __ldg(table + (pos >> c.page_shift));
@@ -229,7 +234,8 @@ __device__ __forceinline__ void choose(const PagedArgs& c, const EvictArgs& e, i
     const unsigned same = __ballot_sync(0xFFFFFFFFu, in && k == least), below = (1u << lane) - 1;
     const bool stays = in && (k > least || (k == least && eq_before + __popc(same & below) < equals));
     const unsigned mask = __ballot_sync(0xFFFFFFFFu, stays);
-    if (stays) kept[e.first + at + __popc(mask & below)] = e.first + i + lane;
+    const int to = at + __popc(mask & below);
+    if (stays && to < want) kept[e.first + to] = e.first + i + lane;
     at += __popc(mask);
     eq_before += __popc(same);
   }

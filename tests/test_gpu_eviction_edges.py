@@ -213,3 +213,31 @@ def test_logits_of_large_and_small_factors(bsr, kind, news, qe, ke, se):
 @pytest.mark.parametrize("ke,se", [(0, 0), (119, 60), (119, -100), (-117, 60), (-117, -100)])
 def test_rows_of_zeros_weigh_all_keys_alike(bsr, kind, news, ke, se):
     check_scaled(bsr, kind, news, -200, ke, se)
+
+
+@pytest.mark.parametrize("to", [False, True])
+def test_pages_that_must_not_be_shared(bsr, to):
+    """Two sequences of one table's row over their budget, longer than the weights
+    that shared memory holds: what stays is anyone's guess, but all of it are
+    positions, and nothing lies outside of the call's tensors."""
+    H, page, n, keep = 80, 128, 50001, 20000
+    need, more = -(-n // page), -(-keep // page)
+    pages = need + 2 * more + 1
+    k, v, ke, ve = bsr.paged_cache(pages, H, page, "e4m3")
+    for t in (k, v):
+        t.view(torch.uint8).fill_(8)
+    ke.fill_(120), ve.fill_(121)
+    w = torch.rand((pages, H, page), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    table = torch.arange(need, dtype=torch.int32, device="cuda").repeat(2, 1)
+    to_table = need + torch.arange(2 * more, dtype=torch.int32, device="cuda").reshape(2, more)
+    kl = torch.full((2,), n, dtype=torch.int32, device="cuda")
+    pool = torch.full((2 * H * keep + 2048,), -5, dtype=torch.int32, device="cuda")
+    kept = pool[1024:-1024].view(2, H, keep)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    spare = w[-1].clone()
+    _, new_len = bsr.cache_evict(k, v, w, table, kl, keep, first=3, last=70, to_table=to_table if to else None, k_exp=ke, v_exp=ve,
+                                 kept=kept, ws=ws)
+    assert bsr.sparse_attn_last_device_status(ws) == 0 and new_len.tolist() == [keep] * 2
+    assert int(kept.min()) >= 0 and int(kept.max()) < n
+    assert (pool[:1024] == -5).all() and (pool[-1024:] == -5).all() and torch.equal(w[-1], spare)
+    assert (kept[:, :, :3] == torch.arange(3, device="cuda")).all() and (kept[:, :, -70:] == torch.arange(n - 70, n, device="cuda")).all()
